@@ -35,7 +35,8 @@ EXPORTS = ("fsdp_layout_create", "fsdp_layout_destroy", "fsdp_layout_query", "fs
            "fsdp_accumulate_grads", "fsdp_hsdp_reduce_scatter_adamw", "fsdp_zero1_adamw_broadcast",
            "fsdp_set_rs_kernel", "fsdp_rs_kernel_for", "fsdp_wait_selftest", "fsdp_adamw_step_consts_make",
            "fsdp_reduce_scatter_adamw_consts", "fsdp_adamw_step_consts_upload", "fsdp_collective_payload",
-           "fsdp_accumulate_reduce_scatter_adamw")
+           "fsdp_accumulate_reduce_scatter_adamw", "fsdp_linear_workspace_bytes", "fsdp_linear_forward",
+           "fsdp_linear_dgrad", "fsdp_linear_wgrad", "fsdp_dropout")
 
 
 class FsdpError(RuntimeError):
@@ -74,6 +75,20 @@ class AdamWStepConsts(C.Structure):
     _fields_ = [("decay", C.c_float), ("om1", C.c_float), ("om2", C.c_float), ("step_size", C.c_float),
                 ("bc2s", C.c_float), ("beta1", C.c_float), ("beta2", C.c_float), ("eps", C.c_float),
                 ("n_avg", C.c_float), ("reserved", C.c_float * 3)]
+
+
+FSDP_ACT_NONE, FSDP_ACT_RELU, FSDP_ACT_GELU, FSDP_ACT_SILU = 0, 1, 2, 3
+ACTIVATIONS = {"none": FSDP_ACT_NONE, "relu": FSDP_ACT_RELU, "gelu": FSDP_ACT_GELU, "silu": FSDP_ACT_SILU}
+
+
+class DropoutSpec(C.Structure):
+    """A dropout with a mask drawn from (seed, layer, row, column) (fsdp_dropout_spec);
+    row0 is the index of the first row of a call's matrix in the whole batch."""
+    _fields_ = [("p", C.c_double), ("seed", C.c_uint64), ("row0", C.c_int64), ("layer", C.c_uint32),
+                ("reserved", C.c_uint32)]
+
+    def __init__(self, p: float, seed: int, layer: int = 0, row0: int = 0):
+        super().__init__(float(p), seed, row0, layer, 0)
 
 
 _lib: Optional[C.CDLL] = None
@@ -115,6 +130,15 @@ def lib() -> C.CDLL:
                                                      C.POINTER(AdamWHparams), i64, vp]
         L.fsdp_zero1_adamw_broadcast.argtypes = [vp, i32, i32, C.POINTER(vp), i32, vp, vp, vp, C.POINTER(vp), i32,
                                                  C.POINTER(AdamWHparams), i64, vp]
+        sz, drop = C.c_size_t, C.POINTER(DropoutSpec)
+        L.fsdp_linear_workspace_bytes.argtypes = [i64, i64, i64, i32, i32]
+        L.fsdp_linear_workspace_bytes.restype = sz
+        L.fsdp_linear_forward.argtypes = [i64, i64, i64, i32, vp, i64, vp, i64, vp, i32, drop, vp, i64, vp, i64, vp,
+                                          i64, vp, sz, vp]
+        L.fsdp_linear_dgrad.argtypes = [i64, i64, i64, i32, vp, i64, vp, i64, i32, vp, i64, drop, vp, i64, vp, i64,
+                                        vp, sz, vp]
+        L.fsdp_linear_wgrad.argtypes = [i64, i64, i64, i32, vp, i64, vp, i64, vp, i64, vp, i32, i32, vp, sz, vp]
+        L.fsdp_dropout.argtypes = [i64, i64, i32, vp, i64, drop, vp, i64, vp, i64, vp]
         L.fsdp_check_status.argtypes = [vp]
         L.fsdp_set_rs_kernel.argtypes = [i32]
         L.fsdp_rs_kernel_for.argtypes = [vp, i32]
@@ -388,7 +412,8 @@ def fsdp_accumulate_reduce_scatter_adamw(layout: Layout, unit_begin: int, unit_e
                                                       _ptr_array(micro), micro_dtype, _ptr(master), _ptr(exp_avg),
                                                       _ptr(exp_avg_sq), _ptr(param_shards), _ptr(grad_shard_out),
                                                       C.byref(h), step, _stream(stream)),
-           "fsdp_accumulate_reduce_scatter_adamw")
+           "fsdp_accumulate_reduce_scatter_adamw", "fsdp_linear_workspace_bytes", "fsdp_linear_forward",
+           "fsdp_linear_dgrad", "fsdp_linear_wgrad", "fsdp_dropout")
 
 
 def fsdp_hsdp_reduce_scatter_adamw(layout: Layout, unit_begin: int, unit_end: int, n_groups: int, grad_replicas,
@@ -419,6 +444,121 @@ def fsdp_zero1_adamw_broadcast(layout: Layout, unit_begin: int, unit_end: int, g
                                             grad_dtype, _ptr(master), _ptr(exp_avg), _ptr(exp_avg_sq),
                                             _ptr_array(param_replicas), param_dtype, C.byref(_hp(hp)), step,
                                             _stream(stream)), "fsdp_zero1_adamw_broadcast")
+
+
+# -- layers between the all-gather and the reduce-scatter -------------------------
+def _matrix(x, name: str, rows: int, cols: int, dtype):
+    """(address, row stride) of a 2-D tensor of the given shape whose rows are contiguous."""
+    if x is None:
+        return None, 0
+    if x.dtype != dtype:
+        raise TypeError(f"{name} is {x.dtype}, expected {dtype}")
+    if x.dim() != 2 or x.shape[0] != rows or x.shape[1] != cols:
+        raise ValueError(f"{name} is {tuple(x.shape)}, expected {(rows, cols)}")
+    ld, one = x.stride()
+    if one != 1 and cols > 1:
+        raise ValueError(f"{name}: a row's elements must be contiguous")
+    if rows <= 1 and ld < cols:
+        ld = cols                                # torch leaves a single row's stride arbitrary
+    return x.data_ptr(), ld
+
+
+def _vector(x, name: str, n: int, dtype):
+    if x is None:
+        return None
+    if x.dtype != dtype:
+        raise TypeError(f"{name} is {x.dtype}, expected {dtype}")
+    if x.dim() != 1 or x.shape[0] != n:
+        raise ValueError(f"{name} is {tuple(x.shape)}, expected {(n,)}")
+    if n > 1 and x.stride(0) != 1:
+        raise ValueError(f"{name} must be contiguous")
+    return x.data_ptr()
+
+
+def _act(act) -> int:
+    if isinstance(act, str):
+        if act not in ACTIVATIONS:
+            raise ValueError(f"unknown activation {act!r}: {sorted(ACTIVATIONS)}")
+        return ACTIVATIONS[act]
+    return int(act)
+
+
+def _workspace(ws):
+    return (None, 0) if ws is None else (_ptr(ws), ws.numel() * ws.element_size())
+
+
+def _drop(spec):
+    return None if spec is None else C.byref(spec)
+
+
+def fsdp_linear_workspace_bytes(rows: int, cols_in: int, cols_out: int, dtype, aligned: Optional[bool] = None) -> int:
+    """Scratch bytes of the three linear calls at these sizes.  aligned: every x, w and dz
+    has a base address and row stride that are multiples of 16 bytes (default: widths of
+    whole 16-byte rows, as contiguous tensors of their own have)."""
+    import torch
+    code = dtype if isinstance(dtype, int) else {torch.float32: FSDP_F32, torch.bfloat16: FSDP_BF16}[dtype]
+    if aligned is None:
+        e = 4 if code == FSDP_F32 else 2
+        aligned = cols_in * e % 16 == 0 and cols_out * e % 16 == 0
+    return int(lib().fsdp_linear_workspace_bytes(rows, cols_in, cols_out, code, int(aligned)))
+
+
+def fsdp_linear_forward(x, w, y, bias=None, act="none", preact=None, dropout: Optional[DropoutSpec] = None,
+                        residual=None, workspace=None, stream=None) -> None:
+    """y = residual + drop(act(x w^T + bias)); z = x w^T + bias into preact where given.
+    x [rows, in], w [out, in], y / preact / residual [rows, out], bias [out], one dtype."""
+    code, dt = _dtype_code(x), x.dtype
+    (rows, cin), cout = x.shape, w.shape[0]
+    px, ldx = _matrix(x, "x", rows, cin, dt)
+    pw, ldw = _matrix(w, "w", cout, cin, dt)
+    py, ldy = _matrix(y, "y", rows, cout, dt)
+    pr, ldr = _matrix(residual, "residual", rows, cout, dt)
+    pz, ldz = _matrix(preact, "preact", rows, cout, dt)
+    pws, nws = _workspace(workspace)
+    _check(lib().fsdp_linear_forward(rows, cin, cout, code, px, ldx, pw, ldw, _vector(bias, "bias", cout, dt), _act(act),
+                                     _drop(dropout), pr, ldr, py, ldy, pz, ldz, pws, nws, _stream(stream)),
+           "fsdp_linear_forward")
+
+
+def fsdp_linear_dgrad(dz, w, dx, act="none", preact=None, dropout: Optional[DropoutSpec] = None, residual=None,
+                      workspace=None, stream=None) -> None:
+    """dx = residual + act'(preact) * drop(dz w): dz [rows, out], w [out, in], dx / preact /
+    residual [rows, in]; act, preact and dropout are those of the layer before."""
+    code, dt = _dtype_code(dz), dz.dtype
+    (rows, cout), cin = dz.shape, w.shape[1]
+    pg, ldg = _matrix(dz, "dz", rows, cout, dt)
+    pw, ldw = _matrix(w, "w", cout, cin, dt)
+    px, ldx = _matrix(dx, "dx", rows, cin, dt)
+    pz, ldz = _matrix(preact, "preact", rows, cin, dt)
+    pr, ldr = _matrix(residual, "residual", rows, cin, dt)
+    pws, nws = _workspace(workspace)
+    _check(lib().fsdp_linear_dgrad(rows, cin, cout, code, pg, ldg, pw, ldw, _act(act), pz, ldz, _drop(dropout), pr, ldr,
+                                   px, ldx, pws, nws, _stream(stream)), "fsdp_linear_dgrad")
+
+
+def fsdp_linear_wgrad(dz, x, dw, db=None, accumulate: bool = False, workspace=None, stream=None) -> None:
+    """dw (+)= dz^T x and db (+)= the column sums of dz: dz [rows, out], x [rows, in] of one
+    dtype, dw [out, in] and db [out] of one dtype (a gradient replica's, or fp32)."""
+    code, dt = _dtype_code(dz), dz.dtype
+    (rows, cout), cin = dz.shape, x.shape[1]
+    pg, ldg = _matrix(dz, "dz", rows, cout, dt)
+    px, ldx = _matrix(x, "x", rows, cin, dt)
+    pw, ldw = _matrix(dw, "dw", cout, cin, dw.dtype)
+    pws, nws = _workspace(workspace)
+    _check(lib().fsdp_linear_wgrad(rows, cin, cout, code, pg, ldg, px, ldx, pw, ldw, _vector(db, "db", cout, dw.dtype),
+                                   _dtype_code(dw), int(bool(accumulate)), pws, nws, _stream(stream)),
+           "fsdp_linear_wgrad")
+
+
+def fsdp_dropout(x, y, dropout: Optional[DropoutSpec], residual=None, stream=None) -> None:
+    """y = residual + drop(x), [rows, cols] each; the same call on the gradient is its backward."""
+    code, dt = _dtype_code(x), x.dtype
+    rows, cols = x.shape
+    px, ldx = _matrix(x, "x", rows, cols, dt)
+    py, ldy = _matrix(y, "y", rows, cols, dt)
+    pr, ldr = _matrix(residual, "residual", rows, cols, dt)
+    _check(lib().fsdp_dropout(rows, cols, code, px, ldx, _drop(dropout), pr, ldr, py, ldy, _stream(stream)),
+           "fsdp_dropout")
 
 
 def fsdp_reshard(layout: Layout, unit_begin: int, unit_end: int, full=None, master=None, param_shards=None,

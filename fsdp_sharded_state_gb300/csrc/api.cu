@@ -17,6 +17,7 @@
 #include "internal.hpp"
 #include "kernels.hpp"
 #include "layout.hpp"
+#include "linear.hpp"
 #include "staged.hpp"
 
 using fsdp::Seg;
@@ -513,6 +514,12 @@ int fsdp_check_status(fsdp_stream_t stream) {
     unsigned int gave_up = 0;
     e = fsdp::take_wait_error(&gave_up);
     if (e != cudaSuccess) return cuda_fail(e, "wait status read");
+    for (auto take : {fsdp::take_wait_error_forward, fsdp::take_wait_error_dgrad, fsdp::take_wait_error_wgrad}) {
+        unsigned int linear = 0;
+        e = take(&linear);
+        if (e != cudaSuccess) return cuda_fail(e, "wait status read");
+        gave_up |= linear;
+    }
     return gave_up ? FSDP_ETIMEOUT : FSDP_OK;
 }
 

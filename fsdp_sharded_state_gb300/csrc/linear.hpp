@@ -1,0 +1,77 @@
+// linear.hpp -- host-side types and launchers of the linear-layer kernels.
+#pragma once
+
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+#include "philox.cuh"
+
+namespace fsdp {
+
+// A linear layer's three products, as D[M, N] = sum over k of A[M, k] B[N, k]:
+//   forward   A = w  (out features), B = x   (rows), K = in features;  out[row = N][col = M]
+//   dgrad     A = w^T (in features), B = dz  (rows), K = out features; out[row = N][col = M]
+//   wgrad     A = dz^T (out features), B = x^T (in features), K = rows; out[row = M][col = N]
+enum LinMode { kForward = 0, kDgrad = 1, kWgrad = 2 };
+
+// The epilogue of a product; pointers in the output's element type.
+struct LinEpi {
+    void* out;
+    int64_t ldo;
+    const void* bias;          // forward
+    const void* residual;      // forward, dgrad: added last
+    int64_t ldr;
+    void* preact;              // forward: written; dgrad: read
+    int64_t ldz;
+    int64_t rows, cols;        // of out
+    int32_t act;               // fsdp_act
+    int32_t accumulate;        // wgrad: out += instead of out =
+    int32_t vec;               // every matrix here has 16-byte aligned rows
+    Drop drop;
+};
+
+// One operand as the tensor maps see it: `planes` row-major bf16 matrices of rows x cols,
+// 16-byte aligned base, ld a multiple of 8 elements, plane a multiple of 8 elements.
+struct LinOperand {
+    const void* ptr;
+    int64_t rows, cols, ld, plane;
+};
+
+struct LinProblem {
+    LinMode mode;
+    int64_t M, N, K;
+    LinOperand a, b;
+    int planes;                // 1: bf16 operands; 3: fp32 operands as three bf16 terms
+    bool out_bf16;
+    LinEpi epi;
+};
+
+cudaError_t launch_linear_forward(const LinProblem& p, cudaStream_t st);
+cudaError_t launch_linear_dgrad(const LinProblem& p, cudaStream_t st);
+cudaError_t launch_linear_wgrad(const LinProblem& p, cudaStream_t st);
+
+// Operands brought into the form of LinOperand: a bf16 matrix copied to aligned rows, or
+// an fp32 matrix split into three bf16 planes (see linear_pack.cu).  Up to two per launch.
+struct PackJob {
+    const void* src;
+    int64_t rows, cols, ld;
+    void* dst;
+    int64_t dld, plane;
+};
+cudaError_t launch_pack(const PackJob* jobs, int n, bool f32, cudaStream_t st);
+
+// db[c] (+)= sum over rows of dz[r][c].
+cudaError_t launch_colsum(const void* dz, bool dz_bf16, int64_t rows, int64_t cols, int64_t ld, void* db, bool db_bf16,
+                          bool accumulate, cudaStream_t st);
+
+// y = residual + drop(x); drop.on = 0 copies.
+cudaError_t launch_dropout(const void* x, int64_t ldx, const void* residual, int64_t ldr, void* y, int64_t ldy, bool bf16,
+                           int64_t rows, int64_t cols, const Drop& d, cudaStream_t st);
+
+// Reads and clears the wait words of the linear kernels (synchronous).
+cudaError_t take_wait_error_forward(unsigned int* flag);   // linear_forward.cu
+cudaError_t take_wait_error_dgrad(unsigned int* flag);     // linear_dgrad.cu
+cudaError_t take_wait_error_wgrad(unsigned int* flag);     // linear_wgrad.cu
+
+}  // namespace fsdp

@@ -1,0 +1,14 @@
+// linear_dgrad.cu -- dx = residual + act'(z) drop(dz w): the input gradient of a linear
+// layer, through the dropout and the activation of the layer before it.
+#include "linear_kernel.cuh"
+
+namespace fsdp {
+
+cudaError_t launch_linear_dgrad(const LinProblem& p, cudaStream_t st) {
+    if (p.planes == 3) return launch_cfg<LinCfg<kDgrad, float, 1, 128, 3, 4, false>>(p, 1, st);
+    return launch_cfg<LinCfg<kDgrad, uint16_t, 1, 128, 1, 0, false>>(p, 1, st);
+}
+
+cudaError_t take_wait_error_dgrad(unsigned int* flag) { return take_local_wait_error(flag); }
+
+}  // namespace fsdp

@@ -1,0 +1,574 @@
+// linear_kernel.cuh -- the matrix kernel of the linear layers (sm_103a).
+//
+// D[M, N] = sum over k of A[M, k] B[N, k] on the 5th-generation tensor cores, fp32
+// accumulators in TMEM, with the layer's epilogue (bias, activation or its derivative,
+// dropout, residual, accumulation) applied before the one rounding to the output type.
+//
+// Roles of a CTA (10 warps): warp 8 loads the operand tiles with tensor-map copies into a
+// ring of stages, warp 9 issues the MMAs, warps 0-7 empty the accumulators.  The
+// accumulators are double-buffered, so a persistent CTA's epilogue runs beside the next
+// tile's products.  Operands keep the row-major layout that the user's tensors have: the
+// matrix descriptors take K-major tiles (forward: w and x; dgrad: dz) and MN-major tiles
+// (dgrad: w; wgrad: dz and x), so nothing is transposed in memory.
+//
+// Every wait on an mbarrier is bounded; a role that gives up records it (g_wait_error of
+// this translation unit, read by fsdp_check_status), lets copies in flight land and goes
+// to the teardown, which every thread of the CTA (and of the cluster) reaches on every path.
+#pragma once
+
+#include "internal.hpp"
+#include "linear.hpp"
+#include "tc5.cuh"
+
+namespace fsdp {
+namespace {
+
+constexpr int kEpiWarps = 8;
+constexpr int kLinThreads = (kEpiWarps + 2) * 32;
+constexpr int kKb = 64;                        // K elements per stage: 128-byte swizzled rows
+constexpr int kLinMaxStages = 8;
+constexpr int kUnitFloats = 32 * 32;           // an epilogue unit: 32 rows x 32 columns
+
+// ---- loads and stores of n <= 8 consecutive elements as fp32 ------------------------
+__device__ __forceinline__ void load8(const uint16_t* p, float (&v)[8]) {
+    const uint4 u = ldu4(p);
+    v[0] = bf16lo(u.x); v[1] = bf16hi(u.x); v[2] = bf16lo(u.y); v[3] = bf16hi(u.y);
+    v[4] = bf16lo(u.z); v[5] = bf16hi(u.z); v[6] = bf16lo(u.w); v[7] = bf16hi(u.w);
+}
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+    const float4 a = ld4(p), b = ld4(p + 4);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+__device__ __forceinline__ void store8(uint16_t* p, const float (&v)[8]) {
+    stu4(p, make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])));
+}
+__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+    st4(p, make_float4(v[0], v[1], v[2], v[3]));
+    st4(p + 4, make_float4(v[4], v[5], v[6], v[7]));
+}
+__device__ __forceinline__ float load1(const uint16_t* p) { return bf16f(*p); }
+__device__ __forceinline__ float load1(const float* p) { return *p; }
+__device__ __forceinline__ void store1(uint16_t* p, float v) { *p = to_bf16(v); }
+__device__ __forceinline__ void store1(float* p, float v) { *p = v; }
+
+// n elements of p, by vectors when all 8 are there; V = 1 loads one element.
+template <int V, typename T>
+__device__ __forceinline__ void load_n(const T* p, float (&v)[V], int n) {
+    if constexpr (V == 8) {
+        if (n == 8) {
+            load8(p, v);
+            return;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = i < n ? load1(p + i) : 0.f;
+}
+template <int V, typename T>
+__device__ __forceinline__ void store_n(T* p, const float (&v)[V], int n) {
+    if constexpr (V == 8) {
+        if (n == 8) {
+            store8(p, v);
+            return;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        if (i < n) store1(p + i, v[i]);
+}
+
+// ---- activations (fp32) --------------------------------------------------------------
+// gelu(z) = z Phi(z), silu(z) = z / (1 + exp(-z)).
+__device__ __forceinline__ float phi(float z) { return fmaf(0.5f, erff(z * 0.70710678118654752f), 0.5f); }
+__device__ __forceinline__ float act1(float z, int act) {
+    if (act == FSDP_ACT_RELU) return z < 0.f ? 0.f : z;      // NaN stays NaN
+    if (act == FSDP_ACT_GELU) return z * phi(z);
+    if (act == FSDP_ACT_SILU) return z / (1.f + expf(-z));
+    return z;
+}
+// g * act'(z): gelu' = Phi(z) + z exp(-z^2/2) / sqrt(2 pi), silu' = s (1 + z (1 - s)).
+__device__ __forceinline__ float act1_grad(float g, float z, int act) {
+    if (act == FSDP_ACT_RELU) return z > 0.f ? g : (z != z ? z : 0.f);
+    if (act == FSDP_ACT_GELU) return g * fmaf(z * 0.39894228040143268f, expf(-0.5f * z * z), phi(z));
+    if (act == FSDP_ACT_SILU) {
+        const float s = 1.f / (1.f + expf(-z));
+        return g * (s * fmaf(z, 1.f - s, 1.f));
+    }
+    return g;
+}
+
+template <int V>
+__device__ __forceinline__ void drop_n(const Drop& d, int64_t row, int64_t col, float (&v)[V]) {
+    if constexpr (V == 8) {                                   // col is a multiple of 8
+        const uint4 a = drop_words(d, row, col >> 2), b = drop_words(d, row, (col >> 2) + 1);
+        v[0] = drop1(d, a.x, v[0]); v[1] = drop1(d, a.y, v[1]); v[2] = drop1(d, a.z, v[2]); v[3] = drop1(d, a.w, v[3]);
+        v[4] = drop1(d, b.x, v[4]); v[5] = drop1(d, b.y, v[5]); v[6] = drop1(d, b.z, v[6]); v[7] = drop1(d, b.w, v[7]);
+    } else {
+        const uint4 a = drop_words(d, row, col >> 2);
+        const int k = int(col & 3);
+        v[0] = drop1(d, k == 0 ? a.x : k == 1 ? a.y : k == 2 ? a.z : a.w, v[0]);
+    }
+}
+
+// The epilogue of V consecutive columns of one row (n of them inside the matrix).
+template <int MODE, typename OT, int V>
+__device__ __forceinline__ void emit(const LinEpi& ep, int64_t row, int64_t col, float (&v)[V], int n) {
+    OT* const out = static_cast<OT*>(ep.out) + row * ep.ldo + col;
+    float t[V];
+    if constexpr (MODE == kForward) {
+        if (ep.bias) {
+            load_n<V>(static_cast<const OT*>(ep.bias) + col, t, n);
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[i] += t[i];
+        }
+        if (ep.preact) store_n<V>(static_cast<OT*>(ep.preact) + row * ep.ldz + col, v, n);
+        if (ep.act != FSDP_ACT_NONE) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[i] = act1(v[i], ep.act);
+        }
+        if (ep.drop.on) drop_n<V>(ep.drop, row, col, v);
+    }
+    if constexpr (MODE == kDgrad) {
+        if (ep.drop.on) drop_n<V>(ep.drop, row, col, v);
+        if (ep.act != FSDP_ACT_NONE) {
+            load_n<V>(static_cast<const OT*>(ep.preact) + row * ep.ldz + col, t, n);
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[i] = act1_grad(v[i], t[i], ep.act);
+        }
+    }
+    if constexpr (MODE != kWgrad) {
+        if (ep.residual) {
+            load_n<V>(static_cast<const OT*>(ep.residual) + row * ep.ldr + col, t, n);
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[i] += t[i];
+        }
+    } else if (ep.accumulate) {
+        load_n<V>(out, t, n);
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] += t[i];
+    }
+    store_n<V>(out, v, n);
+}
+
+// A unit in shared memory: [32 rows][32 columns] fp32, the 16-byte groups of row r at
+// group index g ^ (r & 7), so that both ways of writing it (a lane holds a row, a lane
+// holds a column) and the row-wise reads are free of bank conflicts.
+__device__ __forceinline__ int unit_at(int r, int c) { return r * 32 + ((((c >> 2) ^ (r & 7)) << 2) | (c & 3)); }
+
+// Adds the `slots` copies of a unit (kUnitFloats apart, in order) and emits it.
+template <int MODE, typename OT>
+__device__ __forceinline__ void emit_unit(const LinEpi& ep, const float* unit, int slots, int64_t row0, int64_t col0, int lane) {
+    if (ep.vec) {
+        const int64_t col = col0 + (lane & 3) * 8;
+        const int64_t left = ep.cols - col;
+        const int n = left >= 8 ? 8 : int(left);
+#pragma unroll
+        for (int it = 0; it < 4; ++it) {
+            const int r = it * 8 + (lane >> 2);
+            float v[8];
+            const float* p = unit + unit_at(r, (lane & 3) * 8);
+            const float* q = unit + unit_at(r, (lane & 3) * 8 + 4);
+            float4 a = ld4(p), b = ld4(q);
+            for (int s = 1; s < slots; ++s) {
+                const float4 c = ld4(p + s * kUnitFloats), d = ld4(q + s * kUnitFloats);
+                a.x += c.x; a.y += c.y; a.z += c.z; a.w += c.w;
+                b.x += d.x; b.y += d.y; b.z += d.z; b.w += d.w;
+            }
+            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+            if (row0 + r < ep.rows && n > 0) emit<MODE, OT, 8>(ep, row0 + r, col, v, n);
+        }
+    } else {                                     // any alignment: a lane per column
+        const int64_t col = col0 + lane;
+#pragma unroll 1
+        for (int r = 0; r < 32; ++r) {
+            float v[1] = {unit[unit_at(r, lane)]};
+            for (int s = 1; s < slots; ++s) v[0] += unit[unit_at(r, lane) + s * kUnitFloats];
+            if (row0 + r < ep.rows && col < ep.cols) emit<MODE, OT, 1>(ep, row0 + r, col, v, 1);
+        }
+    }
+}
+
+// A kernel configuration.  CG CTAs share a tile of 128 CG x BN; PL bf16 planes per operand
+// (3 planes: six products, of the terms whose exponents add up to at most two steps); CH:
+// K steps after which the accumulators are added to fp32 registers (0: never).  SPLIT: the
+// CTAs of a cluster (2, 4 or 8, CG = 1) take a share of K each and join through shared memory.
+template <int MODE_, typename OT_, int CG_, int BN_, int PL_, int CH_, bool SPLIT_>
+struct LinCfg {
+    using OT = OT_;
+    static constexpr int MODE = MODE_, CG = CG_, BN = BN_, PL = PL_, CH = CH_;
+    static constexpr bool SPLIT = SPLIT_;
+    static constexpr bool A_MN = MODE != kForward, B_MN = MODE == kWgrad;
+    static constexpr int BROWS = BN / CG;                        // B rows a CTA loads
+    static constexpr int A_BYTES = 128 * 128, B_BYTES = BROWS * 128;
+    static constexpr int STAGE = PL * (A_BYTES + B_BYTES);
+    // the epilogue's shared memory: a unit per warp, or the join's slots
+    static constexpr int EPI = SPLIT ? (BN >= 128 ? 64 : 32) * 1024 : kEpiWarps * kUnitFloats * 4;
+    static constexpr int FIT = (227 * 1024 - 2048 - EPI) / STAGE;
+    static constexpr int STAGES = FIT < kLinMaxStages ? FIT : kLinMaxStages;
+    static constexpr int SMEM = STAGES * STAGE + EPI + 2048;     // + alignment, barriers
+    static constexpr int TMEM = 2 * BN < 32 ? 32 : 2 * BN;
+    static_assert(STAGES >= 2, "two stages");
+    static_assert(SMEM > 114 * 1024 && SMEM <= 227 * 1024, "one CTA per SM: its TMEM is never contended");
+    static_assert(!B_MN || BROWS % 64 == 0, "MN-major tiles come in chunks of 64");
+    static_assert(!SPLIT || CG == 1, "a cluster is a pair or a split");
+};
+
+struct LinShape {
+    int32_t m_tiles, n_tiles, n_kb, splits;
+};
+
+template <class C>
+__global__ void __launch_bounds__(kLinThreads, 1)
+k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const LinShape sh,
+         const __grid_constant__ LinEpi ep, uint64_t wait_ns) {
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    unsigned char* const smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t rank = (C::CG == 2 || C::SPLIT) ? cluster_rank() : 0;
+    float* const epi_smem = reinterpret_cast<float*>(smem + C::STAGES * C::STAGE);
+    const uint32_t bars = smem_addr(smem + C::STAGES * C::STAGE + C::EPI);
+    const uint32_t full = bars, empty = bars + 8 * kLinMaxStages, acc_full = empty + 8 * kLinMaxStages,
+                   acc_empty = acc_full + 16, tmem_word = acc_empty + 16;
+    const bool leader = C::CG == 1 || rank == 0;
+
+    if (warp == 0) tmem_alloc<C::CG>(tmem_word, C::TMEM);
+    if (tid == kEpiWarps * 32) {
+        tma_prefetch_map(&map_a);
+        tma_prefetch_map(&map_b);
+        for (int s = 0; s < C::STAGES; ++s) {
+            mbar_init(full + 8 * s, 1);
+            mbar_init(empty + 8 * s, 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(acc_full + 8 * b, 1);
+            mbar_init(acc_empty + 8 * b, kEpiWarps * C::CG);
+        }
+        mbar_fence_init();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if constexpr (C::CG == 2 || C::SPLIT) {      // every CTA's barriers exist before any is signalled
+        cluster_arrive();
+        cluster_wait();
+    }
+    tc_fence_after();
+    uint32_t tmem;
+    asm volatile("ld.shared::cta.u32 %0, [%1];" : "=r"(tmem) : "r"(tmem_word) : "memory");
+    pdl_wait();
+
+    const int n_tiles = sh.m_tiles * sh.n_tiles;
+    const int n_clusters = C::CG == 2 ? gridDim.x / 2 : C::SPLIT ? gridDim.x / sh.splits : gridDim.x;
+    const int cluster = C::CG == 2 ? blockIdx.x / 2 : C::SPLIT ? blockIdx.x / sh.splits : blockIdx.x;
+    // this CTA's K steps
+    const int kb0 = C::SPLIT ? int(int64_t(sh.n_kb) * rank / sh.splits) : 0;
+    const int kb1 = C::SPLIT ? int(int64_t(sh.n_kb) * (rank + 1) / sh.splits) : sh.n_kb;
+    const int chunk = C::CH ? C::CH : sh.n_kb;
+
+    // Tiles in bands of 8 along M, N outer inside a band: concurrently running tiles share
+    // operand rows in L2.
+    auto tile_at = [&](int t, int& mt, int& nt) {
+        const int band = 8 * sh.n_tiles, g = t / band, first = g * 8;
+        const int high = sh.m_tiles - first < 8 ? sh.m_tiles - first : 8;
+        const int r = t - g * band;
+        mt = first + r % high;
+        nt = r / high;
+    };
+
+    if (warp == kEpiWarps) {
+        // ---- loads ----
+        if (lane == 0) {
+            bool ok = true;
+            uint32_t it = 0;
+            for (int t = cluster; ok && t < n_tiles; t += n_clusters) {
+                int mt, nt;
+                tile_at(t, mt, nt);
+                const int m0 = (mt * C::CG + (C::CG == 2 ? int(rank) : 0)) * 128;
+                const int n0 = nt * C::BN + (C::CG == 2 ? int(rank) * C::BROWS : 0);
+                for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                    const uint32_t s = it % C::STAGES, use = it / C::STAGES;
+                    if (use > 0 && !mbar_wait_bounded(empty + 8 * s, (use - 1) & 1, wait_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    if (leader) mbar_arrive_tx(full + 8 * s, C::CG * C::STAGE);
+                    const uint32_t bar = C::CG == 2 ? map_rank(full + 8 * s, 0) : full + 8 * s;
+                    const uint32_t st = smem_addr(smem + s * C::STAGE);
+#pragma unroll
+                    for (int p = 0; p < C::PL; ++p) {
+                        const uint32_t a = st + p * C::A_BYTES, b = st + C::PL * C::A_BYTES + p * C::B_BYTES;
+                        if constexpr (C::A_MN) {
+                            tma_load<C::CG>(a, &map_a, m0, kb * kKb, p, bar);
+                            tma_load<C::CG>(a + 8192, &map_a, m0 + 64, kb * kKb, p, bar);
+                        } else {
+                            tma_load<C::CG>(a, &map_a, kb * kKb, m0, p, bar);
+                        }
+                        if constexpr (C::B_MN) {
+#pragma unroll
+                            for (int c = 0; c < C::BROWS / 64; ++c)
+                                tma_load<C::CG>(b + c * 8192, &map_b, n0 + c * 64, kb * kKb, p, bar);
+                        } else {
+                            tma_load<C::CG>(b, &map_b, kb * kKb, n0, p, bar);
+                        }
+                    }
+                }
+            }
+            // the last use of every stage: its MMAs are done (and, in a pair, their arrivals
+            // on this CTA have landed) before the CTA may leave
+            for (uint32_t k = it > C::STAGES ? it - C::STAGES : 0; ok && k < it; ++k)
+                ok = mbar_wait_bounded(empty + 8 * (k % C::STAGES), (k / C::STAGES) & 1, wait_ns);
+            if (!ok) {
+                atomicOr(&g_wait_error, 1u);
+                const uint64_t t0 = global_ns();             // copies in flight land within this
+                for (int i = 0; i < (1 << 20) && global_ns() - t0 < 2000000ull; ++i) __nanosleep(1000);
+            }
+        }
+        __syncwarp();
+    } else if (warp == kEpiWarps + 1) {
+        // ---- products ----
+        if (lane == 0 && leader) {
+            constexpr uint32_t idesc = mma_idesc(128 * C::CG, C::BN, C::A_MN, C::B_MN);
+            bool ok = true;
+            uint32_t it = 0, ac = 0;
+            for (int t = cluster; ok && t < n_tiles; t += n_clusters) {
+                for (int kc = kb0; ok && kc < kb1; kc += chunk, ++ac) {
+                    const uint32_t buf = ac & 1, use = ac >> 1;
+                    if (use > 0 && !mbar_wait_bounded(acc_empty + 8 * buf, (use - 1) & 1, wait_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t d = tmem + buf * C::BN;
+                    const int ke = kc + chunk < kb1 ? kc + chunk : kb1;
+                    for (int kb = kc; kb < ke; ++kb, ++it) {
+                        const uint32_t s = it % C::STAGES;
+                        if (!mbar_wait_bounded(full + 8 * s, (it / C::STAGES) & 1, wait_ns)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t st = smem_addr(smem + s * C::STAGE);
+#pragma unroll
+                        for (int pr = 0; pr < (C::PL == 3 ? 6 : 1); ++pr) {
+                            // plane pairs (0,0) (0,1) (1,0) (1,1) (0,2) (2,0): the other three are
+                            // below 2^-24 of the product
+                            const int pa = pr == 2 || pr == 3 ? 1 : pr == 5 ? 2 : 0;
+                            const int pb = pr == 1 || pr == 3 ? 1 : pr == 4 ? 2 : 0;
+                            const uint32_t a = st + pa * C::A_BYTES, b = st + C::PL * C::A_BYTES + pb * C::B_BYTES;
+#pragma unroll
+                            for (int k = 0; k < kKb / 16; ++k) {
+                                // 16 K elements on: 32 bytes along a K-major row, 16 rows of an MN-major tile
+                                const uint64_t da = smem_desc(a + (C::A_MN ? k * 2048 : k * 32), C::A_MN ? 8192 : 16, 1024);
+                                const uint64_t db = smem_desc(b + (C::B_MN ? k * 2048 : k * 32), C::B_MN ? 8192 : 16, 1024);
+                                mma_bf16<C::CG>(d, da, db, idesc, kb > kc || pr > 0 || k > 0);
+                            }
+                        }
+                        mma_commit<C::CG>(empty + 8 * s);
+                    }
+                    if (ok) mma_commit<C::CG>(acc_full + 8 * buf);
+                }
+            }
+            if (!ok) atomicOr(&g_wait_error, 1u);
+        }
+        __syncwarp();
+    } else {
+        // ---- epilogue ----
+        // Warp w reads TMEM lanes 32 (w mod 4) on: rows 32 q of the CTA's part of the tile; the
+        // two halves of the warps take alternate groups of 32 columns.
+        const int q = warp & 3, half = warp >> 2;
+        constexpr int NJ = (C::BN + 63) / 64;                // groups of 32 columns per warp
+        bool ok = true;
+        uint32_t ac = 0;
+        for (int t = cluster; ok && t < n_tiles; t += n_clusters) {
+            int mt, nt;
+            tile_at(t, mt, nt);
+            const int64_t m0 = int64_t(mt * C::CG + (C::CG == 2 ? int(rank) : 0)) * 128 + q * 32;
+            const int64_t n0 = int64_t(nt) * C::BN;
+            float sum[C::CH ? NJ : 1][32];
+            if constexpr (C::CH != 0) {
+#pragma unroll
+                for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) sum[j][i] = 0.f;
+            }
+            auto finish = [&](int jj, const float (&v)[32]) {
+                const int j = 2 * jj + half;                 // this group of 32 columns
+                const int64_t row0 = C::MODE == kWgrad ? m0 : n0 + j * 32, col0 = C::MODE == kWgrad ? n0 + j * 32 : m0;
+                if constexpr (C::SPLIT) {
+                    const uint32_t u = 4 * j + q;            // unit u joins in CTA u mod splits
+                    const uint32_t slot = (u / sh.splits) * sh.splits + rank;
+                    const uint32_t dst = map_rank(smem_addr(epi_smem + slot * kUnitFloats), u % sh.splits);
+#pragma unroll
+                    for (int c = 0; c < 32; ++c)
+                        st_cluster(dst + 4 * (C::MODE == kWgrad ? unit_at(lane, c) : unit_at(c, lane)), v[c]);
+                } else {
+                    float* const unit = epi_smem + warp * kUnitFloats;
+                    __syncwarp();
+                    if constexpr (C::MODE == kWgrad) {       // a lane holds a row
+#pragma unroll
+                        for (int g = 0; g < 8; ++g)
+                            st4(unit + unit_at(lane, 4 * g), make_float4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]));
+                    } else {                                 // a lane holds a column
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) unit[unit_at(c, lane)] = v[c];
+                    }
+                    __syncwarp();
+                    emit_unit<C::MODE, typename C::OT>(ep, unit, 1, row0, col0, lane);
+                }
+            };
+            for (int kc = kb0; ok && kc < kb1; kc += chunk, ++ac) {
+                const uint32_t buf = ac & 1;
+                ok = __all_sync(0xffffffffu, mbar_wait_bounded(acc_full + 8 * buf, (ac >> 1) & 1, wait_ns));
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t src = tmem + buf * C::BN + (uint32_t(q * 32) << 16);
+#pragma unroll
+                for (int jj = 0; jj < NJ; ++jj) {
+                    if ((2 * jj + half) * 32 < C::BN) {
+                        float v[32];
+                        tmem_ld32(src + (2 * jj + half) * 32, v);
+                        if constexpr (C::CH != 0) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) sum[jj][i] += v[i];
+                        } else {
+                            finish(jj, v);
+                        }
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (C::CG == 2) mbar_arrive_cluster(map_rank(acc_empty + 8 * buf, 0));
+                    else mbar_arrive(acc_empty + 8 * buf);
+                }
+            }
+            if constexpr (C::CH != 0) {
+#pragma unroll
+                for (int jj = 0; jj < NJ; ++jj)
+                    if (ok && (2 * jj + half) * 32 < C::BN) finish(jj, sum[jj]);
+            }
+        }
+        if (!ok && lane == 0) atomicOr(&g_wait_error, 1u);
+    }
+
+    // ---- join and teardown: every thread of the cluster gets here ----
+    if constexpr (C::SPLIT) {
+        __syncwarp();
+        cluster_arrive();
+        cluster_wait();
+        if (warp < kEpiWarps) {
+            int mt, nt;
+            tile_at(cluster, mt, nt);
+            for (int u = int(rank) + warp * sh.splits; u < C::BN / 8; u += kEpiWarps * sh.splits) {
+                const int q = u & 3, j = u >> 2;
+                const int64_t m0 = int64_t(mt) * 128 + q * 32, n0 = int64_t(nt) * C::BN + j * 32;
+                emit_unit<C::MODE, typename C::OT>(ep, epi_smem + (u / sh.splits) * sh.splits * kUnitFloats, sh.splits,
+                                                   C::MODE == kWgrad ? m0 : n0, C::MODE == kWgrad ? n0 : m0, lane);
+            }
+        }
+    }
+    tc_fence_before();
+    if constexpr (C::CG == 2) {
+        __syncwarp();
+        cluster_arrive();
+        cluster_wait();
+    } else {
+        __syncthreads();
+    }
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc<C::CG>(tmem, C::TMEM);
+    }
+}
+
+// ---- host side ------------------------------------------------------------------------
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The driver's tensor-map encoder, looked up once.
+EncodeTiled encode_tiled() {
+    static std::atomic<EncodeTiled> fn{nullptr};
+    EncodeTiled f = fn.load(std::memory_order_relaxed);
+    if (!f) {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess) {
+            f = reinterpret_cast<EncodeTiled>(p);
+            fn.store(f, std::memory_order_relaxed);
+        }
+    }
+    return f;
+}
+
+// The map of an operand: boxes of 64 columns (128 bytes, 128-byte swizzle) x box_rows rows
+// of one plane; what lies outside the matrix reads as 0.
+cudaError_t make_map(CUtensorMap* m, const LinOperand& o, int planes, int box_rows) {
+    const EncodeTiled enc = encode_tiled();
+    if (!enc) return cudaErrorNotSupported;
+    const cuuint64_t dims[3] = {cuuint64_t(o.cols), cuuint64_t(o.rows), cuuint64_t(planes)};
+    const cuuint64_t strides[2] = {cuuint64_t(o.ld) * 2, cuuint64_t(planes > 1 ? o.plane : o.ld) * 2};
+    const cuuint32_t box[3] = {64, cuuint32_t(box_rows), 1}, ones[3] = {1, 1, 1};
+    const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(o.ptr), dims, strides, box, ones,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+int sm_count(int dev) {
+    static std::atomic<int> n[64];
+    if (dev < 0 || dev >= 64) return 0;
+    int v = n[dev].load(std::memory_order_relaxed);
+    if (v == 0 && cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess)
+        n[dev].store(v, std::memory_order_relaxed);
+    return v;
+}
+
+// Shared-memory attribute of a kernel, set once per device.
+template <class C>
+cudaError_t prepare_kernel(int dev) {
+    static std::atomic<uint64_t> done{0};
+    if (dev < 64 && (done.load(std::memory_order_relaxed) >> dev & 1)) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(k_linear<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e == cudaSuccess && dev < 64) done.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
+    return e;
+}
+
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Launches one configuration: splits CTAs per tile (SPLIT), else a persistent grid.
+template <class C>
+cudaError_t launch_cfg(const LinProblem& p, int splits, cudaStream_t st) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if ((e = prepare_kernel<C>(dev)) != cudaSuccess) return e;
+    CUtensorMap ma, mb;
+    if ((e = make_map(&ma, p.a, C::PL, C::A_MN ? kKb : 128)) != cudaSuccess) return e;
+    if ((e = make_map(&mb, p.b, C::PL, C::B_MN ? kKb : C::BROWS)) != cudaSuccess) return e;
+    const int64_t mt = ceil_div(p.M, 128 * C::CG), nt = ceil_div(p.N, C::BN), kb = ceil_div(p.K, kKb);
+    const int per = C::CG == 2 ? 2 : C::SPLIT ? splits : 1;
+    // tile numbers, K steps and tile coordinates are 32-bit
+    if (mt * nt * per > INT32_MAX / 16 || kb > INT32_MAX / 128 || p.M > INT32_MAX - 512 || p.N > INT32_MAX - 512)
+        return cudaErrorInvalidValue;
+    LinShape sh{int32_t(mt), int32_t(nt), int32_t(kb), splits};
+    int64_t clusters = mt * nt;
+    const int64_t room = sm_count(dev) / per;
+    if (!C::SPLIT && clusters > room) clusters = room > 0 ? room : 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = unsigned(per);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(clusters * per));
+    cfg.blockDim = dim3(kLinThreads);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = per > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, k_linear<C>, ma, mb, sh, p.epi, detail::kWaitNs);
+}
+
+}  // namespace
+}  // namespace fsdp

@@ -543,6 +543,98 @@ int fsdp_reduce_scatter_adamw_noalloc(const fsdp_layout* layout, int32_t unit_be
                                       void* param_shards, float* grad_shard_out,
                                       const fsdp_adamw_hparams* hp, int64_t step, fsdp_stream_t stream);
 
+/* ---- Layers between the all-gather and the reduce-scatter --------------------------
+ * The pages leave the layers of the model to the framework around them; these calls
+ * compute linear layers and dropout where the sharded step puts their parameters and
+ * takes their gradients: weights and biases are read as views of the full buffer that
+ * fsdp_unshard fills, weight gradients are written as views of a gradient replica (or
+ * added to an fp32 accumulator of fsdp_accumulate_grads).
+ *
+ *   forward   z = x w^T + bias;   y = residual + drop(act(z))
+ *   dgrad     dx = residual + act'(z) * drop(dz w)
+ *   wgrad     dw (+)= dz^T x;     db[o] (+)= sum over rows t of dz[t][o]
+ *   dropout   y = residual + drop(x)
+ *
+ * where x is [rows][in], w [out][in] (a Linear's weight), z and y [rows][out], and dz is
+ * the gradient of the layer's own z.  For layers 1, 2 with z2 = drop(act(z1)) w2^T + b2,
+ * dgrad with layer 2's weight, layer 1's preact, activation and dropout gives the
+ * gradient of z1.
+ *
+ * Conventions shared by the four calls
+ *   - Matrices are row-major with a row stride (ld*, in elements) of at least their width;
+ *     unlike the shard buffers they need only their element's alignment (else
+ *     FSDP_EALIGN): a FLAT layout's tensors start at any element.
+ *   - elem_dtype is the type of every matrix and of bias; wgrad's dw and db have
+ *     grad_dtype.  Products accumulate in fp32; everything up to the store is fp32 and each
+ *     output is rounded once, to nearest even.  fp32 operands are split exactly into three
+ *     bf16 terms and multiplied as six bf16 products (relative error of the order of
+ *     2^-24 per product, as fp32 products have); where an fp32 operand holds an infinity or
+ *     a NaN, the results that depend on it are not finite, but an infinity may come out as
+ *     a NaN.
+ *   - rows may be 0 (nothing is read; wgrad without accumulate writes zeros); in and out
+ *     are at least 1; all three and the strides are below 2^31 (else FSDP_EOVERFLOW).
+ *   - residual, bias and preact may be NULL.  With an activation, dgrad needs preact, the z
+ *     that forward wrote; forward writes it where preact is given.  y (dx) may be the very
+ *     residual buffer, with its stride; no other output may overlap an input.
+ *   - act: FSDP_ACT_GELU is z Phi(z) with the error function, FSDP_ACT_SILU z / (1 + e^-z);
+ *     relu's derivative at 0 is 0.
+ *   - workspace: device scratch, 16-byte aligned, of at least
+ *     fsdp_linear_workspace_bytes(...) bytes (else FSDP_EINVAL); NULL where that is 0.  No
+ *     initial contents needed; it is in use until the call's work has run: calls whose work
+ *     may overlap on the GPU need workspaces of their own.
+ *   - Results are the same bits in every run of the same call on the same device type. */
+typedef enum { FSDP_ACT_NONE = 0, FSDP_ACT_RELU = 1, FSDP_ACT_GELU = 2, FSDP_ACT_SILU = 3 } fsdp_act;
+
+/* A dropout whose mask is a function of (seed, layer, row, column) and is never stored.
+ * With word(r, c) = word c mod 4 of the Philox4x32-10 block (Salmon et al., "Parallel random
+ * numbers: as easy as 1, 2, 3", SC 2011) of counter (c / 4, r mod 2^32, r / 2^32, layer)
+ * and key (seed mod 2^32, seed / 2^32), element (t, c) of a dropped matrix is kept when
+ * word(row0 + t, c) >= floor(p * 2^32), and then multiplied by fp32(1 / (1 - p)); a dropped
+ * element is 0 whatever it held.  In forward and dropout the matrix is the layer's output;
+ * in dgrad it is dx's [rows][in], the output of the layer before: the same spec there gives
+ * the same mask.  row0 lets a batch be split over calls: pass the index of its first row.
+ * 0 <= p < 1, row0 >= 0 (else FSDP_EINVAL); a NULL spec or p = 0 drops nothing. */
+typedef struct {
+    double p;
+    uint64_t seed;
+    int64_t row0;
+    uint32_t layer;
+    uint32_t reserved;
+} fsdp_dropout_spec;
+
+/* Scratch bytes of the three linear calls at these sizes: an upper bound over forward,
+ * dgrad and wgrad.  aligned != 0: every x, w and dz has a base address and a row stride
+ * that are multiples of 16 bytes, which for FSDP_BF16 makes it 0; otherwise room for
+ * aligned copies of two operands is counted, and for FSDP_F32 always room for their three
+ * bf16 terms.  0 for arguments that the calls refuse.  Host only. */
+size_t fsdp_linear_workspace_bytes(int64_t rows, int64_t in, int64_t out, int32_t elem_dtype, int32_t aligned);
+
+/* y = residual + drop(act(x w^T + bias)); z to preact where given. */
+int fsdp_linear_forward(int64_t rows, int64_t in, int64_t out, int32_t elem_dtype, const void* x, int64_t ldx,
+                        const void* w, int64_t ldw, const void* bias, int32_t act, const fsdp_dropout_spec* drop,
+                        const void* residual, int64_t ldr, void* y, int64_t ldy, void* preact, int64_t ldz,
+                        void* workspace, size_t workspace_bytes, fsdp_stream_t stream);
+
+/* dx = residual + act'(preact) * drop(dz w): dz [rows][out], w [out][in], the others
+ * [rows][in]. */
+int fsdp_linear_dgrad(int64_t rows, int64_t in, int64_t out, int32_t elem_dtype, const void* dz, int64_t lddz,
+                      const void* w, int64_t ldw, int32_t act, const void* preact, int64_t ldz,
+                      const fsdp_dropout_spec* drop, const void* residual, int64_t ldr, void* dx, int64_t lddx,
+                      void* workspace, size_t workspace_bytes, fsdp_stream_t stream);
+
+/* dw (+)= dz^T x and, where db is given, db (+)= the column sums of dz; accumulate != 0
+ * adds to what dw and db hold (in fp32, rounded once), otherwise they are overwritten.
+ * The columns of dw between in and lddw are not touched. */
+int fsdp_linear_wgrad(int64_t rows, int64_t in, int64_t out, int32_t elem_dtype, const void* dz, int64_t lddz,
+                      const void* x, int64_t ldx, void* dw, int64_t lddw, void* db, int32_t grad_dtype,
+                      int32_t accumulate, void* workspace, size_t workspace_bytes, fsdp_stream_t stream);
+
+/* y = residual + drop(x), all [rows][cols] of elem_dtype; y may be x or residual (with its
+ * stride).  rows * cols < 2^40. */
+int fsdp_dropout(int64_t rows, int64_t cols, int32_t elem_dtype, const void* x, int64_t ldx,
+                 const fsdp_dropout_spec* drop, const void* residual, int64_t ldr, void* y, int64_t ldy,
+                 fsdp_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
