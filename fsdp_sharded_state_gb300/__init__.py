@@ -12,6 +12,8 @@ import ctypes as C
 import os
 from typing import Optional, Sequence
 
+import torch
+
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "_build", "libfsdpstate.so")
 
@@ -172,7 +174,8 @@ def _ptr(x) -> Optional[int]:
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
+        if torch.cuda.is_initialized():          # the raw handle alone: a Stream object costs 3 us
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
         return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else None
     if isinstance(stream, int):
         return stream
@@ -180,7 +183,6 @@ def _stream(stream) -> Optional[int]:
 
 
 def _dtype_code(t) -> int:
-    import torch
     if t.dtype == torch.float32:
         return FSDP_F32
     if t.dtype == torch.bfloat16:
@@ -448,13 +450,15 @@ def fsdp_zero1_adamw_broadcast(layout: Layout, unit_begin: int, unit_end: int, g
 
 # -- layers between the all-gather and the reduce-scatter -------------------------
 def _matrix(x, name: str, rows: int, cols: int, dtype):
-    """(address, row stride) of a 2-D tensor of the given shape whose rows are contiguous."""
+    """(address, row stride) of a 2-D CUDA tensor of the given shape whose rows are contiguous."""
     if x is None:
         return None, 0
-    if x.dtype != dtype:
+    if x.dtype is not dtype:
         raise TypeError(f"{name} is {x.dtype}, expected {dtype}")
-    if x.dim() != 2 or x.shape[0] != rows or x.shape[1] != cols:
+    if x.shape != (rows, cols):
         raise ValueError(f"{name} is {tuple(x.shape)}, expected {(rows, cols)}")
+    if not x.is_cuda:
+        raise ValueError(f"{name} is not a CUDA tensor")
     ld, one = x.stride()
     if one != 1 and cols > 1:
         raise ValueError(f"{name}: a row's elements must be contiguous")
@@ -466,13 +470,21 @@ def _matrix(x, name: str, rows: int, cols: int, dtype):
 def _vector(x, name: str, n: int, dtype):
     if x is None:
         return None
-    if x.dtype != dtype:
+    if x.dtype is not dtype:
         raise TypeError(f"{name} is {x.dtype}, expected {dtype}")
-    if x.dim() != 1 or x.shape[0] != n:
+    if x.shape != (n,):
         raise ValueError(f"{name} is {tuple(x.shape)}, expected {(n,)}")
+    if not x.is_cuda:
+        raise ValueError(f"{name} is not a CUDA tensor")
     if n > 1 and x.stride(0) != 1:
         raise ValueError(f"{name} must be contiguous")
     return x.data_ptr()
+
+
+def _two_dims(**named) -> None:
+    for name, x in named.items():
+        if x.dim() != 2:
+            raise ValueError(f"{name} is {tuple(x.shape)}, expected a matrix")
 
 
 def _act(act) -> int:
@@ -495,7 +507,6 @@ def fsdp_linear_workspace_bytes(rows: int, cols_in: int, cols_out: int, dtype, a
     """Scratch bytes of the three linear calls at these sizes.  aligned: every x, w and dz
     has a base address and row stride that are multiples of 16 bytes (default: widths of
     whole 16-byte rows, as contiguous tensors of their own have)."""
-    import torch
     code = dtype if isinstance(dtype, int) else {torch.float32: FSDP_F32, torch.bfloat16: FSDP_BF16}[dtype]
     if aligned is None:
         e = 4 if code == FSDP_F32 else 2
@@ -508,6 +519,7 @@ def fsdp_linear_forward(x, w, y, bias=None, act="none", preact=None, dropout: Op
     """y = residual + drop(act(x w^T + bias)); z = x w^T + bias into preact where given.
     x [rows, in], w [out, in], y / preact / residual [rows, out], bias [out], one dtype."""
     code, dt = _dtype_code(x), x.dtype
+    _two_dims(x=x, w=w)
     (rows, cin), cout = x.shape, w.shape[0]
     px, ldx = _matrix(x, "x", rows, cin, dt)
     pw, ldw = _matrix(w, "w", cout, cin, dt)
@@ -525,6 +537,7 @@ def fsdp_linear_dgrad(dz, w, dx, act="none", preact=None, dropout: Optional[Drop
     """dx = residual + act'(preact) * drop(dz w): dz [rows, out], w [out, in], dx / preact /
     residual [rows, in]; act, preact and dropout are those of the layer before."""
     code, dt = _dtype_code(dz), dz.dtype
+    _two_dims(dz=dz, w=w)
     (rows, cout), cin = dz.shape, w.shape[1]
     pg, ldg = _matrix(dz, "dz", rows, cout, dt)
     pw, ldw = _matrix(w, "w", cout, cin, dt)
@@ -540,6 +553,7 @@ def fsdp_linear_wgrad(dz, x, dw, db=None, accumulate: bool = False, workspace=No
     """dw (+)= dz^T x and db (+)= the column sums of dz: dz [rows, out], x [rows, in] of one
     dtype, dw [out, in] and db [out] of one dtype (a gradient replica's, or fp32)."""
     code, dt = _dtype_code(dz), dz.dtype
+    _two_dims(dz=dz, x=x)
     (rows, cout), cin = dz.shape, x.shape[1]
     pg, ldg = _matrix(dz, "dz", rows, cout, dt)
     px, ldx = _matrix(x, "x", rows, cin, dt)
@@ -553,6 +567,7 @@ def fsdp_linear_wgrad(dz, x, dw, db=None, accumulate: bool = False, workspace=No
 def fsdp_dropout(x, y, dropout: Optional[DropoutSpec], residual=None, stream=None) -> None:
     """y = residual + drop(x), [rows, cols] each; the same call on the gradient is its backward."""
     code, dt = _dtype_code(x), x.dtype
+    _two_dims(x=x)
     rows, cols = x.shape
     px, ldx = _matrix(x, "x", rows, cols, dt)
     py, ldy = _matrix(y, "y", rows, cols, dt)

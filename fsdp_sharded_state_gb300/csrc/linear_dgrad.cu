@@ -5,8 +5,8 @@
 namespace fsdp {
 
 cudaError_t launch_linear_dgrad(const LinProblem& p, cudaStream_t st) {
-    if (p.planes == 3) return launch_cfg<LinCfg<kDgrad, float, 1, 128, 3, 4, false>>(p, 1, st);
-    return launch_cfg<LinCfg<kDgrad, uint16_t, 1, 128, 1, 0, false>>(p, 1, st);
+    if (p.planes == 3) return launch_product<kDgrad, float, 3, 2>(p, st);
+    return launch_product<kDgrad, uint16_t, 1, 0>(p, st);
 }
 
 cudaError_t take_wait_error_dgrad(unsigned int* flag) { return take_local_wait_error(flag); }

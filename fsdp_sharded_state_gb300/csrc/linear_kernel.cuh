@@ -29,15 +29,29 @@ constexpr int kKb = 64;                        // K elements per stage: 128-byte
 constexpr int kLinMaxStages = 8;
 constexpr int kUnitFloats = 32 * 32;           // an epilogue unit: 32 rows x 32 columns
 
-// ---- loads and stores of n <= 8 consecutive elements as fp32 ------------------------
-__device__ __forceinline__ void load8(const uint16_t* p, float (&v)[8]) {
-    const uint4 u = ldu4(p);
+// ---- 8 consecutive elements, as they lie in memory and as fp32 ------------------------
+template <typename T>
+struct Raw8 {
+    uint4 q[sizeof(T) / 2];
+};
+template <typename T>
+__device__ __forceinline__ Raw8<T> load_raw(const T* p) {
+    Raw8<T> r;
+#pragma unroll
+    for (int i = 0; i < int(sizeof(T) / 2); ++i) r.q[i] = ldu4(reinterpret_cast<const char*>(p) + 16 * i);
+    return r;
+}
+__device__ __forceinline__ void widen(const Raw8<uint16_t>& r, float (&v)[8]) {
+    const uint4 u = r.q[0];
     v[0] = bf16lo(u.x); v[1] = bf16hi(u.x); v[2] = bf16lo(u.y); v[3] = bf16hi(u.y);
     v[4] = bf16lo(u.z); v[5] = bf16hi(u.z); v[6] = bf16lo(u.w); v[7] = bf16hi(u.w);
 }
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-    const float4 a = ld4(p), b = ld4(p + 4);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+__device__ __forceinline__ void widen(const Raw8<float>& r, float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        v[4 * i] = __uint_as_float(r.q[i].x); v[4 * i + 1] = __uint_as_float(r.q[i].y);
+        v[4 * i + 2] = __uint_as_float(r.q[i].z); v[4 * i + 3] = __uint_as_float(r.q[i].w);
+    }
 }
 __device__ __forceinline__ void store8(uint16_t* p, const float (&v)[8]) {
     stu4(p, make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])));
@@ -51,102 +65,107 @@ __device__ __forceinline__ float load1(const float* p) { return *p; }
 __device__ __forceinline__ void store1(uint16_t* p, float v) { *p = to_bf16(v); }
 __device__ __forceinline__ void store1(float* p, float v) { *p = v; }
 
-// n elements of p, by vectors when all 8 are there; V = 1 loads one element.
-template <int V, typename T>
-__device__ __forceinline__ void load_n(const T* p, float (&v)[V], int n) {
-    if constexpr (V == 8) {
-        if (n == 8) {
-            load8(p, v);
-            return;
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = i < n ? load1(p + i) : 0.f;
-}
-template <int V, typename T>
-__device__ __forceinline__ void store_n(T* p, const float (&v)[V], int n) {
-    if constexpr (V == 8) {
-        if (n == 8) {
-            store8(p, v);
-            return;
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-        if (i < n) store1(p + i, v[i]);
-}
-
 // ---- activations (fp32) --------------------------------------------------------------
-// gelu(z) = z Phi(z), silu(z) = z / (1 + exp(-z)).
-__device__ __forceinline__ float phi(float z) { return fmaf(0.5f, erff(z * 0.70710678118654752f), 0.5f); }
-__device__ __forceinline__ float act1(float z, int act) {
-    if (act == FSDP_ACT_RELU) return z < 0.f ? 0.f : z;      // NaN stays NaN
-    if (act == FSDP_ACT_GELU) return z * phi(z);
-    if (act == FSDP_ACT_SILU) return z / (1.f + expf(-z));
-    return z;
-}
-// g * act'(z): gelu' = Phi(z) + z exp(-z^2/2) / sqrt(2 pi), silu' = s (1 + z (1 - s)).
-__device__ __forceinline__ float act1_grad(float g, float z, int act) {
-    if (act == FSDP_ACT_RELU) return z > 0.f ? g : (z != z ? z : 0.f);
-    if (act == FSDP_ACT_GELU) return g * fmaf(z * 0.39894228040143268f, expf(-0.5f * z * z), phi(z));
-    if (act == FSDP_ACT_SILU) {
-        const float s = 1.f / (1.f + expf(-z));
-        return g * (s * fmaf(z, 1.f - s, 1.f));
-    }
-    return g;
-}
-
-template <int V>
-__device__ __forceinline__ void drop_n(const Drop& d, int64_t row, int64_t col, float (&v)[V]) {
-    if constexpr (V == 8) {                                   // col is a multiple of 8
-        const uint4 a = drop_words(d, row, col >> 2), b = drop_words(d, row, (col >> 2) + 1);
-        v[0] = drop1(d, a.x, v[0]); v[1] = drop1(d, a.y, v[1]); v[2] = drop1(d, a.z, v[2]); v[3] = drop1(d, a.w, v[3]);
-        v[4] = drop1(d, b.x, v[4]); v[5] = drop1(d, b.y, v[5]); v[6] = drop1(d, b.z, v[6]); v[7] = drop1(d, b.w, v[7]);
+// gelu(z) = z Phi(z), gelu'(z) = Phi(z) + z exp(-z^2/2) / sqrt(2 pi);
+// silu(z) = z s, silu'(z) = s (1 + z (1 - s)), s = 1 / (1 + exp(-z)).
+// For fp32 results, CUDA's erff and expf.  For bf16 results (rounded to 2^-8 afterwards)
+// the fast exponential and reciprocal, and for Phi formula 7.1.26 of Abramowitz and Stegun,
+// Handbook of Mathematical Functions: erf(x) = 1 - (a1 t + .. + a5 t^5) exp(-x^2), t = 1 /
+// (1 + 0.3275911 x), for x >= 0, error at most 1.5e-7; its exponential is also the
+// derivative's.  The fast forms also keep the epilogue's code small: with CUDA's erff, expf
+// and division unrolled over a unit it did not fit the instruction caches, and a 256 x 256
+// tile's epilogue took 26,000 clocks instead of its arithmetic's 4,000.
+struct PhiExp {
+    float phi, e;              // Phi(z), exp(-z^2 / 2)
+};
+template <bool FAST>
+__device__ __forceinline__ PhiExp phi_exp(float z, bool want_e) {
+    PhiExp r;
+    if constexpr (FAST) {
+        const float x = fabsf(z) * 0.70710678118654752f;
+        r.e = __expf(-x * x);
+        const float t = __fdividef(1.f, fmaf(0.3275911f, x, 1.f));
+        float q = fmaf(t, 1.061405429f, -1.453152027f);
+        q = fmaf(t, q, 1.421413741f);
+        q = fmaf(t, q, -0.284496736f);
+        q = fmaf(t, q, 0.254829592f);
+        const float half_tail = 0.5f * (t * q * r.e);            // (1 - erf(x)) / 2
+        r.phi = z < 0.f ? half_tail : 1.f - half_tail;           // NaN stays NaN
     } else {
-        const uint4 a = drop_words(d, row, col >> 2);
-        const int k = int(col & 3);
-        v[0] = drop1(d, k == 0 ? a.x : k == 1 ? a.y : k == 2 ? a.z : a.w, v[0]);
+        r.phi = fmaf(0.5f, erff(z * 0.70710678118654752f), 0.5f);
+        r.e = want_e ? expf(-0.5f * z * z) : 0.f;
+    }
+    return r;
+}
+template <bool FAST>
+__device__ __forceinline__ float sigmoid(float z) {
+    if constexpr (FAST) return __fdividef(1.f, 1.f + __expf(-z));
+    return 1.f / (1.f + expf(-z));
+}
+template <bool FAST, int V>
+__device__ __forceinline__ void activate(float (&v)[V], int act) {
+    if (act == FSDP_ACT_RELU) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = v[i] < 0.f ? 0.f : v[i];              // NaN stays NaN
+    } else if (act == FSDP_ACT_GELU) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] *= phi_exp<FAST>(v[i], false).phi;
+    } else if (act == FSDP_ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] *= sigmoid<FAST>(v[i]);
+    }
+}
+// v *= act'(z)
+template <bool FAST, int V>
+__device__ __forceinline__ void activate_grad(float (&v)[V], const float (&z)[V], int act) {
+    if (act == FSDP_ACT_RELU) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = z[i] > 0.f ? v[i] : (z[i] != z[i] ? z[i] : 0.f);
+    } else if (act == FSDP_ACT_GELU) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const PhiExp p = phi_exp<FAST>(z[i], true);
+            v[i] *= fmaf(z[i] * 0.39894228040143268f, p.e, p.phi);
+        }
+    } else if (act == FSDP_ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const float s = sigmoid<FAST>(z[i]);
+            v[i] *= s * fmaf(z[i], 1.f - s, 1.f);
+        }
     }
 }
 
-// The epilogue of V consecutive columns of one row (n of them inside the matrix).
-template <int MODE, typename OT, int V>
-__device__ __forceinline__ void emit(const LinEpi& ep, int64_t row, int64_t col, float (&v)[V], int n) {
+// The epilogue of one element: what emit_unit does for 8, at any alignment.
+template <int MODE, typename OT>
+__device__ __noinline__ void emit1(const LinEpi& ep, int64_t row, int64_t col, float x) {
+    constexpr bool FAST = sizeof(OT) == 2;
     OT* const out = static_cast<OT*>(ep.out) + row * ep.ldo + col;
-    float t[V];
+    float v[1] = {x};
     if constexpr (MODE == kForward) {
-        if (ep.bias) {
-            load_n<V>(static_cast<const OT*>(ep.bias) + col, t, n);
-#pragma unroll
-            for (int i = 0; i < V; ++i) v[i] += t[i];
+        if (ep.bias) v[0] += load1(static_cast<const OT*>(ep.bias) + col);
+        if (ep.preact) store1(static_cast<OT*>(ep.preact) + row * ep.ldz + col, v[0]);
+        activate<FAST, 1>(v, ep.act);
+    }
+    if constexpr (MODE != kWgrad) {
+        if (ep.drop.on) {
+            const uint4 a = drop_words(ep.drop, row, col >> 2);
+            const int k = int(col & 3);
+            v[0] = drop1(ep.drop, k == 0 ? a.x : k == 1 ? a.y : k == 2 ? a.z : a.w, v[0]);
         }
-        if (ep.preact) store_n<V>(static_cast<OT*>(ep.preact) + row * ep.ldz + col, v, n);
-        if (ep.act != FSDP_ACT_NONE) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) v[i] = act1(v[i], ep.act);
-        }
-        if (ep.drop.on) drop_n<V>(ep.drop, row, col, v);
     }
     if constexpr (MODE == kDgrad) {
-        if (ep.drop.on) drop_n<V>(ep.drop, row, col, v);
         if (ep.act != FSDP_ACT_NONE) {
-            load_n<V>(static_cast<const OT*>(ep.preact) + row * ep.ldz + col, t, n);
-#pragma unroll
-            for (int i = 0; i < V; ++i) v[i] = act1_grad(v[i], t[i], ep.act);
+            const float z[1] = {load1(static_cast<const OT*>(ep.preact) + row * ep.ldz + col)};
+            activate_grad<FAST, 1>(v, z, ep.act);
         }
     }
     if constexpr (MODE != kWgrad) {
-        if (ep.residual) {
-            load_n<V>(static_cast<const OT*>(ep.residual) + row * ep.ldr + col, t, n);
-#pragma unroll
-            for (int i = 0; i < V; ++i) v[i] += t[i];
-        }
-    } else if (ep.accumulate) {
-        load_n<V>(out, t, n);
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[i] += t[i];
+        if (ep.residual) v[0] += load1(static_cast<const OT*>(ep.residual) + row * ep.ldr + col);
+    } else {
+        if (ep.accumulate) v[0] += load1(out);
     }
-    store_n<V>(out, v, n);
+    store1(out, v[0]);
 }
 
 // A unit in shared memory: [32 rows][32 columns] fp32, the 16-byte groups of row r at
@@ -154,35 +173,91 @@ __device__ __forceinline__ void emit(const LinEpi& ep, int64_t row, int64_t col,
 // holds a column) and the row-wise reads are free of bank conflicts.
 __device__ __forceinline__ int unit_at(int r, int c) { return r * 32 + ((((c >> 2) ^ (r & 7)) << 2) | (c & 3)); }
 
-// Adds the `slots` copies of a unit (kUnitFloats apart, in order) and emits it.
+// Adds the `slots` copies of a unit (kUnitFloats apart, in order) and emits it: 4 lanes per
+// row, 8 columns per lane, 8 rows at a time; what the epilogue reads of the next 8 rows is
+// loaded before these are computed.
 template <int MODE, typename OT>
 __device__ __forceinline__ void emit_unit(const LinEpi& ep, const float* unit, int slots, int64_t row0, int64_t col0, int lane) {
-    if (ep.vec) {
-        const int64_t col = col0 + (lane & 3) * 8;
-        const int64_t left = ep.cols - col;
-        const int n = left >= 8 ? 8 : int(left);
-#pragma unroll
-        for (int it = 0; it < 4; ++it) {
+    constexpr bool FAST = sizeof(OT) == 2;
+    const int64_t col = col0 + (lane & 3) * 8;
+    if (ep.vec && ep.cols - col0 >= 32) {
+        const int64_t row1 = row0 + (lane >> 2);
+        const int n_it = ep.rows > row1 ? (ep.rows - row1 >= 32 ? 4 : int((ep.rows - row1 + 7) >> 3)) : 0;
+        OT* out = static_cast<OT*>(ep.out) + row1 * ep.ldo + col;
+        // the addend (residual, or what wgrad accumulates to) and the pre-activation
+        const OT* add = MODE == kWgrad ? (ep.accumulate ? out : nullptr)
+                        : ep.residual  ? static_cast<const OT*>(ep.residual) + row1 * ep.ldr + col
+                                       : nullptr;
+        const int64_t add_step = 8 * (MODE == kWgrad ? ep.ldo : ep.ldr);
+        OT* z = MODE != kWgrad && ep.preact ? static_cast<OT*>(ep.preact) + row1 * ep.ldz + col : nullptr;
+        Raw8<OT> add_r = {}, z_r = {};
+        float bias[8] = {};
+        if (n_it > 0) {
+            if (add) add_r = load_raw(add);
+            if (MODE == kDgrad && z) z_r = load_raw(z);
+            if (MODE == kForward && ep.bias) widen(load_raw(static_cast<const OT*>(ep.bias) + col), bias);
+        }
+#pragma unroll 1
+        for (int it = 0; it < n_it; ++it) {
             const int r = it * 8 + (lane >> 2);
-            float v[8];
             const float* p = unit + unit_at(r, (lane & 3) * 8);
             const float* q = unit + unit_at(r, (lane & 3) * 8 + 4);
             float4 a = ld4(p), b = ld4(q);
+#pragma unroll 1
             for (int s = 1; s < slots; ++s) {
                 const float4 c = ld4(p + s * kUnitFloats), d = ld4(q + s * kUnitFloats);
                 a.x += c.x; a.y += c.y; a.z += c.z; a.w += c.w;
                 b.x += d.x; b.y += d.y; b.z += d.z; b.w += d.w;
             }
-            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-            if (row0 + r < ep.rows && n > 0) emit<MODE, OT, 8>(ep, row0 + r, col, v, n);
+            float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+            const Raw8<OT> add_c = add_r, z_c = z_r;
+            if (it + 1 < n_it) {
+                if (add) add_r = load_raw(add += add_step);
+                if (MODE == kDgrad && z) z_r = load_raw(z += 8 * ep.ldz);
+            }
+            if constexpr (MODE == kForward) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] += bias[i];
+                if (z) {
+                    store8(z, v);
+                    z += 8 * ep.ldz;
+                }
+                activate<FAST, 8>(v, ep.act);
+            }
+            if constexpr (MODE != kWgrad) {
+                if (ep.drop.on) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint4 w = drop_words(ep.drop, row0 + r, (col >> 2) + h);
+                        v[4 * h] = drop1(ep.drop, w.x, v[4 * h]);
+                        v[4 * h + 1] = drop1(ep.drop, w.y, v[4 * h + 1]);
+                        v[4 * h + 2] = drop1(ep.drop, w.z, v[4 * h + 2]);
+                        v[4 * h + 3] = drop1(ep.drop, w.w, v[4 * h + 3]);
+                    }
+                }
+            }
+            float t[8];
+            if constexpr (MODE == kDgrad) {
+                if (z) {
+                    widen(z_c, t);
+                    activate_grad<FAST, 8>(v, t, ep.act);
+                }
+            }
+            if (add) {
+                widen(add_c, t);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] += t[i];
+            }
+            store8(out, v);
+            out += 8 * ep.ldo;
         }
-    } else {                                     // any alignment: a lane per column
-        const int64_t col = col0 + lane;
+    } else {                                     // any alignment, and a ragged right edge: a lane per column
+        const int64_t c = col0 + lane;
 #pragma unroll 1
         for (int r = 0; r < 32; ++r) {
-            float v[1] = {unit[unit_at(r, lane)]};
-            for (int s = 1; s < slots; ++s) v[0] += unit[unit_at(r, lane) + s * kUnitFloats];
-            if (row0 + r < ep.rows && col < ep.cols) emit<MODE, OT, 1>(ep, row0 + r, col, v, 1);
+            float v = unit[unit_at(r, lane)];
+            for (int s = 1; s < slots; ++s) v += unit[unit_at(r, lane) + s * kUnitFloats];
+            if (row0 + r < ep.rows && c < ep.cols) emit1<MODE, OT>(ep, row0 + r, c, v);
         }
     }
 }
@@ -275,20 +350,20 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
 
     if (warp == kEpiWarps) {
         // ---- loads ----
-        if (lane == 0) {
-            bool ok = true;
-            uint32_t it = 0;
-            for (int t = cluster; ok && t < n_tiles; t += n_clusters) {
-                int mt, nt;
-                tile_at(t, mt, nt);
-                const int m0 = (mt * C::CG + (C::CG == 2 ? int(rank) : 0)) * 128;
-                const int n0 = nt * C::BN + (C::CG == 2 ? int(rank) * C::BROWS : 0);
-                for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                    const uint32_t s = it % C::STAGES, use = it / C::STAGES;
-                    if (use > 0 && !mbar_wait_bounded(empty + 8 * s, (use - 1) & 1, wait_ns)) {
-                        ok = false;
-                        break;
-                    }
+        bool ok = true;
+        uint32_t it = 0;
+        for (int t = cluster; ok && t < n_tiles; t += n_clusters) {
+            int mt, nt;
+            tile_at(t, mt, nt);
+            const int m0 = (mt * C::CG + (C::CG == 2 ? int(rank) : 0)) * 128;
+            const int n0 = nt * C::BN + (C::CG == 2 ? int(rank) * C::BROWS : 0);
+            for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                const uint32_t s = it % C::STAGES, use = it / C::STAGES;
+                if (use > 0 && !mbar_wait_bounded(empty + 8 * s, (use - 1) & 1, wait_ns)) {
+                    ok = false;
+                    break;
+                }
+                if (elect_one()) {
                     if (leader) mbar_arrive_tx(full + 8 * s, C::CG * C::STAGE);
                     const uint32_t bar = C::CG == 2 ? map_rank(full + 8 * s, 0) : full + 8 * s;
                     const uint32_t st = smem_addr(smem + s * C::STAGE);
@@ -310,22 +385,27 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
                         }
                     }
                 }
+                __syncwarp();
             }
-            // the last use of every stage: its MMAs are done (and, in a pair, their arrivals
-            // on this CTA have landed) before the CTA may leave
-            for (uint32_t k = it > C::STAGES ? it - C::STAGES : 0; ok && k < it; ++k)
-                ok = mbar_wait_bounded(empty + 8 * (k % C::STAGES), (k / C::STAGES) & 1, wait_ns);
-            if (!ok) {
-                atomicOr(&g_wait_error, 1u);
-                const uint64_t t0 = global_ns();             // copies in flight land within this
-                for (int i = 0; i < (1 << 20) && global_ns() - t0 < 2000000ull; ++i) __nanosleep(1000);
-            }
+        }
+        // the last use of every stage: its MMAs are done (and, in a pair, their arrivals on
+        // this CTA have landed) before the CTA may leave
+        for (uint32_t k = it > C::STAGES ? it - C::STAGES : 0; ok && k < it; ++k)
+            ok = mbar_wait_bounded(empty + 8 * (k % C::STAGES), (k / C::STAGES) & 1, wait_ns);
+        if (!__all_sync(0xffffffffu, ok)) {
+            if (lane == 0) atomicOr(&g_wait_error, 1u);
+            const uint64_t t0 = global_ns();                 // copies in flight land within this
+            for (int i = 0; i < (1 << 20) && global_ns() - t0 < 2000000ull; ++i) __nanosleep(1000);
         }
         __syncwarp();
     } else if (warp == kEpiWarps + 1) {
         // ---- products ----
-        if (lane == 0 && leader) {
+        if (leader) {
             constexpr uint32_t idesc = mma_idesc(128 * C::CG, C::BN, C::A_MN, C::B_MN);
+            // 16 K elements on: 32 bytes along a K-major row, 16 rows of an MN-major tile
+            constexpr uint32_t a_step = C::A_MN ? 2048 / 16 : 32 / 16, b_step = C::B_MN ? 2048 / 16 : 32 / 16;
+            const uint64_t da0 = smem_desc(smem_addr(smem), C::A_MN ? 8192 : 16, 1024);
+            const uint64_t db0 = smem_desc(smem_addr(smem) + C::PL * C::A_BYTES, C::B_MN ? 8192 : 16, 1024);
             bool ok = true;
             uint32_t it = 0, ac = 0;
             for (int t = cluster; ok && t < n_tiles; t += n_clusters) {
@@ -345,28 +425,28 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
                             break;
                         }
                         tc_fence_after();
-                        const uint32_t st = smem_addr(smem + s * C::STAGE);
+                        // stages are far below the descriptor's 256 KB, so offsets add to its low bits
+                        const uint64_t das = da0 + s * (C::STAGE / 16), dbs = db0 + s * (C::STAGE / 16);
+                        if (elect_one()) {
 #pragma unroll
-                        for (int pr = 0; pr < (C::PL == 3 ? 6 : 1); ++pr) {
-                            // plane pairs (0,0) (0,1) (1,0) (1,1) (0,2) (2,0): the other three are
-                            // below 2^-24 of the product
-                            const int pa = pr == 2 || pr == 3 ? 1 : pr == 5 ? 2 : 0;
-                            const int pb = pr == 1 || pr == 3 ? 1 : pr == 4 ? 2 : 0;
-                            const uint32_t a = st + pa * C::A_BYTES, b = st + C::PL * C::A_BYTES + pb * C::B_BYTES;
+                            for (int pr = 0; pr < (C::PL == 3 ? 6 : 1); ++pr) {
+                                // plane pairs (0,2) (2,0) (1,1) (0,1) (1,0) (0,0), smallest first (the other
+                                // three are below 2^-24 of the product)
+                                const int pa = C::PL == 1 ? 0 : pr == 1 ? 2 : pr == 2 || pr == 4 ? 1 : 0;
+                                const int pb = C::PL == 1 ? 0 : pr == 0 ? 2 : pr == 2 || pr == 3 ? 1 : 0;
 #pragma unroll
-                            for (int k = 0; k < kKb / 16; ++k) {
-                                // 16 K elements on: 32 bytes along a K-major row, 16 rows of an MN-major tile
-                                const uint64_t da = smem_desc(a + (C::A_MN ? k * 2048 : k * 32), C::A_MN ? 8192 : 16, 1024);
-                                const uint64_t db = smem_desc(b + (C::B_MN ? k * 2048 : k * 32), C::B_MN ? 8192 : 16, 1024);
-                                mma_bf16<C::CG>(d, da, db, idesc, kb > kc || pr > 0 || k > 0);
+                                for (int k = 0; k < kKb / 16; ++k)
+                                    mma_bf16<C::CG>(d, das + pa * (C::A_BYTES / 16) + k * a_step,
+                                                    dbs + pb * (C::B_BYTES / 16) + k * b_step, idesc, kb > kc || pr > 0 || k > 0);
                             }
+                            mma_commit<C::CG>(empty + 8 * s);
+                            if (kb + 1 == ke) mma_commit<C::CG>(acc_full + 8 * buf);
                         }
-                        mma_commit<C::CG>(empty + 8 * s);
+                        __syncwarp();
                     }
-                    if (ok) mma_commit<C::CG>(acc_full + 8 * buf);
                 }
             }
-            if (!ok) atomicOr(&g_wait_error, 1u);
+            if (!__all_sync(0xffffffffu, ok) && lane == 0) atomicOr(&g_wait_error, 1u);
         }
         __syncwarp();
     } else {
@@ -568,6 +648,100 @@ cudaError_t launch_cfg(const LinProblem& p, int splits, cudaStream_t st) {
     cfg.attrs = attr;
     cfg.numAttrs = per > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, k_linear<C>, ma, mb, sh, p.epi, detail::kWaitNs);
+}
+
+// Clusters of `per` CTAs of a kernel that the device holds at once, queried once.
+template <class C>
+int max_clusters(int dev, int per) {
+    static std::atomic<int> known[64][4];
+    const int slot = per == 2 ? 1 : per == 4 ? 2 : 3;
+    if (per == 1) return sm_count(dev);
+    if (dev < 0 || dev >= 64) return sm_count(dev) / (2 * per);
+    int n = known[dev][slot].load(std::memory_order_relaxed);
+    if (n > 0) return n;
+    if (prepare_kernel<C>(dev) != cudaSuccess) return 0;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = unsigned(per);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(per));
+    cfg.blockDim = dim3(kLinThreads);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, k_linear<C>, &cfg) != cudaSuccess || n < 1) {
+        cudaGetLastError();
+        n = sm_count(dev) / (2 * per);
+        if (n < 1) n = 1;
+    }
+    known[dev][slot].store(n, std::memory_order_relaxed);
+    return n;
+}
+
+// What a configuration costs, in us, measured on GB300 with the operands in L2 or streaming
+// from HBM: `fixed` from launch to the first product and from the last store to the end, `kb`
+// per K step of 64, `epi` for a tile's epilogue where nothing runs beside it.
+struct LinCost {
+    float fixed, kb, epi;
+};
+
+// A persistent configuration works through its tiles in waves, the epilogues beside the next
+// tile's products; a split one runs a cluster per tile, wave after wave.
+template <class C>
+float estimate(const LinProblem& p, int splits, int dev, LinCost c) {
+    const int64_t tiles = ceil_div(p.M, 128 * C::CG) * ceil_div(p.N, C::BN), kb = ceil_div(p.K, kKb);
+    if (splits > kb) return 1e30f;
+    const int64_t room = C::SPLIT ? max_clusters<C>(dev, splits) : sm_count(dev) / C::CG;
+    if (room < 1) return 1e30f;
+    const float waves = float(ceil_div(tiles, room));
+    if (C::SPLIT) return waves * (c.fixed + float(ceil_div(kb, splits)) * c.kb + c.epi);
+    return c.fixed + waves * float(kb) * c.kb + c.epi;
+}
+
+// The configuration with the lowest estimate.  Measured on GB300 (us, forward, bf16, rows x in
+// x out; 256 x 256 pair / 256 x 128 pair / best split): 8192 x 4096 x 11008 382 / 452 / 1248;
+// 2048^3 18.8 / 18.7 / 42; 333 x 2048 x 2048 - / 11 / 11; 1 x 2048 x 2048 13.3 / 9.2 / 5.8 (32
+// columns, 4 CTAs per tile), where one CTA per tile takes 9.8 and 8 CTAs, two waves of
+// clusters, 9.3.
+template <int MODE, typename OT, int PL, int CH>
+cudaError_t launch_product(const LinProblem& p, cudaStream_t st) {
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    using P256 = LinCfg<MODE, OT, 2, 256, PL, CH, false>;
+    using P128 = LinCfg<MODE, OT, 2, 128, PL, CH, false>;
+    using S128 = LinCfg<MODE, OT, 1, 128, 1, CH, true>;
+    using S64 = LinCfg<MODE, OT, 1, 64, PL, CH, true>;
+    using S32 = LinCfg<MODE, OT, 1, MODE == kWgrad ? 64 : 32, PL, CH, true>;
+    constexpr float f = PL == 1 ? 1.f : 6.f;
+    float best = estimate<P256>(p, 1, dev, {5.0f, 0.275f * f, 4.0f});
+    int which = 0, splits = 1;
+    auto consider = [&](float cost, int w, int s) {
+        if (cost < best) {
+            best = cost;
+            which = w;
+            splits = s;
+        }
+    };
+    consider(estimate<P128>(p, 1, dev, {3.9f, PL == 1 ? 0.18f : 1.05f, 2.5f}), 1, 1);
+    for (int s = 1; s <= 8; s *= 2) {
+        if constexpr (PL == 1) consider(estimate<S128>(p, s, dev, {4.3f, 0.25f, 2.0f}), 2, s);
+        consider(estimate<S64>(p, s, dev, {4.2f, PL == 1 ? 0.21f : 0.70f, 1.0f}), 3, s);
+        if constexpr (MODE != kWgrad) consider(estimate<S32>(p, s, dev, {4.0f, PL == 1 ? 0.20f : 0.63f, 0.5f}), 4, s);
+    }
+    switch (which) {
+        case 0: return launch_cfg<P256>(p, 1, st);
+        case 1: return launch_cfg<P128>(p, 1, st);
+        case 2:
+            if constexpr (PL == 1) return launch_cfg<S128>(p, splits, st);
+            break;
+        case 3: return launch_cfg<S64>(p, splits, st);
+        case 4:
+            if constexpr (MODE != kWgrad) return launch_cfg<S32>(p, splits, st);
+            break;
+    }
+    return cudaErrorInvalidValue;
 }
 
 }  // namespace

@@ -6,10 +6,10 @@ namespace fsdp {
 
 cudaError_t launch_linear_wgrad(const LinProblem& p, cudaStream_t st) {
     if (p.planes == 3)
-        return p.out_bf16 ? launch_cfg<LinCfg<kWgrad, uint16_t, 1, 128, 3, 4, false>>(p, 1, st)
-                          : launch_cfg<LinCfg<kWgrad, float, 1, 128, 3, 4, false>>(p, 1, st);
-    return p.out_bf16 ? launch_cfg<LinCfg<kWgrad, uint16_t, 1, 128, 1, 0, false>>(p, 1, st)
-                      : launch_cfg<LinCfg<kWgrad, float, 1, 128, 1, 0, false>>(p, 1, st);
+        return p.out_bf16 ? launch_product<kWgrad, uint16_t, 3, 0>(p, st)
+                          : launch_product<kWgrad, float, 3, 2>(p, st);
+    return p.out_bf16 ? launch_product<kWgrad, uint16_t, 1, 0>(p, st)
+                      : launch_product<kWgrad, float, 1, 8>(p, st);
 }
 
 // ---------------------------------------------------------------------------------------
