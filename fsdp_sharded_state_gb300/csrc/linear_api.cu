@@ -45,8 +45,10 @@ int make_drop(const fsdp_dropout_spec* s, int64_t rows, Drop* d) {
     d->thr = uint32_t(std::floor(s->p * 4294967296.0));
     d->on = s->p > 0.0;
     d->scale = float(1.0 / (1.0 - s->p));
-    d->k0 = uint32_t(s->seed);
-    d->k1 = uint32_t(s->seed >> 32);
+    for (uint32_t i = 0; i < 10; ++i) {
+        d->key[i][0] = uint32_t(s->seed) + i * 0x9E3779B9u;
+        d->key[i][1] = uint32_t(s->seed >> 32) + i * 0xBB67AE85u;
+    }
     d->layer = s->layer;
     d->row0 = s->row0;
     return FSDP_OK;
