@@ -71,13 +71,14 @@ k_dropout8(const T* x, int64_t ldx, const T* res, int64_t ldr, T* y, int64_t ldy
         }
     }
     const uint64_t r = uint64_t(row0 + d.row0);
+    const uint32_t u = __umulhi(0xCD9E8D57u, uint32_t(r >> 32));
     const DropCol c0 = drop_col(d, 2 * g, uint32_t(r >> 32)), c1 = drop_col(d, 2 * g + 1, uint32_t(r >> 32));
 #pragma unroll
     for (int k = 0; k < kDropRows; ++k) {
         if (k >= n) break;
         uint4 w[2] = {};
         if (d.on) {
-            const DropRow dr = drop_row(d, r + k);
+            const DropRow dr = drop_row(d, uint32_t(r) + k, u);
             w[0] = drop_words(d, dr, c0);
             w[1] = drop_words(d, dr, c1);
         }

@@ -28,6 +28,7 @@ struct LinEpi {
     int32_t act;               // fsdp_act
     int32_t accumulate;        // wgrad: out += instead of out =
     int32_t vec;               // every matrix here has 16-byte aligned rows
+    void* db;                  // wgrad: the column sums of dz, or NULL
     Drop drop;
 };
 
@@ -60,10 +61,6 @@ struct PackJob {
     int64_t dld, plane;
 };
 cudaError_t launch_pack(const PackJob* jobs, int n, bool f32, cudaStream_t st);
-
-// db[c] (+)= sum over rows of dz[r][c].
-cudaError_t launch_colsum(const void* dz, bool dz_bf16, int64_t rows, int64_t cols, int64_t ld, void* db, bool db_bf16,
-                          bool accumulate, cudaStream_t st);
 
 // y = residual + drop(x); drop.on = 0 copies.
 cudaError_t launch_dropout(const void* x, int64_t ldx, const void* residual, int64_t ldr, void* y, int64_t ldy, bool bf16,

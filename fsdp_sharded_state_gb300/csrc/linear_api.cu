@@ -220,12 +220,8 @@ int fsdp_linear_wgrad(int64_t rows, int64_t in, int64_t out, int32_t elem_dtype,
     ep.cols = in;
     ep.accumulate = accumulate != 0;
     ep.vec = rows16(dw, lddw, gs);
-    if ((rc = run_product(p, pk, elem_dtype, st))) return rc;
-    if (db) {
-        const cudaError_t e = launch_colsum(dz, elem_dtype == FSDP_BF16, rows, out, lddz, db, p.out_bf16, accumulate != 0, st);
-        if (e != cudaSuccess) return cuda_fail(e, "k_colsum launch");
-    }
-    return FSDP_OK;
+    ep.db = db;
+    return run_product(p, pk, elem_dtype, st);
 }
 
 int fsdp_dropout(int64_t rows, int64_t cols, int32_t elem_dtype, const void* x, int64_t ldx, const fsdp_dropout_spec* drop,

@@ -4,8 +4,9 @@
 // accumulators in TMEM, with the layer's epilogue (bias, activation or its derivative,
 // dropout, residual, accumulation) applied before the one rounding to the output type.
 //
-// Roles of a CTA (10 warps): warp 8 loads the operand tiles with tensor-map copies into a
-// ring of stages, warp 9 issues the MMAs, warps 0-7 empty the accumulators.  The
+// Roles of a CTA (12 warps): warp 8 loads the operand tiles with tensor-map copies into a
+// ring of stages, warp 9 issues the MMAs, warps 0-7 empty the accumulators, and in wgrad
+// warps 10 and 11 add up the columns of the dz tiles for db.  The
 // accumulators are double-buffered, so a persistent CTA's epilogue runs beside the next
 // tile's products.  Operands keep the row-major layout that the user's tensors have: the
 // matrix descriptors take K-major tiles (forward: w and x; dgrad: dz) and MN-major tiles
@@ -24,7 +25,8 @@ namespace fsdp {
 namespace {
 
 constexpr int kEpiWarps = 8;
-constexpr int kLinThreads = (kEpiWarps + 2) * 32;
+constexpr int kSumWarps = 2;
+constexpr int kLinThreads = (kEpiWarps + 2 + kSumWarps) * 32;
 constexpr int kKb = 64;                        // K elements per stage: 128-byte swizzled rows
 constexpr int kLinMaxStages = 8;
 constexpr int kUnitFloats = 32 * 32;           // an epilogue unit: 32 rows x 32 columns
@@ -65,107 +67,138 @@ __device__ __forceinline__ float load1(const float* p) { return *p; }
 __device__ __forceinline__ void store1(uint16_t* p, float v) { *p = to_bf16(v); }
 __device__ __forceinline__ void store1(float* p, float v) { *p = v; }
 
+// ---- packed pairs of fp32 --------------------------------------------------------------
+// One instruction for two elements: the epilogue is bound by instruction issue.
+struct F2 {
+    uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ F2 f2(float a) { return f2(a, a); }
+__device__ __forceinline__ void unpack(F2 x, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x.v)); }
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+// The fast base-2 exponential and reciprocal, of both.
+__device__ __forceinline__ F2 exp2_fast(F2 x) {
+    float a, b;
+    unpack(x, a, b);
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(a));
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(b));
+    return f2(a, b);
+}
+__device__ __forceinline__ F2 rcp_fast(F2 x) {
+    float a, b;
+    unpack(x, a, b);
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(a));
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(b));
+    return f2(a, b);
+}
+
 // ---- activations (fp32) --------------------------------------------------------------
 // gelu(z) = z Phi(z), gelu'(z) = Phi(z) + z exp(-z^2/2) / sqrt(2 pi);
 // silu(z) = z s, silu'(z) = s (1 + z (1 - s)), s = 1 / (1 + exp(-z)).
 // For fp32 results, CUDA's erff and expf.  For bf16 results (rounded to 2^-8 afterwards)
-// the fast exponential and reciprocal, and for Phi formula 7.1.26 of Abramowitz and Stegun,
-// Handbook of Mathematical Functions: erf(x) = 1 - (a1 t + .. + a5 t^5) exp(-x^2), t = 1 /
-// (1 + 0.3275911 x), for x >= 0, error at most 1.5e-7; its exponential is also the
-// derivative's.  The fast forms also keep the epilogue's code small: with CUDA's erff, expf
-// and division unrolled over a unit it did not fit the instruction caches, and a 256 x 256
-// tile's epilogue took 26,000 clocks instead of its arithmetic's 4,000.
+// the fast exponential and reciprocal, in pairs, and for Phi formula 7.1.26 of Abramowitz
+// and Stegun, Handbook of Mathematical Functions: erf(x) = 1 - (a1 t + .. + a5 t^5) exp(-x^2),
+// t = 1 / (1 + 0.3275911 x), for x >= 0, error at most 1.5e-7; its exponential is also the
+// derivative's.  A tile of 256 x 256 leaves the epilogue 16,000 clocks beside the products of
+// K = 2048: 64 issue slots per element.  With CUDA's erff, expf and division unrolled over a
+// unit, its code did not fit the instruction caches, and the tile's epilogue took 26,000
+// clocks even with no activation asked for.
 struct PhiExp {
-    float phi, e;              // Phi(z), exp(-z^2 / 2)
+    F2 phi, e;                 // Phi(z), exp(-z^2 / 2)
 };
-template <bool FAST>
-__device__ __forceinline__ PhiExp phi_exp(float z, bool want_e) {
+__device__ __forceinline__ PhiExp phi_exp(float z0, float z1) {
+    const F2 x = f2(fabsf(z0), fabsf(z1)) * f2(0.70710678118654752f);
     PhiExp r;
-    if constexpr (FAST) {
-        const float x = fabsf(z) * 0.70710678118654752f;
-        r.e = __expf(-x * x);
-        const float t = __fdividef(1.f, fmaf(0.3275911f, x, 1.f));
-        float q = fmaf(t, 1.061405429f, -1.453152027f);
-        q = fmaf(t, q, 1.421413741f);
-        q = fmaf(t, q, -0.284496736f);
-        q = fmaf(t, q, 0.254829592f);
-        const float half_tail = 0.5f * (t * q * r.e);            // (1 - erf(x)) / 2
-        r.phi = z < 0.f ? half_tail : 1.f - half_tail;           // NaN stays NaN
-    } else {
-        r.phi = fmaf(0.5f, erff(z * 0.70710678118654752f), 0.5f);
-        r.e = want_e ? expf(-0.5f * z * z) : 0.f;
-    }
+    r.e = exp2_fast(x * x * f2(-1.4426950408889634f));
+    const F2 t = rcp_fast(fma(f2(0.3275911f), x, f2(1.f)));
+    F2 q = fma(t, f2(0.5f * 1.061405429f), f2(0.5f * -1.453152027f));
+    q = fma(t, q, f2(0.5f * 1.421413741f));
+    q = fma(t, q, f2(0.5f * -0.284496736f));
+    q = fma(t, q, f2(0.5f * 0.254829592f));
+    // (1 - erf(x)) / 2 = t q e, so Phi = 1/2 +- (1/2 - t q e)
+    float a, b;
+    unpack(fma(t * q * f2(-1.f), r.e, f2(0.5f)), a, b);
+    r.phi = f2(copysignf(a, z0), copysignf(b, z1)) + f2(0.5f);
     return r;
 }
+__device__ __forceinline__ F2 sigmoid(F2 z) { return rcp_fast(exp2_fast(z * f2(-1.4426950408889634f)) + f2(1.f)); }
+
 template <bool FAST>
-__device__ __forceinline__ float sigmoid(float z) {
-    if constexpr (FAST) return __fdividef(1.f, 1.f + __expf(-z));
-    return 1.f / (1.f + expf(-z));
-}
-template <bool FAST, int V>
-__device__ __forceinline__ void activate(float (&v)[V], int act) {
+__device__ __forceinline__ void activate(float (&v)[8], int act) {
     if (act == FSDP_ACT_RELU) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = v[i] < 0.f ? 0.f : v[i];              // NaN stays NaN
+        for (int i = 0; i < 8; ++i) v[i] = v[i] < 0.f ? 0.f : v[i];              // NaN stays NaN
     } else if (act == FSDP_ACT_GELU) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[i] *= phi_exp<FAST>(v[i], false).phi;
-    } else if (act == FSDP_ACT_SILU) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[i] *= sigmoid<FAST>(v[i]);
-    }
-}
-// v *= act'(z)
-template <bool FAST, int V>
-__device__ __forceinline__ void activate_grad(float (&v)[V], const float (&z)[V], int act) {
-    if (act == FSDP_ACT_RELU) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = z[i] > 0.f ? v[i] : (z[i] != z[i] ? z[i] : 0.f);
-    } else if (act == FSDP_ACT_GELU) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const PhiExp p = phi_exp<FAST>(z[i], true);
-            v[i] *= fmaf(z[i] * 0.39894228040143268f, p.e, p.phi);
+        for (int i = 0; i < 8; i += FAST ? 2 : 1) {
+            if constexpr (FAST) unpack(f2(v[i], v[i + 1]) * phi_exp(v[i], v[i + 1]).phi, v[i], v[i + 1]);
+            else v[i] *= __fmaf_rn(0.5f, erff(v[i] * 0.70710678118654752f), 0.5f);
         }
     } else if (act == FSDP_ACT_SILU) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const float s = sigmoid<FAST>(z[i]);
-            v[i] *= s * fmaf(z[i], 1.f - s, 1.f);
+        for (int i = 0; i < 8; i += FAST ? 2 : 1) {
+            if constexpr (FAST) {
+                const F2 z = f2(v[i], v[i + 1]);
+                unpack(z * sigmoid(z), v[i], v[i + 1]);
+            } else {
+                v[i] = v[i] / (1.f + expf(-v[i]));
+            }
+        }
+    }
+}
+// v *= act'(z)
+template <bool FAST>
+__device__ __forceinline__ void activate_grad(float (&v)[8], const float (&z)[8], int act) {
+    if (act == FSDP_ACT_RELU) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = z[i] > 0.f ? v[i] : (z[i] != z[i] ? z[i] : 0.f);
+    } else if (act == FSDP_ACT_GELU) {
+#pragma unroll
+        for (int i = 0; i < 8; i += FAST ? 2 : 1) {
+            if constexpr (FAST) {
+                const PhiExp p = phi_exp(z[i], z[i + 1]);
+                unpack(f2(v[i], v[i + 1]) * fma(f2(z[i], z[i + 1]) * f2(0.39894228040143268f), p.e, p.phi), v[i], v[i + 1]);
+            } else {
+                const float phi = __fmaf_rn(0.5f, erff(z[i] * 0.70710678118654752f), 0.5f);
+                v[i] *= __fmaf_rn(z[i] * 0.39894228040143268f, expf(-0.5f * z[i] * z[i]), phi);
+            }
+        }
+    } else if (act == FSDP_ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < 8; i += FAST ? 2 : 1) {
+            if constexpr (FAST) {
+                const F2 x = f2(z[i], z[i + 1]), s = sigmoid(x);
+                unpack(f2(v[i], v[i + 1]) * (s * fma(x, fma(s, f2(-1.f), f2(1.f)), f2(1.f))), v[i], v[i + 1]);
+            } else {
+                const float s = 1.f / (1.f + expf(-z[i]));
+                v[i] *= s * __fmaf_rn(z[i], 1.f - s, 1.f);
+            }
         }
     }
 }
 
-// The epilogue of one element: what emit_unit does for 8, at any alignment.
-template <int MODE, typename OT>
-__device__ __noinline__ void emit1(const LinEpi& ep, int64_t row, int64_t col, float x) {
-    constexpr bool FAST = sizeof(OT) == 2;
-    OT* const out = static_cast<OT*>(ep.out) + row * ep.ldo + col;
-    float v[1] = {x};
-    if constexpr (MODE == kForward) {
-        if (ep.bias) v[0] += load1(static_cast<const OT*>(ep.bias) + col);
-        if (ep.preact) store1(static_cast<OT*>(ep.preact) + row * ep.ldz + col, v[0]);
-        activate<FAST, 1>(v, ep.act);
-    }
-    if constexpr (MODE != kWgrad) {
-        if (ep.drop.on) {
-            const uint4 a = drop_words(ep.drop, row, col >> 2);
-            const int k = int(col & 3);
-            v[0] = drop1(ep.drop, k == 0 ? a.x : k == 1 ? a.y : k == 2 ? a.z : a.w, v[0]);
-        }
-    }
-    if constexpr (MODE == kDgrad) {
-        if (ep.act != FSDP_ACT_NONE) {
-            const float z[1] = {load1(static_cast<const OT*>(ep.preact) + row * ep.ldz + col)};
-            activate_grad<FAST, 1>(v, z, ep.act);
-        }
-    }
-    if constexpr (MODE != kWgrad) {
-        if (ep.residual) v[0] += load1(static_cast<const OT*>(ep.residual) + row * ep.ldr + col);
-    } else {
-        if (ep.accumulate) v[0] += load1(out);
-    }
-    store1(out, v[0]);
+template <typename OT>
+__device__ __forceinline__ void emit_db(const LinEpi& ep, int64_t c, float t) {
+    OT* const p = static_cast<OT*>(ep.db) + c;
+    store1(p, ep.accumulate ? t + load1(p) : t);
 }
 
 // A unit in shared memory: [32 rows][32 columns] fp32, the 16-byte groups of row r at
@@ -190,6 +223,8 @@ __device__ __forceinline__ void emit_unit(const LinEpi& ep, const float* unit, i
                                        : nullptr;
         const int64_t add_step = 8 * (MODE == kWgrad ? ep.ldo : ep.ldr);
         OT* z = MODE != kWgrad && ep.preact ? static_cast<OT*>(ep.preact) + row1 * ep.ldz + col : nullptr;
+        DropCol dc[2] = {};                      // the generator's column products, for all rows of the unit
+        uint32_t row_hi = 0, row_u = 0;
         Raw8<OT> add_r = {}, z_r = {};
         float bias[8] = {};
         if (n_it > 0) {
@@ -222,13 +257,21 @@ __device__ __forceinline__ void emit_unit(const LinEpi& ep, const float* unit, i
                     store8(z, v);
                     z += 8 * ep.ldz;
                 }
-                activate<FAST, 8>(v, ep.act);
+                activate<FAST>(v, ep.act);
             }
             if constexpr (MODE != kWgrad) {
                 if (ep.drop.on) {
+                    const uint64_t gr = uint64_t(row0 + r + ep.drop.row0);
+                    if (it == 0 || uint32_t(gr >> 32) != row_hi) {
+                        row_hi = uint32_t(gr >> 32);
+                        dc[0] = drop_col(ep.drop, uint32_t(col >> 2), row_hi);
+                        dc[1] = drop_col(ep.drop, uint32_t(col >> 2) + 1, row_hi);
+                        row_u = __umulhi(0xCD9E8D57u, row_hi);
+                    }
+                    const DropRow dr = drop_row(ep.drop, uint32_t(gr), row_u);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const uint4 w = drop_words(ep.drop, row0 + r, (col >> 2) + h);
+                        const uint4 w = drop_words(ep.drop, dr, dc[h]);
                         v[4 * h] = drop1(ep.drop, w.x, v[4 * h]);
                         v[4 * h + 1] = drop1(ep.drop, w.y, v[4 * h + 1]);
                         v[4 * h + 2] = drop1(ep.drop, w.z, v[4 * h + 2]);
@@ -240,7 +283,7 @@ __device__ __forceinline__ void emit_unit(const LinEpi& ep, const float* unit, i
             if constexpr (MODE == kDgrad) {
                 if (z) {
                     widen(z_c, t);
-                    activate_grad<FAST, 8>(v, t, ep.act);
+                    activate_grad<FAST>(v, t, ep.act);
                 }
             }
             if (add) {
@@ -251,14 +294,117 @@ __device__ __forceinline__ void emit_unit(const LinEpi& ep, const float* unit, i
             store8(out, v);
             out += 8 * ep.ldo;
         }
-    } else {                                     // any alignment, and a ragged right edge: a lane per column
+    } else {
+        // any alignment, and a ragged right edge: a lane per column, 8 rows at a time
         const int64_t c = col0 + lane;
+        const bool in = c < ep.cols;
+        const float bias = MODE == kForward && ep.bias && in ? load1(static_cast<const OT*>(ep.bias) + c) : 0.f;
+        OT* out = static_cast<OT*>(ep.out) + row0 * ep.ldo + c;
+        const OT* add = MODE == kWgrad ? (ep.accumulate ? out : nullptr)
+                        : ep.residual  ? static_cast<const OT*>(ep.residual) + row0 * ep.ldr + c
+                                       : nullptr;
+        const int64_t add_ld = MODE == kWgrad ? ep.ldo : ep.ldr;
+        OT* z = MODE != kWgrad && ep.preact ? static_cast<OT*>(ep.preact) + row0 * ep.ldz + c : nullptr;
 #pragma unroll 1
-        for (int r = 0; r < 32; ++r) {
-            float v = unit[unit_at(r, lane)];
-            for (int s = 1; s < slots; ++s) v += unit[unit_at(r, lane) + s * kUnitFloats];
-            if (row0 + r < ep.rows && c < ep.cols) emit1<MODE, OT>(ep, row0 + r, c, v);
+        for (int r0 = 0; r0 < 32 && row0 + r0 < ep.rows; r0 += 8) {
+            const int n = !in ? 0 : ep.rows - row0 - r0 >= 8 ? 8 : int(ep.rows - row0 - r0);
+            float v[8], a[8], zs[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                a[i] = add && i < n ? load1(add + (r0 + i) * add_ld) : 0.f;
+                zs[i] = MODE == kDgrad && z && i < n ? load1(z + (r0 + i) * ep.ldz) : 0.f;
+                v[i] = unit[unit_at(r0 + i, lane)];
+            }
+#pragma unroll 1
+            for (int s = 1; s < slots; ++s) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] += unit[unit_at(r0 + i, lane) + s * kUnitFloats];
+            }
+            if constexpr (MODE == kForward) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    v[i] += bias;
+                    if (z && i < n) store1(z + (r0 + i) * ep.ldz, v[i]);
+                }
+                activate<FAST>(v, ep.act);
+            }
+            if constexpr (MODE != kWgrad) {
+                if (ep.drop.on) {
+                    // lane l draws the blocks of columns 4 (l mod 8) on of rows l / 8 and l / 8 + 4, as keep
+                    // bits; column `lane` of row i is bit lane mod 4 of what lane 8 (i mod 4) + lane / 4 drew
+                    uint32_t keep = 0;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint4 w = drop_words(ep.drop, row0 + r0 + (lane >> 3) + 4 * h, (col0 >> 2) + (lane & 7));
+                        keep |= (uint32_t(w.x >= ep.drop.thr) | uint32_t(w.y >= ep.drop.thr) << 1 |
+                                 uint32_t(w.z >= ep.drop.thr) << 2 | uint32_t(w.w >= ep.drop.thr) << 3) << (4 * h);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t b = __shfl_sync(0xffffffffu, keep, 8 * i + (lane >> 2)) >> (lane & 3);
+                        v[i] = b & 1 ? v[i] * ep.drop.scale : 0.f;
+                        v[i + 4] = b >> 4 & 1 ? v[i + 4] * ep.drop.scale : 0.f;
+                    }
+                }
+            }
+            if constexpr (MODE == kDgrad) {
+                if (z) activate_grad<FAST>(v, zs, ep.act);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < n) store1(out + (r0 + i) * ep.ldo, v[i] + a[i]);
         }
+    }
+}
+
+// ---- column sums of dz (wgrad's db) ---------------------------------------------------
+// Two warps add up the dz tiles that the products of the first column of tiles read anyway,
+// from shared memory: no byte of dz is read for db.  A tile (one plane) is two chunks of 64
+// columns, each 64 rows of 128 bytes whose 16-byte groups are swizzled: group p of row r holds
+// columns 8 (p ^ (r mod 8)) on.  A warp takes a chunk; lane l reads group l mod 8 of rows l / 8
+// + 4 h + 8 j: the same columns for all j.  A tile's 8 rows are added in a tree before they
+// meet the running sums.
+struct ColSum {
+    float v[2][8];
+};
+template <int PL>
+__device__ __forceinline__ void colsum_row(float (&x)[8], const unsigned char* p, int plane_bytes) {
+    widen(load_raw(reinterpret_cast<const uint16_t*>(p)), x);
+    if constexpr (PL == 3) {                                 // hi + (mid + lo): both sums exact
+        float a[8], b[8];
+        widen(load_raw(reinterpret_cast<const uint16_t*>(p + plane_bytes)), a);
+        widen(load_raw(reinterpret_cast<const uint16_t*>(p + 2 * plane_bytes)), b);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] += a[e] + b[e];
+    }
+}
+template <int PL>
+__device__ __forceinline__ void colsum_add(ColSum& s, const unsigned char* chunk, int plane_bytes, int lane) {
+    const unsigned char* p = chunk + (lane >> 3) * 128 + (lane & 7) * 16;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        float t[2][8];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            float x[4][8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) colsum_row<PL>(x[j], p + h * 512 + (4 * k + j) * 1024, plane_bytes);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) t[k][e] = (x[0][e] + x[1][e]) + (x[2][e] + x[3][e]);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s.v[h][e] += t[0][e] + t[1][e];
+    }
+}
+// Column u * 8 + e of the chunk to t[e] of lane u < 8, in a fixed order.
+__device__ __forceinline__ void colsum_lanes(const ColSum& s, float (&t)[8], int lane) {
+    const int row = lane >> 3, u = lane & 7;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        t[e] = __shfl_sync(0xffffffffu, s.v[0][e], (row << 3) | (u ^ row)) +
+               __shfl_sync(0xffffffffu, s.v[1][e], (row << 3) | (u ^ (row + 4)));
+        t[e] += __shfl_xor_sync(0xffffffffu, t[e], 8);
+        t[e] += __shfl_xor_sync(0xffffffffu, t[e], 16);
     }
 }
 
@@ -277,9 +423,10 @@ struct LinCfg {
     static constexpr int STAGE = PL * (A_BYTES + B_BYTES);
     // the epilogue's shared memory: a unit per warp, or the join's slots
     static constexpr int EPI = SPLIT ? (BN >= 128 ? 64 : 32) * 1024 : kEpiWarps * kUnitFloats * 4;
-    static constexpr int FIT = (227 * 1024 - 2048 - EPI) / STAGE;
+    static constexpr int MORE = SPLIT && MODE == kWgrad ? 2560 : 2048;   // alignment, barriers, a split's column sums
+    static constexpr int FIT = (227 * 1024 - MORE - EPI) / STAGE;
     static constexpr int STAGES = FIT < kLinMaxStages ? FIT : kLinMaxStages;
-    static constexpr int SMEM = STAGES * STAGE + EPI + 2048;     // + alignment, barriers
+    static constexpr int SMEM = STAGES * STAGE + EPI + MORE;
     static constexpr int TMEM = 2 * BN < 32 ? 32 : 2 * BN;
     static_assert(STAGES >= 2, "two stages");
     static_assert(SMEM > 114 * 1024 && SMEM <= 227 * 1024, "one CTA per SM: its TMEM is never contended");
@@ -303,6 +450,9 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
     const uint32_t bars = smem_addr(smem + C::STAGES * C::STAGE + C::EPI);
     const uint32_t full = bars, empty = bars + 8 * kLinMaxStages, acc_full = empty + 8 * kLinMaxStages,
                    acc_empty = acc_full + 16, tmem_word = acc_empty + 16;
+    const uint32_t summed = tmem_word + 8;       // wgrad: a stage's dz tile has been added
+    static_assert(8 * (3 * kLinMaxStages + 6) <= 256, "barriers");
+    float* const db_part = reinterpret_cast<float*>(smem + C::STAGES * C::STAGE + C::EPI + 256);   // SPLIT: [128]
     const bool leader = C::CG == 1 || rank == 0;
 
     if (warp == 0) tmem_alloc<C::CG>(tmem_word, C::TMEM);
@@ -312,6 +462,7 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
         for (int s = 0; s < C::STAGES; ++s) {
             mbar_init(full + 8 * s, 1);
             mbar_init(empty + 8 * s, 1);
+            mbar_init(summed + 8 * s, kSumWarps);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(acc_full + 8 * b, 1);
@@ -339,22 +490,32 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
     const int chunk = C::CH ? C::CH : sh.n_kb;
 
     // Tiles in bands of 8 along M, N outer inside a band: concurrently running tiles share
-    // operand rows in L2.
+    // operand rows in L2.  wgrad takes the first column of tiles before all others, so that a
+    // CTA's tiles with column sums are its first.
     auto tile_at = [&](int t, int& mt, int& nt) {
-        const int band = 8 * sh.n_tiles, g = t / band, first = g * 8;
+        const int lead = C::MODE == kWgrad ? sh.m_tiles : 0;
+        if (t < lead) {
+            mt = t;
+            nt = 0;
+            return;
+        }
+        const int cols = C::MODE == kWgrad ? sh.n_tiles - 1 : sh.n_tiles;
+        const int band = 8 * cols, u = t - lead, g = u / band, first = g * 8;
         const int high = sh.m_tiles - first < 8 ? sh.m_tiles - first : 8;
-        const int r = t - g * band;
+        const int r = u - g * band;
         mt = first + r % high;
-        nt = r / high;
+        nt = r / high + (C::MODE == kWgrad ? 1 : 0);
     };
 
     if (warp == kEpiWarps) {
         // ---- loads ----
         bool ok = true;
         uint32_t it = 0;
+        uint32_t adding = 0, parity = 0;             // per stage: its tile is being added; phase of `summed`
         for (int t = cluster; ok && t < n_tiles; t += n_clusters) {
             int mt, nt;
             tile_at(t, mt, nt);
+            const bool db_tile = C::MODE == kWgrad && ep.db && t < sh.m_tiles;
             const int m0 = (mt * C::CG + (C::CG == 2 ? int(rank) : 0)) * 128;
             const int n0 = nt * C::BN + (C::CG == 2 ? int(rank) * C::BROWS : 0);
             for (int kb = kb0; kb < kb1; ++kb, ++it) {
@@ -363,6 +524,15 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
                     ok = false;
                     break;
                 }
+                if (C::MODE == kWgrad && (adding >> s & 1)) {
+                    if (!mbar_wait_bounded(summed + 8 * s, parity >> s & 1, wait_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    parity ^= 1u << s;
+                    adding ^= 1u << s;
+                }
+                if (db_tile) adding |= 1u << s;
                 if (elect_one()) {
                     if (leader) mbar_arrive_tx(full + 8 * s, C::CG * C::STAGE);
                     const uint32_t bar = C::CG == 2 ? map_rank(full + 8 * s, 0) : full + 8 * s;
@@ -449,6 +619,39 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
             if (!__all_sync(0xffffffffu, ok) && lane == 0) atomicOr(&g_wait_error, 1u);
         }
         __syncwarp();
+    } else if (warp >= kEpiWarps + 2) {
+        // ---- column sums of dz ----
+        // A stage is read once it is loaded (in a pair, where only the leader sees that, once its
+        // products are done), and loaded again once it has been added.
+        if (C::MODE == kWgrad && ep.db) {
+            const int chunk_at = warp - (kEpiWarps + 2);
+            bool ok = true;
+            uint32_t it = 0;
+            for (int mt = cluster; ok && mt < sh.m_tiles; mt += n_clusters) {   // the tiles mt, 0: the first ones
+                ColSum db = {};
+                for (int kb = kb0; ok && kb < kb1; ++kb, ++it) {
+                    const uint32_t s = it % C::STAGES;
+                    ok = __all_sync(0xffffffffu, mbar_wait_bounded((C::CG == 2 ? empty : full) + 8 * s, (it / C::STAGES) & 1, wait_ns));
+                    if (!ok) break;
+                    colsum_add<C::PL>(db, smem + s * C::STAGE + chunk_at * 8192, C::A_BYTES, lane);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(summed + 8 * s);
+                }
+                float v[8];
+                colsum_lanes(db, v, lane);
+                const int c = chunk_at * 64 + lane * 8;
+                if (ok && lane < 8) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int64_t col = int64_t(mt * C::CG + (C::CG == 2 ? int(rank) : 0)) * 128 + c + e;
+                        if (C::SPLIT) db_part[c + e] = v[e];
+                        else if (col < ep.rows) emit_db<typename C::OT>(ep, col, v[e]);
+                    }
+                }
+            }
+            if (!ok && lane == 0) atomicOr(&g_wait_error, 1u);
+        }
+        __syncwarp();
     } else {
         // ---- epilogue ----
         // Warp w reads TMEM lanes 32 (w mod 4) on: rows 32 q of the CTA's part of the tile; the
@@ -503,12 +706,17 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
 #pragma unroll
                 for (int jj = 0; jj < NJ; ++jj) {
                     if ((2 * jj + half) * 32 < C::BN) {
-                        float v[32];
-                        tmem_ld32(src + (2 * jj + half) * 32, v);
                         if constexpr (C::CH != 0) {
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) sum[jj][i] += v[i];
+                            for (int h = 0; h < 2; ++h) {
+                                float v[16];
+                                tmem_ld16(src + (2 * jj + half) * 32 + 16 * h, v);
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) sum[jj][16 * h + i] += v[i];
+                            }
                         } else {
+                            float v[32];
+                            tmem_ld32(src + (2 * jj + half) * 32, v);
                             finish(jj, v);
                         }
                     }
@@ -542,6 +750,21 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
                 const int64_t m0 = int64_t(mt) * 128 + q * 32, n0 = int64_t(nt) * C::BN + j * 32;
                 emit_unit<C::MODE, typename C::OT>(ep, epi_smem + (u / sh.splits) * sh.splits * kUnitFloats, sh.splits,
                                                    C::MODE == kWgrad ? m0 : n0, C::MODE == kWgrad ? n0 : m0, lane);
+            }
+        }
+        if constexpr (C::MODE == kWgrad) {
+            if (ep.db) {                         // the CTAs' shares of the column sums, in order
+                int mt, nt;
+                tile_at(cluster, mt, nt);
+                const int64_t c = int64_t(mt) * 128 + tid;
+                if (rank == 0 && nt == 0 && tid < 128 && c < ep.rows) {
+                    float t = 0.f;
+                    for (int r = 0; r < sh.splits; ++r) t += ld_cluster(map_rank(smem_addr(db_part + tid), r));
+                    emit_db<typename C::OT>(ep, c, t);
+                }
+                __syncwarp();
+                cluster_arrive();                // no CTA leaves while its share is read
+                cluster_wait();
             }
         }
     }

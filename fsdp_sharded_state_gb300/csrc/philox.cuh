@@ -61,9 +61,9 @@ __device__ __forceinline__ DropCol drop_col(const Drop& d, uint32_t q, uint32_t 
     const uint64_t a3 = uint64_t(0xD2511F53u) * (uint32_t(b2 >> 32) ^ u ^ d.key[1][0]);
     return {uint32_t(a1), uint32_t(b2) ^ d.key[2][0], uint32_t(a3 >> 32) ^ d.key[2][1], uint32_t(a3)};
 }
-__device__ __forceinline__ DropRow drop_row(const Drop& d, uint64_t r) {
-    const uint32_t hi = __umulhi(0xCD9E8D57u, uint32_t(r >> 32));
-    const uint64_t a2 = uint64_t(0xD2511F53u) * (hi ^ uint32_t(r) ^ d.key[0][0]);
+// row: its low word; u: the high word of the round constant times the row's high word.
+__device__ __forceinline__ DropRow drop_row(const Drop& d, uint32_t row, uint32_t u) {
+    const uint64_t a2 = uint64_t(0xD2511F53u) * (u ^ row ^ d.key[0][0]);
     return {uint32_t(a2 >> 32) ^ d.key[1][1], uint32_t(a2)};
 }
 __device__ __forceinline__ uint4 drop_words(const Drop& d, const DropRow& r, const DropCol& c) {
