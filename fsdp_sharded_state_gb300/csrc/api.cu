@@ -514,7 +514,8 @@ int fsdp_check_status(fsdp_stream_t stream) {
     unsigned int gave_up = 0;
     e = fsdp::take_wait_error(&gave_up);
     if (e != cudaSuccess) return cuda_fail(e, "wait status read");
-    for (auto take : {fsdp::take_wait_error_forward, fsdp::take_wait_error_dgrad, fsdp::take_wait_error_wgrad}) {
+    for (auto take : {fsdp::take_wait_error_forward, fsdp::take_wait_error_forward_pair, fsdp::take_wait_error_dgrad,
+                      fsdp::take_wait_error_dgrad_pair, fsdp::take_wait_error_wgrad}) {
         unsigned int linear = 0;
         e = take(&linear);
         if (e != cudaSuccess) return cuda_fail(e, "wait status read");

@@ -9,10 +9,10 @@
 
 namespace fsdp {
 
-// A linear layer's three products, as D[M, N] = sum over k of A[M, k] B[N, k]:
-//   forward   A = w  (out features), B = x   (rows), K = in features;  out[row = N][col = M]
-//   dgrad     A = w^T (in features), B = dz  (rows), K = out features; out[row = N][col = M]
-//   wgrad     A = dz^T (out features), B = x^T (in features), K = rows; out[row = M][col = N]
+// A linear layer's three products: out[r][c] = sum over k of R[r, k] C[c, k].
+//   forward   R = x,    C = w,    K = in features
+//   dgrad     R = dz,   C = w^T,  K = out features
+//   wgrad     R = dz^T, C = x^T,  K = rows of the batch
 enum LinMode { kForward = 0, kDgrad = 1, kWgrad = 2 };
 
 // The epilogue of a product; pointers in the output's element type.
@@ -41,8 +41,8 @@ struct LinOperand {
 
 struct LinProblem {
     LinMode mode;
-    int64_t M, N, K;
-    LinOperand a, b;
+    int64_t K;
+    LinOperand rows_op, cols_op;   // R and C, as the caller stores them
     int planes;                // 1: bf16 operands; 3: fp32 operands as three bf16 terms
     bool out_bf16;
     LinEpi epi;
@@ -51,6 +51,9 @@ struct LinProblem {
 cudaError_t launch_linear_forward(const LinProblem& p, cudaStream_t st);
 cudaError_t launch_linear_dgrad(const LinProblem& p, cudaStream_t st);
 cudaError_t launch_linear_wgrad(const LinProblem& p, cudaStream_t st);
+// The CTA-pair kernels with bf16 operands and results, tiles of 256 x bn.
+cudaError_t launch_pair_forward(const LinProblem& p, int bn, cudaStream_t st);
+cudaError_t launch_pair_dgrad(const LinProblem& p, int bn, cudaStream_t st);
 
 // Operands brought into the form of LinOperand: a bf16 matrix copied to aligned rows, or
 // an fp32 matrix split into three bf16 planes (see linear_pack.cu).  Up to two per launch.
@@ -66,9 +69,11 @@ cudaError_t launch_pack(const PackJob* jobs, int n, bool f32, cudaStream_t st);
 cudaError_t launch_dropout(const void* x, int64_t ldx, const void* residual, int64_t ldr, void* y, int64_t ldy, bool bf16,
                            int64_t rows, int64_t cols, const Drop& d, cudaStream_t st);
 
-// Reads and clears the wait words of the linear kernels (synchronous).
-cudaError_t take_wait_error_forward(unsigned int* flag);   // linear_forward.cu
-cudaError_t take_wait_error_dgrad(unsigned int* flag);     // linear_dgrad.cu
-cudaError_t take_wait_error_wgrad(unsigned int* flag);     // linear_wgrad.cu
+// Read and clear the wait words of the linear kernels (synchronous), one per translation unit.
+cudaError_t take_wait_error_forward(unsigned int* flag);
+cudaError_t take_wait_error_forward_pair(unsigned int* flag);
+cudaError_t take_wait_error_dgrad(unsigned int* flag);
+cudaError_t take_wait_error_dgrad_pair(unsigned int* flag);
+cudaError_t take_wait_error_wgrad(unsigned int* flag);
 
 }  // namespace fsdp

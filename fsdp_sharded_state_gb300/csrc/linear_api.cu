@@ -124,10 +124,8 @@ int fsdp_linear_forward(int64_t rows, int64_t in, int64_t out, int32_t elem_dtyp
     if ((rc = make_drop(drop, rows, &p.epi.drop))) return rc;
     if (rows == 0) return FSDP_OK;
     Packer pk{static_cast<unsigned char*>(workspace), workspace_bytes, {}};
-    if ((rc = pk.operand(w, out, in, ldw, elem_dtype, &p.a)) || (rc = pk.operand(x, rows, in, ldx, elem_dtype, &p.b))) return rc;
+    if ((rc = pk.operand(w, out, in, ldw, elem_dtype, &p.cols_op)) || (rc = pk.operand(x, rows, in, ldx, elem_dtype, &p.rows_op))) return rc;
     p.mode = kForward;
-    p.M = out;
-    p.N = rows;
     p.K = in;
     p.planes = elem_dtype == FSDP_F32 ? 3 : 1;
     p.out_bf16 = elem_dtype == FSDP_BF16;
@@ -165,10 +163,8 @@ int fsdp_linear_dgrad(int64_t rows, int64_t in, int64_t out, int32_t elem_dtype,
     if ((rc = make_drop(drop, rows, &p.epi.drop))) return rc;
     if (rows == 0) return FSDP_OK;
     Packer pk{static_cast<unsigned char*>(workspace), workspace_bytes, {}};
-    if ((rc = pk.operand(w, out, in, ldw, elem_dtype, &p.a)) || (rc = pk.operand(dz, rows, out, lddz, elem_dtype, &p.b))) return rc;
+    if ((rc = pk.operand(w, out, in, ldw, elem_dtype, &p.cols_op)) || (rc = pk.operand(dz, rows, out, lddz, elem_dtype, &p.rows_op))) return rc;
     p.mode = kDgrad;
-    p.M = in;
-    p.N = rows;
     p.K = out;
     p.planes = elem_dtype == FSDP_F32 ? 3 : 1;
     p.out_bf16 = elem_dtype == FSDP_BF16;
@@ -206,10 +202,8 @@ int fsdp_linear_wgrad(int64_t rows, int64_t in, int64_t out, int32_t elem_dtype,
     }
     LinProblem p = {};
     Packer pk{static_cast<unsigned char*>(workspace), workspace_bytes, {}};
-    if ((rc = pk.operand(dz, rows, out, lddz, elem_dtype, &p.a)) || (rc = pk.operand(x, rows, in, ldx, elem_dtype, &p.b))) return rc;
+    if ((rc = pk.operand(dz, rows, out, lddz, elem_dtype, &p.rows_op)) || (rc = pk.operand(x, rows, in, ldx, elem_dtype, &p.cols_op))) return rc;
     p.mode = kWgrad;
-    p.M = out;
-    p.N = in;
     p.K = rows;
     p.planes = elem_dtype == FSDP_F32 ? 3 : 1;
     p.out_bf16 = grad_dtype == FSDP_BF16;

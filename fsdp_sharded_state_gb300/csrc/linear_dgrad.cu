@@ -5,8 +5,8 @@
 namespace fsdp {
 
 cudaError_t launch_linear_dgrad(const LinProblem& p, cudaStream_t st) {
-    if (p.planes == 3) return launch_product<kDgrad, float, 3, 2>(p, st);
-    return launch_product<kDgrad, uint16_t, 1, 0>(p, st);
+    if (p.planes == 3) return launch_product<kDgrad, float, 3, 2>(p, launch_pair_as<kDgrad, float, 3, 2>, st);
+    return launch_product<kDgrad, uint16_t, 1, 0>(p, launch_pair_dgrad, st);
 }
 
 cudaError_t take_wait_error_dgrad(unsigned int* flag) { return take_local_wait_error(flag); }

@@ -206,32 +206,59 @@ __device__ __forceinline__ void emit_db(const LinEpi& ep, int64_t c, float t) {
 // holds a column) and the row-wise reads are free of bank conflicts.
 __device__ __forceinline__ int unit_at(int r, int c) { return r * 32 + ((((c >> 2) ^ (r & 7)) << 2) | (c & 3)); }
 
-// Adds the `slots` copies of a unit (kUnitFloats apart, in order) and emits it: 4 lanes per
-// row, 8 columns per lane, 8 rows at a time; what the epilogue reads of the next 8 rows is
-// loaded before these are computed.
-template <int MODE, typename OT>
-__device__ __forceinline__ void emit_unit(const LinEpi& ep, const float* unit, int slots, int64_t row0, int64_t col0, int lane) {
-    constexpr bool FAST = sizeof(OT) == 2;
-    const int64_t col = col0 + (lane & 3) * 8;
-    if (ep.vec && ep.cols - col0 >= 32) {
-        const int64_t row1 = row0 + (lane >> 2);
-        const int n_it = ep.rows > row1 ? (ep.rows - row1 >= 32 ? 4 : int((ep.rows - row1 + 7) >> 3)) : 0;
-        OT* out = static_cast<OT*>(ep.out) + row1 * ep.ldo + col;
-        // the addend (residual, or what wgrad accumulates to) and the pre-activation
-        const OT* add = MODE == kWgrad ? (ep.accumulate ? out : nullptr)
-                        : ep.residual  ? static_cast<const OT*>(ep.residual) + row1 * ep.ldr + col
-                                       : nullptr;
-        const int64_t add_step = 8 * (MODE == kWgrad ? ep.ldo : ep.ldr);
-        OT* z = MODE != kWgrad && ep.preact ? static_cast<OT*>(ep.preact) + row1 * ep.ldz + col : nullptr;
+// The epilogue of one unit: 4 lanes per row, 8 columns per lane, 8 rows at a time.  What it
+// reads of memory (the addend: the residual, or what wgrad accumulates to; the
+// pre-activation) is asked for AHEAD steps ahead, the first ones by begin(), which a caller
+// runs before it fetches the accumulators: with one step ahead, the reads of a 256 x 256
+// tile's residual cost 10,000 clocks of latency.
+// EP: the activation (+ 4 with dropout) that the kernel is compiled for, or -1 for the
+// call's.  Jumping over what a call does not use costs more than computing it: the loop
+// outgrows the innermost instruction cache, and a unit with neither took 2,150 clocks with
+// EP = -1 where 1,150 do.
+template <int MODE, typename OT, int AHEAD, int EP>
+struct UnitEmit {
+    static constexpr bool FAST = sizeof(OT) == 2;
+    static __device__ __forceinline__ int act(const LinEpi& ep) { return EP >= 0 ? EP & 3 : ep.act; }
+    static __device__ __forceinline__ bool drop(const LinEpi& ep) { return EP >= 0 ? EP >= 4 : ep.drop.on != 0; }
+    OT* out;
+    const OT* add;
+    OT* z;
+    int64_t add_step, z_step, row0, col0;
+    int n_it;                                    // steps of 8 rows; -1: not by vectors
+    Raw8<OT> aq[AHEAD], zq[AHEAD];
+
+    __device__ __forceinline__ void begin(const LinEpi& ep, int64_t row0_, int64_t col0_, int lane) {
+        row0 = row0_;
+        col0 = col0_;
+        n_it = -1;
+        if (!ep.vec || ep.cols - col0 < 32) return;
+        const int64_t col = col0 + (lane & 3) * 8, row1 = row0 + (lane >> 2);
+        n_it = ep.rows > row1 ? (ep.rows - row1 >= 32 ? 4 : int((ep.rows - row1 + 7) >> 3)) : 0;
+        out = static_cast<OT*>(ep.out) + row1 * ep.ldo + col;
+        add = MODE == kWgrad ? (ep.accumulate ? out : nullptr)
+              : ep.residual  ? static_cast<const OT*>(ep.residual) + row1 * ep.ldr + col
+                             : nullptr;
+        add_step = 8 * (MODE == kWgrad ? ep.ldo : ep.ldr);
+        z = MODE != kWgrad && ep.preact ? static_cast<OT*>(ep.preact) + row1 * ep.ldz + col : nullptr;
+        z_step = 8 * ep.ldz;
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            if (add && i < n_it) aq[i] = load_raw(add + i * add_step);
+            if (MODE == kDgrad && z && i < n_it) zq[i] = load_raw(z + i * z_step);
+        }
+    }
+
+    // Adds the `slots` copies of the unit (kUnitFloats apart, in order) and emits it.
+    __device__ __forceinline__ void run(const LinEpi& ep, const float* unit, int slots, int lane) {
+        if (n_it < 0) {
+            by_columns(ep, unit, slots, lane);
+            return;
+        }
+        const int64_t col = col0 + (lane & 3) * 8;
         DropCol dc[2] = {};                      // the generator's column products, for all rows of the unit
         uint32_t row_hi = 0, row_u = 0;
-        Raw8<OT> add_r = {}, z_r = {};
         float bias[8] = {};
-        if (n_it > 0) {
-            if (add) add_r = load_raw(add);
-            if (MODE == kDgrad && z) z_r = load_raw(z);
-            if (MODE == kForward && ep.bias) widen(load_raw(static_cast<const OT*>(ep.bias) + col), bias);
-        }
+        if (MODE == kForward && ep.bias && n_it > 0) widen(load_raw(static_cast<const OT*>(ep.bias) + col), bias);
 #pragma unroll 1
         for (int it = 0; it < n_it; ++it) {
             const int r = it * 8 + (lane >> 2);
@@ -245,22 +272,24 @@ __device__ __forceinline__ void emit_unit(const LinEpi& ep, const float* unit, i
                 b.x += d.x; b.y += d.y; b.z += d.z; b.w += d.w;
             }
             float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-            const Raw8<OT> add_c = add_r, z_c = z_r;
-            if (it + 1 < n_it) {
-                if (add) add_r = load_raw(add += add_step);
-                if (MODE == kDgrad && z) z_r = load_raw(z += 8 * ep.ldz);
+            const Raw8<OT> add_c = aq[0], z_c = zq[0];
+#pragma unroll
+            for (int i = 0; i + 1 < AHEAD; ++i) {
+                aq[i] = aq[i + 1];
+                zq[i] = zq[i + 1];
+            }
+            if (it + AHEAD < n_it) {
+                if (add) aq[AHEAD - 1] = load_raw(add + (it + AHEAD) * add_step);
+                if (MODE == kDgrad && z) zq[AHEAD - 1] = load_raw(z + (it + AHEAD) * z_step);
             }
             if constexpr (MODE == kForward) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) v[i] += bias[i];
-                if (z) {
-                    store8(z, v);
-                    z += 8 * ep.ldz;
-                }
-                activate<FAST>(v, ep.act);
+                if (z) store8(z + it * z_step, v);
+                activate<FAST>(v, act(ep));
             }
             if constexpr (MODE != kWgrad) {
-                if (ep.drop.on) {
+                if (drop(ep)) {
                     const uint64_t gr = uint64_t(row0 + r + ep.drop.row0);
                     if (it == 0 || uint32_t(gr >> 32) != row_hi) {
                         row_hi = uint32_t(gr >> 32);
@@ -283,7 +312,7 @@ __device__ __forceinline__ void emit_unit(const LinEpi& ep, const float* unit, i
             if constexpr (MODE == kDgrad) {
                 if (z) {
                     widen(z_c, t);
-                    activate_grad<FAST>(v, t, ep.act);
+                    activate_grad<FAST>(v, t, act(ep));
                 }
             }
             if (add) {
@@ -294,25 +323,27 @@ __device__ __forceinline__ void emit_unit(const LinEpi& ep, const float* unit, i
             store8(out, v);
             out += 8 * ep.ldo;
         }
-    } else {
-        // any alignment, and a ragged right edge: a lane per column, 8 rows at a time
+    }
+
+    // Any alignment, and a ragged right edge: a lane per column, 8 rows at a time.
+    __device__ __forceinline__ void by_columns(const LinEpi& ep, const float* unit, int slots, int lane) const {
         const int64_t c = col0 + lane;
         const bool in = c < ep.cols;
         const float bias = MODE == kForward && ep.bias && in ? load1(static_cast<const OT*>(ep.bias) + c) : 0.f;
-        OT* out = static_cast<OT*>(ep.out) + row0 * ep.ldo + c;
-        const OT* add = MODE == kWgrad ? (ep.accumulate ? out : nullptr)
+        OT* o = static_cast<OT*>(ep.out) + row0 * ep.ldo + c;
+        const OT* addp = MODE == kWgrad ? (ep.accumulate ? o : nullptr)
                         : ep.residual  ? static_cast<const OT*>(ep.residual) + row0 * ep.ldr + c
                                        : nullptr;
         const int64_t add_ld = MODE == kWgrad ? ep.ldo : ep.ldr;
-        OT* z = MODE != kWgrad && ep.preact ? static_cast<OT*>(ep.preact) + row0 * ep.ldz + c : nullptr;
+        OT* zp = MODE != kWgrad && ep.preact ? static_cast<OT*>(ep.preact) + row0 * ep.ldz + c : nullptr;
 #pragma unroll 1
         for (int r0 = 0; r0 < 32 && row0 + r0 < ep.rows; r0 += 8) {
             const int n = !in ? 0 : ep.rows - row0 - r0 >= 8 ? 8 : int(ep.rows - row0 - r0);
             float v[8], a[8], zs[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                a[i] = add && i < n ? load1(add + (r0 + i) * add_ld) : 0.f;
-                zs[i] = MODE == kDgrad && z && i < n ? load1(z + (r0 + i) * ep.ldz) : 0.f;
+                a[i] = addp && i < n ? load1(addp + (r0 + i) * add_ld) : 0.f;
+                zs[i] = MODE == kDgrad && zp && i < n ? load1(zp + (r0 + i) * ep.ldz) : 0.f;
                 v[i] = unit[unit_at(r0 + i, lane)];
             }
 #pragma unroll 1
@@ -324,12 +355,12 @@ __device__ __forceinline__ void emit_unit(const LinEpi& ep, const float* unit, i
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     v[i] += bias;
-                    if (z && i < n) store1(z + (r0 + i) * ep.ldz, v[i]);
+                    if (zp && i < n) store1(zp + (r0 + i) * ep.ldz, v[i]);
                 }
-                activate<FAST>(v, ep.act);
+                activate<FAST>(v, act(ep));
             }
             if constexpr (MODE != kWgrad) {
-                if (ep.drop.on) {
+                if (drop(ep)) {
                     // lane l draws the blocks of columns 4 (l mod 8) on of rows l / 8 and l / 8 + 4, as keep
                     // bits; column `lane` of row i is bit lane mod 4 of what lane 8 (i mod 4) + lane / 4 drew
                     uint32_t keep = 0;
@@ -348,14 +379,14 @@ __device__ __forceinline__ void emit_unit(const LinEpi& ep, const float* unit, i
                 }
             }
             if constexpr (MODE == kDgrad) {
-                if (z) activate_grad<FAST>(v, zs, ep.act);
+                if (zp) activate_grad<FAST>(v, zs, act(ep));
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                if (i < n) store1(out + (r0 + i) * ep.ldo, v[i] + a[i]);
+                if (i < n) store1(o + (r0 + i) * ep.ldo, v[i] + a[i]);
         }
     }
-}
+};
 
 // ---- column sums of dz (wgrad's db) ---------------------------------------------------
 // Two warps add up the dz tiles that the products of the first column of tiles read anyway,
@@ -412,12 +443,19 @@ __device__ __forceinline__ void colsum_lanes(const ColSum& s, float (&t)[8], int
 // (3 planes: six products, of the terms whose exponents add up to at most two steps); CH:
 // K steps after which the accumulators are added to fp32 registers (0: never).  SPLIT: the
 // CTAs of a cluster (2, 4 or 8, CG = 1) take a share of K each and join through shared memory.
-template <int MODE_, typename OT_, int CG_, int BN_, int PL_, int CH_, bool SPLIT_>
+template <int MODE_, typename OT_, int CG_, int BN_, int PL_, int CH_, bool SPLIT_, int EP_ = -1>
 struct LinCfg {
     using OT = OT_;
-    static constexpr int MODE = MODE_, CG = CG_, BN = BN_, PL = PL_, CH = CH_;
+    static constexpr int MODE = MODE_, CG = CG_, BN = BN_, PL = PL_, CH = CH_, EP = EP_;
     static constexpr bool SPLIT = SPLIT_;
-    static constexpr bool A_MN = MODE != kForward, B_MN = MODE == kWgrad;
+    // Which of out's axes runs along M.  A split tile of forward or dgrad has the features
+    // there, so that few rows need few columns of the tile; the others have out's rows, which
+    // a lane then holds 32 consecutive columns of (wider stores to shared memory: 1,150 clocks
+    // for a unit against 2,200 with a column per lane).
+    static constexpr bool ROWS_M = MODE == kWgrad || !SPLIT;
+    static constexpr bool A_MN = MODE == kWgrad || (MODE == kDgrad && !ROWS_M);
+    static constexpr bool B_MN = MODE == kWgrad || (MODE == kDgrad && ROWS_M);
+    static constexpr int AHEAD = sizeof(OT) == 2 && CH == 0 ? 4 : 1;        // registers allow it
     static constexpr int BROWS = BN / CG;                        // B rows a CTA loads
     static constexpr int A_BYTES = 128 * 128, B_BYTES = BROWS * 128;
     static constexpr int STAGE = PL * (A_BYTES + B_BYTES);
@@ -432,6 +470,41 @@ struct LinCfg {
     static_assert(SMEM > 114 * 1024 && SMEM <= 227 * 1024, "one CTA per SM: its TMEM is never contended");
     static_assert(!B_MN || BROWS % 64 == 0, "MN-major tiles come in chunks of 64");
     static_assert(!SPLIT || CG == 1, "a cluster is a pair or a split");
+};
+
+// What the epilogue of a persistent CTA's tile will read of residual and preact, brought
+// into L2 by the load warp while the tile's products run: a line of 128 bytes per lane, a few
+// per K step.
+template <class C>
+struct EpiPrefetch {
+    static constexpr bool ON = !C::SPLIT && C::MODE != kWgrad;
+    static constexpr int LINES = C::BN * int(sizeof(typename C::OT)) / 128 + 1;      // of a row, which may start inside a line
+    int64_t row0, col0;
+    int at, total, per;        // 32-row steps done, of all; steps per K step
+
+    __device__ __forceinline__ EpiPrefetch(const LinEpi& ep, int64_t row0_, int64_t col0_, int n_kb) : row0(row0_), col0(col0_) {
+        at = total = per = 0;
+        if constexpr (ON) {
+            const int tensors = (ep.residual != nullptr) + (C::MODE == kDgrad && ep.preact != nullptr);
+            total = tensors * 4 * LINES;
+            per = (total + n_kb - 1) / n_kb;
+        }
+    }
+    __device__ __forceinline__ void step(const LinEpi& ep, int lane) {
+        if constexpr (ON) {
+            for (int k = 0; k < per && at < total; ++k, ++at) {
+                const int which = at / (4 * LINES), rest = at - which * 4 * LINES;
+                const bool second = which == 1 || ep.residual == nullptr;
+                const char* base = static_cast<const char*>(second ? ep.preact : ep.residual);
+                const int64_t row = row0 + (rest / LINES) * 32 + lane, ld = second ? ep.ldz : ep.ldr;
+                const int64_t width = (ep.cols - col0 < C::BN ? ep.cols - col0 : C::BN) * int64_t(sizeof(typename C::OT));
+                int64_t off = int64_t(rest % LINES) * 128;
+                if (off >= width) off = width - 1;
+                if (row < ep.rows)
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(base + (row * ld + col0) * int64_t(sizeof(typename C::OT)) + off));
+            }
+        }
+    }
 };
 
 struct LinShape {
@@ -518,7 +591,9 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
             const bool db_tile = C::MODE == kWgrad && ep.db && t < sh.m_tiles;
             const int m0 = (mt * C::CG + (C::CG == 2 ? int(rank) : 0)) * 128;
             const int n0 = nt * C::BN + (C::CG == 2 ? int(rank) * C::BROWS : 0);
+            EpiPrefetch<C> ahead(ep, m0, nt * C::BN, kb1 - kb0);
             for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                ahead.step(ep, lane);
                 const uint32_t s = it % C::STAGES, use = it / C::STAGES;
                 if (use > 0 && !mbar_wait_bounded(empty + 8 * s, (use - 1) & 1, wait_ns)) {
                     ok = false;
@@ -672,20 +747,24 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
 #pragma unroll
                     for (int i = 0; i < 32; ++i) sum[j][i] = 0.f;
             }
+            UnitEmit<C::MODE, typename C::OT, C::AHEAD, C::EP> io;
+            auto begin = [&](int jj) {
+                const int64_t n = n0 + (2 * jj + half) * 32;
+                if constexpr (!C::SPLIT) io.begin(ep, C::ROWS_M ? m0 : n, C::ROWS_M ? n : m0, lane);
+            };
             auto finish = [&](int jj, const float (&v)[32]) {
                 const int j = 2 * jj + half;                 // this group of 32 columns
-                const int64_t row0 = C::MODE == kWgrad ? m0 : n0 + j * 32, col0 = C::MODE == kWgrad ? n0 + j * 32 : m0;
                 if constexpr (C::SPLIT) {
                     const uint32_t u = 4 * j + q;            // unit u joins in CTA u mod splits
                     const uint32_t slot = (u / sh.splits) * sh.splits + rank;
                     const uint32_t dst = map_rank(smem_addr(epi_smem + slot * kUnitFloats), u % sh.splits);
 #pragma unroll
                     for (int c = 0; c < 32; ++c)
-                        st_cluster(dst + 4 * (C::MODE == kWgrad ? unit_at(lane, c) : unit_at(c, lane)), v[c]);
+                        st_cluster(dst + 4 * (C::ROWS_M ? unit_at(lane, c) : unit_at(c, lane)), v[c]);
                 } else {
                     float* const unit = epi_smem + warp * kUnitFloats;
                     __syncwarp();
-                    if constexpr (C::MODE == kWgrad) {       // a lane holds a row
+                    if constexpr (C::ROWS_M) {               // a lane holds a row
 #pragma unroll
                         for (int g = 0; g < 8; ++g)
                             st4(unit + unit_at(lane, 4 * g), make_float4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]));
@@ -694,7 +773,7 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
                         for (int c = 0; c < 32; ++c) unit[unit_at(c, lane)] = v[c];
                     }
                     __syncwarp();
-                    emit_unit<C::MODE, typename C::OT>(ep, unit, 1, row0, col0, lane);
+                    io.run(ep, unit, 1, lane);
                 }
             };
             for (int kc = kb0; ok && kc < kb1; kc += chunk, ++ac) {
@@ -716,6 +795,7 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
                             }
                         } else {
                             float v[32];
+                            begin(jj);
                             tmem_ld32(src + (2 * jj + half) * 32, v);
                             finish(jj, v);
                         }
@@ -731,7 +811,10 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
             if constexpr (C::CH != 0) {
 #pragma unroll
                 for (int jj = 0; jj < NJ; ++jj)
-                    if (ok && (2 * jj + half) * 32 < C::BN) finish(jj, sum[jj]);
+                    if (ok && (2 * jj + half) * 32 < C::BN) {
+                        begin(jj);
+                        finish(jj, sum[jj]);
+                    }
             }
         }
         if (!ok && lane == 0) atomicOr(&g_wait_error, 1u);
@@ -748,8 +831,9 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
             for (int u = int(rank) + warp * sh.splits; u < C::BN / 8; u += kEpiWarps * sh.splits) {
                 const int q = u & 3, j = u >> 2;
                 const int64_t m0 = int64_t(mt) * 128 + q * 32, n0 = int64_t(nt) * C::BN + j * 32;
-                emit_unit<C::MODE, typename C::OT>(ep, epi_smem + (u / sh.splits) * sh.splits * kUnitFloats, sh.splits,
-                                                   C::MODE == kWgrad ? m0 : n0, C::MODE == kWgrad ? n0 : m0, lane);
+                UnitEmit<C::MODE, typename C::OT, C::AHEAD, C::EP> io;
+                io.begin(ep, C::ROWS_M ? m0 : n0, C::ROWS_M ? n0 : m0, lane);
+                io.run(ep, epi_smem + (u / sh.splits) * sh.splits * kUnitFloats, sh.splits, lane);
             }
         }
         if constexpr (C::MODE == kWgrad) {
@@ -846,12 +930,13 @@ cudaError_t launch_cfg(const LinProblem& p, int splits, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     if ((e = prepare_kernel<C>(dev)) != cudaSuccess) return e;
     CUtensorMap ma, mb;
-    if ((e = make_map(&ma, p.a, C::PL, C::A_MN ? kKb : 128)) != cudaSuccess) return e;
-    if ((e = make_map(&mb, p.b, C::PL, C::B_MN ? kKb : C::BROWS)) != cudaSuccess) return e;
-    const int64_t mt = ceil_div(p.M, 128 * C::CG), nt = ceil_div(p.N, C::BN), kb = ceil_div(p.K, kKb);
+    if ((e = make_map(&ma, C::ROWS_M ? p.rows_op : p.cols_op, C::PL, C::A_MN ? kKb : 128)) != cudaSuccess) return e;
+    if ((e = make_map(&mb, C::ROWS_M ? p.cols_op : p.rows_op, C::PL, C::B_MN ? kKb : C::BROWS)) != cudaSuccess) return e;
+    const int64_t M = C::ROWS_M ? p.epi.rows : p.epi.cols, N = C::ROWS_M ? p.epi.cols : p.epi.rows;
+    const int64_t mt = ceil_div(M, 128 * C::CG), nt = ceil_div(N, C::BN), kb = ceil_div(p.K, kKb);
     const int per = C::CG == 2 ? 2 : C::SPLIT ? splits : 1;
     // tile numbers, K steps and tile coordinates are 32-bit
-    if (mt * nt * per > INT32_MAX / 16 || kb > INT32_MAX / 128 || p.M > INT32_MAX - 512 || p.N > INT32_MAX - 512)
+    if (mt * nt * per > INT32_MAX / 16 || kb > INT32_MAX / 128 || M > INT32_MAX - 512 || N > INT32_MAX - 512)
         return cudaErrorInvalidValue;
     LinShape sh{int32_t(mt), int32_t(nt), int32_t(kb), splits};
     int64_t clusters = mt * nt;
@@ -913,9 +998,12 @@ struct LinCost {
 // tile's products; a split one runs a cluster per tile, wave after wave.
 template <class C>
 float estimate(const LinProblem& p, int splits, int dev, LinCost c) {
-    const int64_t tiles = ceil_div(p.M, 128 * C::CG) * ceil_div(p.N, C::BN), kb = ceil_div(p.K, kKb);
+    const int64_t M = C::ROWS_M ? p.epi.rows : p.epi.cols, N = C::ROWS_M ? p.epi.cols : p.epi.rows;
+    const int64_t tiles = ceil_div(M, 128 * C::CG) * ceil_div(N, C::BN), kb = ceil_div(p.K, kKb);
     if (splits > kb) return 1e30f;
-    const int64_t room = C::SPLIT ? max_clusters<C>(dev, splits) : sm_count(dev) / C::CG;
+    int64_t room;
+    if constexpr (C::SPLIT) room = max_clusters<C>(dev, splits);
+    else room = sm_count(dev) / C::CG;
     if (room < 1) return 1e30f;
     const float waves = float(ceil_div(tiles, room));
     if (C::SPLIT) return waves * (c.fixed + float(ceil_div(kb, splits)) * c.kb + c.epi);
@@ -927,8 +1015,12 @@ float estimate(const LinProblem& p, int splits, int dev, LinCost c) {
 // 2048^3 18.8 / 18.7 / 42; 333 x 2048 x 2048 - / 11 / 11; 1 x 2048 x 2048 13.3 / 9.2 / 5.8 (32
 // columns, 4 CTAs per tile), where one CTA per tile takes 9.8 and 8 CTAs, two waves of
 // clusters, 9.3.
+//
+// For bf16 results the pair configurations are compiled for each activation and dropout
+// (launch_pair, in a translation unit of its own); the others take them at run time: split
+// tiles run their epilogue once, and fp32 tiles have six times the products to run it beside.
 template <int MODE, typename OT, int PL, int CH>
-cudaError_t launch_product(const LinProblem& p, cudaStream_t st) {
+cudaError_t launch_product(const LinProblem& p, cudaError_t (*launch_pair)(const LinProblem&, int, cudaStream_t), cudaStream_t st) {
     int dev = 0;
     const cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -939,7 +1031,7 @@ cudaError_t launch_product(const LinProblem& p, cudaStream_t st) {
     using S32 = LinCfg<MODE, OT, 1, MODE == kWgrad ? 64 : 32, PL, CH, true>;
     constexpr float f = PL == 1 ? 1.f : 6.f;
     float best = estimate<P256>(p, 1, dev, {5.0f, 0.275f * f, 4.0f});
-    int which = 0, splits = 1;
+    int which = 256, splits = 1;
     auto consider = [&](float cost, int w, int s) {
         if (cost < best) {
             best = cost;
@@ -947,24 +1039,29 @@ cudaError_t launch_product(const LinProblem& p, cudaStream_t st) {
             splits = s;
         }
     };
-    consider(estimate<P128>(p, 1, dev, {3.9f, PL == 1 ? 0.18f : 1.05f, 2.5f}), 1, 1);
+    consider(estimate<P128>(p, 1, dev, {3.9f, PL == 1 ? 0.18f : 1.05f, 2.5f}), 128, 1);
     for (int s = 1; s <= 8; s *= 2) {
         if constexpr (PL == 1) consider(estimate<S128>(p, s, dev, {4.3f, 0.25f, 2.0f}), 2, s);
-        consider(estimate<S64>(p, s, dev, {4.2f, PL == 1 ? 0.21f : 0.70f, 1.0f}), 3, s);
-        if constexpr (MODE != kWgrad) consider(estimate<S32>(p, s, dev, {4.0f, PL == 1 ? 0.20f : 0.63f, 0.5f}), 4, s);
+        consider(estimate<S64>(p, s, dev, {4.2f, PL == 1 ? 0.21f : 0.70f, 1.0f}), 1, s);
+        if constexpr (MODE != kWgrad) consider(estimate<S32>(p, s, dev, {4.0f, PL == 1 ? 0.20f : 0.63f, 0.5f}), 0, s);
     }
     switch (which) {
-        case 0: return launch_cfg<P256>(p, 1, st);
-        case 1: return launch_cfg<P128>(p, 1, st);
+        case 0:
+            if constexpr (MODE != kWgrad) return launch_cfg<S32>(p, splits, st);
+            break;
+        case 1: return launch_cfg<S64>(p, splits, st);
         case 2:
             if constexpr (PL == 1) return launch_cfg<S128>(p, splits, st);
             break;
-        case 3: return launch_cfg<S64>(p, splits, st);
-        case 4:
-            if constexpr (MODE != kWgrad) return launch_cfg<S32>(p, splits, st);
-            break;
+        default: return launch_pair(p, which, st);
     }
     return cudaErrorInvalidValue;
+}
+
+template <int MODE, typename OT, int PL, int CH, int EP = -1>
+cudaError_t launch_pair_as(const LinProblem& p, int bn, cudaStream_t st) {
+    return bn == 256 ? launch_cfg<LinCfg<MODE, OT, 2, 256, PL, CH, false, EP>>(p, 1, st)
+                     : launch_cfg<LinCfg<MODE, OT, 2, 128, PL, CH, false, EP>>(p, 1, st);
 }
 
 }  // namespace
