@@ -27,7 +27,7 @@ struct LinEpi {
     int64_t rows, cols;        // of out
     int32_t act;               // fsdp_act
     int32_t accumulate;        // wgrad: out += instead of out =
-    int32_t vec;               // every matrix here has 16-byte aligned rows
+    int32_t vec;               // every matrix here has rows aligned to 16 bytes (1), 32 bytes (2), or not (0)
     void* db;                  // wgrad: the column sums of dz, or NULL
     Drop drop;
 };

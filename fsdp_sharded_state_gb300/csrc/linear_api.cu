@@ -56,6 +56,14 @@ int make_drop(const fsdp_dropout_spec* s, int64_t rows, Drop* d) {
 
 bool rows16(const void* p, int64_t ld, int esize) { return aligned16(p) && ld * esize % 16 == 0; }
 
+// How the rows of an epilogue's matrix are aligned: to 32 bytes (2), 16 (1), or not (0); a
+// matrix that is not there is aligned.
+int row_class(const void* p, int64_t ld, int esize) {
+    if (!p) return 2;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p) | uintptr_t(ld * esize);
+    return a % 32 == 0 ? 2 : a % 16 == 0 ? 1 : 0;
+}
+
 int64_t round_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 
 // Elements of one packed plane, and bytes of a packed operand.
@@ -140,8 +148,8 @@ int fsdp_linear_forward(int64_t rows, int64_t in, int64_t out, int32_t elem_dtyp
     ep.rows = rows;
     ep.cols = out;
     ep.act = act;
-    ep.vec = rows16(y, ldy, es) && (!residual || rows16(residual, ldr, es)) && (!preact || rows16(preact, ldz, es)) &&
-             (!bias || aligned16(bias));
+    ep.vec = std::min({row_class(y, ldy, es), row_class(residual, ldr, es), row_class(preact, ldz, es)});
+    if (bias && !aligned16(bias)) ep.vec = 0;
     return run_product(p, pk, elem_dtype, reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -178,7 +186,7 @@ int fsdp_linear_dgrad(int64_t rows, int64_t in, int64_t out, int32_t elem_dtype,
     ep.rows = rows;
     ep.cols = in;
     ep.act = act;
-    ep.vec = rows16(dx, lddx, es) && (!residual || rows16(residual, ldr, es)) && (!ep.preact || rows16(preact, ldz, es));
+    ep.vec = std::min({row_class(dx, lddx, es), row_class(residual, ldr, es), row_class(ep.preact, ldz, es)});
     return run_product(p, pk, elem_dtype, reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -213,7 +221,7 @@ int fsdp_linear_wgrad(int64_t rows, int64_t in, int64_t out, int32_t elem_dtype,
     ep.rows = out;
     ep.cols = in;
     ep.accumulate = accumulate != 0;
-    ep.vec = rows16(dw, lddw, gs);
+    ep.vec = row_class(dw, lddw, gs);
     ep.db = db;
     return run_product(p, pk, elem_dtype, st);
 }

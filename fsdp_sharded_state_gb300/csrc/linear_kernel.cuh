@@ -141,20 +141,20 @@ __device__ __forceinline__ PhiExp phi_exp(float z0, float z1) {
 }
 __device__ __forceinline__ F2 sigmoid(F2 z) { return rcp_fast(exp2_fast(z * f2(-1.4426950408889634f)) + f2(1.f)); }
 
-template <bool FAST>
-__device__ __forceinline__ void activate(float (&v)[8], int act) {
+template <bool FAST, int N>
+__device__ __forceinline__ void activate(float (&v)[N], int act) {
     if (act == FSDP_ACT_RELU) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = v[i] < 0.f ? 0.f : v[i];              // NaN stays NaN
+        for (int i = 0; i < N; ++i) v[i] = v[i] < 0.f ? 0.f : v[i];              // NaN stays NaN
     } else if (act == FSDP_ACT_GELU) {
 #pragma unroll
-        for (int i = 0; i < 8; i += FAST ? 2 : 1) {
+        for (int i = 0; i < N; i += FAST ? 2 : 1) {
             if constexpr (FAST) unpack(f2(v[i], v[i + 1]) * phi_exp(v[i], v[i + 1]).phi, v[i], v[i + 1]);
             else v[i] *= __fmaf_rn(0.5f, erff(v[i] * 0.70710678118654752f), 0.5f);
         }
     } else if (act == FSDP_ACT_SILU) {
 #pragma unroll
-        for (int i = 0; i < 8; i += FAST ? 2 : 1) {
+        for (int i = 0; i < N; i += FAST ? 2 : 1) {
             if constexpr (FAST) {
                 const F2 z = f2(v[i], v[i + 1]);
                 unpack(z * sigmoid(z), v[i], v[i + 1]);
@@ -165,14 +165,14 @@ __device__ __forceinline__ void activate(float (&v)[8], int act) {
     }
 }
 // v *= act'(z)
-template <bool FAST>
-__device__ __forceinline__ void activate_grad(float (&v)[8], const float (&z)[8], int act) {
+template <bool FAST, int N>
+__device__ __forceinline__ void activate_grad(float (&v)[N], const float (&z)[N], int act) {
     if (act == FSDP_ACT_RELU) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = z[i] > 0.f ? v[i] : (z[i] != z[i] ? z[i] : 0.f);
+        for (int i = 0; i < N; ++i) v[i] = z[i] > 0.f ? v[i] : 0.f;
     } else if (act == FSDP_ACT_GELU) {
 #pragma unroll
-        for (int i = 0; i < 8; i += FAST ? 2 : 1) {
+        for (int i = 0; i < N; i += FAST ? 2 : 1) {
             if constexpr (FAST) {
                 const PhiExp p = phi_exp(z[i], z[i + 1]);
                 unpack(f2(v[i], v[i + 1]) * fma(f2(z[i], z[i + 1]) * f2(0.39894228040143268f), p.e, p.phi), v[i], v[i + 1]);
@@ -183,7 +183,7 @@ __device__ __forceinline__ void activate_grad(float (&v)[8], const float (&z)[8]
         }
     } else if (act == FSDP_ACT_SILU) {
 #pragma unroll
-        for (int i = 0; i < 8; i += FAST ? 2 : 1) {
+        for (int i = 0; i < N; i += FAST ? 2 : 1) {
             if constexpr (FAST) {
                 const F2 x = f2(z[i], z[i + 1]), s = sigmoid(x);
                 unpack(f2(v[i], v[i + 1]) * (s * fma(x, fma(s, f2(-1.f), f2(1.f)), f2(1.f))), v[i], v[i + 1]);
@@ -286,7 +286,7 @@ struct UnitEmit {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) v[i] += bias[i];
                 if (z) store8(z + it * z_step, v);
-                activate<FAST>(v, act(ep));
+                activate<FAST, 8>(v, act(ep));
             }
             if constexpr (MODE != kWgrad) {
                 if (drop(ep)) {
@@ -312,7 +312,7 @@ struct UnitEmit {
             if constexpr (MODE == kDgrad) {
                 if (z) {
                     widen(z_c, t);
-                    activate_grad<FAST>(v, t, act(ep));
+                    activate_grad<FAST, 8>(v, t, act(ep));
                 }
             }
             if (add) {
@@ -357,7 +357,7 @@ struct UnitEmit {
                     v[i] += bias;
                     if (zp && i < n) store1(zp + (r0 + i) * ep.ldz, v[i]);
                 }
-                activate<FAST>(v, act(ep));
+                activate<FAST, 8>(v, act(ep));
             }
             if constexpr (MODE != kWgrad) {
                 if (drop(ep)) {
@@ -379,7 +379,7 @@ struct UnitEmit {
                 }
             }
             if constexpr (MODE == kDgrad) {
-                if (zp) activate_grad<FAST>(v, zs, act(ep));
+                if (zp) activate_grad<FAST, 8>(v, zs, act(ep));
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -387,6 +387,112 @@ struct UnitEmit {
         }
     }
 };
+
+// 16 bf16 elements in one access of 32 bytes (32-byte aligned).
+struct Raw16 {
+    uint32_t w[8];
+};
+__device__ __forceinline__ Raw16 load_raw16(const uint16_t* p) {
+    Raw16 r;
+    asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3]), "=r"(r.w[4]), "=r"(r.w[5]), "=r"(r.w[6]), "=r"(r.w[7])
+                 : "l"(p)
+                 : "memory");
+    return r;
+}
+__device__ __forceinline__ void widen(const Raw16& r, float (&v)[16]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        v[2 * i] = bf16lo(r.w[i]);
+        v[2 * i + 1] = bf16hi(r.w[i]);
+    }
+}
+__device__ __forceinline__ void store16(uint16_t* p, const float (&v)[16]) {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                 "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
+// The epilogue straight from the accumulators, a lane per row: no trip through shared memory,
+// whose bandwidth the products of a CTA pair use up.  For bf16 results of persistent tiles with
+// 32-byte aligned rows: an access of a warp touches 32 lines whatever its width, so these take
+// whole 32-byte sectors.  The warp takes units of 32 columns, 64 apart from col0 on, while they
+// lie wholly inside the matrix, NU at most, and returns how many; a unit's two halves are read
+// (residual, pre-activation) while the unit before it is computed.  dcol: the generator's
+// column products of the units' columns, in shared memory; dr: the lane's row's.
+template <int MODE, int EP, int NU>
+__device__ __forceinline__ int emit_rows(const LinEpi& ep, uint32_t acc, int64_t row, int64_t col0, const DropRow& dr,
+                                         const DropCol* dcol) {
+    const int act = EP >= 0 ? EP & 3 : ep.act;
+    const bool drop = MODE != kWgrad && (EP >= 0 ? EP >= 4 : ep.drop.on != 0);
+    const bool in = row < ep.rows;
+    const int64_t left = ep.cols - col0;
+    const int units = left < 32 ? 0 : (left - 32) / 64 + 1 < NU ? int((left - 32) / 64 + 1) : NU;
+    uint16_t* out = static_cast<uint16_t*>(ep.out) + row * ep.ldo + col0;
+    const uint16_t* add = MODE == kWgrad ? (ep.accumulate ? out : nullptr)
+                          : ep.residual  ? static_cast<const uint16_t*>(ep.residual) + row * ep.ldr + col0
+                                         : nullptr;
+    uint16_t* z = MODE != kWgrad && ep.preact ? static_cast<uint16_t*>(ep.preact) + row * ep.ldz + col0 : nullptr;
+    const uint16_t* bias = MODE == kForward && ep.bias ? static_cast<const uint16_t*>(ep.bias) + col0 : nullptr;
+    Raw16 aq[2] = {}, zq[2] = {};
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+        if (add && in && units > 0) aq[g] = load_raw16(add + 16 * g);
+        if (MODE == kDgrad && z && in && units > 0) zq[g] = load_raw16(z + 16 * g);
+    }
+#pragma unroll 1
+    for (int u = 0; u < units; ++u) {
+        const bool more = in && u + 1 < units;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            const int c = 64 * u + 16 * g;
+            float v[16], t[16];
+            tmem_ld16(acc + c, v);
+            if constexpr (MODE == kForward) {
+                if (bias) {
+                    float b[8];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        widen(load_raw(bias + c + 8 * h), b);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) v[8 * h + i] += b[i];
+                    }
+                }
+                if (z && in) store16(z + c, v);
+                activate<true, 16>(v, act);
+            }
+            if (drop) {
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    const uint4 q = ldu4(dcol + 8 * u + 4 * g + b);
+                    const uint4 w = drop_words(ep.drop, dr, DropCol{q.x, q.y, q.z, q.w});
+                    v[4 * b] = drop1(ep.drop, w.x, v[4 * b]);
+                    v[4 * b + 1] = drop1(ep.drop, w.y, v[4 * b + 1]);
+                    v[4 * b + 2] = drop1(ep.drop, w.z, v[4 * b + 2]);
+                    v[4 * b + 3] = drop1(ep.drop, w.w, v[4 * b + 3]);
+                }
+            }
+            if constexpr (MODE == kDgrad) {
+                if (z) {
+                    widen(zq[g], t);
+                    if (more) zq[g] = load_raw16(z + c + 64);
+                    activate_grad<true, 16>(v, t, act);
+                }
+            }
+            if (add) {
+                widen(aq[g], t);
+                if (more) aq[g] = load_raw16(add + c + 64);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[i] += t[i];
+            }
+            if (in) store16(out + c, v);
+        }
+    }
+    return units;
+}
 
 // ---- column sums of dz (wgrad's db) ---------------------------------------------------
 // Two warps add up the dz tiles that the products of the first column of tiles read anyway,
@@ -455,7 +561,8 @@ struct LinCfg {
     static constexpr bool ROWS_M = MODE == kWgrad || !SPLIT;
     static constexpr bool A_MN = MODE == kWgrad || (MODE == kDgrad && !ROWS_M);
     static constexpr bool B_MN = MODE == kWgrad || (MODE == kDgrad && ROWS_M);
-    static constexpr int AHEAD = sizeof(OT) == 2 && CH == 0 ? 4 : 1;        // registers allow it
+    static constexpr bool DIRECT = !SPLIT && CH == 0 && sizeof(OT) == 2;    // emit_rows where rows are aligned
+    static constexpr int AHEAD = 1;
     static constexpr int BROWS = BN / CG;                        // B rows a CTA loads
     static constexpr int A_BYTES = 128 * 128, B_BYTES = BROWS * 128;
     static constexpr int STAGE = PL * (A_BYTES + B_BYTES);
@@ -782,8 +889,32 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t src = tmem + buf * C::BN + (uint32_t(q * 32) << 16);
-#pragma unroll
-                for (int jj = 0; jj < NJ; ++jj) {
+                DropRow dr = {};
+                DropCol* const dcol = reinterpret_cast<DropCol*>(epi_smem + warp * kUnitFloats);
+                bool direct = C::DIRECT && ep.vec == 2;
+                if constexpr (C::DIRECT && C::MODE != kWgrad) {
+                    if (direct && (C::EP >= 0 ? C::EP >= 4 : ep.drop.on != 0)) {
+                        // the generator's products of the lane's row, and, one block per lane, of this
+                        // warp's columns; a batch that crosses 2^32 rows takes the other path
+                        const uint64_t r0 = uint64_t(m0 + ep.drop.row0);
+                        const uint32_t hi = uint32_t(r0 >> 32);
+                        direct = hi == uint32_t((r0 + 31) >> 32);
+                        dr = drop_row(ep.drop, uint32_t(r0) + lane, __umulhi(0xCD9E8D57u, hi));
+                        __syncwarp();
+                        if (lane < NJ * 8)
+                            dcol[lane] = drop_col(ep.drop, uint32_t((n0 + (2 * (lane >> 3) + half) * 32) >> 2) + (lane & 7), hi);
+                        __syncwarp();
+                    }
+                }
+                int done = 0;                                // units of the direct path
+                if constexpr (C::DIRECT) {
+                    if (direct)
+                        done = m0 >= ep.rows ? NJ
+                                             : emit_rows<C::MODE, C::EP, NJ>(ep, src + half * 32, m0 + lane, n0 + half * 32, dr, dcol);
+                }
+                constexpr int kUnrollUnits = C::CH != 0 ? NJ : 1;
+#pragma unroll kUnrollUnits
+                for (int jj = C::DIRECT ? done : 0; jj < NJ; ++jj) {
                     if ((2 * jj + half) * 32 < C::BN) {
                         if constexpr (C::CH != 0) {
 #pragma unroll

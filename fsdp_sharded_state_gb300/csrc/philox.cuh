@@ -48,7 +48,7 @@ __device__ __forceinline__ uint4 drop_words(const Drop& d, int64_t row, int64_t 
 // first three rounds one word at a time: five of their six products depend on the column
 // alone or on the row alone, and are shared along the other.  A block then costs 15 products,
 // the column's two and the row's one spread over the grid, instead of 20.
-struct DropCol {
+struct alignas(16) DropCol {
     uint32_t c3, x0, x2, y3;   // after round 1: word 3; of round 3: what words 0, 2 and 3 take from the column
 };
 struct DropRow {
