@@ -394,7 +394,7 @@ struct Raw16 {
 };
 __device__ __forceinline__ Raw16 load_raw16(const uint16_t* p) {
     Raw16 r;
-    asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                  : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3]), "=r"(r.w[4]), "=r"(r.w[5]), "=r"(r.w[6]), "=r"(r.w[7])
                  : "l"(p)
                  : "memory");
@@ -443,6 +443,8 @@ __device__ __forceinline__ int emit_rows(const LinEpi& ep, uint32_t acc, int64_t
         if (add && in && units > 0) aq[g] = load_raw16(add + 16 * g);
         if (MODE == kDgrad && z && in && units > 0) zq[g] = load_raw16(z + 16 * g);
     }
+    Acc16 next;                                              // the accumulators of the half to come
+    if (units > 0) tmem_ld16_async(acc, next);
 #pragma unroll 1
     for (int u = 0; u < units; ++u) {
         const bool more = in && u + 1 < units;
@@ -450,7 +452,9 @@ __device__ __forceinline__ int emit_rows(const LinEpi& ep, uint32_t acc, int64_t
         for (int g = 0; g < 2; ++g) {
             const int c = 64 * u + 16 * g;
             float v[16], t[16];
-            tmem_ld16(acc + c, v);
+            tmem_wait_ld16(next, v);
+            if (g == 0) tmem_ld16_async(acc + c + 16, next);
+            else if (u + 1 < units) tmem_ld16_async(acc + c + 48, next);
             if constexpr (MODE == kForward) {
                 if (bias) {
                     float b[8];
@@ -579,41 +583,6 @@ struct LinCfg {
     static_assert(!SPLIT || CG == 1, "a cluster is a pair or a split");
 };
 
-// What the epilogue of a persistent CTA's tile will read of residual and preact, brought
-// into L2 by the load warp while the tile's products run: a line of 128 bytes per lane, a few
-// per K step.
-template <class C>
-struct EpiPrefetch {
-    static constexpr bool ON = !C::SPLIT && C::MODE != kWgrad;
-    static constexpr int LINES = C::BN * int(sizeof(typename C::OT)) / 128 + 1;      // of a row, which may start inside a line
-    int64_t row0, col0;
-    int at, total, per;        // 32-row steps done, of all; steps per K step
-
-    __device__ __forceinline__ EpiPrefetch(const LinEpi& ep, int64_t row0_, int64_t col0_, int n_kb) : row0(row0_), col0(col0_) {
-        at = total = per = 0;
-        if constexpr (ON) {
-            const int tensors = (ep.residual != nullptr) + (C::MODE == kDgrad && ep.preact != nullptr);
-            total = tensors * 4 * LINES;
-            per = (total + n_kb - 1) / n_kb;
-        }
-    }
-    __device__ __forceinline__ void step(const LinEpi& ep, int lane) {
-        if constexpr (ON) {
-            for (int k = 0; k < per && at < total; ++k, ++at) {
-                const int which = at / (4 * LINES), rest = at - which * 4 * LINES;
-                const bool second = which == 1 || ep.residual == nullptr;
-                const char* base = static_cast<const char*>(second ? ep.preact : ep.residual);
-                const int64_t row = row0 + (rest / LINES) * 32 + lane, ld = second ? ep.ldz : ep.ldr;
-                const int64_t width = (ep.cols - col0 < C::BN ? ep.cols - col0 : C::BN) * int64_t(sizeof(typename C::OT));
-                int64_t off = int64_t(rest % LINES) * 128;
-                if (off >= width) off = width - 1;
-                if (row < ep.rows)
-                    asm volatile("prefetch.global.L2 [%0];" ::"l"(base + (row * ld + col0) * int64_t(sizeof(typename C::OT)) + off));
-            }
-        }
-    }
-};
-
 struct LinShape {
     int32_t m_tiles, n_tiles, n_kb, splits;
 };
@@ -698,9 +667,7 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
             const bool db_tile = C::MODE == kWgrad && ep.db && t < sh.m_tiles;
             const int m0 = (mt * C::CG + (C::CG == 2 ? int(rank) : 0)) * 128;
             const int n0 = nt * C::BN + (C::CG == 2 ? int(rank) * C::BROWS : 0);
-            EpiPrefetch<C> ahead(ep, m0, nt * C::BN, kb1 - kb0);
             for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                ahead.step(ep, lane);
                 const uint32_t s = it % C::STAGES, use = it / C::STAGES;
                 if (use > 0 && !mbar_wait_bounded(empty + 8 * s, (use - 1) & 1, wait_ns)) {
                     ok = false;
@@ -919,8 +886,10 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
                         if constexpr (C::CH != 0) {
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
+                                Acc16 a;
                                 float v[16];
-                                tmem_ld16(src + (2 * jj + half) * 32 + 16 * h, v);
+                                tmem_ld16_async(src + (2 * jj + half) * 32 + 16 * h, a);
+                                tmem_wait_ld16(a, v);
 #pragma unroll
                                 for (int i = 0; i < 16; ++i) sum[jj][16 * h + i] += v[i];
                             }

@@ -36,8 +36,11 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr) {
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
     return v;
 }
+// An arrival on another CTA's barrier.  Release at CTA scope only: what it hands over are
+// accumulators in TMEM, ordered by the tcgen05 fences; at cluster scope the arrival would wait
+// for the warp's stores to global memory.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // One box of a 3-D tensor map (x: innermost) into shared memory; its bytes are counted on
@@ -99,9 +102,12 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, float (&v)[32]) {
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// 16 columns of them.
-__device__ __forceinline__ void tmem_ld16(uint32_t addr, float (&v)[16]) {
+// 16 columns of them; the registers hold them after tmem_wait_ld16 only.
+struct Acc16 {
     uint32_t r[16];
+};
+__device__ __forceinline__ void tmem_ld16_async(uint32_t addr, Acc16& a) {
+    uint32_t(&r)[16] = a.r;
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
         "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
@@ -109,7 +115,15 @@ __device__ __forceinline__ void tmem_ld16(uint32_t addr, float (&v)[16]) {
           "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(addr)
         : "memory");
-    tmem_wait_ld();
+}
+// Waits for the warp's loads; the registers pass through, so that no use moves ahead of it.
+__device__ __forceinline__ void tmem_wait_ld16(Acc16& a, float (&v)[16]) {
+    uint32_t(&r)[16] = a.r;
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                   "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
