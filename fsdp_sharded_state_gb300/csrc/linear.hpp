@@ -46,7 +46,17 @@ struct LinProblem {
     int planes;                // 1: bf16 operands; 3: fp32 operands as three bf16 terms
     bool out_bf16;
     LinEpi epi;
+    int slabs;                 // wgrad: K ranges that may get partial sums of their own (0: none), and
+    float* partial;            // room for them, wgrad_slab_floats() floats
 };
+
+// wgrad with a small out: how many slabs its rows are cut into, a cluster of kSlabSplits CTAs on
+// each tile of each (0: out alone fills the device), and the floats of their partial sums
+// (out's rows padded to 8 columns, then db).
+constexpr int kSlabSplits = 4;
+int wgrad_slabs(int64_t rows, int64_t in, int64_t out);
+int64_t wgrad_slab_floats(int64_t rows, int64_t in, int64_t out);
+cudaError_t launch_wgrad_slabs(const LinProblem& p, cudaStream_t st);
 
 cudaError_t launch_linear_forward(const LinProblem& p, cudaStream_t st);
 cudaError_t launch_linear_dgrad(const LinProblem& p, cudaStream_t st);

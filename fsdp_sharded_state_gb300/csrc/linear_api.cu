@@ -108,10 +108,11 @@ extern "C" {
 
 size_t fsdp_linear_workspace_bytes(int64_t rows, int64_t in, int64_t out, int32_t elem_dtype, int32_t aligned) {
     if (check_dims(rows, in, out, elem_dtype)) return 0;
-    if (elem_dtype == FSDP_BF16 && aligned) return 0;
+    const size_t slabs = size_t(round_up(wgrad_slab_floats(rows, in, out) * 4, 256));
+    if (elem_dtype == FSDP_BF16 && aligned) return slabs;
     const int planes = elem_dtype == FSDP_F32 ? 3 : 1;
     const int64_t x = packed_bytes(rows, in, planes), w = packed_bytes(out, in, planes), z = packed_bytes(rows, out, planes);
-    return size_t(x + w + z - std::min({x, w, z}));   // the two largest: no call reads all three
+    return size_t(x + w + z - std::min({x, w, z})) + slabs;   // the two largest: no call reads all three
 }
 
 int fsdp_linear_forward(int64_t rows, int64_t in, int64_t out, int32_t elem_dtype, const void* x, int64_t ldx, const void* w,
@@ -223,6 +224,11 @@ int fsdp_linear_wgrad(int64_t rows, int64_t in, int64_t out, int32_t elem_dtype,
     ep.accumulate = accumulate != 0;
     ep.vec = row_class(dw, lddw, gs);
     ep.db = db;
+    p.slabs = wgrad_slabs(rows, in, out);
+    if (p.slabs) {
+        if (!pk.ws || pk.left < size_t(wgrad_slab_floats(rows, in, out) * 4)) return FSDP_EINVAL;
+        p.partial = reinterpret_cast<float*>(pk.ws);
+    }
     return run_product(p, pk, elem_dtype, st);
 }
 

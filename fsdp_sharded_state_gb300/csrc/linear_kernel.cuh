@@ -223,18 +223,20 @@ struct UnitEmit {
     OT* out;
     const OT* add;
     OT* z;
-    int64_t add_step, z_step, row0, col0;
+    int64_t add_step, z_step, row0, col0, shift;
     int n_it;                                    // steps of 8 rows; -1: not by vectors
     Raw8<OT> aq[AHEAD], zq[AHEAD];
 
-    __device__ __forceinline__ void begin(const LinEpi& ep, int64_t row0_, int64_t col0_, int lane) {
+    // shift: rows that out starts further down (a slab of partial sums)
+    __device__ __forceinline__ void begin(const LinEpi& ep, int64_t row0_, int64_t col0_, int lane, int64_t shift_ = 0) {
         row0 = row0_;
         col0 = col0_;
+        shift = shift_;
         n_it = -1;
         if (!ep.vec || ep.cols - col0 < 32) return;
         const int64_t col = col0 + (lane & 3) * 8, row1 = row0 + (lane >> 2);
         n_it = ep.rows > row1 ? (ep.rows - row1 >= 32 ? 4 : int((ep.rows - row1 + 7) >> 3)) : 0;
-        out = static_cast<OT*>(ep.out) + row1 * ep.ldo + col;
+        out = static_cast<OT*>(ep.out) + (row1 + shift) * ep.ldo + col;
         add = MODE == kWgrad ? (ep.accumulate ? out : nullptr)
               : ep.residual  ? static_cast<const OT*>(ep.residual) + row1 * ep.ldr + col
                              : nullptr;
@@ -330,7 +332,7 @@ struct UnitEmit {
         const int64_t c = col0 + lane;
         const bool in = c < ep.cols;
         const float bias = MODE == kForward && ep.bias && in ? load1(static_cast<const OT*>(ep.bias) + c) : 0.f;
-        OT* o = static_cast<OT*>(ep.out) + row0 * ep.ldo + c;
+        OT* o = static_cast<OT*>(ep.out) + (row0 + shift) * ep.ldo + c;
         const OT* addp = MODE == kWgrad ? (ep.accumulate ? o : nullptr)
                         : ep.residual  ? static_cast<const OT*>(ep.residual) + row0 * ep.ldr + c
                                        : nullptr;
@@ -583,8 +585,9 @@ struct LinCfg {
     static_assert(!SPLIT || CG == 1, "a cluster is a pair or a split");
 };
 
+// splits: CTAs per tile; slabs (wgrad): K ranges with an output of their own each, [slabs][rows][ldo].
 struct LinShape {
-    int32_t m_tiles, n_tiles, n_kb, splits;
+    int32_t m_tiles, n_tiles, n_kb, splits, slabs;
 };
 
 template <class C>
@@ -632,10 +635,12 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
 
     const int n_tiles = sh.m_tiles * sh.n_tiles;
     const int n_clusters = C::CG == 2 ? gridDim.x / 2 : C::SPLIT ? gridDim.x / sh.splits : gridDim.x;
-    const int cluster = C::CG == 2 ? blockIdx.x / 2 : C::SPLIT ? blockIdx.x / sh.splits : blockIdx.x;
+    const int slab = C::SPLIT && C::MODE == kWgrad ? blockIdx.x / sh.splits / n_tiles : 0;
+    const int cluster = C::CG == 2 ? blockIdx.x / 2 : C::SPLIT ? blockIdx.x / sh.splits - slab * n_tiles : blockIdx.x;
     // this CTA's K steps
-    const int kb0 = C::SPLIT ? int(int64_t(sh.n_kb) * rank / sh.splits) : 0;
-    const int kb1 = C::SPLIT ? int(int64_t(sh.n_kb) * (rank + 1) / sh.splits) : sh.n_kb;
+    const int parts = C::SPLIT ? sh.splits * sh.slabs : 1, part = C::SPLIT ? slab * sh.splits + int(rank) : 0;
+    const int kb0 = C::SPLIT ? int(int64_t(sh.n_kb) * part / parts) : 0;
+    const int kb1 = C::SPLIT ? int(int64_t(sh.n_kb) * (part + 1) / parts) : sh.n_kb;
     const int chunk = C::CH ? C::CH : sh.n_kb;
 
     // Tiles in bands of 8 along M, N outer inside a band: concurrently running tiles share
@@ -832,9 +837,14 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
                     const uint32_t u = 4 * j + q;            // unit u joins in CTA u mod splits
                     const uint32_t slot = (u / sh.splits) * sh.splits + rank;
                     const uint32_t dst = map_rank(smem_addr(epi_smem + slot * kUnitFloats), u % sh.splits);
+                    if constexpr (C::ROWS_M) {               // a lane holds a row
 #pragma unroll
-                    for (int c = 0; c < 32; ++c)
-                        st_cluster(dst + 4 * (C::ROWS_M ? unit_at(lane, c) : unit_at(c, lane)), v[c]);
+                        for (int g = 0; g < 8; ++g)
+                            st_cluster4(dst + 4 * unit_at(lane, 4 * g), v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]);
+                    } else {                                 // a lane holds a column
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) st_cluster(dst + 4 * unit_at(c, lane), v[c]);
+                    }
                 } else {
                     float* const unit = epi_smem + warp * kUnitFloats;
                     __syncwarp();
@@ -932,7 +942,7 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
                 const int q = u & 3, j = u >> 2;
                 const int64_t m0 = int64_t(mt) * 128 + q * 32, n0 = int64_t(nt) * C::BN + j * 32;
                 UnitEmit<C::MODE, typename C::OT, C::AHEAD, C::EP> io;
-                io.begin(ep, C::ROWS_M ? m0 : n0, C::ROWS_M ? n0 : m0, lane);
+                io.begin(ep, C::ROWS_M ? m0 : n0, C::ROWS_M ? n0 : m0, lane, C::MODE == kWgrad ? slab * ep.rows : 0);
                 io.run(ep, epi_smem + (u / sh.splits) * sh.splits * kUnitFloats, sh.splits, lane);
             }
         }
@@ -944,7 +954,7 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
                 if (rank == 0 && nt == 0 && tid < 128 && c < ep.rows) {
                     float t = 0.f;
                     for (int r = 0; r < sh.splits; ++r) t += ld_cluster(map_rank(smem_addr(db_part + tid), r));
-                    emit_db<typename C::OT>(ep, c, t);
+                    emit_db<typename C::OT>(ep, c + slab * ep.rows, t);
                 }
                 __syncwarp();
                 cluster_arrive();                // no CTA leaves while its share is read
@@ -1024,7 +1034,7 @@ inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Launches one configuration: splits CTAs per tile (SPLIT), else a persistent grid.
 template <class C>
-cudaError_t launch_cfg(const LinProblem& p, int splits, cudaStream_t st) {
+cudaError_t launch_cfg(const LinProblem& p, int splits, cudaStream_t st, int slabs = 1) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -1038,8 +1048,8 @@ cudaError_t launch_cfg(const LinProblem& p, int splits, cudaStream_t st) {
     // tile numbers, K steps and tile coordinates are 32-bit
     if (mt * nt * per > INT32_MAX / 16 || kb > INT32_MAX / 128 || M > INT32_MAX - 512 || N > INT32_MAX - 512)
         return cudaErrorInvalidValue;
-    LinShape sh{int32_t(mt), int32_t(nt), int32_t(kb), splits};
-    int64_t clusters = mt * nt;
+    LinShape sh{int32_t(mt), int32_t(nt), int32_t(kb), splits, slabs};
+    int64_t clusters = mt * nt * slabs;
     const int64_t room = sm_count(dev) / per;
     if (!C::SPLIT && clusters > room) clusters = room > 0 ? room : 1;
     cudaLaunchAttribute attr[2];
@@ -1144,6 +1154,10 @@ cudaError_t launch_product(const LinProblem& p, cudaError_t (*launch_pair)(const
         if constexpr (PL == 1) consider(estimate<S128>(p, s, dev, {4.3f, 0.25f, 2.0f}), 2, s);
         consider(estimate<S64>(p, s, dev, {4.2f, PL == 1 ? 0.21f : 0.70f, 1.0f}), 1, s);
         if constexpr (MODE != kWgrad) consider(estimate<S32>(p, s, dev, {4.0f, PL == 1 ? 0.20f : 0.63f, 0.5f}), 0, s);
+    }
+    if (p.slabs > 1 && best > 4.2f + float(ceil_div(ceil_div(p.K, kKb), kSlabSplits * p.slabs)) * (PL == 1 ? 0.21f : 0.70f) + 4.5f) {
+        // a small out and many rows: slabs of K over clusters, and a launch that adds them up
+        if constexpr (MODE == kWgrad) return launch_wgrad_slabs(p, st);
     }
     switch (which) {
         case 0:
