@@ -619,3 +619,4 @@ def fsdp_error_string(status: int) -> str:
 
 from .state import ShardedState, StepGraph, step_schedule  # noqa: E402  (harness over the calls above)
 from .hostfeed import HostFeed  # noqa: E402  (host-fed steps over ShardedState)
+from .mlp import ResidualMLP, tensor_views  # noqa: E402  (layers between the all-gather and the reduce-scatter)

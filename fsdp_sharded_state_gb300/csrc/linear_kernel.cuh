@@ -1116,7 +1116,7 @@ float estimate(const LinProblem& p, int splits, int dev, LinCost c) {
     else room = sm_count(dev) / C::CG;
     if (room < 1) return 1e30f;
     const float waves = float(ceil_div(tiles, room));
-    if (C::SPLIT) return waves * (c.fixed + float(ceil_div(kb, splits)) * c.kb + c.epi);
+    if (C::SPLIT) return waves * (c.fixed + (splits > 1 ? 0.7f : 0.f) + float(ceil_div(kb, splits)) * c.kb + c.epi);
     return c.fixed + waves * float(kb) * c.kb + c.epi;
 }
 
@@ -1140,7 +1140,7 @@ cudaError_t launch_product(const LinProblem& p, cudaError_t (*launch_pair)(const
     using S64 = LinCfg<MODE, OT, 1, 64, PL, CH, true>;
     using S32 = LinCfg<MODE, OT, 1, MODE == kWgrad ? 64 : 32, PL, CH, true>;
     constexpr float f = PL == 1 ? 1.f : 6.f;
-    float best = estimate<P256>(p, 1, dev, {5.0f, 0.275f * f, 4.0f});
+    float best = estimate<P256>(p, 1, dev, {6.0f, 0.275f * f, 4.5f});
     int which = 256, splits = 1;
     auto consider = [&](float cost, int w, int s) {
         if (cost < best) {

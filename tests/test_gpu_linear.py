@@ -133,3 +133,157 @@ def test_wgrad(shape, pad, offset, accumulate, dtype, grad_dtype):
     lu.check(db, want_b, bb, "db")
     assert lu.untouched(dw, wbuf)
     assert bbuf[:offset].isnan().all() and bbuf[offset + cout:].isnan().all()
+
+
+def test_binding_refuses_wrong_tensors():
+    x, w, y = (torch.zeros(s, dtype=BF16, device="cuda") for s in ((4, 16), (32, 16), (4, 32)))
+    with pytest.raises(TypeError, match="w is"):
+        fs.fsdp_linear_forward(x, w.float(), y)
+    with pytest.raises(ValueError, match="w is"):
+        fs.fsdp_linear_forward(x, torch.zeros(32, 17, dtype=BF16, device="cuda"), y)
+    with pytest.raises(ValueError, match="y is"):
+        fs.fsdp_linear_forward(x, w, y[:3])
+    with pytest.raises(ValueError, match="contiguous"):
+        fs.fsdp_linear_forward(torch.zeros(16, 4, dtype=BF16, device="cuda").t(), w, y)
+    with pytest.raises(ValueError, match="bias is"):
+        fs.fsdp_linear_forward(x, w, y, bias=torch.zeros(31, dtype=BF16, device="cuda"))
+    with pytest.raises(fs.FsdpError, match="FSDP_EINVAL"):          # dgrad through an activation needs preact
+        fs.fsdp_linear_dgrad(y, w, x, act="gelu")
+    with pytest.raises(fs.FsdpError, match="FSDP_EINVAL"):          # fp32 operands need the workspace
+        fs.fsdp_linear_forward(x.float(), w.float(), y.float())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_no_rows(dtype):
+    x, w = torch.zeros(0, 24, dtype=dtype, device="cuda"), torch.ones(40, 24, dtype=dtype, device="cuda")
+    y = torch.zeros(0, 40, dtype=dtype, device="cuda")
+    fs.fsdp_linear_forward(x, w, y)
+    fs.fsdp_linear_dgrad(y, w, x)
+    dw, buf = lu.empty_matrix(40, 24, dtype, 32)
+    db = torch.ones(40, dtype=dtype, device="cuda")
+    dw.fill_(1)
+    fs.fsdp_linear_wgrad(y, x, dw, db, accumulate=True)
+    assert (dw == 1).all() and (db == 1).all()
+    fs.fsdp_linear_wgrad(y, x, dw, db)
+    fs.fsdp_check_status()
+    assert (dw == 0).all() and (db == 0).all() and lu.untouched(dw, buf)
+
+
+def test_special_values_stay_in_their_rows():
+    """An infinity or NaN in a row of x meets that row of y alone; a dropped one becomes 0."""
+    x = torch.randn(64, 96, device="cuda").to(BF16)
+    w = torch.randn(80, 96, device="cuda").to(BF16)
+    spec = fs.DropoutSpec(0.3, 8)
+    clean = torch.empty(64, 80, dtype=BF16, device="cuda")
+    fs.fsdp_linear_forward(x, w, clean, dropout=spec)
+    x[5, 7], x[40, 3] = float("inf"), float("nan")
+    y = torch.empty_like(clean)
+    fs.fsdp_linear_forward(x, w, y, dropout=spec)
+    keep = lu.keep_mask(64, 80, spec)
+    rows = [r for r in range(64) if r not in (5, 40)]
+    assert torch.equal(y[rows], clean[rows])
+    assert (y[~keep] == 0).all()
+    assert y[5][keep[5]].isinf().all() and y[40][keep[40]].isnan().all()
+    assert torch.equal(y[5][keep[5]] > 0, (w[:, 7] > 0)[keep[5]])
+
+
+def test_same_bits_every_run_on_any_stream_and_under_capture():
+    g = lu.gen(9)
+    dz = lu.matrix(3000, 200, BF16, 1.0, g)
+    x = lu.matrix(3000, 120, BF16, 1.0, g)
+    ws = lu.workspace(3000, 120, 200, BF16)
+    outs = [(torch.empty(200, 120, device="cuda"), torch.empty(200, device="cuda")) for _ in range(3)]
+    fs.fsdp_linear_wgrad(dz, x, *outs[0], workspace=ws)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    fs.fsdp_linear_wgrad(dz, x, *outs[1], workspace=ws, stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        fs.fsdp_linear_wgrad(dz, x, *outs[2], workspace=ws)
+    graph.replay()
+    fs.fsdp_check_status()
+    for dw, db in outs[1:]:
+        assert torch.equal(dw, outs[0][0]) and torch.equal(db, outs[0][1])
+
+
+@pytest.mark.parametrize("rows", [1, 7, 300, 2000])
+def test_forward_rows_do_not_depend_on_the_batch(rows):
+    """A row's dropout and residual are its own: rows of a large batch against the same rows
+    alone, at the row index that row0 gives (the products' sums may be grouped differently)."""
+    g = lu.gen(12)
+    x, w = lu.matrix(2000, 256, BF16, 1.0, g), lu.matrix(320, 256, BF16, 0.05, g)
+    res = lu.matrix(2000, 320, BF16, 1.0, g)
+    y, part = torch.empty(2000, 320, dtype=BF16, device="cuda"), torch.empty(rows, 320, dtype=BF16, device="cuda")
+    fs.fsdp_linear_forward(x, w, y, dropout=fs.DropoutSpec(0.5, 3, 1), residual=res)
+    r0 = 2000 - rows
+    fs.fsdp_linear_forward(x[r0:], w, part, dropout=fs.DropoutSpec(0.5, 3, 1, row0=r0), residual=res[r0:])
+    assert (y[r0:].float() - part.float()).abs().max() <= 2.0 ** -6 * y.float().abs().max()
+    assert torch.equal(y[r0:] == res[r0:], part == res[r0:])          # the same elements dropped
+
+
+def test_large_row_index_of_the_mask():
+    """row0 near 2^32: rows on both sides of the counter's word boundary, fused and alone."""
+    g = lu.gen(13)
+    x, w = lu.matrix(600, 64, BF16, 1.0, g), lu.matrix(512, 64, BF16, 0.3, g)
+    spec = fs.DropoutSpec(0.5, 77, 2, row0=2 ** 32 - 290)
+    y = torch.empty(600, 512, dtype=BF16, device="cuda")
+    fs.fsdp_linear_forward(x, w, y, dropout=spec)
+    plain = torch.empty_like(y)
+    fs.fsdp_linear_forward(x, w, plain)
+    keep = lu.keep_mask(600, 512, spec)
+    assert torch.equal(y != 0, keep & (plain != 0))
+    alone = torch.empty_like(y)
+    fs.fsdp_dropout(plain, alone, spec)
+    assert torch.equal(alone != 0, keep & (plain != 0))
+
+
+@pytest.mark.parametrize("act", ["none", "relu", "gelu", "silu"])
+@pytest.mark.parametrize("p", [0.0, 0.3])
+@pytest.mark.parametrize("rows,cin,cout,pad", [(1300, 2048, 1408, 0), (1300, 2048, 1400, 0), (1100, 2048, 1405, 0), (1030, 2048, 1440, 8)])
+def test_pair_kernels_epilogues(rows, cin, cout, pad, act, p):
+    """Sizes with enough tiles for the CTA pairs: rows of 32-byte, 16-byte and no alignment,
+    ragged on every side; forward, then dgrad at the transposed widths."""
+    g = lu.gen(21)
+    x = lu.matrix(rows, cin, BF16, 1.0, g)
+    w = lu.matrix(cout, cin, BF16, 0.02, g)
+    bias = lu.matrix(1, cout, BF16, 0.5, g)[0]
+    ld = cout + pad
+    res = lu.matrix(rows, cout, BF16, 1.0, g, ld)
+    spec = fs.DropoutSpec(p, 5, 6, row0=3) if p else None
+    y, ybuf = lu.empty_matrix(rows, cout, BF16, ld)
+    z, zbuf = lu.empty_matrix(rows, cout, BF16, ld)
+    fs.fsdp_linear_forward(x, w, y, bias=bias, act=act, preact=z, dropout=spec, residual=res,
+                           workspace=lu.workspace(rows, cin, cout, BF16))
+    want, zwant, bound = lu.forward64(x, w, bias, act, spec, res)
+    lu.check(z, zwant, bound, "preact")
+    lu.check(y, want, 1.13 / (1 - p) * bound + 2.0 ** -20 * (zwant.abs() / (1 - p) + res.double().abs()), "y")
+    assert lu.untouched(y, ybuf) and lu.untouched(z, zbuf)
+    # dgrad: dz [rows, cin] through a weight [cin, cout] gives dx [rows, cout]
+    wt = lu.matrix(cin, cout, BF16, 0.02, g)
+    dx, xbuf = lu.empty_matrix(rows, cout, BF16, ld)
+    fs.fsdp_linear_dgrad(x, wt, dx, act=act, preact=z if act != "none" else None, dropout=spec, residual=res,
+                         workspace=lu.workspace(rows, cout, cin, BF16))
+    fs.fsdp_check_status()
+    h = x.double() @ wt.double()
+    M = x.double().abs() @ wt.double().abs()
+    want = lu.drop64(h, spec) * lu.act_grad64(z.double(), act) + res.double()
+    lu.check(dx, want, 1.13 / (1 - p) * lu.product_bound(cin, M, BF16) + 2.0 ** -20 * (2 * h.abs() + res.double().abs()), "dx")
+    assert lu.untouched(dx, xbuf)
+
+
+@pytest.mark.parametrize("dtype,grad_dtype", [(BF16, BF16), (BF16, F32), (F32, F32), (F32, BF16)])
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("rows,cin,cout", [(1500, 1408, 1300), (777, 2100, 1001), (9000, 40, 130), (20000, 8, 3)])
+def test_wgrad_pairs_and_slabs(rows, cin, cout, accumulate, dtype, grad_dtype):
+    g = lu.gen(22)
+    dz, x = lu.matrix(rows, cout, dtype, 1e-3, g), lu.matrix(rows, cin, dtype, 1.0, g)
+    dw = torch.full((cout, cin), 0.25, dtype=grad_dtype, device="cuda")
+    db = torch.full((cout,), 0.25, dtype=grad_dtype, device="cuda")
+    fs.fsdp_linear_wgrad(dz, x, dw, db, accumulate=accumulate, workspace=lu.workspace(rows, cin, cout, dtype))
+    fs.fsdp_check_status()
+    add = 0.25 if accumulate else 0.0
+    want_w, want_b = dz.double().t() @ x.double() + add, dz.double().sum(0) + add
+    Mw, Mb = dz.double().abs().t() @ x.double().abs(), dz.double().abs().sum(0)
+    lu.check(dw, want_w, lu.product_bound(rows, Mw, dtype) + 2.0 ** -23 * want_w.abs(), "dw")
+    lu.check(db, want_b, (rows / 64 + 64) * 2.0 ** -24 * Mb + 2.0 ** -23 * want_b.abs(), "db")
