@@ -182,12 +182,14 @@ def _stream(stream) -> Optional[int]:
     return stream.cuda_stream
 
 
+_DTYPE_CODES = {torch.float32: FSDP_F32, torch.bfloat16: FSDP_BF16}
+
+
 def _dtype_code(t) -> int:
-    if t.dtype == torch.float32:
-        return FSDP_F32
-    if t.dtype == torch.bfloat16:
-        return FSDP_BF16
-    raise TypeError(f"unsupported dtype {t.dtype}: float32 or bfloat16")
+    code = _DTYPE_CODES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {t.dtype}: float32 or bfloat16")
+    return code
 
 
 class Layout:
@@ -481,10 +483,10 @@ def _vector(x, name: str, n: int, dtype):
     return x.data_ptr()
 
 
-def _two_dims(**named) -> None:
-    for name, x in named.items():
-        if x.dim() != 2:
-            raise ValueError(f"{name} is {tuple(x.shape)}, expected a matrix")
+def _dims(x, name: str):
+    if x.dim() != 2:
+        raise ValueError(f"{name} is {tuple(x.shape)}, expected a matrix")
+    return x.shape
 
 
 def _act(act) -> int:
@@ -519,8 +521,7 @@ def fsdp_linear_forward(x, w, y, bias=None, act="none", preact=None, dropout: Op
     """y = residual + drop(act(x w^T + bias)); z = x w^T + bias into preact where given.
     x [rows, in], w [out, in], y / preact / residual [rows, out], bias [out], one dtype."""
     code, dt = _dtype_code(x), x.dtype
-    _two_dims(x=x, w=w)
-    (rows, cin), cout = x.shape, w.shape[0]
+    (rows, cin), (cout, _) = _dims(x, "x"), _dims(w, "w")
     px, ldx = _matrix(x, "x", rows, cin, dt)
     pw, ldw = _matrix(w, "w", cout, cin, dt)
     py, ldy = _matrix(y, "y", rows, cout, dt)
@@ -537,8 +538,7 @@ def fsdp_linear_dgrad(dz, w, dx, act="none", preact=None, dropout: Optional[Drop
     """dx = residual + act'(preact) * drop(dz w): dz [rows, out], w [out, in], dx / preact /
     residual [rows, in]; act, preact and dropout are those of the layer before."""
     code, dt = _dtype_code(dz), dz.dtype
-    _two_dims(dz=dz, w=w)
-    (rows, cout), cin = dz.shape, w.shape[1]
+    (rows, cout), (_, cin) = _dims(dz, "dz"), _dims(w, "w")
     pg, ldg = _matrix(dz, "dz", rows, cout, dt)
     pw, ldw = _matrix(w, "w", cout, cin, dt)
     px, ldx = _matrix(dx, "dx", rows, cin, dt)
@@ -553,8 +553,7 @@ def fsdp_linear_wgrad(dz, x, dw, db=None, accumulate: bool = False, workspace=No
     """dw (+)= dz^T x and db (+)= the column sums of dz: dz [rows, out], x [rows, in] of one
     dtype, dw [out, in] and db [out] of one dtype (a gradient replica's, or fp32)."""
     code, dt = _dtype_code(dz), dz.dtype
-    _two_dims(dz=dz, x=x)
-    (rows, cout), cin = dz.shape, x.shape[1]
+    (rows, cout), (_, cin) = _dims(dz, "dz"), _dims(x, "x")
     pg, ldg = _matrix(dz, "dz", rows, cout, dt)
     px, ldx = _matrix(x, "x", rows, cin, dt)
     pw, ldw = _matrix(dw, "dw", cout, cin, dw.dtype)
@@ -567,8 +566,7 @@ def fsdp_linear_wgrad(dz, x, dw, db=None, accumulate: bool = False, workspace=No
 def fsdp_dropout(x, y, dropout: Optional[DropoutSpec], residual=None, stream=None) -> None:
     """y = residual + drop(x), [rows, cols] each; the same call on the gradient is its backward."""
     code, dt = _dtype_code(x), x.dtype
-    _two_dims(x=x)
-    rows, cols = x.shape
+    rows, cols = _dims(x, "x")
     px, ldx = _matrix(x, "x", rows, cols, dt)
     py, ldy = _matrix(y, "y", rows, cols, dt)
     pr, ldr = _matrix(residual, "residual", rows, cols, dt)

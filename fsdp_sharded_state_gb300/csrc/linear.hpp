@@ -65,6 +65,19 @@ cudaError_t launch_linear_wgrad(const LinProblem& p, cudaStream_t st);
 cudaError_t launch_pair_forward(const LinProblem& p, int bn, cudaStream_t st);
 cudaError_t launch_pair_dgrad(const LinProblem& p, int bn, cudaStream_t st);
 
+// forward (x: its x) or dgrad (x: dz) of a few rows, operands as the caller stores them.
+struct SkinnyProblem {
+    LinMode mode;
+    bool bf16;
+    const void* x;
+    int64_t ldx;
+    const void* w;
+    int64_t ldw, K;
+    LinEpi epi;
+};
+cudaError_t launch_skinny(const SkinnyProblem& p, cudaStream_t st);
+bool use_skinny(LinMode mode, bool bf16, int64_t rows, int64_t in, int64_t out);
+
 // Operands brought into the form of LinOperand: a bf16 matrix copied to aligned rows, or
 // an fp32 matrix split into three bf16 planes (see linear_pack.cu).  Up to two per launch.
 struct PackJob {

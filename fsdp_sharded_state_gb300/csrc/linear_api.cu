@@ -102,6 +102,12 @@ int run_product(LinProblem& p, Packer& pk, int32_t elem_dtype, cudaStream_t st) 
     return e == cudaSuccess ? FSDP_OK : cuda_fail(e, "k_linear launch");
 }
 
+int run_skinny(LinMode mode, int32_t dtype, const void* x, int64_t ldx, const void* w, int64_t ldw, int64_t K, const LinEpi& ep,
+               cudaStream_t st) {
+    const cudaError_t e = launch_skinny(SkinnyProblem{mode, dtype == FSDP_BF16, x, ldx, w, ldw, K, ep}, st);
+    return e == cudaSuccess ? FSDP_OK : cuda_fail(e, "k_skinny launch");
+}
+
 }  // namespace
 
 extern "C" {
@@ -132,8 +138,6 @@ int fsdp_linear_forward(int64_t rows, int64_t in, int64_t out, int32_t elem_dtyp
     LinProblem p = {};
     if ((rc = make_drop(drop, rows, &p.epi.drop))) return rc;
     if (rows == 0) return FSDP_OK;
-    Packer pk{static_cast<unsigned char*>(workspace), workspace_bytes, {}};
-    if ((rc = pk.operand(w, out, in, ldw, elem_dtype, &p.cols_op)) || (rc = pk.operand(x, rows, in, ldx, elem_dtype, &p.rows_op))) return rc;
     p.mode = kForward;
     p.K = in;
     p.planes = elem_dtype == FSDP_F32 ? 3 : 1;
@@ -151,7 +155,12 @@ int fsdp_linear_forward(int64_t rows, int64_t in, int64_t out, int32_t elem_dtyp
     ep.act = act;
     ep.vec = std::min({row_class(y, ldy, es), row_class(residual, ldr, es), row_class(preact, ldz, es)});
     if (bias && !aligned16(bias)) ep.vec = 0;
-    return run_product(p, pk, elem_dtype, reinterpret_cast<cudaStream_t>(stream));
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    Packer pk{static_cast<unsigned char*>(workspace), workspace_bytes, {}};
+    if ((rc = pk.operand(w, out, in, ldw, elem_dtype, &p.cols_op)) || (rc = pk.operand(x, rows, in, ldx, elem_dtype, &p.rows_op))) return rc;
+    if (use_skinny(kForward, elem_dtype == FSDP_BF16, rows, in, out))
+        return run_skinny(kForward, elem_dtype, x, ldx, w, ldw, in, ep, st);
+    return run_product(p, pk, elem_dtype, st);
 }
 
 int fsdp_linear_dgrad(int64_t rows, int64_t in, int64_t out, int32_t elem_dtype, const void* dz, int64_t lddz, const void* w,
@@ -171,8 +180,6 @@ int fsdp_linear_dgrad(int64_t rows, int64_t in, int64_t out, int32_t elem_dtype,
     LinProblem p = {};
     if ((rc = make_drop(drop, rows, &p.epi.drop))) return rc;
     if (rows == 0) return FSDP_OK;
-    Packer pk{static_cast<unsigned char*>(workspace), workspace_bytes, {}};
-    if ((rc = pk.operand(w, out, in, ldw, elem_dtype, &p.cols_op)) || (rc = pk.operand(dz, rows, out, lddz, elem_dtype, &p.rows_op))) return rc;
     p.mode = kDgrad;
     p.K = out;
     p.planes = elem_dtype == FSDP_F32 ? 3 : 1;
@@ -188,7 +195,12 @@ int fsdp_linear_dgrad(int64_t rows, int64_t in, int64_t out, int32_t elem_dtype,
     ep.cols = in;
     ep.act = act;
     ep.vec = std::min({row_class(dx, lddx, es), row_class(residual, ldr, es), row_class(ep.preact, ldz, es)});
-    return run_product(p, pk, elem_dtype, reinterpret_cast<cudaStream_t>(stream));
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    Packer pk{static_cast<unsigned char*>(workspace), workspace_bytes, {}};
+    if ((rc = pk.operand(w, out, in, ldw, elem_dtype, &p.cols_op)) || (rc = pk.operand(dz, rows, out, lddz, elem_dtype, &p.rows_op))) return rc;
+    if (use_skinny(kDgrad, elem_dtype == FSDP_BF16, rows, in, out))
+        return run_skinny(kDgrad, elem_dtype, dz, lddz, w, ldw, out, ep, st);
+    return run_product(p, pk, elem_dtype, st);
 }
 
 int fsdp_linear_wgrad(int64_t rows, int64_t in, int64_t out, int32_t elem_dtype, const void* dz, int64_t lddz, const void* x,

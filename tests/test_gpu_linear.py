@@ -287,3 +287,31 @@ def test_wgrad_pairs_and_slabs(rows, cin, cout, accumulate, dtype, grad_dtype):
     Mw, Mb = dz.double().abs().t() @ x.double().abs(), dz.double().abs().sum(0)
     lu.check(dw, want_w, lu.product_bound(rows, Mw, dtype) + 2.0 ** -23 * want_w.abs(), "dw")
     lu.check(db, want_b, (rows / 64 + 64) * 2.0 ** -24 * Mb + 2.0 ** -23 * want_b.abs(), "db")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows", [1, 2, 3, 4, 5, 8, 9, 13, 16, 17])
+@pytest.mark.parametrize("cin,cout,offset", [(300, 520, 0), (2048, 136, 0), (129, 77, 1), (1, 3, 0)])
+def test_few_rows(rows, cin, cout, offset, dtype):
+    g = lu.gen(31)
+    x, w = lu.matrix(rows, cin, dtype, 1.0, g, None, offset), lu.matrix(cout, cin, dtype, 0.05, g, None, offset)
+    bias = lu.matrix(1, cout, dtype, 0.5, g, None, offset)[0]
+    res = lu.matrix(rows, cout, dtype, 1.0, g)
+    spec = fs.DropoutSpec(0.4, 2 ** 40 + 3, 5, row0=2 ** 32 - 2)
+    y, ybuf = lu.empty_matrix(rows, cout, dtype, None, offset)
+    z, zbuf = lu.empty_matrix(rows, cout, dtype, None, offset)
+    ws = lu.workspace(rows, cin, cout, dtype)
+    fs.fsdp_linear_forward(x, w, y, bias=bias, act="gelu", preact=z, dropout=spec, residual=res, workspace=ws)
+    fs.fsdp_check_status()
+    want, zwant, bound = lu.forward64(x, w, bias, "gelu", spec, res)
+    lu.check(z, zwant, bound, "preact")
+    lu.check(y, want, 1.13 / 0.6 * bound + 2.0 ** -20 * (zwant.abs() / 0.6 + res.double().abs()), "y")
+    assert lu.untouched(y, ybuf) and lu.untouched(z, zbuf)
+    # dgrad at the same sizes: dz = res [rows, cout] through w, with x as the pre-activation
+    dx, xbuf = lu.empty_matrix(rows, cin, dtype, None, offset)
+    fs.fsdp_linear_dgrad(res, w, dx, act="silu", preact=x, dropout=spec, workspace=ws)
+    fs.fsdp_check_status()
+    h, M = res.double() @ w.double(), res.double().abs() @ w.double().abs()
+    want = lu.drop64(h, spec) * lu.act_grad64(x.double(), "silu")
+    lu.check(dx, want, 1.13 / 0.6 * lu.product_bound(cout, M, dtype) + 2.0 ** -20 * 2 * h.abs(), "dx")
+    assert lu.untouched(dx, xbuf)
