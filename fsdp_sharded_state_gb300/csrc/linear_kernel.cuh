@@ -500,9 +500,54 @@ __device__ __forceinline__ int emit_rows(const LinEpi& ep, uint32_t acc, int64_t
     return units;
 }
 
+// wgrad's fp32 epilogue from the sums in registers, a lane per row, 32-byte aligned rows: the
+// columns col0 + 64 u on are written, or added to what is there, which is read further and
+// further ahead into the registers that the written sums leave (the staged path, one step of 8
+// rows ahead, waits out 16 latencies of memory per tile).
+struct Raw8f {
+    float v[8];
+};
+__device__ __forceinline__ void load_8f(const float* p, Raw8f& r) {
+    asm volatile("ld.global.L1::no_allocate.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=f"(r.v[0]), "=f"(r.v[1]), "=f"(r.v[2]), "=f"(r.v[3]), "=f"(r.v[4]), "=f"(r.v[5]), "=f"(r.v[6]), "=f"(r.v[7])
+                 : "l"(p)
+                 : "memory");
+}
+__device__ __forceinline__ void store_8f(float* p, const Raw8f& r) {
+    asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "f"(r.v[0]), "f"(r.v[1]), "f"(r.v[2]), "f"(r.v[3]),
+                 "f"(r.v[4]), "f"(r.v[5]), "f"(r.v[6]), "f"(r.v[7])
+                 : "memory");
+}
+template <int NU>
+__device__ __forceinline__ void emit_sums(const LinEpi& ep, const float (&sum)[NU][32], int64_t row, int64_t col0) {
+    if (row >= ep.rows) return;
+    float* const out = static_cast<float*>(ep.out) + row * ep.ldo + col0;
+    constexpr int G = 4 * NU, FIRST = 2;         // groups of 8 columns; read ahead at the start, one more per group written
+    Raw8f old[G];
+    if (ep.accumulate) {
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+#pragma unroll
+            for (int k = g == 0 ? 0 : 2 * g + FIRST - 2; k < 2 * g + FIRST; ++k)
+                if (k < G) load_8f(out + 64 * (k / 4) + 8 * (k % 4), old[k]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) old[g].v[e] += sum[g / 4][8 * (g % 4) + e];
+            store_8f(out + 64 * (g / 4) + 8 * (g % 4), old[g]);
+        }
+    } else {
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            Raw8f r;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) r.v[e] = sum[g / 4][8 * (g % 4) + e];
+            store_8f(out + 64 * (g / 4) + 8 * (g % 4), r);
+        }
+    }
+}
+
 // ---- column sums of dz (wgrad's db) ---------------------------------------------------
-// Two warps add up the dz tiles that the products of the first column of tiles read anyway,
-// from shared memory: no byte of dz is read for db.  A tile (one plane) is two chunks of 64
+// Where K is split: two warps add up the dz tiles that the products of the first column of tiles
+// read anyway, from shared memory.  A tile (one plane) is two chunks of 64
 // columns, each 64 rows of 128 bytes whose 16-byte groups are swizzled: group p of row r holds
 // columns 8 (p ^ (r mod 8)) on.  A warp takes a chunk; lane l reads group l mod 8 of rows l / 8
 // + 4 h + 8 j: the same columns for all j.  A tile's 8 rows are added in a tree before they
@@ -551,6 +596,64 @@ __device__ __forceinline__ void colsum_lanes(const ColSum& s, float (&t)[8], int
     }
 }
 
+// For the CTA pairs: 64 columns (from col) of 64 rows of dz (from row, `rows` in all) added to
+// the lane's sums straight from memory, which the tiles' own copies have just brought into L2.
+// (From the shared-memory stages it held each of them back from its next load by more than
+// the ring of stages covers: dz^T x of 16384 x 2048 x 2048 took 111 us against 78 without db.)
+// Lane l holds columns E (l mod L) on, L = 64 / E lanes to a row.
+template <typename T>
+struct RowSum {
+    static constexpr int E = 16 / sizeof(T), L = 64 / E;
+    float v[E];
+
+    __device__ __forceinline__ static void wide(const uint4& q, float (&x)[E]) {
+        if constexpr (E == 8) {
+            Raw8<uint16_t> r;
+            r.q[0] = q;
+            widen(r, x);
+        } else {
+            x[0] = __uint_as_float(q.x); x[1] = __uint_as_float(q.y);
+            x[2] = __uint_as_float(q.z); x[3] = __uint_as_float(q.w);
+        }
+    }
+    __device__ __forceinline__ void add(const T* dz, int64_t ld, int64_t row, int64_t rows, int64_t col, int64_t cols, bool vec, int lane) {
+        constexpr int R = 32 / L, N = 64 / R, B = 16;            // rows of a load; loads; of a batch
+        const int64_t c = col + (lane % L) * E;
+#pragma unroll 1
+        for (int b = 0; b < N; b += B) {
+            const int64_t r0 = row + b * R + lane / L;
+            if (vec && col + 64 <= cols && row + 64 <= rows) {
+                uint4 q[B];
+#pragma unroll
+                for (int i = 0; i < B; ++i) q[i] = ldu4(dz + (r0 + i * R) * ld + c);
+#pragma unroll
+                for (int i = 0; i < B; i += 4) {
+                    float x[4][E];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) wide(q[i + k], x[k]);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) v[e] += (x[0][e] + x[1][e]) + (x[2][e] + x[3][e]);
+                }
+            } else {                                         // any alignment, ragged ends
+#pragma unroll 1
+                for (int i = 0; i < B; ++i) {
+                    const int64_t r = r0 + i * R;
+#pragma unroll
+                    for (int e = 0; e < E; ++e) v[e] += r < rows && c + e < cols ? load1(dz + r * ld + c + e) : 0.f;
+                }
+            }
+        }
+    }
+    // Lane l < L: the sums of its columns over the warp.
+    __device__ __forceinline__ void join() {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+#pragma unroll
+            for (int m = L; m < 32; m <<= 1) v[e] += __shfl_xor_sync(0xffffffffu, v[e], m);
+        }
+    }
+};
+
 // A kernel configuration.  CG CTAs share a tile of 128 CG x BN; PL bf16 planes per operand
 // (3 planes: six products, of the terms whose exponents add up to at most two steps); CH:
 // K steps after which the accumulators are added to fp32 registers (0: never).  SPLIT: the
@@ -567,6 +670,7 @@ struct LinCfg {
     static constexpr bool ROWS_M = MODE == kWgrad || !SPLIT;
     static constexpr bool A_MN = MODE == kWgrad || (MODE == kDgrad && !ROWS_M);
     static constexpr bool B_MN = MODE == kWgrad || (MODE == kDgrad && ROWS_M);
+    static constexpr bool REGS = CH != 0 && !SPLIT;                         // sums of a whole tile in registers
     static constexpr bool DIRECT = !SPLIT && CH == 0 && sizeof(OT) == 2;    // emit_rows where rows are aligned
     static constexpr int AHEAD = 1;
     static constexpr int BROWS = BN / CG;                        // B rows a CTA loads
@@ -644,148 +748,144 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
     const int chunk = C::CH ? C::CH : sh.n_kb;
 
     // Tiles in bands of 8 along M, N outer inside a band: concurrently running tiles share
-    // operand rows in L2.  wgrad takes the first column of tiles before all others, so that a
-    // CTA's tiles with column sums are its first.
+    // operand rows in L2.
     auto tile_at = [&](int t, int& mt, int& nt) {
-        const int lead = C::MODE == kWgrad ? sh.m_tiles : 0;
-        if (t < lead) {
-            mt = t;
-            nt = 0;
-            return;
-        }
-        const int cols = C::MODE == kWgrad ? sh.n_tiles - 1 : sh.n_tiles;
-        const int band = 8 * cols, u = t - lead, g = u / band, first = g * 8;
+        const int band = 8 * sh.n_tiles, g = t / band, first = g * 8;
         const int high = sh.m_tiles - first < 8 ? sh.m_tiles - first : 8;
-        const int r = u - g * band;
+        const int r = t - g * band;
         mt = first + r % high;
-        nt = r / high + (C::MODE == kWgrad ? 1 : 0);
+        nt = r / high;
     };
-
-    if (warp == kEpiWarps) {
-        // ---- loads ----
-        bool ok = true;
-        uint32_t it = 0;
-        uint32_t adding = 0, parity = 0;             // per stage: its tile is being added; phase of `summed`
-        for (int t = cluster; ok && t < n_tiles; t += n_clusters) {
-            int mt, nt;
-            tile_at(t, mt, nt);
-            const bool db_tile = C::MODE == kWgrad && ep.db && t < sh.m_tiles;
-            const int m0 = (mt * C::CG + (C::CG == 2 ? int(rank) : 0)) * 128;
-            const int n0 = nt * C::BN + (C::CG == 2 ? int(rank) * C::BROWS : 0);
-            for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                const uint32_t s = it % C::STAGES, use = it / C::STAGES;
-                if (use > 0 && !mbar_wait_bounded(empty + 8 * s, (use - 1) & 1, wait_ns)) {
-                    ok = false;
-                    break;
-                }
-                if (C::MODE == kWgrad && (adding >> s & 1)) {
-                    if (!mbar_wait_bounded(summed + 8 * s, parity >> s & 1, wait_ns)) {
-                        ok = false;
-                        break;
-                    }
-                    parity ^= 1u << s;
-                    adding ^= 1u << s;
-                }
-                if (db_tile) adding |= 1u << s;
-                if (elect_one()) {
-                    if (leader) mbar_arrive_tx(full + 8 * s, C::CG * C::STAGE);
-                    const uint32_t bar = C::CG == 2 ? map_rank(full + 8 * s, 0) : full + 8 * s;
-                    const uint32_t st = smem_addr(smem + s * C::STAGE);
-#pragma unroll
-                    for (int p = 0; p < C::PL; ++p) {
-                        const uint32_t a = st + p * C::A_BYTES, b = st + C::PL * C::A_BYTES + p * C::B_BYTES;
-                        if constexpr (C::A_MN) {
-                            tma_load<C::CG>(a, &map_a, m0, kb * kKb, p, bar);
-                            tma_load<C::CG>(a + 8192, &map_a, m0 + 64, kb * kKb, p, bar);
-                        } else {
-                            tma_load<C::CG>(a, &map_a, kb * kKb, m0, p, bar);
-                        }
-                        if constexpr (C::B_MN) {
-#pragma unroll
-                            for (int c = 0; c < C::BROWS / 64; ++c)
-                                tma_load<C::CG>(b + c * 8192, &map_b, n0 + c * 64, kb * kKb, p, bar);
-                        } else {
-                            tma_load<C::CG>(b, &map_b, kb * kKb, n0, p, bar);
-                        }
-                    }
-                }
-                __syncwarp();
-            }
-        }
-        // the last use of every stage: its MMAs are done (and, in a pair, their arrivals on
-        // this CTA have landed) before the CTA may leave
-        for (uint32_t k = it > C::STAGES ? it - C::STAGES : 0; ok && k < it; ++k)
-            ok = mbar_wait_bounded(empty + 8 * (k % C::STAGES), (k / C::STAGES) & 1, wait_ns);
-        if (!__all_sync(0xffffffffu, ok)) {
-            if (lane == 0) atomicOr(&g_wait_error, 1u);
-            const uint64_t t0 = global_ns();                 // copies in flight land within this
-            for (int i = 0; i < (1 << 20) && global_ns() - t0 < 2000000ull; ++i) __nanosleep(1000);
-        }
-        __syncwarp();
-    } else if (warp == kEpiWarps + 1) {
-        // ---- products ----
-        if (leader) {
-            constexpr uint32_t idesc = mma_idesc(128 * C::CG, C::BN, C::A_MN, C::B_MN);
-            // 16 K elements on: 32 bytes along a K-major row, 16 rows of an MN-major tile
-            constexpr uint32_t a_step = C::A_MN ? 2048 / 16 : 32 / 16, b_step = C::B_MN ? 2048 / 16 : 32 / 16;
-            const uint64_t da0 = smem_desc(smem_addr(smem), C::A_MN ? 8192 : 16, 1024);
-            const uint64_t db0 = smem_desc(smem_addr(smem) + C::PL * C::A_BYTES, C::B_MN ? 8192 : 16, 1024);
+    // Kernels that hold sums in registers: the epilogue's two warpgroups take registers that the
+    // third does not need (the launch has 168 per thread of three warpgroups, which prepare_kernel
+    // checks; 2 x 208 + 88 = 2 x 200 + 104 = 3 x 168).  Spilled, the sums went through an L1 of the 28 KB that shared memory leaves, and a
+    // chunk of 128 columns took a warp 6,000 clocks to add instead of 2,000.
+    if (warp >= kEpiWarps) {
+        if constexpr (C::REGS && C::MODE == kWgrad) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+        else if constexpr (C::REGS) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        if (warp == kEpiWarps) {
+            // ---- loads ----
             bool ok = true;
-            uint32_t it = 0, ac = 0;
+            uint32_t it = 0;
+            uint32_t adding = 0, parity = 0;             // per stage: its tile is being added; phase of `summed`
             for (int t = cluster; ok && t < n_tiles; t += n_clusters) {
-                for (int kc = kb0; ok && kc < kb1; kc += chunk, ++ac) {
-                    const uint32_t buf = ac & 1, use = ac >> 1;
-                    if (use > 0 && !mbar_wait_bounded(acc_empty + 8 * buf, (use - 1) & 1, wait_ns)) {
+                int mt, nt;
+                tile_at(t, mt, nt);
+                const int m0 = (mt * C::CG + (C::CG == 2 ? int(rank) : 0)) * 128;
+                const int n0 = nt * C::BN + (C::CG == 2 ? int(rank) * C::BROWS : 0);
+                for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                    const uint32_t s = it % C::STAGES, use = it / C::STAGES;
+                    if (use > 0 && !mbar_wait_bounded(empty + 8 * s, (use - 1) & 1, wait_ns)) {
                         ok = false;
                         break;
                     }
-                    tc_fence_after();
-                    const uint32_t d = tmem + buf * C::BN;
-                    const int ke = kc + chunk < kb1 ? kc + chunk : kb1;
-                    for (int kb = kc; kb < ke; ++kb, ++it) {
-                        const uint32_t s = it % C::STAGES;
-                        if (!mbar_wait_bounded(full + 8 * s, (it / C::STAGES) & 1, wait_ns)) {
+                    if (C::SPLIT && C::MODE == kWgrad && (adding >> s & 1)) {
+                        if (!mbar_wait_bounded(summed + 8 * s, parity >> s & 1, wait_ns)) {
+                            ok = false;
+                            break;
+                        }
+                        parity ^= 1u << s;
+                        adding ^= 1u << s;
+                    }
+                    if (C::SPLIT && C::MODE == kWgrad && ep.db && nt == 0) adding |= 1u << s;
+                    if (elect_one()) {
+                        if (leader) mbar_arrive_tx(full + 8 * s, C::CG * C::STAGE);
+                        const uint32_t bar = C::CG == 2 ? map_rank(full + 8 * s, 0) : full + 8 * s;
+                        const uint32_t st = smem_addr(smem + s * C::STAGE);
+#pragma unroll
+                        for (int p = 0; p < C::PL; ++p) {
+                            const uint32_t a = st + p * C::A_BYTES, b = st + C::PL * C::A_BYTES + p * C::B_BYTES;
+                            if constexpr (C::A_MN) {
+                                tma_load<C::CG>(a, &map_a, m0, kb * kKb, p, bar);
+                                tma_load<C::CG>(a + 8192, &map_a, m0 + 64, kb * kKb, p, bar);
+                            } else {
+                                tma_load<C::CG>(a, &map_a, kb * kKb, m0, p, bar);
+                            }
+                            if constexpr (C::B_MN) {
+#pragma unroll
+                                for (int c = 0; c < C::BROWS / 64; ++c)
+                                    tma_load<C::CG>(b + c * 8192, &map_b, n0 + c * 64, kb * kKb, p, bar);
+                            } else {
+                                tma_load<C::CG>(b, &map_b, kb * kKb, n0, p, bar);
+                            }
+                        }
+                    }
+                    __syncwarp();
+                }
+            }
+            // the last use of every stage: its MMAs are done (and, in a pair, their arrivals on
+            // this CTA have landed) before the CTA may leave
+            for (uint32_t k = it > C::STAGES ? it - C::STAGES : 0; ok && k < it; ++k)
+                ok = mbar_wait_bounded(empty + 8 * (k % C::STAGES), (k / C::STAGES) & 1, wait_ns);
+            if (!__all_sync(0xffffffffu, ok)) {
+                if (lane == 0) atomicOr(&g_wait_error, 1u);
+                const uint64_t t0 = global_ns();                 // copies in flight land within this
+                for (int i = 0; i < (1 << 20) && global_ns() - t0 < 2000000ull; ++i) __nanosleep(1000);
+            }
+            __syncwarp();
+        } else if (warp == kEpiWarps + 1) {
+            // ---- products ----
+            if (leader) {
+                constexpr uint32_t idesc = mma_idesc(128 * C::CG, C::BN, C::A_MN, C::B_MN);
+                // 16 K elements on: 32 bytes along a K-major row, 16 rows of an MN-major tile
+                constexpr uint32_t a_step = C::A_MN ? 2048 / 16 : 32 / 16, b_step = C::B_MN ? 2048 / 16 : 32 / 16;
+                const uint64_t da0 = smem_desc(smem_addr(smem), C::A_MN ? 8192 : 16, 1024);
+                const uint64_t db0 = smem_desc(smem_addr(smem) + C::PL * C::A_BYTES, C::B_MN ? 8192 : 16, 1024);
+                bool ok = true;
+                uint32_t it = 0, ac = 0;
+                for (int t = cluster; ok && t < n_tiles; t += n_clusters) {
+                    for (int kc = kb0; ok && kc < kb1; kc += chunk, ++ac) {
+                        const uint32_t buf = ac & 1, use = ac >> 1;
+                        if (use > 0 && !mbar_wait_bounded(acc_empty + 8 * buf, (use - 1) & 1, wait_ns)) {
                             ok = false;
                             break;
                         }
                         tc_fence_after();
-                        // stages are far below the descriptor's 256 KB, so offsets add to its low bits
-                        const uint64_t das = da0 + s * (C::STAGE / 16), dbs = db0 + s * (C::STAGE / 16);
-                        if (elect_one()) {
-#pragma unroll
-                            for (int pr = 0; pr < (C::PL == 3 ? 6 : 1); ++pr) {
-                                // plane pairs (0,2) (2,0) (1,1) (0,1) (1,0) (0,0), smallest first (the other
-                                // three are below 2^-24 of the product)
-                                const int pa = C::PL == 1 ? 0 : pr == 1 ? 2 : pr == 2 || pr == 4 ? 1 : 0;
-                                const int pb = C::PL == 1 ? 0 : pr == 0 ? 2 : pr == 2 || pr == 3 ? 1 : 0;
-#pragma unroll
-                                for (int k = 0; k < kKb / 16; ++k)
-                                    mma_bf16<C::CG>(d, das + pa * (C::A_BYTES / 16) + k * a_step,
-                                                    dbs + pb * (C::B_BYTES / 16) + k * b_step, idesc, kb > kc || pr > 0 || k > 0);
+                        const uint32_t d = tmem + buf * C::BN;
+                        const int ke = kc + chunk < kb1 ? kc + chunk : kb1;
+                        for (int kb = kc; kb < ke; ++kb, ++it) {
+                            const uint32_t s = it % C::STAGES;
+                            if (!mbar_wait_bounded(full + 8 * s, (it / C::STAGES) & 1, wait_ns)) {
+                                ok = false;
+                                break;
                             }
-                            mma_commit<C::CG>(empty + 8 * s);
-                            if (kb + 1 == ke) mma_commit<C::CG>(acc_full + 8 * buf);
+                            tc_fence_after();
+                            // stages are far below the descriptor's 256 KB, so offsets add to its low bits
+                            const uint64_t das = da0 + s * (C::STAGE / 16), dbs = db0 + s * (C::STAGE / 16);
+                            if (elect_one()) {
+#pragma unroll
+                                for (int pr = 0; pr < (C::PL == 3 ? 6 : 1); ++pr) {
+                                    // plane pairs (0,2) (2,0) (1,1) (0,1) (1,0) (0,0), smallest first (the other
+                                    // three are below 2^-24 of the product)
+                                    const int pa = C::PL == 1 ? 0 : pr == 1 ? 2 : pr == 2 || pr == 4 ? 1 : 0;
+                                    const int pb = C::PL == 1 ? 0 : pr == 0 ? 2 : pr == 2 || pr == 3 ? 1 : 0;
+#pragma unroll
+                                    for (int k = 0; k < kKb / 16; ++k)
+                                        mma_bf16<C::CG>(d, das + pa * (C::A_BYTES / 16) + k * a_step,
+                                                        dbs + pb * (C::B_BYTES / 16) + k * b_step, idesc, kb > kc || pr > 0 || k > 0);
+                                }
+                                mma_commit<C::CG>(empty + 8 * s);
+                                if (kb + 1 == ke) mma_commit<C::CG>(acc_full + 8 * buf);
+                            }
+                            __syncwarp();
                         }
-                        __syncwarp();
                     }
                 }
+                if (!__all_sync(0xffffffffu, ok) && lane == 0) atomicOr(&g_wait_error, 1u);
             }
-            if (!__all_sync(0xffffffffu, ok) && lane == 0) atomicOr(&g_wait_error, 1u);
-        }
-        __syncwarp();
-    } else if (warp >= kEpiWarps + 2) {
-        // ---- column sums of dz ----
-        // A stage is read once it is loaded (in a pair, where only the leader sees that, once its
-        // products are done), and loaded again once it has been added.
-        if (C::MODE == kWgrad && ep.db) {
+            __syncwarp();
+        } else if (warp >= kEpiWarps + 2) {
+            // ---- column sums of dz ----
             const int chunk_at = warp - (kEpiWarps + 2);
-            bool ok = true;
-            uint32_t it = 0;
-            for (int mt = cluster; ok && mt < sh.m_tiles; mt += n_clusters) {   // the tiles mt, 0: the first ones
+            if (C::MODE == kWgrad && C::SPLIT && ep.db) {
+                // a stage is read once it is loaded, and loaded again once it has been added
+                int mt, nt;
+                tile_at(cluster, mt, nt);
+                bool ok = true;
                 ColSum db = {};
-                for (int kb = kb0; ok && kb < kb1; ++kb, ++it) {
-                    const uint32_t s = it % C::STAGES;
-                    ok = __all_sync(0xffffffffu, mbar_wait_bounded((C::CG == 2 ? empty : full) + 8 * s, (it / C::STAGES) & 1, wait_ns));
+                for (int kb = kb0; nt == 0 && kb < kb1; ++kb) {
+                    const uint32_t it = uint32_t(kb - kb0), s = it % C::STAGES;
+                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(full + 8 * s, (it / C::STAGES) & 1, wait_ns));
                     if (!ok) break;
                     colsum_add<C::PL>(db, smem + s * C::STAGE + chunk_at * 8192, C::A_BYTES, lane);
                     __syncwarp();
@@ -793,20 +893,42 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
                 }
                 float v[8];
                 colsum_lanes(db, v, lane);
-                const int c = chunk_at * 64 + lane * 8;
-                if (ok && lane < 8) {
+                if (lane < 8) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int64_t col = int64_t(mt * C::CG + (C::CG == 2 ? int(rank) : 0)) * 128 + c + e;
-                        if (C::SPLIT) db_part[c + e] = v[e];
-                        else if (col < ep.rows) emit_db<typename C::OT>(ep, col, v[e]);
+                    for (int e = 0; e < 8; ++e) db_part[chunk_at * 64 + lane * 8 + e] = v[e];
+                }
+                if (!ok && lane == 0) atomicOr(&g_wait_error, 1u);
+            }
+            if constexpr (C::MODE == kWgrad && !C::SPLIT) {
+                // the tiles of a row of tiles belong to the same columns of dz: the first db_parts of
+                // them share out the K steps, every db_parts-th each
+                using DT = typename std::conditional<C::PL == 3, float, uint16_t>::type;
+                using RS = RowSum<DT>;
+                for (int t = cluster; ep.db && t < n_tiles; t += n_clusters) {
+                    int mt, nt;
+                    tile_at(t, mt, nt);
+                    if (nt >= ep.db_parts) continue;
+                    const int64_t col = int64_t(mt * C::CG + int(rank)) * 128 + chunk_at * 64;
+                    RS db = {};
+                    for (int kb = nt; kb < sh.n_kb && col < ep.rows; kb += ep.db_parts)
+                        db.add(static_cast<const DT*>(ep.dz), ep.lddz, int64_t(kb) * kKb, ep.dz_rows, col, ep.rows, ep.dz_vec, lane);
+                    db.join();
+                    if (lane < RS::L) {
+#pragma unroll
+                        for (int e = 0; e < RS::E; ++e) {
+                            const int64_t c = col + lane * RS::E + e;
+                            if (c >= ep.rows) break;
+                            if (ep.db_parts > 1) ep.db_sums[nt * ep.rows + c] = db.v[e];
+                            else emit_db<typename C::OT>(ep, c, db.v[e]);
+                        }
                     }
                 }
             }
-            if (!ok && lane == 0) atomicOr(&g_wait_error, 1u);
+            __syncwarp();
         }
-        __syncwarp();
     } else {
+        if constexpr (C::REGS && C::MODE == kWgrad) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+        else if constexpr (C::REGS) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         // ---- epilogue ----
         // Warp w reads TMEM lanes 32 (w mod 4) on: rows 32 q of the CTA's part of the tile; the
         // two halves of the warps take alternate groups of 32 columns.
@@ -919,9 +1041,14 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
                 }
             }
             if constexpr (C::CH != 0) {
+                constexpr bool WHOLE = C::MODE == kWgrad && !C::SPLIT && sizeof(typename C::OT) == 4;
+                const bool whole = WHOLE && ep.vec == 2 && n0 + C::BN <= ep.cols;
+                if constexpr (WHOLE) {
+                    if (ok && whole) emit_sums<NJ>(ep, sum, m0 + lane, n0 + half * 32);
+                }
 #pragma unroll
                 for (int jj = 0; jj < NJ; ++jj)
-                    if (ok && (2 * jj + half) * 32 < C::BN) {
+                    if (ok && !whole && (2 * jj + half) * 32 < C::BN) {
                         begin(jj);
                         finish(jj, sum[jj]);
                     }
@@ -1025,7 +1152,12 @@ template <class C>
 cudaError_t prepare_kernel(int dev) {
     static std::atomic<uint64_t> done{0};
     if (dev < 64 && (done.load(std::memory_order_relaxed) >> dev & 1)) return cudaSuccess;
-    const cudaError_t e = cudaFuncSetAttribute(k_linear<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    cudaError_t e = cudaFuncSetAttribute(k_linear<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (C::REGS && e == cudaSuccess) {             // the registers that the warpgroups share out are there
+        cudaFuncAttributes a;
+        e = cudaFuncGetAttributes(&a, k_linear<C>);
+        if (e == cudaSuccess && a.numRegs != 168) return cudaErrorInvalidConfiguration;
+    }
     if (e == cudaSuccess && dev < 64) done.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
     return e;
 }

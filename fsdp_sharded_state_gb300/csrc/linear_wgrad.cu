@@ -4,12 +4,51 @@
 
 namespace fsdp {
 
+namespace {
+// The sum of `parts` partial sums, in order, for each element of out ([parts][rows][ld], rows x
+// cols of it) and then of db ([parts][rows]).
+template <typename OT>
+__global__ void __launch_bounds__(256)
+k_join(const float* __restrict__ part, const float* __restrict__ db_part, int parts, int64_t rows, int64_t cols, int64_t ld, OT* out,
+       int64_t ldo, OT* db, int accumulate) {
+    pdl_wait();
+    const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x, n = rows * cols;
+    const bool is_db = i >= n;
+    if (i >= n + (db ? rows : 0)) return;
+    const int64_t r = is_db ? i - n : i / cols, c = is_db ? 0 : i - r * cols;
+    const float* p = is_db ? db_part + r : part + r * ld + c;
+    const int64_t step = is_db ? rows : rows * ld;
+    float t = p[0];
+#pragma unroll 16
+    for (int s = 1; s < parts; ++s) t += p[s * step];
+    OT* const o = is_db ? db + r : out + r * ldo + c;
+    store1(o, accumulate ? t + load1(o) : t);
+}
+
+template <typename OT>
+cudaError_t join(const float* part, const float* db_part, int parts, int64_t rows, int64_t cols, int64_t ld, const LinEpi& ep,
+                 cudaStream_t st) {
+    const int64_t blocks = ceil_div(rows * cols + (ep.db ? rows : 0), 256);
+    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+    return launch(k_join<OT>, dim3(unsigned(blocks)), dim3(256), 0, st, part, db_part, parts, rows, cols, ld,
+                  static_cast<OT*>(ep.out), ep.ldo, static_cast<OT*>(ep.db), int(ep.accumulate));
+}
+
+// The pair kernels, and the join of db's partial sums.
+template <typename OT, int PL, int CH>
+cudaError_t launch_pair_wgrad(const LinProblem& p, int bn, cudaStream_t st) {
+    const cudaError_t e = launch_pair_as<kWgrad, OT, PL, CH>(p, bn, st);
+    if (e != cudaSuccess || !p.epi.db || p.epi.db_parts <= 1) return e;
+    return join<OT>(nullptr, p.epi.db_sums, p.epi.db_parts, p.epi.rows, 0, 0, p.epi, st);
+}
+}  // namespace
+
 cudaError_t launch_linear_wgrad(const LinProblem& p, cudaStream_t st) {
     if (p.planes == 3)
-        return p.out_bf16 ? launch_product<kWgrad, uint16_t, 3, 0>(p, launch_pair_as<kWgrad, uint16_t, 3, 0>, st)
-                          : launch_product<kWgrad, float, 3, 2>(p, launch_pair_as<kWgrad, float, 3, 2>, st);
-    return p.out_bf16 ? launch_product<kWgrad, uint16_t, 1, 0>(p, launch_pair_as<kWgrad, uint16_t, 1, 0>, st)
-                      : launch_product<kWgrad, float, 1, 8>(p, launch_pair_as<kWgrad, float, 1, 8>, st);
+        return p.out_bf16 ? launch_product<kWgrad, uint16_t, 3, 0>(p, launch_pair_wgrad<uint16_t, 3, 0>, st)
+                          : launch_product<kWgrad, float, 3, 2>(p, launch_pair_wgrad<float, 3, 2>, st);
+    return p.out_bf16 ? launch_product<kWgrad, uint16_t, 1, 0>(p, launch_pair_wgrad<uint16_t, 1, 0>, st)
+                      : launch_product<kWgrad, float, 1, 8>(p, launch_pair_wgrad<float, 1, 8>, st);
 }
 
 // ---- slabs ------------------------------------------------------------------------------
@@ -26,26 +65,6 @@ int64_t wgrad_slab_floats(int64_t rows, int64_t in, int64_t out) {
     return int64_t(wgrad_slabs(rows, in, out)) * (out * ((in + 7) & ~int64_t(7)) + ((out + 3) & ~int64_t(3)));
 }
 
-namespace {
-template <typename OT>
-__global__ void __launch_bounds__(256)
-k_join_slabs(const float* __restrict__ part, int slabs, int64_t rows, int64_t cols, int64_t ld, OT* out, int64_t ldo, OT* db,
-             int accumulate) {
-    pdl_wait();
-    const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x, n = rows * cols;
-    const bool is_db = i >= n;
-    if (i >= n + (db ? rows : 0)) return;
-    const int64_t r = is_db ? i - n : i / cols, c = is_db ? 0 : i - r * cols;
-    const float* p = is_db ? part + slabs * rows * ld + r : part + r * ld + c;
-    const int64_t step = is_db ? rows : rows * ld;
-    float t = p[0];
-#pragma unroll 16
-    for (int s = 1; s < slabs; ++s) t += p[s * step];
-    OT* const o = is_db ? db + r : out + r * ldo + c;
-    store1(o, accumulate ? t + load1(o) : t);
-}
-}  // namespace
-
 cudaError_t launch_wgrad_slabs(const LinProblem& p, cudaStream_t st) {
     LinProblem q = p;
     const int64_t rows = p.epi.rows, cols = p.epi.cols, ld = (cols + 7) & ~int64_t(7);
@@ -57,11 +76,15 @@ cudaError_t launch_wgrad_slabs(const LinProblem& p, cudaStream_t st) {
     cudaError_t e = p.planes == 3 ? launch_cfg<LinCfg<kWgrad, float, 1, 64, 3, 2, true>>(q, kSlabSplits, st, p.slabs)
                                   : launch_cfg<LinCfg<kWgrad, float, 1, 64, 1, 8, true>>(q, kSlabSplits, st, p.slabs);
     if (e != cudaSuccess) return e;
-    const int64_t blocks = ceil_div(rows * cols + (p.epi.db ? rows : 0), 256);
-    return p.out_bf16 ? launch(k_join_slabs<uint16_t>, dim3(unsigned(blocks)), dim3(256), 0, st, p.partial, p.slabs, rows, cols, ld,
-                               static_cast<uint16_t*>(p.epi.out), p.epi.ldo, static_cast<uint16_t*>(p.epi.db), p.epi.accumulate)
-                      : launch(k_join_slabs<float>, dim3(unsigned(blocks)), dim3(256), 0, st, p.partial, p.slabs, rows, cols, ld,
-                               static_cast<float*>(p.epi.out), p.epi.ldo, static_cast<float*>(p.epi.db), p.epi.accumulate);
+    const float* const db_part = p.partial + p.slabs * rows * ld;
+    return p.out_bf16 ? join<uint16_t>(p.partial, db_part, p.slabs, rows, cols, ld, p.epi, st)
+                      : join<float>(p.partial, db_part, p.slabs, rows, cols, ld, p.epi, st);
+}
+
+int wgrad_db_parts(int64_t rows, int64_t in) {
+    const int64_t kb = ceil_div(rows, kKb), tiles = ceil_div(in, 256);
+    const int64_t n = kb < tiles ? kb : tiles;
+    return n > 8 ? 8 : int(n);
 }
 
 cudaError_t take_wait_error_wgrad(unsigned int* flag) { return take_local_wait_error(flag); }

@@ -45,7 +45,6 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr) {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-
 // One box of a 3-D tensor map (x: innermost) into shared memory; its bytes are counted on
 // `bar`, which with CG = 2 may be the other CTA's of the pair (a shared::cluster address).
 template <int CG>
