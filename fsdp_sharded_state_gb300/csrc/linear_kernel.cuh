@@ -426,79 +426,92 @@ __device__ __forceinline__ void store16(uint16_t* p, const float (&v)[16]) {
 // (residual, pre-activation) while the unit before it is computed.  dcol: the generator's
 // column products of the units' columns, in shared memory; dr: the lane's row's.
 template <int MODE, int EP, int NU>
-__device__ __forceinline__ int emit_rows(const LinEpi& ep, uint32_t acc, int64_t row, int64_t col0, const DropRow& dr,
-                                         const DropCol* dcol) {
-    const int act = EP >= 0 ? EP & 3 : ep.act;
-    const bool drop = MODE != kWgrad && (EP >= 0 ? EP >= 4 : ep.drop.on != 0);
-    const bool in = row < ep.rows;
-    const int64_t left = ep.cols - col0;
-    const int units = left < 32 ? 0 : (left - 32) / 64 + 1 < NU ? int((left - 32) / 64 + 1) : NU;
-    uint16_t* out = static_cast<uint16_t*>(ep.out) + row * ep.ldo + col0;
-    const uint16_t* add = MODE == kWgrad ? (ep.accumulate ? out : nullptr)
-                          : ep.residual  ? static_cast<const uint16_t*>(ep.residual) + row * ep.ldr + col0
-                                         : nullptr;
-    uint16_t* z = MODE != kWgrad && ep.preact ? static_cast<uint16_t*>(ep.preact) + row * ep.ldz + col0 : nullptr;
-    const uint16_t* bias = MODE == kForward && ep.bias ? static_cast<const uint16_t*>(ep.bias) + col0 : nullptr;
-    Raw16 aq[2] = {}, zq[2] = {};
-#pragma unroll
-    for (int g = 0; g < 2; ++g) {
-        if (add && in && units > 0) aq[g] = load_raw16(add + 16 * g);
-        if (MODE == kDgrad && z && in && units > 0) zq[g] = load_raw16(z + 16 * g);
-    }
-    Acc16 next;                                              // the accumulators of the half to come
-    if (units > 0) tmem_ld16_async(acc, next);
-#pragma unroll 1
-    for (int u = 0; u < units; ++u) {
-        const bool more = in && u + 1 < units;
+struct RowsEmit {
+    uint16_t* out;
+    const uint16_t* add;
+    uint16_t* z;
+    const uint16_t* bias;
+    int units;
+    bool in;
+    Raw16 aq[2], zq[2];
+
+    // Before the accumulators are there: the first unit's reads.
+    __device__ __forceinline__ void begin(const LinEpi& ep, int64_t row, int64_t col0) {
+        in = row < ep.rows;
+        const int64_t left = ep.cols - col0;
+        units = left < 32 ? 0 : (left - 32) / 64 + 1 < NU ? int((left - 32) / 64 + 1) : NU;
+        out = static_cast<uint16_t*>(ep.out) + row * ep.ldo + col0;
+        add = MODE == kWgrad ? (ep.accumulate ? out : nullptr)
+              : ep.residual  ? static_cast<const uint16_t*>(ep.residual) + row * ep.ldr + col0
+                             : nullptr;
+        z = MODE != kWgrad && ep.preact ? static_cast<uint16_t*>(ep.preact) + row * ep.ldz + col0 : nullptr;
+        bias = MODE == kForward && ep.bias ? static_cast<const uint16_t*>(ep.bias) + col0 : nullptr;
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
-            const int c = 64 * u + 16 * g;
-            float v[16], t[16];
-            tmem_wait_ld16(next, v);
-            if (g == 0) tmem_ld16_async(acc + c + 16, next);
-            else if (u + 1 < units) tmem_ld16_async(acc + c + 48, next);
-            if constexpr (MODE == kForward) {
-                if (bias) {
-                    float b[8];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        widen(load_raw(bias + c + 8 * h), b);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) v[8 * h + i] += b[i];
-                    }
-                }
-                if (z && in) store16(z + c, v);
-                activate<true, 16>(v, act);
-            }
-            if (drop) {
-#pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    const uint4 q = ldu4(dcol + 8 * u + 4 * g + b);
-                    const uint4 w = drop_words(ep.drop, dr, DropCol{q.x, q.y, q.z, q.w});
-                    v[4 * b] = drop1(ep.drop, w.x, v[4 * b]);
-                    v[4 * b + 1] = drop1(ep.drop, w.y, v[4 * b + 1]);
-                    v[4 * b + 2] = drop1(ep.drop, w.z, v[4 * b + 2]);
-                    v[4 * b + 3] = drop1(ep.drop, w.w, v[4 * b + 3]);
-                }
-            }
-            if constexpr (MODE == kDgrad) {
-                if (z) {
-                    widen(zq[g], t);
-                    if (more) zq[g] = load_raw16(z + c + 64);
-                    activate_grad<true, 16>(v, t, act);
-                }
-            }
-            if (add) {
-                widen(aq[g], t);
-                if (more) aq[g] = load_raw16(add + c + 64);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) v[i] += t[i];
-            }
-            if (in) store16(out + c, v);
+            aq[g] = zq[g] = Raw16{};
+            if (add && in && units > 0) aq[g] = load_raw16(add + 16 * g);
+            if (MODE == kDgrad && z && in && units > 0) zq[g] = load_raw16(z + 16 * g);
         }
     }
-    return units;
-}
+
+    __device__ __forceinline__ int run(const LinEpi& ep, uint32_t acc, const DropRow& dr, const DropCol* dcol) {
+        const int act = EP >= 0 ? EP & 3 : ep.act;
+        const bool drop = MODE != kWgrad && (EP >= 0 ? EP >= 4 : ep.drop.on != 0);
+        Acc16 next;                                              // the accumulators of the half to come
+        if (units > 0) tmem_ld16_async(acc, next);
+#pragma unroll 1
+        for (int u = 0; u < units; ++u) {
+            const bool more = in && u + 1 < units;
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                const int c = 64 * u + 16 * g;
+                float v[16], t[16];
+                tmem_wait_ld16(next, v);
+                if (g == 0) tmem_ld16_async(acc + c + 16, next);
+                else if (u + 1 < units) tmem_ld16_async(acc + c + 48, next);
+                if constexpr (MODE == kForward) {
+                    if (bias) {
+                        float b[8];
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            widen(load_raw(bias + c + 8 * h), b);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) v[8 * h + i] += b[i];
+                        }
+                    }
+                    if (z && in) store16(z + c, v);
+                    activate<true, 16>(v, act);
+                }
+                if (drop) {
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        const uint4 q = ldu4(dcol + 8 * u + 4 * g + b);
+                        const uint4 w = drop_words(ep.drop, dr, DropCol{q.x, q.y, q.z, q.w});
+                        v[4 * b] = drop1(ep.drop, w.x, v[4 * b]);
+                        v[4 * b + 1] = drop1(ep.drop, w.y, v[4 * b + 1]);
+                        v[4 * b + 2] = drop1(ep.drop, w.z, v[4 * b + 2]);
+                        v[4 * b + 3] = drop1(ep.drop, w.w, v[4 * b + 3]);
+                    }
+                }
+                if constexpr (MODE == kDgrad) {
+                    if (z) {
+                        widen(zq[g], t);
+                        if (more) zq[g] = load_raw16(z + c + 64);
+                        activate_grad<true, 16>(v, t, act);
+                    }
+                }
+                if (add) {
+                    widen(aq[g], t);
+                    if (more) aq[g] = load_raw16(add + c + 64);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) v[i] += t[i];
+                }
+                if (in) store16(out + c, v);
+            }
+        }
+        return units;
+    }
+};
 
 // wgrad's fp32 epilogue from the sums in registers, a lane per row, 32-byte aligned rows: the
 // columns col0 + 64 u on are written, or added to what is there, which is read further and
@@ -671,7 +684,7 @@ struct LinCfg {
     static constexpr bool A_MN = MODE == kWgrad || (MODE == kDgrad && !ROWS_M);
     static constexpr bool B_MN = MODE == kWgrad || (MODE == kDgrad && ROWS_M);
     static constexpr bool REGS = CH != 0 && !SPLIT;                         // sums of a whole tile in registers
-    static constexpr bool DIRECT = !SPLIT && CH == 0 && sizeof(OT) == 2;    // emit_rows where rows are aligned
+    static constexpr bool DIRECT = !SPLIT && CH == 0 && sizeof(OT) == 2;    // RowsEmit where rows are aligned
     static constexpr int AHEAD = 1;
     static constexpr int BROWS = BN / CG;                        // B rows a CTA loads
     static constexpr int A_BYTES = 128 * 128, B_BYTES = BROWS * 128;
@@ -984,13 +997,17 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
             };
             for (int kc = kb0; ok && kc < kb1; kc += chunk, ++ac) {
                 const uint32_t buf = ac & 1;
+                RowsEmit<C::MODE, C::EP, NJ> rows;           // of direct tiles
+                bool direct = C::DIRECT && ep.vec == 2;
+                if constexpr (C::DIRECT) {
+                    if (direct) rows.begin(ep, m0 + lane, n0 + half * 32);
+                }
                 ok = __all_sync(0xffffffffu, mbar_wait_bounded(acc_full + 8 * buf, (ac >> 1) & 1, wait_ns));
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t src = tmem + buf * C::BN + (uint32_t(q * 32) << 16);
                 DropRow dr = {};
                 DropCol* const dcol = reinterpret_cast<DropCol*>(epi_smem + warp * kUnitFloats);
-                bool direct = C::DIRECT && ep.vec == 2;
                 if constexpr (C::DIRECT && C::MODE != kWgrad) {
                     if (direct && (C::EP >= 0 ? C::EP >= 4 : ep.drop.on != 0)) {
                         // the generator's products of the lane's row, and, one block per lane, of this
@@ -1008,8 +1025,7 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
                 int done = 0;                                // units of the direct path
                 if constexpr (C::DIRECT) {
                     if (direct)
-                        done = m0 >= ep.rows ? NJ
-                                             : emit_rows<C::MODE, C::EP, NJ>(ep, src + half * 32, m0 + lane, n0 + half * 32, dr, dcol);
+                        done = m0 >= ep.rows ? NJ : rows.run(ep, src + half * 32, dr, dcol);
                 }
                 constexpr int kUnrollUnits = C::CH != 0 ? NJ : 1;
 #pragma unroll kUnrollUnits
