@@ -1,10 +1,11 @@
 // linear_dgrad_pair.cu -- the CTA-pair kernels of dgrad with bf16 results, one per
-// activation, with and without dropout.
+// activation, with and without dropout, and one for rows of any alignment.
 #include "linear_kernel.cuh"
 
 namespace fsdp {
 
 cudaError_t launch_pair_dgrad(const LinProblem& p, int bn, cudaStream_t st) {
+    if (p.epi.vec != 2) return launch_pair_as<kDgrad, uint16_t, 1, 0, -1, true>(p, bn, st);
     switch (p.epi.act + (p.epi.drop.on ? 4 : 0)) {
         case 0: return launch_pair_as<kDgrad, uint16_t, 1, 0, 0>(p, bn, st);
         case 1: return launch_pair_as<kDgrad, uint16_t, 1, 0, 1>(p, bn, st);

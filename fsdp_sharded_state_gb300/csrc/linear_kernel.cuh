@@ -418,28 +418,130 @@ __device__ __forceinline__ void store16(uint16_t* p, const float (&v)[16]) {
                  : "memory");
 }
 
+// 16 bf16 elements that start o elements into a 16-byte window (0 <= o < 8), as the three
+// windows that hold them, the third only where it is needed.
+struct Win16 {
+    uint32_t w[12];
+};
+__device__ __forceinline__ int window_offset(const uint16_t* p) { return int(reinterpret_cast<uintptr_t>(p) & 15) >> 1; }
+__device__ __forceinline__ Win16 load_win16(const uint16_t* p) {
+    const uint16_t* const a = p - window_offset(p);
+    Win16 r;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        uint4 q = make_uint4(0, 0, 0, 0);
+        if (k < 2 || a != p) q = ldu4(a + 8 * k);
+        r.w[4 * k] = q.x; r.w[4 * k + 1] = q.y; r.w[4 * k + 2] = q.z; r.w[4 * k + 3] = q.w;
+    }
+    return r;
+}
+__device__ __forceinline__ void widen(const Win16& r, int o, float (&v)[16]) {
+    uint32_t u[11];                              // by half a word, then by 2 words, then by 1
+#pragma unroll
+    for (int i = 0; i < 11; ++i) u[i] = __funnelshift_r(r.w[i], r.w[i + 1], 16 * (o & 1));
+#pragma unroll
+    for (int i = 0; i < 9; ++i) u[i] = o & 4 ? u[i + 2] : u[i];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t w = o & 2 ? u[i + 1] : u[i];
+        v[2 * i] = bf16lo(w);
+        v[2 * i + 1] = bf16hi(w);
+    }
+}
+// The other way: groups of 16 elements that follow one another in memory from p on, written as
+// whole 16-byte windows; the elements before the first and after the last whole window, which
+// neighbours share, in pieces of 8, 4 and 2 bytes.
+struct WinOut {
+    uint16_t* at;              // the window that the next group starts in
+    int o;                     // elements of it that are already there
+    uint32_t carry[4];         // those, where an earlier group left them
+    bool first;
+
+    __device__ __forceinline__ void begin(uint16_t* p) {
+        o = window_offset(p);
+        at = p - o;
+        carry[0] = carry[1] = carry[2] = carry[3] = 0;
+        first = true;
+    }
+    // elements [lo, 8) or [0, hi) of a window, from its words
+    __device__ __forceinline__ static void tail(uint16_t* a, const uint32_t (&w)[4], int lo) {
+        if (lo & 1) a[lo] = uint16_t((lo & 2 ? (lo & 4 ? w[3] : w[1]) : (lo & 4 ? w[2] : w[0])) >> 16);
+        const int e = (lo + 1) & ~1;             // even
+        if (e & 2) *reinterpret_cast<uint32_t*>(a + e) = e & 4 ? w[3] : w[1];
+        const int f = (e + 3) & ~3;              // 0, 4 or 8; 0 only where the window is whole
+        if (f == 4) *reinterpret_cast<uint2*>(a + 4) = make_uint2(w[2], w[3]);
+    }
+    __device__ __forceinline__ static void head(uint16_t* a, const uint32_t (&w)[4], int hi) {
+        if (hi & 4) *reinterpret_cast<uint2*>(a) = make_uint2(w[0], w[1]);
+        if (hi & 2) *reinterpret_cast<uint32_t*>(a + (hi & 4)) = hi & 4 ? w[2] : w[0];
+        if (hi & 1) a[hi & 6] = uint16_t(hi & 4 ? (hi & 2 ? w[3] : w[2]) : (hi & 2 ? w[1] : w[0]));
+    }
+    __device__ __forceinline__ void put(const float (&v)[16]) {
+        uint32_t t[12];                          // the elements shifted o up: by half a word, 1 word, 2 words
+        uint32_t prev = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t x = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+            t[i] = o & 1 ? __funnelshift_l(prev, x, 16) : x;
+            prev = x;
+        }
+        t[8] = o & 1 ? prev >> 16 : 0;
+        t[9] = t[10] = t[11] = 0;
+#pragma unroll
+        for (int i = 11; i >= 0; --i) {
+            if (i <= 9) t[i] = o & 2 ? (i >= 1 ? t[i - 1] : 0) : t[i];
+        }
+#pragma unroll
+        for (int i = 11; i >= 0; --i) t[i] = o & 4 ? (i >= 2 ? t[i - 2] : 0) : t[i];
+        const uint32_t w0[4] = {t[0] | carry[0], t[1] | carry[1], t[2] | carry[2], t[3] | carry[3]};
+        if (first && o) tail(at, w0, o);
+        else stu4(at, make_uint4(w0[0], w0[1], w0[2], w0[3]));
+        stu4(at + 8, make_uint4(t[4], t[5], t[6], t[7]));
+        carry[0] = t[8]; carry[1] = t[9]; carry[2] = t[10]; carry[3] = t[11];
+        at += 16;
+        first = false;
+    }
+    __device__ __forceinline__ void end() {
+        if (!first && o) head(at, carry, o);
+    }
+};
+
 // The epilogue straight from the accumulators, a lane per row: no trip through shared memory,
-// whose bandwidth the products of a CTA pair use up.  For bf16 results of persistent tiles with
-// 32-byte aligned rows: an access of a warp touches 32 lines whatever its width, so these take
-// whole 32-byte sectors.  The warp takes units of 32 columns, 64 apart from col0 on, while they
-// lie wholly inside the matrix, NU at most, and returns how many; a unit's two halves are read
-// (residual, pre-activation) while the unit before it is computed.  dcol: the generator's
-// column products of the units' columns, in shared memory; dr: the lane's row's.
-template <int MODE, int EP, int NU>
+// whose bandwidth the products of a CTA pair use up.  For bf16 results of persistent tiles.  An
+// access of a warp touches 32 lines whatever its width, so rows aligned to 32 bytes (ALIGNED)
+// are read and written by whole 32-byte sectors; rows that start anywhere by whole 16-byte
+// windows, the elements shifted into place in registers (through shared memory and by single
+// elements, a lane per column, the tile took 30,000 clocks).  The warp takes units of 32
+// columns, STEP apart from col0 on, while they lie wholly inside the matrix, NU at most, and
+// returns how many; a unit's two halves are read (residual, pre-activation) while the unit before it is
+// computed.  dcol: the generator's column products of the units' columns, in shared memory;
+// dr: the lane's row's.
+template <int MODE, int EP, int NU, bool ALIGNED>
 struct RowsEmit {
+    using In = typename std::conditional<ALIGNED, Raw16, Win16>::type;
+    static constexpr int STEP = ALIGNED ? 64 : 32;
     uint16_t* out;
     const uint16_t* add;
     uint16_t* z;
     const uint16_t* bias;
     int units;
     bool in;
-    Raw16 aq[2], zq[2];
+    In aq[2], zq[2];
+
+    __device__ __forceinline__ static In load(const uint16_t* p) {
+        if constexpr (ALIGNED) return load_raw16(p);
+        else return load_win16(p);
+    }
+    __device__ __forceinline__ static void value(const In& r, const uint16_t* p, float (&v)[16]) {
+        if constexpr (ALIGNED) widen(r, v);
+        else widen(r, window_offset(p), v);      // the same for all groups of a row: 16 elements are two windows
+    }
 
     // Before the accumulators are there: the first unit's reads.
     __device__ __forceinline__ void begin(const LinEpi& ep, int64_t row, int64_t col0) {
         in = row < ep.rows;
         const int64_t left = ep.cols - col0;
-        units = left < 32 ? 0 : (left - 32) / 64 + 1 < NU ? int((left - 32) / 64 + 1) : NU;
+        units = left < 32 ? 0 : (left - 32) / STEP + 1 < NU ? int((left - 32) / STEP + 1) : NU;
         out = static_cast<uint16_t*>(ep.out) + row * ep.ldo + col0;
         add = MODE == kWgrad ? (ep.accumulate ? out : nullptr)
               : ep.residual  ? static_cast<const uint16_t*>(ep.residual) + row * ep.ldr + col0
@@ -448,15 +550,20 @@ struct RowsEmit {
         bias = MODE == kForward && ep.bias ? static_cast<const uint16_t*>(ep.bias) + col0 : nullptr;
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
-            aq[g] = zq[g] = Raw16{};
-            if (add && in && units > 0) aq[g] = load_raw16(add + 16 * g);
-            if (MODE == kDgrad && z && in && units > 0) zq[g] = load_raw16(z + 16 * g);
+            aq[g] = zq[g] = In{};
+            if (add && in && units > 0) aq[g] = load(add + 16 * g);
+            if (MODE == kDgrad && z && in && units > 0) zq[g] = load(z + 16 * g);
         }
     }
 
     __device__ __forceinline__ int run(const LinEpi& ep, uint32_t acc, const DropRow& dr, const DropCol* dcol) {
         const int act = EP >= 0 ? EP & 3 : ep.act;
         const bool drop = MODE != kWgrad && (EP >= 0 ? EP >= 4 : ep.drop.on != 0);
+        WinOut wo, wz;
+        if constexpr (!ALIGNED) {
+            wo.begin(out);
+            if (MODE == kForward && z) wz.begin(z);
+        }
         Acc16 next;                                              // the accumulators of the half to come
         if (units > 0) tmem_ld16_async(acc, next);
 #pragma unroll 1
@@ -464,22 +571,29 @@ struct RowsEmit {
             const bool more = in && u + 1 < units;
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
-                const int c = 64 * u + 16 * g;
+                const int c = STEP * u + 16 * g;
                 float v[16], t[16];
                 tmem_wait_ld16(next, v);
-                if (g == 0) tmem_ld16_async(acc + c + 16, next);
-                else if (u + 1 < units) tmem_ld16_async(acc + c + 48, next);
+                if (g == 0 || u + 1 < units) tmem_ld16_async(acc + c + (g == 0 ? 16 : STEP - 16), next);
                 if constexpr (MODE == kForward) {
                     if (bias) {
-                        float b[8];
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            widen(load_raw(bias + c + 8 * h), b);
+                            float b[8];
+                            if constexpr (ALIGNED) {
+                                widen(load_raw(bias + c + 8 * h), b);
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) b[i] = load1(bias + c + 8 * h + i);
+                            }
 #pragma unroll
                             for (int i = 0; i < 8; ++i) v[8 * h + i] += b[i];
                         }
                     }
-                    if (z && in) store16(z + c, v);
+                    if (z && in) {
+                        if constexpr (ALIGNED) store16(z + c, v);
+                        else wz.put(v);
+                    }
                     activate<true, 16>(v, act);
                 }
                 if (drop) {
@@ -495,18 +609,27 @@ struct RowsEmit {
                 }
                 if constexpr (MODE == kDgrad) {
                     if (z) {
-                        widen(zq[g], t);
-                        if (more) zq[g] = load_raw16(z + c + 64);
+                        value(zq[g], z, t);
+                        if (more) zq[g] = load(z + c + STEP);
                         activate_grad<true, 16>(v, t, act);
                     }
                 }
                 if (add) {
-                    widen(aq[g], t);
-                    if (more) aq[g] = load_raw16(add + c + 64);
+                    value(aq[g], add, t);
+                    if (more) aq[g] = load(add + c + STEP);
 #pragma unroll
                     for (int i = 0; i < 16; ++i) v[i] += t[i];
                 }
-                if (in) store16(out + c, v);
+                if (in) {
+                    if constexpr (ALIGNED) store16(out + c, v);
+                    else wo.put(v);
+                }
+            }
+        }
+        if constexpr (!ALIGNED) {
+            if (in) {
+                wo.end();
+                if (MODE == kForward && z) wz.end();
             }
         }
         return units;
@@ -671,7 +794,7 @@ struct RowSum {
 // (3 planes: six products, of the terms whose exponents add up to at most two steps); CH:
 // K steps after which the accumulators are added to fp32 registers (0: never).  SPLIT: the
 // CTAs of a cluster (2, 4 or 8, CG = 1) take a share of K each and join through shared memory.
-template <int MODE_, typename OT_, int CG_, int BN_, int PL_, int CH_, bool SPLIT_, int EP_ = -1>
+template <int MODE_, typename OT_, int CG_, int BN_, int PL_, int CH_, bool SPLIT_, int EP_ = -1, bool ANY_ = false>
 struct LinCfg {
     using OT = OT_;
     static constexpr int MODE = MODE_, CG = CG_, BN = BN_, PL = PL_, CH = CH_, EP = EP_;
@@ -683,7 +806,10 @@ struct LinCfg {
     static constexpr bool ROWS_M = MODE == kWgrad || !SPLIT;
     static constexpr bool A_MN = MODE == kWgrad || (MODE == kDgrad && !ROWS_M);
     static constexpr bool B_MN = MODE == kWgrad || (MODE == kDgrad && ROWS_M);
-    static constexpr bool REGS = CH != 0 && !SPLIT;                         // sums of a whole tile in registers
+    static constexpr bool REGS = !SPLIT;                                    // see setmaxnreg below
+    // ANY: rows of the epilogue's matrices start anywhere, else (DIRECT) they are aligned to 32
+    // bytes; kernels of their own, since one with both forms was 6 % slower for its code's size.
+    static constexpr bool ANY = ANY_;
     static constexpr bool DIRECT = !SPLIT && CH == 0 && sizeof(OT) == 2;    // RowsEmit where rows are aligned
     static constexpr int AHEAD = 1;
     static constexpr int BROWS = BN / CG;                        // B rows a CTA loads
@@ -944,9 +1070,12 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
         else if constexpr (C::REGS) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         // ---- epilogue ----
         // Warp w reads TMEM lanes 32 (w mod 4) on: rows 32 q of the CTA's part of the tile; the
-        // two halves of the warps take alternate groups of 32 columns.
+        // two halves of the warps take alternate groups of 32 columns, so that they write a line of
+        // 128 bytes at about the same time; where rows are not aligned (RowsEmit's windows run on
+        // from group to group) half of the columns each.
         const int q = warp & 3, half = warp >> 2;
         constexpr int NJ = (C::BN + 63) / 64;                // groups of 32 columns per warp
+        auto group = [&](int jj) { return C::DIRECT && C::ANY ? half * NJ + jj : 2 * jj + half; };
         bool ok = true;
         uint32_t ac = 0;
         for (int t = cluster; ok && t < n_tiles; t += n_clusters) {
@@ -963,11 +1092,11 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
             }
             UnitEmit<C::MODE, typename C::OT, C::AHEAD, C::EP> io;
             auto begin = [&](int jj) {
-                const int64_t n = n0 + (2 * jj + half) * 32;
+                const int64_t n = n0 + group(jj) * 32;
                 if constexpr (!C::SPLIT) io.begin(ep, C::ROWS_M ? m0 : n, C::ROWS_M ? n : m0, lane);
             };
             auto finish = [&](int jj, const float (&v)[32]) {
-                const int j = 2 * jj + half;                 // this group of 32 columns
+                const int j = group(jj);                     // this group of 32 columns
                 if constexpr (C::SPLIT) {
                     const uint32_t u = 4 * j + q;            // unit u joins in CTA u mod splits
                     const uint32_t slot = (u / sh.splits) * sh.splits + rank;
@@ -997,11 +1126,9 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
             };
             for (int kc = kb0; ok && kc < kb1; kc += chunk, ++ac) {
                 const uint32_t buf = ac & 1;
-                RowsEmit<C::MODE, C::EP, NJ> rows;           // of direct tiles
-                bool direct = C::DIRECT && ep.vec == 2;
-                if constexpr (C::DIRECT) {
-                    if (direct) rows.begin(ep, m0 + lane, n0 + half * 32);
-                }
+                RowsEmit<C::MODE, C::EP, NJ, !C::ANY> rows;
+                bool direct = C::DIRECT;
+                if constexpr (C::DIRECT) rows.begin(ep, m0 + lane, n0 + group(0) * 32);
                 ok = __all_sync(0xffffffffu, mbar_wait_bounded(acc_full + 8 * buf, (ac >> 1) & 1, wait_ns));
                 if (!ok) break;
                 tc_fence_after();
@@ -1018,25 +1145,24 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
                         dr = drop_row(ep.drop, uint32_t(r0) + lane, __umulhi(0xCD9E8D57u, hi));
                         __syncwarp();
                         if (lane < NJ * 8)
-                            dcol[lane] = drop_col(ep.drop, uint32_t((n0 + (2 * (lane >> 3) + half) * 32) >> 2) + (lane & 7), hi);
+                            dcol[lane] = drop_col(ep.drop, uint32_t((n0 + group(lane >> 3) * 32) >> 2) + (lane & 7), hi);
                         __syncwarp();
                     }
                 }
                 int done = 0;                                // units of the direct path
                 if constexpr (C::DIRECT) {
-                    if (direct)
-                        done = m0 >= ep.rows ? NJ : rows.run(ep, src + half * 32, dr, dcol);
+                    if (direct) done = m0 >= ep.rows ? NJ : rows.run(ep, src + group(0) * 32, dr, dcol);
                 }
                 constexpr int kUnrollUnits = C::CH != 0 ? NJ : 1;
 #pragma unroll kUnrollUnits
                 for (int jj = C::DIRECT ? done : 0; jj < NJ; ++jj) {
-                    if ((2 * jj + half) * 32 < C::BN) {
+                    if (group(jj) * 32 < C::BN) {
                         if constexpr (C::CH != 0) {
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
                                 Acc16 a;
                                 float v[16];
-                                tmem_ld16_async(src + (2 * jj + half) * 32 + 16 * h, a);
+                                tmem_ld16_async(src + group(jj) * 32 + 16 * h, a);
                                 tmem_wait_ld16(a, v);
 #pragma unroll
                                 for (int i = 0; i < 16; ++i) sum[jj][16 * h + i] += v[i];
@@ -1044,7 +1170,7 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
                         } else {
                             float v[32];
                             begin(jj);
-                            tmem_ld32(src + (2 * jj + half) * 32, v);
+                            tmem_ld32(src + group(jj) * 32, v);
                             finish(jj, v);
                         }
                     }
@@ -1064,7 +1190,7 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
                 }
 #pragma unroll
                 for (int jj = 0; jj < NJ; ++jj)
-                    if (ok && !whole && (2 * jj + half) * 32 < C::BN) {
+                    if (ok && !whole && group(jj) * 32 < C::BN) {
                         begin(jj);
                         finish(jj, sum[jj]);
                     }
@@ -1274,9 +1400,10 @@ float estimate(const LinProblem& p, int splits, int dev, LinCost c) {
 // columns, 4 CTAs per tile), where one CTA per tile takes 9.8 and 8 CTAs, two waves of
 // clusters, 9.3.
 //
-// For bf16 results the pair configurations are compiled for each activation and dropout
-// (launch_pair, in a translation unit of its own); the others take them at run time: split
-// tiles run their epilogue once, and fp32 tiles have six times the products to run it beside.
+// For bf16 results with aligned rows the pair configurations are compiled for each activation
+// and dropout (launch_pair, in a translation unit of its own); the others take them at run
+// time: split tiles run their epilogue once, and fp32 tiles have six times the products to run
+// it beside.
 template <int MODE, typename OT, int PL, int CH>
 cudaError_t launch_product(const LinProblem& p, cudaError_t (*launch_pair)(const LinProblem&, int, cudaStream_t), cudaStream_t st) {
     int dev = 0;
@@ -1320,10 +1447,10 @@ cudaError_t launch_product(const LinProblem& p, cudaError_t (*launch_pair)(const
     return cudaErrorInvalidValue;
 }
 
-template <int MODE, typename OT, int PL, int CH, int EP = -1>
+template <int MODE, typename OT, int PL, int CH, int EP = -1, bool ANY = false>
 cudaError_t launch_pair_as(const LinProblem& p, int bn, cudaStream_t st) {
-    return bn == 256 ? launch_cfg<LinCfg<MODE, OT, 2, 256, PL, CH, false, EP>>(p, 1, st)
-                     : launch_cfg<LinCfg<MODE, OT, 2, 128, PL, CH, false, EP>>(p, 1, st);
+    return bn == 256 ? launch_cfg<LinCfg<MODE, OT, 2, 256, PL, CH, false, EP, ANY>>(p, 1, st)
+                     : launch_cfg<LinCfg<MODE, OT, 2, 128, PL, CH, false, EP, ANY>>(p, 1, st);
 }
 
 }  // namespace

@@ -37,7 +37,9 @@ cudaError_t join(const float* part, const float* db_part, int parts, int64_t row
 // The pair kernels, and the join of db's partial sums.
 template <typename OT, int PL, int CH>
 cudaError_t launch_pair_wgrad(const LinProblem& p, int bn, cudaStream_t st) {
-    const cudaError_t e = launch_pair_as<kWgrad, OT, PL, CH>(p, bn, st);
+    cudaError_t e;
+    if (CH == 0 && p.epi.vec != 2) e = launch_pair_as<kWgrad, OT, PL, CH, -1, CH == 0>(p, bn, st);
+    else e = launch_pair_as<kWgrad, OT, PL, CH>(p, bn, st);
     if (e != cudaSuccess || !p.epi.db || p.epi.db_parts <= 1) return e;
     return join<OT>(nullptr, p.epi.db_sums, p.epi.db_parts, p.epi.rows, 0, 0, p.epi, st);
 }
