@@ -66,8 +66,11 @@ int row_class(const void* p, int64_t ld, int esize) {
 
 int64_t round_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 
-// Elements of one packed plane, and bytes of a packed operand.
-int64_t plane_elems(int64_t rows, int64_t cols) { return rows * round_up(cols, 8); }
+// Elements of a packed row (whole lines of 128 bytes, so that a box row of 64 elements is one
+// line: with rows of 16-byte multiples, each is two, and 4000 x 4001 x 4001 took 120 us instead
+// of 91), of one packed plane, and bytes of a packed operand.
+int64_t packed_ld(int64_t cols) { return round_up(cols, 64); }
+int64_t plane_elems(int64_t rows, int64_t cols) { return rows * packed_ld(cols); }
 int64_t packed_bytes(int64_t rows, int64_t cols, int planes) { return round_up(planes * plane_elems(rows, cols) * 2, 256); }
 
 // The operands of a product: a matrix that the tensor maps can read where it is, or its
@@ -86,7 +89,7 @@ struct Packer {
         const int planes = dtype == FSDP_F32 ? 3 : 1;
         const int64_t need = packed_bytes(rows, cols, planes);
         if (!ws || left < size_t(need)) return FSDP_EINVAL;
-        const int64_t dld = round_up(cols, 8), plane = plane_elems(rows, cols);
+        const int64_t dld = packed_ld(cols), plane = plane_elems(rows, cols);
         jobs[n++] = PackJob{p, rows, cols, ld, ws, dld, plane};
         *o = LinOperand{ws, rows, cols, dld, plane};
         ws += need;

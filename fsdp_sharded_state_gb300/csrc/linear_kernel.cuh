@@ -206,16 +206,14 @@ __device__ __forceinline__ void emit_db(const LinEpi& ep, int64_t c, float t) {
 // holds a column) and the row-wise reads are free of bank conflicts.
 __device__ __forceinline__ int unit_at(int r, int c) { return r * 32 + ((((c >> 2) ^ (r & 7)) << 2) | (c & 3)); }
 
-// The epilogue of one unit: 4 lanes per row, 8 columns per lane, 8 rows at a time.  What it
-// reads of memory (the addend: the residual, or what wgrad accumulates to; the
-// pre-activation) is asked for AHEAD steps ahead, the first ones by begin(), which a caller
-// runs before it fetches the accumulators: with one step ahead, the reads of a 256 x 256
-// tile's residual cost 10,000 clocks of latency.
-// EP: the activation (+ 4 with dropout) that the kernel is compiled for, or -1 for the
-// call's.  Jumping over what a call does not use costs more than computing it: the loop
-// outgrows the innermost instruction cache, and a unit with neither took 2,150 clocks with
-// EP = -1 where 1,150 do.
-template <int MODE, typename OT, int AHEAD, int EP>
+// The epilogue of one unit from shared memory: 4 lanes per row, 8 columns per lane, 8 rows at a
+// time; what it reads of memory (the addend: the residual, or what wgrad accumulates to; the
+// pre-activation) one step of 8 rows ahead, the first step by begin(), which a caller runs
+// before it fetches the accumulators.  EP: the activation (+ 4 with dropout) that the kernel is
+// compiled for, or -1 for the call's.  Jumping over what a call does not use costs more than
+// computing it: the loop outgrows the innermost instruction cache, and a unit with neither took
+// 2,150 clocks with EP = -1 where 1,150 do.
+template <int MODE, typename OT, int EP>
 struct UnitEmit {
     static constexpr bool FAST = sizeof(OT) == 2;
     static __device__ __forceinline__ int act(const LinEpi& ep) { return EP >= 0 ? EP & 3 : ep.act; }
@@ -225,7 +223,7 @@ struct UnitEmit {
     OT* z;
     int64_t add_step, z_step, row0, col0, shift;
     int n_it;                                    // steps of 8 rows; -1: not by vectors
-    Raw8<OT> aq[AHEAD], zq[AHEAD];
+    Raw8<OT> aq, zq;
 
     // shift: rows that out starts further down (a slab of partial sums)
     __device__ __forceinline__ void begin(const LinEpi& ep, int64_t row0_, int64_t col0_, int lane, int64_t shift_ = 0) {
@@ -243,11 +241,8 @@ struct UnitEmit {
         add_step = 8 * (MODE == kWgrad ? ep.ldo : ep.ldr);
         z = MODE != kWgrad && ep.preact ? static_cast<OT*>(ep.preact) + row1 * ep.ldz + col : nullptr;
         z_step = 8 * ep.ldz;
-#pragma unroll
-        for (int i = 0; i < AHEAD; ++i) {
-            if (add && i < n_it) aq[i] = load_raw(add + i * add_step);
-            if (MODE == kDgrad && z && i < n_it) zq[i] = load_raw(z + i * z_step);
-        }
+        if (add && n_it > 0) aq = load_raw(add);
+        if (MODE == kDgrad && z && n_it > 0) zq = load_raw(z);
     }
 
     // Adds the `slots` copies of the unit (kUnitFloats apart, in order) and emits it.
@@ -274,15 +269,10 @@ struct UnitEmit {
                 b.x += d.x; b.y += d.y; b.z += d.z; b.w += d.w;
             }
             float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-            const Raw8<OT> add_c = aq[0], z_c = zq[0];
-#pragma unroll
-            for (int i = 0; i + 1 < AHEAD; ++i) {
-                aq[i] = aq[i + 1];
-                zq[i] = zq[i + 1];
-            }
-            if (it + AHEAD < n_it) {
-                if (add) aq[AHEAD - 1] = load_raw(add + (it + AHEAD) * add_step);
-                if (MODE == kDgrad && z) zq[AHEAD - 1] = load_raw(z + (it + AHEAD) * z_step);
+            const Raw8<OT> add_c = aq, z_c = zq;
+            if (it + 1 < n_it) {
+                if (add) aq = load_raw(add + (it + 1) * add_step);
+                if (MODE == kDgrad && z) zq = load_raw(z + (it + 1) * z_step);
             }
             if constexpr (MODE == kForward) {
 #pragma unroll
@@ -800,9 +790,9 @@ struct LinCfg {
     static constexpr int MODE = MODE_, CG = CG_, BN = BN_, PL = PL_, CH = CH_, EP = EP_;
     static constexpr bool SPLIT = SPLIT_;
     // Which of out's axes runs along M.  A split tile of forward or dgrad has the features
-    // there, so that few rows need few columns of the tile; the others have out's rows, which
-    // a lane then holds 32 consecutive columns of (wider stores to shared memory: 1,150 clocks
-    // for a unit against 2,200 with a column per lane).
+    // there, so that few rows need few columns of the tile; the others have out's rows, of which
+    // a lane then holds consecutive columns (a unit through shared memory took 1,150 clocks,
+    // 2,200 with a column per lane).
     static constexpr bool ROWS_M = MODE == kWgrad || !SPLIT;
     static constexpr bool A_MN = MODE == kWgrad || (MODE == kDgrad && !ROWS_M);
     static constexpr bool B_MN = MODE == kWgrad || (MODE == kDgrad && ROWS_M);
@@ -811,7 +801,6 @@ struct LinCfg {
     // bytes; kernels of their own, since one with both forms was 6 % slower for its code's size.
     static constexpr bool ANY = ANY_;
     static constexpr bool DIRECT = !SPLIT && CH == 0 && sizeof(OT) == 2;    // RowsEmit where rows are aligned
-    static constexpr int AHEAD = 1;
     static constexpr int BROWS = BN / CG;                        // B rows a CTA loads
     static constexpr int A_BYTES = 128 * 128, B_BYTES = BROWS * 128;
     static constexpr int STAGE = PL * (A_BYTES + B_BYTES);
@@ -1090,7 +1079,7 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
 #pragma unroll
                     for (int i = 0; i < 32; ++i) sum[j][i] = 0.f;
             }
-            UnitEmit<C::MODE, typename C::OT, C::AHEAD, C::EP> io;
+            UnitEmit<C::MODE, typename C::OT, C::EP> io;
             auto begin = [&](int jj) {
                 const int64_t n = n0 + group(jj) * 32;
                 if constexpr (!C::SPLIT) io.begin(ep, C::ROWS_M ? m0 : n, C::ROWS_M ? n : m0, lane);
@@ -1210,7 +1199,7 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
             for (int u = int(rank) + warp * sh.splits; u < C::BN / 8; u += kEpiWarps * sh.splits) {
                 const int q = u & 3, j = u >> 2;
                 const int64_t m0 = int64_t(mt) * 128 + q * 32, n0 = int64_t(nt) * C::BN + j * 32;
-                UnitEmit<C::MODE, typename C::OT, C::AHEAD, C::EP> io;
+                UnitEmit<C::MODE, typename C::OT, C::EP> io;
                 io.begin(ep, C::ROWS_M ? m0 : n0, C::ROWS_M ? n0 : m0, lane, C::MODE == kWgrad ? slab * ep.rows : 0);
                 io.run(ep, epi_smem + (u / sh.splits) * sh.splits * kUnitFloats, sh.splits, lane);
             }

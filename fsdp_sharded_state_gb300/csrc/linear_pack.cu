@@ -36,44 +36,81 @@ __device__ __forceinline__ void split3(float x, uint32_t (&t)[3]) {
     t[2] = term(r - bf16f(uint16_t(t[1])));
 }
 
-// A thread: 8 destination columns of one row (a whole 16-byte group; past the last column 0).
+// The terms of two neighbours, packed.  Values whose high term would round to an infinity, and
+// infinities and NaNs themselves, go through split3.
+__device__ __forceinline__ void split3_pair(float a, float b, uint32_t& t0, uint32_t& t1, uint32_t& t2) {
+    const uint32_t big = 0x7f7f8000u;
+    if ((__float_as_uint(a) & 0x7fffffffu) >= big || (__float_as_uint(b) & 0x7fffffffu) >= big) {
+        uint32_t x[3], y[3];
+        split3(a, x);
+        split3(b, y);
+        t0 = x[0] | y[0] << 16;
+        t1 = x[1] | y[1] << 16;
+        t2 = x[2] | y[2] << 16;
+        return;
+    }
+    t0 = pack_bf16x2(a, b);
+    a -= bf16lo(t0);
+    b -= bf16hi(t0);
+    t1 = pack_bf16x2(a, b);
+    t2 = pack_bf16x2(a - bf16lo(t1), b - bf16hi(t1));
+}
+
+// A thread: 8 destination columns (a whole 16-byte group; past the last column 0) of kPackRows
+// rows, their loads first.
+constexpr int kPackRows = 4;
+
 template <bool F32>
-__global__ void __launch_bounds__(kPackThreads) k_pack(const PackJobs jobs) {
+__global__ void __launch_bounds__(kPackThreads) k_pack(const __grid_constant__ PackJobs jobs) {
     const int which = blockIdx.x >= jobs.first[1];
     const PackJob& j = jobs.j[which];
     pdl_wait();
-    const int64_t groups = j.dld / 8;
+    const uint32_t groups = uint32_t((j.cols + 7) / 8);
     const int64_t i = (int64_t(blockIdx.x) - jobs.first[which]) * kPackThreads + threadIdx.x;
-    const int64_t r = i / groups, c = (i - r * groups) * 8;
-    if (r >= j.rows) return;
-    const int n = j.cols - c >= 8 ? 8 : int(j.cols - c);
-    uint16_t* const dst = static_cast<uint16_t*>(j.dst) + r * j.dld + c;
+    const int64_t quad = i / groups, r0 = quad * kPackRows, c = (i - quad * groups) * 8;
+    if (r0 >= j.rows) return;
+    const int n = j.cols - c >= 8 ? 8 : int(j.cols - c), rows = j.rows - r0 < kPackRows ? int(j.rows - r0) : kPackRows;
+    uint16_t* const dst = static_cast<uint16_t*>(j.dst) + r0 * j.dld + c;
     if constexpr (F32) {
-        const float* const p = static_cast<const float*>(j.src) + r * j.ld + c;
-        float x[8];
-        if (n == 8 && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
-            const float4 a = ld4(p), b = ld4(p + 4);
-            x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-        } else {
+        const float* const p = static_cast<const float*>(j.src) + r0 * j.ld + c;
+        float x[kPackRows][8];
+        const bool vec = n == 8 && ((reinterpret_cast<uintptr_t>(p) | uintptr_t(j.ld * 4)) & 15) == 0;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) x[k] = k < n ? p[k] : 0.f;
-        }
-        uint32_t w[3][4] = {};
+        for (int r = 0; r < kPackRows; ++r) {
+            if (r >= rows) break;
+            if (vec) {
+                const float4 a = ld4(p + r * j.ld), b = ld4(p + r * j.ld + 4);
+                x[r][0] = a.x; x[r][1] = a.y; x[r][2] = a.z; x[r][3] = a.w;
+                x[r][4] = b.x; x[r][5] = b.y; x[r][6] = b.z; x[r][7] = b.w;
+            } else {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            uint32_t t[3];
-            split3(x[k], t);
-#pragma unroll
-            for (int s = 0; s < 3; ++s) w[s][k / 2] |= t[s] << (16 * (k & 1));
+                for (int k = 0; k < 8; ++k) x[r][k] = k < n ? p[r * j.ld + k] : 0.f;
+            }
         }
 #pragma unroll
-        for (int s = 0; s < 3; ++s) stu4(dst + s * j.plane, make_uint4(w[s][0], w[s][1], w[s][2], w[s][3]));
+        for (int r = 0; r < kPackRows; ++r) {
+            if (r >= rows) break;
+            uint32_t w[3][4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) split3_pair(x[r][2 * k], x[r][2 * k + 1], w[0][k], w[1][k], w[2][k]);
+#pragma unroll
+            for (int s = 0; s < 3; ++s) stu4(dst + s * j.plane + r * j.dld, make_uint4(w[s][0], w[s][1], w[s][2], w[s][3]));
+        }
     } else {
-        const uint16_t* const p = static_cast<const uint16_t*>(j.src) + r * j.ld + c;
-        uint32_t w[4] = {};
+        const uint16_t* const p = static_cast<const uint16_t*>(j.src) + r0 * j.ld + c;
+        uint32_t x[kPackRows][8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) w[k / 2] |= (k < n ? uint32_t(p[k]) : 0u) << (16 * (k & 1));
-        stu4(dst, make_uint4(w[0], w[1], w[2], w[3]));
+        for (int r = 0; r < kPackRows; ++r) {
+            if (r >= rows) break;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[r][k] = k < n ? uint32_t(p[r * j.ld + k]) : 0u;
+        }
+#pragma unroll
+        for (int r = 0; r < kPackRows; ++r) {
+            if (r >= rows) break;
+            stu4(dst + r * j.dld, make_uint4(x[r][0] | x[r][1] << 16, x[r][2] | x[r][3] << 16, x[r][4] | x[r][5] << 16,
+                                             x[r][6] | x[r][7] << 16));
+        }
     }
 }
 
@@ -85,7 +122,7 @@ cudaError_t launch_pack(const PackJob* jobs, int n, bool f32, cudaStream_t st) {
     for (int k = 0; k < 2; ++k) {
         if (k < n) pj.j[k] = jobs[k];
         pj.first[k] = total;
-        if (k < n) total += (jobs[k].rows * (jobs[k].dld / 8) + kPackThreads - 1) / kPackThreads;
+        if (k < n) total += ((jobs[k].rows + kPackRows - 1) / kPackRows * ((jobs[k].cols + 7) / 8) + kPackThreads - 1) / kPackThreads;
     }
     pj.first[2] = total;
     if (n < 2) pj.first[1] = total;

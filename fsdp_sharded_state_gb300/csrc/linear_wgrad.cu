@@ -74,7 +74,7 @@ cudaError_t launch_wgrad_slabs(const LinProblem& p, cudaStream_t st) {
     q.epi.ldo = ld;
     q.epi.db = p.epi.db ? p.partial + p.slabs * rows * ld : nullptr;
     q.epi.accumulate = 0;
-    q.epi.vec = 2;
+    q.epi.vec = 1;
     cudaError_t e = p.planes == 3 ? launch_cfg<LinCfg<kWgrad, float, 1, 64, 3, 2, true>>(q, kSlabSplits, st, p.slabs)
                                   : launch_cfg<LinCfg<kWgrad, float, 1, 64, 1, 8, true>>(q, kSlabSplits, st, p.slabs);
     if (e != cudaSuccess) return e;

@@ -315,3 +315,42 @@ def test_few_rows(rows, cin, cout, offset, dtype):
     want = lu.drop64(h, spec) * lu.act_grad64(x.double(), "silu")
     lu.check(dx, want, 1.13 / 0.6 * lu.product_bound(cout, M, dtype) + 2.0 ** -20 * 2 * h.abs(), "dx")
     assert lu.untouched(dx, xbuf)
+
+
+def test_offsets_past_32_bits():
+    """Outputs of more than 2^31 elements: the last rows against the same rows computed alone."""
+    rows, cin, cout = 70000, 64, 32000
+    g = lu.gen(41)
+    x, w = lu.matrix(rows, cin, BF16, 1.0, g), lu.matrix(cout, cin, BF16, 0.1, g)
+    spec = fs.DropoutSpec(0.2, 11, 3)
+    y = torch.empty(rows, cout, dtype=BF16, device="cuda")
+    fs.fsdp_linear_forward(x, w, y, act="gelu", dropout=spec)
+    part = torch.empty(300, cout, dtype=BF16, device="cuda")
+    fs.fsdp_linear_forward(x[-300:], w, part, act="gelu", dropout=fs.DropoutSpec(0.2, 11, 3, row0=rows - 300))
+    fs.fsdp_check_status()
+    assert torch.equal(y[-300:] == 0, part == 0)
+    assert (y[-300:].float() - part.float()).abs().max() <= 2.0 ** -6 * part.float().abs().max()
+    z = torch.empty_like(y)
+    fs.fsdp_dropout(y, z, spec)
+    small = torch.empty_like(part)
+    fs.fsdp_dropout(y[-300:], small, fs.DropoutSpec(0.2, 11, 3, row0=rows - 300))
+    fs.fsdp_check_status()
+    assert torch.equal(z[-300:], small)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_views_of_wide_buffers(dtype):
+    """Operands and results as column ranges of wider matrices, weights as a view of a flat
+    buffer at an odd element."""
+    g = lu.gen(42)
+    big = lu.matrix(900, 1500, dtype, 1.0, g)
+    x, res = big[:, 100:612], big[:, 700:1100]
+    flat = lu.matrix(1, 400 * 512 + 3, dtype, 0.05, g)[0]
+    w = flat[3:].view(400, 512)
+    out = torch.full((900, 1000), 7.0, dtype=dtype, device="cuda")
+    y = out[:, 333:733]
+    fs.fsdp_linear_forward(x, w, y, residual=res, workspace=lu.workspace(900, 512, 400, dtype))
+    fs.fsdp_check_status()
+    want, z, bound = lu.forward64(x, w, None, "none", None, res)
+    lu.check(y, want, bound + 2.0 ** -20 * (z.abs() + res.double().abs()), "y")
+    assert (out[:, :333] == 7).all() and (out[:, 733:] == 7).all()
