@@ -416,8 +416,7 @@ def fsdp_accumulate_reduce_scatter_adamw(layout: Layout, unit_begin: int, unit_e
                                                       _ptr_array(micro), micro_dtype, _ptr(master), _ptr(exp_avg),
                                                       _ptr(exp_avg_sq), _ptr(param_shards), _ptr(grad_shard_out),
                                                       C.byref(h), step, _stream(stream)),
-           "fsdp_accumulate_reduce_scatter_adamw", "fsdp_linear_workspace_bytes", "fsdp_linear_forward",
-           "fsdp_linear_dgrad", "fsdp_linear_wgrad", "fsdp_dropout")
+           "fsdp_accumulate_reduce_scatter_adamw")
 
 
 def fsdp_hsdp_reduce_scatter_adamw(layout: Layout, unit_begin: int, unit_end: int, n_groups: int, grad_replicas,
