@@ -1,6 +1,6 @@
 // linear_dgrad.cu -- dx = residual + act'(z) drop(dz w): the input gradient of a linear
 // layer, through the dropout and the activation of the layer before it.
-#include "linear_kernel.cuh"
+#include "linear_launch.cuh"
 
 namespace fsdp {
 

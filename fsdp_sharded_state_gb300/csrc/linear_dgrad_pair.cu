@@ -1,6 +1,6 @@
 // linear_dgrad_pair.cu -- the CTA-pair kernels of dgrad with bf16 results, one per
 // activation, with and without dropout, and one for rows of any alignment.
-#include "linear_kernel.cuh"
+#include "linear_launch.cuh"
 
 namespace fsdp {
 

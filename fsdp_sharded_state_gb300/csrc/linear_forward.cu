@@ -1,6 +1,6 @@
 // linear_forward.cu -- y = residual + drop(act(x w^T + bias)): the forward product of a
 // linear layer and its epilogue.
-#include "linear_kernel.cuh"
+#include "linear_launch.cuh"
 
 namespace fsdp {
 

@@ -1,6 +1,6 @@
 // linear_forward_pair.cu -- the CTA-pair kernels of forward with bf16 results, one per
 // activation, with and without dropout, and one for rows of any alignment.
-#include "linear_kernel.cuh"
+#include "linear_launch.cuh"
 
 namespace fsdp {
 

@@ -4,7 +4,7 @@
 //
 // Bound by the weight's bytes.  Products and sums are fp32; the order of a sum depends on the
 // sizes alone.
-#include "linear_kernel.cuh"
+#include "linear_launch.cuh"
 
 namespace fsdp {
 namespace {

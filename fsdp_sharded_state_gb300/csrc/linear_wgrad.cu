@@ -1,6 +1,6 @@
 // linear_wgrad.cu -- dw (+)= dz^T x, the weight gradient of a linear layer, and db (+)= the
 // column sums of dz.
-#include "linear_kernel.cuh"
+#include "linear_launch.cuh"
 
 namespace fsdp {
 
