@@ -99,6 +99,8 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
     const uint32_t summed = tmem_word + 8;       // wgrad: a stage's dz tile has been added
     static_assert(8 * (3 * kLinMaxStages + 6) <= 256, "barriers");
     float* const db_part = reinterpret_cast<float*>(smem + C::STAGES * C::STAGE + C::EPI + 256);   // SPLIT: [128]
+    // a stage's plane may be loaded again: plane 0 with the stage, planes 1 and 2 earlier
+    auto plane_empty = [&](int p) { return p == 0 ? empty : bars + 768 + 8 * kLinMaxStages * (p - 1); };
     const bool leader = C::CG == 1 || rank == 0;
 
     if (warp == 0) tmem_alloc<C::CG>(tmem_word, C::TMEM);
@@ -107,7 +109,7 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
         tma_prefetch_map(&map_b);
         for (int s = 0; s < C::STAGES; ++s) {
             mbar_init(full + 8 * s, 1);
-            mbar_init(empty + 8 * s, 1);
+            for (int p = 0; p < C::PL; ++p) mbar_init(plane_empty(p) + 8 * s, 1);
             mbar_init(summed + 8 * s, kSumWarps);
         }
         for (int b = 0; b < 2; ++b) {
@@ -165,10 +167,6 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
                 const int n0 = nt * C::BN + (C::CG == 2 ? int(rank) * C::BROWS : 0);
                 for (int kb = kb0; kb < kb1; ++kb, ++it) {
                     const uint32_t s = it % C::STAGES, use = it / C::STAGES;
-                    if (use > 0 && !mbar_wait_bounded(empty + 8 * s, (use - 1) & 1, wait_ns)) {
-                        ok = false;
-                        break;
-                    }
                     if (C::SPLIT && C::MODE == kWgrad && (adding >> s & 1)) {
                         if (!mbar_wait_bounded(summed + 8 * s, parity >> s & 1, wait_ns)) {
                             ok = false;
@@ -178,12 +176,16 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
                         adding ^= 1u << s;
                     }
                     if (C::SPLIT && C::MODE == kWgrad && ep.db && nt == 0) adding |= 1u << s;
-                    if (elect_one()) {
-                        if (leader) mbar_arrive_tx(full + 8 * s, C::CG * C::STAGE);
-                        const uint32_t bar = C::CG == 2 ? map_rank(full + 8 * s, 0) : full + 8 * s;
-                        const uint32_t st = smem_addr(smem + s * C::STAGE);
+                    const uint32_t bar = C::CG == 2 ? map_rank(full + 8 * s, 0) : full + 8 * s;
+                    const uint32_t st = smem_addr(smem + s * C::STAGE);
 #pragma unroll
-                        for (int p = 0; p < C::PL; ++p) {
+                    for (int p = C::PL - 1; p >= 0; --p) {           // in the order in which the products free the planes
+                        if (use > 0 && !mbar_wait_bounded(plane_empty(p) + 8 * s, (use - 1) & 1, wait_ns)) {
+                            ok = false;
+                            break;
+                        }
+                        if (elect_one()) {
+                            if (leader && p == C::PL - 1) mbar_arrive_tx(full + 8 * s, C::CG * C::STAGE);
                             const uint32_t a = st + p * C::A_BYTES, b = st + C::PL * C::A_BYTES + p * C::B_BYTES;
                             if constexpr (C::A_MN) {
                                 tma_load<C::CG>(a, &map_a, m0, kb * kKb, p, bar);
@@ -199,8 +201,9 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
                                 tma_load<C::CG>(b, &map_b, kb * kKb, n0, p, bar);
                             }
                         }
+                        __syncwarp();
                     }
-                    __syncwarp();
+                    if (!ok) break;
                 }
             }
             // the last use of every stage: its MMAs are done (and, in a pair, their arrivals on
@@ -253,6 +256,10 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
                                     for (int k = 0; k < kKb / 16; ++k)
                                         mma_bf16<C::CG>(d, das + pa * (C::A_BYTES / 16) + k * a_step,
                                                         dbs + pb * (C::B_BYTES / 16) + k * b_step, idesc, kb > kc || pr > 0 || k > 0);
+                                    // the low planes are in the first two products alone, the middle ones in the
+                                    // next three: their places can be loaded again before the stage is done
+                                    if (C::PL == 3 && pr == 1) mma_commit<C::CG>(plane_empty(2) + 8 * s);
+                                    if (C::PL == 3 && pr == 4) mma_commit<C::CG>(plane_empty(1) + 8 * s);
                                 }
                                 mma_commit<C::CG>(empty + 8 * s);
                                 if (kb + 1 == ke) mma_commit<C::CG>(acc_full + 8 * buf);
