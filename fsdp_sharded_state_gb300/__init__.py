@@ -450,27 +450,35 @@ def fsdp_zero1_adamw_broadcast(layout: Layout, unit_begin: int, unit_end: int, g
 
 
 # -- layers between the all-gather and the reduce-scatter -------------------------
-def _matrix(x, name: str, rows: int, cols: int, dtype):
-    """(address, row stride) of a 2-D CUDA tensor of the given shape whose rows are contiguous."""
-    if x is None:
-        return None, 0
+def _operand(x, name: str, dtype):
+    """(rows, cols, address, row stride) of a CUDA matrix whose rows are contiguous."""
     if x.dtype is not dtype:
         raise TypeError(f"{name} is {x.dtype}, expected {dtype}")
-    if x.shape != (rows, cols):
-        raise ValueError(f"{name} is {tuple(x.shape)}, expected {(rows, cols)}")
+    if x.dim() != 2:
+        raise ValueError(f"{name} is {tuple(x.shape)}, expected a matrix")
     if not x.is_cuda:
         raise ValueError(f"{name} is not a CUDA tensor")
+    rows, cols = x.shape
     ld, one = x.stride()
     if one != 1 and cols > 1:
         raise ValueError(f"{name}: a row's elements must be contiguous")
     if rows <= 1 and ld < cols:
         ld = cols                                # torch leaves a single row's stride arbitrary
-    return x.data_ptr(), ld
+    return rows, cols, x.data_ptr(), ld
+
+
+def _matrix(x, name: str, rows: int, cols: int, dtype):
+    """(address, row stride) of such a matrix of the given shape."""
+    r, c, p, ld = _operand(x, name, dtype)
+    if r != rows or c != cols:
+        raise ValueError(f"{name} is {tuple(x.shape)}, expected {(rows, cols)}")
+    return p, ld
+
+
+_NO_MATRIX = (None, 0)
 
 
 def _vector(x, name: str, n: int, dtype):
-    if x is None:
-        return None
     if x.dtype is not dtype:
         raise TypeError(f"{name} is {x.dtype}, expected {dtype}")
     if x.shape != (n,):
@@ -482,22 +490,17 @@ def _vector(x, name: str, n: int, dtype):
     return x.data_ptr()
 
 
-def _dims(x, name: str):
-    if x.dim() != 2:
-        raise ValueError(f"{name} is {tuple(x.shape)}, expected a matrix")
-    return x.shape
-
-
 def _act(act) -> int:
-    if isinstance(act, str):
-        if act not in ACTIVATIONS:
+    code = ACTIVATIONS.get(act)
+    if code is None:
+        if isinstance(act, str):
             raise ValueError(f"unknown activation {act!r}: {sorted(ACTIVATIONS)}")
-        return ACTIVATIONS[act]
-    return int(act)
+        code = int(act)
+    return code
 
 
 def _workspace(ws):
-    return (None, 0) if ws is None else (_ptr(ws), ws.numel() * ws.element_size())
+    return (_ptr(ws), ws.numel() * ws.element_size())
 
 
 def _drop(spec):
@@ -520,16 +523,19 @@ def fsdp_linear_forward(x, w, y, bias=None, act="none", preact=None, dropout: Op
     """y = residual + drop(act(x w^T + bias)); z = x w^T + bias into preact where given.
     x [rows, in], w [out, in], y / preact / residual [rows, out], bias [out], one dtype."""
     code, dt = _dtype_code(x), x.dtype
-    (rows, cin), (cout, _) = _dims(x, "x"), _dims(w, "w")
-    px, ldx = _matrix(x, "x", rows, cin, dt)
-    pw, ldw = _matrix(w, "w", cout, cin, dt)
+    rows, cin, px, ldx = _operand(x, "x", dt)
+    cout, wcols, pw, ldw = _operand(w, "w", dt)
+    if wcols != cin:
+        raise ValueError(f"w is {tuple(w.shape)}, expected {(cout, cin)}")
     py, ldy = _matrix(y, "y", rows, cout, dt)
-    pr, ldr = _matrix(residual, "residual", rows, cout, dt)
-    pz, ldz = _matrix(preact, "preact", rows, cout, dt)
-    pws, nws = _workspace(workspace)
-    _check(lib().fsdp_linear_forward(rows, cin, cout, code, px, ldx, pw, ldw, _vector(bias, "bias", cout, dt), _act(act),
-                                     _drop(dropout), pr, ldr, py, ldy, pz, ldz, pws, nws, _stream(stream)),
-           "fsdp_linear_forward")
+    pr, ldr = _NO_MATRIX if residual is None else _matrix(residual, "residual", rows, cout, dt)
+    pz, ldz = _NO_MATRIX if preact is None else _matrix(preact, "preact", rows, cout, dt)
+    pb = None if bias is None else _vector(bias, "bias", cout, dt)
+    pws, nws = _NO_MATRIX if workspace is None else _workspace(workspace)
+    rc = lib().fsdp_linear_forward(rows, cin, cout, code, px, ldx, pw, ldw, pb, _act(act), _drop(dropout), pr, ldr, py, ldy,
+                                   pz, ldz, pws, nws, _stream(stream))
+    if rc:
+        _check(rc, "fsdp_linear_forward")
 
 
 def fsdp_linear_dgrad(dz, w, dx, act="none", preact=None, dropout: Optional[DropoutSpec] = None, residual=None,
@@ -537,40 +543,46 @@ def fsdp_linear_dgrad(dz, w, dx, act="none", preact=None, dropout: Optional[Drop
     """dx = residual + act'(preact) * drop(dz w): dz [rows, out], w [out, in], dx / preact /
     residual [rows, in]; act, preact and dropout are those of the layer before."""
     code, dt = _dtype_code(dz), dz.dtype
-    (rows, cout), (_, cin) = _dims(dz, "dz"), _dims(w, "w")
-    pg, ldg = _matrix(dz, "dz", rows, cout, dt)
-    pw, ldw = _matrix(w, "w", cout, cin, dt)
+    rows, cout, pg, ldg = _operand(dz, "dz", dt)
+    wrows, cin, pw, ldw = _operand(w, "w", dt)
+    if wrows != cout:
+        raise ValueError(f"w is {tuple(w.shape)}, expected {(cout, cin)}")
     px, ldx = _matrix(dx, "dx", rows, cin, dt)
-    pz, ldz = _matrix(preact, "preact", rows, cin, dt)
-    pr, ldr = _matrix(residual, "residual", rows, cin, dt)
-    pws, nws = _workspace(workspace)
-    _check(lib().fsdp_linear_dgrad(rows, cin, cout, code, pg, ldg, pw, ldw, _act(act), pz, ldz, _drop(dropout), pr, ldr,
-                                   px, ldx, pws, nws, _stream(stream)), "fsdp_linear_dgrad")
+    pz, ldz = _NO_MATRIX if preact is None else _matrix(preact, "preact", rows, cin, dt)
+    pr, ldr = _NO_MATRIX if residual is None else _matrix(residual, "residual", rows, cin, dt)
+    pws, nws = _NO_MATRIX if workspace is None else _workspace(workspace)
+    rc = lib().fsdp_linear_dgrad(rows, cin, cout, code, pg, ldg, pw, ldw, _act(act), pz, ldz, _drop(dropout), pr, ldr, px,
+                                 ldx, pws, nws, _stream(stream))
+    if rc:
+        _check(rc, "fsdp_linear_dgrad")
 
 
 def fsdp_linear_wgrad(dz, x, dw, db=None, accumulate: bool = False, workspace=None, stream=None) -> None:
     """dw (+)= dz^T x and db (+)= the column sums of dz: dz [rows, out], x [rows, in] of one
     dtype, dw [out, in] and db [out] of one dtype (a gradient replica's, or fp32)."""
     code, dt = _dtype_code(dz), dz.dtype
-    (rows, cout), (_, cin) = _dims(dz, "dz"), _dims(x, "x")
-    pg, ldg = _matrix(dz, "dz", rows, cout, dt)
-    px, ldx = _matrix(x, "x", rows, cin, dt)
+    rows, cout, pg, ldg = _operand(dz, "dz", dt)
+    xrows, cin, px, ldx = _operand(x, "x", dt)
+    if xrows != rows:
+        raise ValueError(f"x is {tuple(x.shape)}, expected {(rows, cin)}")
     pw, ldw = _matrix(dw, "dw", cout, cin, dw.dtype)
-    pws, nws = _workspace(workspace)
-    _check(lib().fsdp_linear_wgrad(rows, cin, cout, code, pg, ldg, px, ldx, pw, ldw, _vector(db, "db", cout, dw.dtype),
-                                   _dtype_code(dw), int(bool(accumulate)), pws, nws, _stream(stream)),
-           "fsdp_linear_wgrad")
+    pb = None if db is None else _vector(db, "db", cout, dw.dtype)
+    pws, nws = _NO_MATRIX if workspace is None else _workspace(workspace)
+    rc = lib().fsdp_linear_wgrad(rows, cin, cout, code, pg, ldg, px, ldx, pw, ldw, pb, _dtype_code(dw), 1 if accumulate else 0,
+                                 pws, nws, _stream(stream))
+    if rc:
+        _check(rc, "fsdp_linear_wgrad")
 
 
 def fsdp_dropout(x, y, dropout: Optional[DropoutSpec], residual=None, stream=None) -> None:
     """y = residual + drop(x), [rows, cols] each; the same call on the gradient is its backward."""
     code, dt = _dtype_code(x), x.dtype
-    rows, cols = _dims(x, "x")
-    px, ldx = _matrix(x, "x", rows, cols, dt)
+    rows, cols, px, ldx = _operand(x, "x", dt)
     py, ldy = _matrix(y, "y", rows, cols, dt)
-    pr, ldr = _matrix(residual, "residual", rows, cols, dt)
-    _check(lib().fsdp_dropout(rows, cols, code, px, ldx, _drop(dropout), pr, ldr, py, ldy, _stream(stream)),
-           "fsdp_dropout")
+    pr, ldr = _NO_MATRIX if residual is None else _matrix(residual, "residual", rows, cols, dt)
+    rc = lib().fsdp_dropout(rows, cols, code, px, ldx, _drop(dropout), pr, ldr, py, ldy, _stream(stream))
+    if rc:
+        _check(rc, "fsdp_dropout")
 
 
 def fsdp_reshard(layout: Layout, unit_begin: int, unit_end: int, full=None, master=None, param_shards=None,
