@@ -488,11 +488,11 @@ struct WinOut {
 // are read and written by whole 32-byte sectors; rows that start anywhere by whole 16-byte
 // windows, the elements shifted into place in registers (through shared memory and by single
 // elements, a lane per column, the tile took 30,000 clocks).  The warp takes units of 32
-// columns, STEP apart from col0 on, while they lie wholly inside the matrix, NU at most, and
+// columns, STEP apart from col0 on, while they lie wholly inside the matrix, `most` of them, and
 // returns how many; a unit's two halves are read (residual, pre-activation) while the unit before it is
 // computed.  dcol: the generator's column products of the units' columns, in shared memory;
 // dr: the lane's row's.
-template <int MODE, int EP, int NU, bool ALIGNED>
+template <int MODE, int EP, bool ALIGNED>
 struct RowsEmit {
     using In = typename std::conditional<ALIGNED, Raw16, Win16>::type;
     static constexpr int STEP = ALIGNED ? 64 : 32;
@@ -514,10 +514,10 @@ struct RowsEmit {
     }
 
     // Before the accumulators are there: the first unit's reads.
-    __device__ __forceinline__ void begin(const LinEpi& ep, int64_t row, int64_t col0) {
+    __device__ __forceinline__ void begin(const LinEpi& ep, int64_t row, int64_t col0, int most) {
         in = row < ep.rows;
         const int64_t left = ep.cols - col0;
-        units = left < 32 ? 0 : (left - 32) / STEP + 1 < NU ? int((left - 32) / STEP + 1) : NU;
+        units = left < 32 ? 0 : (left - 32) / STEP + 1 < most ? int((left - 32) / STEP + 1) : most;
         out = static_cast<uint16_t*>(ep.out) + row * ep.ldo + col0;
         add = MODE == kWgrad ? (ep.accumulate ? out : nullptr)
               : ep.residual  ? static_cast<const uint16_t*>(ep.residual) + row * ep.ldr + col0

@@ -64,6 +64,8 @@ struct LinCfg {
     static constexpr bool ANY = ANY_;
     static constexpr bool DIRECT = !SPLIT && CH == 0 && sizeof(OT) == 2;    // RowsEmit where rows are aligned
     static constexpr int BROWS = BN / CG;                        // B rows a CTA loads
+    static constexpr bool CUT = CG == 2 && BN == 256;            // tiles of the last wave may be halved
+    static constexpr int BBOX = CUT ? BROWS / 2 : BROWS;         // rows of a K-major copy: half a tile's, or all
     static constexpr int A_BYTES = 128 * 128, B_BYTES = BROWS * 128;
     static constexpr int STAGE = PL * (A_BYTES + B_BYTES);
     // the epilogue's shared memory: a unit per warp, or the join's slots
@@ -80,8 +82,10 @@ struct LinCfg {
 };
 
 // splits: CTAs per tile; slabs (wgrad): K ranges with an output of their own each, [slabs][rows][ldo].
+// The work of the 256-column pairs: the first `whole` tiles as they are, the others, less than
+// half a wave, in halves of 128 columns, so that the last wave is spread over the pairs.
 struct LinShape {
-    int32_t m_tiles, n_tiles, n_kb, splits, slabs;
+    int32_t m_tiles, n_tiles, n_kb, splits, slabs, whole;
 };
 
 template <class C>
@@ -148,6 +152,19 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
         mt = first + r % high;
         nt = r / high;
     };
+    // Work item w: its tile, and whether that is whole (cut 1) or which half of it (cut 2).
+    const int n_items = C::CUT ? 2 * n_tiles - sh.whole : n_tiles;
+    struct Item {
+        int mt, nt, sub, cut;
+    };
+    auto item_at = [&](int w) {
+        Item it;
+        it.cut = C::CUT && w >= sh.whole ? 2 : 1;
+        it.sub = it.cut == 2 ? (w - sh.whole) & 1 : 0;
+        tile_at(it.cut == 2 ? sh.whole + (w - sh.whole) / 2 : w, it.mt, it.nt);
+        return it;
+    };
+
     // Kernels that hold sums in registers: the epilogue's two warpgroups take registers that the
     // third does not need (the launch has 168 per thread of three warpgroups, which prepare_kernel
     // checks; 2 x 208 + 88 = 2 x 200 + 104 = 3 x 168).  Spilled, the sums went through an L1 of the 28 KB that shared memory leaves, and a
@@ -160,11 +177,14 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
             bool ok = true;
             uint32_t it = 0;
             uint32_t adding = 0, parity = 0;             // per stage: its tile is being added; phase of `summed`
-            for (int t = cluster; ok && t < n_tiles; t += n_clusters) {
-                int mt, nt;
-                tile_at(t, mt, nt);
-                const int m0 = (mt * C::CG + (C::CG == 2 ? int(rank) : 0)) * 128;
-                const int n0 = nt * C::BN + (C::CG == 2 ? int(rank) * C::BROWS : 0);
+            for (int t = cluster; ok && t < n_items; t += n_clusters) {
+                const Item w = item_at(t);
+                const int nt = w.nt, brows = C::BROWS / w.cut;
+                const int m0 = (w.mt * C::CG + (C::CG == 2 ? int(rank) : 0)) * 128;
+                const int n0 = nt * C::BN + w.sub * (C::BN / w.cut) + (C::CG == 2 ? int(rank) * brows : 0);
+                constexpr int BBOX_BYTES = C::B_MN ? 8192 : C::BBOX * 128;
+                const int bboxes = C::B_BYTES / BBOX_BYTES / w.cut;
+                const uint32_t bytes = C::CG * C::PL * (C::A_BYTES + C::B_BYTES / w.cut);
                 for (int kb = kb0; kb < kb1; ++kb, ++it) {
                     const uint32_t s = it % C::STAGES, use = it / C::STAGES;
                     if (C::SPLIT && C::MODE == kWgrad && (adding >> s & 1)) {
@@ -185,7 +205,7 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
                             break;
                         }
                         if (elect_one()) {
-                            if (leader && p == C::PL - 1) mbar_arrive_tx(full + 8 * s, C::CG * C::STAGE);
+                            if (leader && p == C::PL - 1) mbar_arrive_tx(full + 8 * s, bytes);
                             const uint32_t a = st + p * C::A_BYTES, b = st + C::PL * C::A_BYTES + p * C::B_BYTES;
                             if constexpr (C::A_MN) {
                                 tma_load<C::CG>(a, &map_a, m0, kb * kKb, p, bar);
@@ -193,12 +213,11 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
                             } else {
                                 tma_load<C::CG>(a, &map_a, kb * kKb, m0, p, bar);
                             }
-                            if constexpr (C::B_MN) {
 #pragma unroll
-                                for (int c = 0; c < C::BROWS / 64; ++c)
-                                    tma_load<C::CG>(b + c * 8192, &map_b, n0 + c * 64, kb * kKb, p, bar);
-                            } else {
-                                tma_load<C::CG>(b, &map_b, kb * kKb, n0, p, bar);
+                            for (int c = 0; c < C::B_BYTES / BBOX_BYTES; ++c) {
+                                if (c >= bboxes) break;
+                                if constexpr (C::B_MN) tma_load<C::CG>(b + c * BBOX_BYTES, &map_b, n0 + c * 64, kb * kKb, p, bar);
+                                else tma_load<C::CG>(b + c * BBOX_BYTES, &map_b, kb * kKb, n0 + c * C::BBOX, p, bar);
                             }
                         }
                         __syncwarp();
@@ -219,14 +238,15 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
         } else if (warp == kEpiWarps + 1) {
             // ---- products ----
             if (leader) {
-                constexpr uint32_t idesc = mma_idesc(128 * C::CG, C::BN, C::A_MN, C::B_MN);
                 // 16 K elements on: 32 bytes along a K-major row, 16 rows of an MN-major tile
                 constexpr uint32_t a_step = C::A_MN ? 2048 / 16 : 32 / 16, b_step = C::B_MN ? 2048 / 16 : 32 / 16;
                 const uint64_t da0 = smem_desc(smem_addr(smem), C::A_MN ? 8192 : 16, 1024);
                 const uint64_t db0 = smem_desc(smem_addr(smem) + C::PL * C::A_BYTES, C::B_MN ? 8192 : 16, 1024);
                 bool ok = true;
                 uint32_t it = 0, ac = 0;
-                for (int t = cluster; ok && t < n_tiles; t += n_clusters) {
+                for (int t = cluster; ok && t < n_items; t += n_clusters) {
+                    const uint32_t idesc = C::CUT && t >= sh.whole ? mma_idesc(128 * C::CG, C::BN / 2, C::A_MN, C::B_MN)
+                                                                   : mma_idesc(128 * C::CG, C::BN, C::A_MN, C::B_MN);
                     for (int kc = kb0; ok && kc < kb1; kc += chunk, ++ac) {
                         const uint32_t buf = ac & 1, use = ac >> 1;
                         if (use > 0 && !mbar_wait_bounded(acc_empty + 8 * buf, (use - 1) & 1, wait_ns)) {
@@ -301,11 +321,11 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
                 // them share out the K steps, every db_parts-th each
                 using DT = typename std::conditional<C::PL == 3, float, uint16_t>::type;
                 using RS = RowSum<DT>;
-                for (int t = cluster; ep.db && t < n_tiles; t += n_clusters) {
-                    int mt, nt;
-                    tile_at(t, mt, nt);
-                    if (nt >= ep.db_parts) continue;
-                    const int64_t col = int64_t(mt * C::CG + int(rank)) * 128 + chunk_at * 64;
+                for (int t = cluster; ep.db && t < n_items; t += n_clusters) {
+                    const Item w = item_at(t);
+                    const int nt = w.nt;
+                    if (nt >= ep.db_parts || w.sub > 0) continue;
+                    const int64_t col = int64_t(w.mt * C::CG + int(rank)) * 128 + chunk_at * 64;
                     RS db = {};
                     for (int kb = nt; kb < sh.n_kb && col < ep.rows; kb += ep.db_parts)
                         db.add(static_cast<const DT*>(ep.dz), ep.lddz, int64_t(kb) * kKb, ep.dz_rows, col, ep.rows, ep.dz_vec, lane);
@@ -333,14 +353,14 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
         // from group to group) half of the columns each.
         const int q = warp & 3, half = warp >> 2;
         constexpr int NJ = (C::BN + 63) / 64;                // groups of 32 columns per warp
-        auto group = [&](int jj) { return C::DIRECT && C::ANY ? half * NJ + jj : 2 * jj + half; };
         bool ok = true;
         uint32_t ac = 0;
-        for (int t = cluster; ok && t < n_tiles; t += n_clusters) {
-            int mt, nt;
-            tile_at(t, mt, nt);
-            const int64_t m0 = int64_t(mt * C::CG + (C::CG == 2 ? int(rank) : 0)) * 128 + q * 32;
-            const int64_t n0 = int64_t(nt) * C::BN;
+        for (int t = cluster; ok && t < n_items; t += n_clusters) {
+            const Item w = item_at(t);
+            const int nj = NJ / w.cut;                               // of this item
+            auto group = [&](int jj) { return C::DIRECT && C::ANY ? half * nj + jj : 2 * jj + half; };
+            const int64_t m0 = int64_t(w.mt * C::CG + (C::CG == 2 ? int(rank) : 0)) * 128 + q * 32;
+            const int64_t n0 = int64_t(w.nt) * C::BN + w.sub * (C::BN / w.cut);
             float sum[C::CH ? NJ : 1][32];
             if constexpr (C::CH != 0) {
 #pragma unroll
@@ -384,9 +404,9 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
             };
             for (int kc = kb0; ok && kc < kb1; kc += chunk, ++ac) {
                 const uint32_t buf = ac & 1;
-                RowsEmit<C::MODE, C::EP, NJ, !C::ANY> rows;
+                RowsEmit<C::MODE, C::EP, !C::ANY> rows;
                 bool direct = C::DIRECT;
-                if constexpr (C::DIRECT) rows.begin(ep, m0 + lane, n0 + group(0) * 32);
+                if constexpr (C::DIRECT) rows.begin(ep, m0 + lane, n0 + group(0) * 32, nj);
                 ok = __all_sync(0xffffffffu, mbar_wait_bounded(acc_full + 8 * buf, (ac >> 1) & 1, wait_ns));
                 if (!ok) break;
                 tc_fence_after();
@@ -414,7 +434,7 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
                 constexpr int kUnrollUnits = C::CH != 0 ? NJ : 1;
 #pragma unroll kUnrollUnits
                 for (int jj = C::DIRECT ? done : 0; jj < NJ; ++jj) {
-                    if (group(jj) * 32 < C::BN) {
+                    if (jj < nj && group(jj) * 32 < C::BN) {
                         if constexpr (C::CH != 0) {
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
@@ -442,13 +462,13 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
             }
             if constexpr (C::CH != 0) {
                 constexpr bool WHOLE = C::MODE == kWgrad && !C::SPLIT && sizeof(typename C::OT) == 4;
-                const bool whole = WHOLE && ep.vec == 2 && n0 + C::BN <= ep.cols;
+                const bool whole = WHOLE && ep.vec == 2 && w.cut == 1 && n0 + C::BN <= ep.cols;
                 if constexpr (WHOLE) {
                     if (ok && whole) emit_sums<NJ>(ep, sum, m0 + lane, n0 + half * 32);
                 }
 #pragma unroll
                 for (int jj = 0; jj < NJ; ++jj)
-                    if (ok && !whole && group(jj) * 32 < C::BN) {
+                    if (ok && !whole && jj < nj && group(jj) * 32 < C::BN) {
                         begin(jj);
                         finish(jj, sum[jj]);
                     }

@@ -67,6 +67,17 @@ cudaError_t prepare_kernel(int dev) {
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// How many tiles of a 256-column pair configuration stay whole: all, or all but those of a
+// last wave that is at most half full.  Those run in halves: a half's K step takes two thirds
+// of a whole tile's (as the 256 x 128 tile's does; quarters took no less), the last wave is
+// that much shorter, and so is its epilogue.  4000 x 4000 x 4000 with GELU, dropout and residual:
+// 93 us uncut, 88 with 28 of 256 tiles halved.
+template <class C>
+int64_t whole_tiles(int64_t tiles, int64_t room) {
+    const int64_t rem = room > 0 ? tiles % room : 0;
+    return C::CUT && 2 * rem <= room ? tiles - rem : tiles;
+}
+
 // Launches one configuration: splits CTAs per tile (SPLIT), else a persistent grid.
 template <class C>
 cudaError_t launch_cfg(const LinProblem& p, int splits, cudaStream_t st, int slabs = 1) {
@@ -76,16 +87,17 @@ cudaError_t launch_cfg(const LinProblem& p, int splits, cudaStream_t st, int sla
     if ((e = prepare_kernel<C>(dev)) != cudaSuccess) return e;
     CUtensorMap ma, mb;
     if ((e = make_map(&ma, C::ROWS_M ? p.rows_op : p.cols_op, C::PL, C::A_MN ? kKb : 128)) != cudaSuccess) return e;
-    if ((e = make_map(&mb, C::ROWS_M ? p.cols_op : p.rows_op, C::PL, C::B_MN ? kKb : C::BROWS)) != cudaSuccess) return e;
+    if ((e = make_map(&mb, C::ROWS_M ? p.cols_op : p.rows_op, C::PL, C::B_MN ? kKb : C::BBOX)) != cudaSuccess) return e;
     const int64_t M = C::ROWS_M ? p.epi.rows : p.epi.cols, N = C::ROWS_M ? p.epi.cols : p.epi.rows;
     const int64_t mt = ceil_div(M, 128 * C::CG), nt = ceil_div(N, C::BN), kb = ceil_div(p.K, kKb);
     const int per = C::CG == 2 ? 2 : C::SPLIT ? splits : 1;
     // tile numbers, K steps and tile coordinates are 32-bit
     if (mt * nt * per > INT32_MAX / 16 || kb > INT32_MAX / 128 || M > INT32_MAX - 512 || N > INT32_MAX - 512)
         return cudaErrorInvalidValue;
-    LinShape sh{int32_t(mt), int32_t(nt), int32_t(kb), splits, slabs};
-    int64_t clusters = mt * nt * slabs;
-    const int64_t room = sm_count(dev) / per;
+    const int64_t room = sm_count(dev) / per, tiles = mt * nt;
+    const int64_t whole = whole_tiles<C>(tiles, room);
+    const LinShape sh{int32_t(mt), int32_t(nt), int32_t(kb), splits, slabs, int32_t(whole)};
+    int64_t clusters = (2 * tiles - whole) * slabs;
     if (!C::SPLIT && clusters > room) clusters = room > 0 ? room : 1;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -150,14 +162,16 @@ float estimate(const LinProblem& p, int splits, int dev, LinCost c) {
     if constexpr (C::SPLIT) room = max_clusters<C>(dev, splits);
     else room = sm_count(dev) / C::CG;
     if (room < 1) return 1e30f;
-    const float waves = float(ceil_div(tiles, room));
-    if (C::SPLIT) return waves * (c.fixed + (splits > 1 ? 0.7f : 0.f) + float(ceil_div(kb, splits)) * c.kb + c.epi);
-    return c.fixed + waves * float(kb) * c.kb + c.epi;
+    if (C::SPLIT)
+        return float(ceil_div(tiles, room)) * (c.fixed + (splits > 1 ? 0.7f : 0.f) + float(ceil_div(kb, splits)) * c.kb + c.epi);
+    const bool cut = whole_tiles<C>(tiles, room) < tiles;
+    const float waves = float(tiles / room) + (cut ? 0.66f : tiles % room ? 1.f : 0.f);
+    return c.fixed + waves * float(kb) * c.kb + (cut ? 0.5f : 1.f) * c.epi;
 }
 
 // The configuration with the lowest estimate.  Measured on GB300 (us, forward, bf16, rows x in
 // x out; 256 x 256 pair / 256 x 128 pair / best split): 8192 x 4096 x 11008 382 / 452 / 1248;
-// 2048^3 18.8 / 18.7 / 42; 333 x 2048 x 2048 - / 11 / 11; 1 x 2048 x 2048 13.3 / 9.2 / 5.8 (32
+// 2048^3 15.6 / 16.4 / 27; 333 x 2048 x 2048 - / 11 / 11; 1 x 2048 x 2048 13.3 / 9.2 / 5.8 (32
 // columns, 4 CTAs per tile), where one CTA per tile takes 9.8 and 8 CTAs, two waves of
 // clusters, 9.3.
 //
