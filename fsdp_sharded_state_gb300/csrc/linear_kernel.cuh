@@ -368,6 +368,11 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
 #pragma unroll
                     for (int i = 0; i < 32; ++i) sum[j][i] = 0.f;
             }
+            constexpr bool WHOLE = C::CH != 0 && C::MODE == kWgrad && !C::SPLIT && sizeof(typename C::OT) == 4;
+            const bool whole = WHOLE && ep.vec == 2 && w.cut == 1 && n0 + C::BN <= ep.cols;
+            if constexpr (WHOLE) {
+                if (whole && ep.accumulate) read_sums<NJ>(ep, sum, m0 + lane, n0 + half * 32);
+            }
             UnitEmit<C::MODE, typename C::OT, C::EP> io;
             auto begin = [&](int jj) {
                 const int64_t n = n0 + group(jj) * 32;
@@ -461,8 +466,6 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
                 }
             }
             if constexpr (C::CH != 0) {
-                constexpr bool WHOLE = C::MODE == kWgrad && !C::SPLIT && sizeof(typename C::OT) == 4;
-                const bool whole = WHOLE && ep.vec == 2 && w.cut == 1 && n0 + C::BN <= ep.cols;
                 if constexpr (WHOLE) {
                     if (ok && whole) emit_sums<NJ>(ep, sum, m0 + lane, n0 + half * 32);
                 }
