@@ -29,8 +29,6 @@ struct LinEpi {
     int32_t accumulate;        // wgrad: out += instead of out =
     int32_t vec;               // every matrix here has rows aligned to 16 bytes (1), 32 bytes (2), or not (0)
     void* db;                  // wgrad: the column sums of dz, or NULL
-    float* db_sums;            // [db_parts][rows] partial sums of db, where db_parts > 1
-    int32_t db_parts;
     const void* dz;            // and dz itself (fp32: as the caller holds it)
     int64_t lddz, dz_rows;
     int32_t dz_vec;            // 16-byte aligned rows
@@ -62,10 +60,6 @@ constexpr int kSlabSplits = 4;
 int wgrad_slabs(int64_t rows, int64_t in, int64_t out);
 int64_t wgrad_slab_floats(int64_t rows, int64_t in, int64_t out);
 cudaError_t launch_wgrad_slabs(const LinProblem& p, cudaStream_t st);
-
-// The partial sums of db that the tiles of a row of 256-column tiles share out (at most 8, of
-// one K step or more each).
-int wgrad_db_parts(int64_t rows, int64_t in);
 
 cudaError_t launch_linear_forward(const LinProblem& p, cudaStream_t st);
 cudaError_t launch_linear_dgrad(const LinProblem& p, cudaStream_t st);

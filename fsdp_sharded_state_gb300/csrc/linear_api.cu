@@ -111,19 +111,13 @@ int run_skinny(LinMode mode, int32_t dtype, const void* x, int64_t ldx, const vo
     return e == cudaSuccess ? FSDP_OK : cuda_fail(e, "k_skinny launch");
 }
 
-// Floats of wgrad's partial sums: slabs of a small out, or parts of db.
-int64_t partial_floats(int64_t rows, int64_t in, int64_t out) {
-    const int64_t parts = wgrad_db_parts(rows, in);
-    return std::max(wgrad_slab_floats(rows, in, out), parts > 1 ? parts * out : 0);
-}
-
 }  // namespace
 
 extern "C" {
 
 size_t fsdp_linear_workspace_bytes(int64_t rows, int64_t in, int64_t out, int32_t elem_dtype, int32_t aligned) {
     if (check_dims(rows, in, out, elem_dtype)) return 0;
-    const size_t slabs = size_t(round_up(partial_floats(rows, in, out) * 4, 256));
+    const size_t slabs = size_t(round_up(wgrad_slab_floats(rows, in, out) * 4, 256));
     if (elem_dtype == FSDP_BF16 && aligned) return slabs;
     const int planes = elem_dtype == FSDP_F32 ? 3 : 1;
     const int64_t x = packed_bytes(rows, in, planes), w = packed_bytes(out, in, planes), z = packed_bytes(rows, out, planes);
@@ -245,17 +239,16 @@ int fsdp_linear_wgrad(int64_t rows, int64_t in, int64_t out, int32_t elem_dtype,
     ep.accumulate = accumulate != 0;
     ep.vec = row_class(dw, lddw, gs);
     ep.db = db;
-    // partial sums: room for slabs, always where the sizes allow them, and for db's parts
+    // partial sums: room for slabs, always where the sizes allow them
     p.slabs = wgrad_slabs(rows, in, out);
-    ep.db_parts = db ? wgrad_db_parts(rows, in) : 0;
     ep.dz = elem_dtype == FSDP_F32 ? dz : p.rows_op.ptr;
     ep.lddz = elem_dtype == FSDP_F32 ? lddz : p.rows_op.ld;
     ep.dz_rows = rows;
     ep.dz_vec = rows16(ep.dz, ep.lddz, es);
-    const int64_t floats = std::max(wgrad_slab_floats(rows, in, out), ep.db_parts > 1 ? ep.db_parts * out : 0);
+    const int64_t floats = wgrad_slab_floats(rows, in, out);
     if (floats) {
         if (!pk.ws || pk.left < size_t(floats * 4)) return FSDP_EINVAL;
-        p.partial = ep.db_sums = reinterpret_cast<float*>(pk.ws);
+        p.partial = reinterpret_cast<float*>(pk.ws);
     }
     return run_product(p, pk, elem_dtype, st);
 }

@@ -706,16 +706,17 @@ __device__ __forceinline__ void colsum_lanes(const ColSum& s, float (&t)[8], int
     }
 }
 
-// For the CTA pairs: 64 columns (from col) of 64 rows of dz (from row, `rows` in all) added to
-// the lane's sums straight from memory, which the tiles' own copies have just brought into L2.
-// (From the shared-memory stages it held each of them back from its next load by more than
-// the ring of stages covers: dz^T x of 16384 x 2048 x 2048 took 111 us against 78 without db.)
-// Lane l holds columns E (l mod L) on, L = 64 / E lanes to a row.
-// Loads are 16 bytes wherever rows start at multiples of 16, ragged ends included: with the last
-// columns' tile read by single elements, 4096 x 777 x 1001 took 110 us (25 now, 22 without db).
+// For the CTA pairs: 16 to 128 columns of every second group of rows of dz added up straight
+// from memory, which the tiles' own copies bring into L2.  (From the shared-memory stages it
+// held each of them back from its next load by more than the ring of stages covers: dz^T x of
+// 16384 x 2048 x 2048 took 111 us against 78 without db.)  The tiles of a row of tiles share out
+// its columns; with their rows shared out instead, a launch of 3 us had to join the sums.
+// Lane l holds columns E (l mod L) on, L lanes to a row.  Loads are 16 bytes wherever rows start
+// at multiples of 16, ragged ends included: with the last columns' tile read by single elements,
+// 4096 x 777 x 1001 took 110 us instead of 25.
 template <typename T>
 struct RowSum {
-    static constexpr int E = 16 / sizeof(T), L = 64 / E;
+    static constexpr int E = 16 / sizeof(T), B = 16;             // elements of a load; loads in flight
     float v[E];
 
     __device__ __forceinline__ static void wide(const uint4& q, float (&x)[E]) {
@@ -728,19 +729,27 @@ struct RowSum {
             x[2] = __uint_as_float(q.z); x[3] = __uint_as_float(q.w);
         }
     }
-    __device__ __forceinline__ void add(const T* dz, int64_t ld, int64_t row, int64_t rows, int64_t col, int64_t cols, bool vec, int lane) {
-        constexpr int R = 32 / L, N = 64 / R, B = 16;            // rows of a load; loads; of a batch
-        const int64_t c = col + (lane % L) * E;
+    // Columns col on, L lanes to a row, of the groups of 32 / L rows, every second from the half-th on.
+    __device__ __forceinline__ void add(const T* dz, int64_t ld, int half, int64_t rows, int64_t col, int64_t cols, bool vec, int L,
+                                        int lane) {
+        const int64_t c = col + (lane & (L - 1)) * E;
+        const int every = 64 / L, first = (half * 32 + lane) / L;
+        int64_t r = first;
+        if (c >= cols) return;
+        const T* p = dz + r * ld + c;
+        const int64_t step = every * ld;
+        if (vec) {
+            // rows start at multiples of 16 bytes, so a row's last load ends before the next row;
+            // what is left of the very last row is added below
+            const int64_t end = c + E <= cols ? rows : rows - 1;
 #pragma unroll 1
-        for (int b = 0; b < N; b += B) {
-            const int64_t r0 = row + b * R + lane / L;
-            if (vec && c < cols) {
-                // rows start at multiples of 16 bytes, so a row's last load ends before the next row
+            while (r < end) {
                 uint4 q[B];
 #pragma unroll
                 for (int i = 0; i < B; ++i) {
-                    const int64_t r = r0 + i * R;
-                    q[i] = r < rows - 1 || (r < rows && c + E <= cols) ? ldu4(dz + r * ld + c) : make_uint4(0, 0, 0, 0);
+                    q[i] = r < end ? ldu4(p) : make_uint4(0, 0, 0, 0);
+                    r += every;
+                    p += step;
                 }
 #pragma unroll
                 for (int i = 0; i < B; i += 4) {
@@ -751,29 +760,32 @@ struct RowSum {
                     for (int e = 0; e < E; ++e) v[e] += (x[0][e] + x[1][e]) + (x[2][e] + x[3][e]);
                 }
             }
-            const bool at_end = c + E > cols && (rows - 1 - r0) % R == 0 && rows > r0 && rows <= r0 + B * R;
-            if (c < cols && (!vec || at_end)) {              // any alignment (fp32 only), and the last row's ragged end
+            if (end < rows && (rows - 1) % every == first) {
+#pragma unroll
+                for (int e = 0; e < E; ++e) v[e] += c + e < cols ? load1(dz + (rows - 1) * ld + c + e) : 0.f;
+            }
+        } else {                                             // any alignment (fp32 only)
 #pragma unroll 1
-                for (int i = vec ? int((rows - 1 - r0) / R) : 0; i < B; i += 4) {
-                    float x[4][E];
+            while (r < rows) {
+                float x[8][E];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int64_t r = r0 + (i + k) * R;
+                for (int k = 0; k < 8; ++k) {
 #pragma unroll
-                        for (int e = 0; e < E; ++e) x[k][e] = r < rows && i + k < B && c + e < cols ? load1(dz + r * ld + c + e) : 0.f;
-                    }
-#pragma unroll
-                    for (int e = 0; e < E; ++e) v[e] += (x[0][e] + x[1][e]) + (x[2][e] + x[3][e]);
+                    for (int e = 0; e < E; ++e) x[k][e] = r < rows && c + e < cols ? load1(p + e) : 0.f;
+                    r += every;
+                    p += step;
                 }
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    v[e] += ((x[0][e] + x[1][e]) + (x[2][e] + x[3][e])) + ((x[4][e] + x[5][e]) + (x[6][e] + x[7][e]));
             }
         }
     }
     // Lane l < L: the sums of its columns over the warp.
-    __device__ __forceinline__ void join() {
+    __device__ __forceinline__ void join(int L) {
+        for (int m = L; m < 32; m <<= 1) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-#pragma unroll
-            for (int m = L; m < 32; m <<= 1) v[e] += __shfl_xor_sync(0xffffffffu, v[e], m);
+            for (int e = 0; e < E; ++e) v[e] += __shfl_xor_sync(0xffffffffu, v[e], m);
         }
     }
 };

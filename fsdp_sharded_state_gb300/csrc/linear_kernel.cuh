@@ -88,6 +88,9 @@ struct LinShape {
     int32_t m_tiles, n_tiles, n_kb, splits, slabs, whole;
 };
 
+// The two warps that add dz up, and no others.
+__device__ __forceinline__ void sum_warps_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kSumWarps) : "memory"); }
+
 template <class C>
 __global__ void __launch_bounds__(kLinThreads, 1)
 k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const LinShape sh,
@@ -102,7 +105,7 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
                    acc_empty = acc_full + 16, tmem_word = acc_empty + 16;
     const uint32_t summed = tmem_word + 8;       // wgrad: a stage's dz tile has been added
     static_assert(8 * (3 * kLinMaxStages + 6) <= 256, "barriers");
-    float* const db_part = reinterpret_cast<float*>(smem + C::STAGES * C::STAGE + C::EPI + 256);   // SPLIT: [128]
+    float* const db_part = reinterpret_cast<float*>(smem + C::STAGES * C::STAGE + C::EPI + 256);   // [128]
     // a stage's plane may be loaded again: plane 0 with the stage, planes 1 and 2 earlier
     auto plane_empty = [&](int p) { return p == 0 ? empty : bars + 768 + 8 * kLinMaxStages * (p - 1); };
     const bool leader = C::CG == 1 || rank == 0;
@@ -317,28 +320,31 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
                 if (!ok && lane == 0) atomicOr(&g_wait_error, 1u);
             }
             if constexpr (C::MODE == kWgrad && !C::SPLIT) {
-                // the tiles of a row of tiles belong to the same columns of dz: the first db_parts of
-                // them share out the K steps, every db_parts-th each
+                // the tiles of a row of tiles belong to the same columns of dz, 128 a CTA: the first
+                // eight of them (four, two) take 16 (32, 64) each, whose rows the two warps share
                 using DT = typename std::conditional<C::PL == 3, float, uint16_t>::type;
                 using RS = RowSum<DT>;
+                const int parts = sh.n_tiles >= 8 ? 8 : sh.n_tiles >= 4 ? 4 : sh.n_tiles >= 2 ? 2 : 1, lanes = 128 / RS::E / parts;
                 for (int t = cluster; ep.db && t < n_items; t += n_clusters) {
                     const Item w = item_at(t);
-                    const int nt = w.nt;
-                    if (nt >= ep.db_parts || w.sub > 0) continue;
-                    const int64_t col = int64_t(w.mt * C::CG + int(rank)) * 128 + chunk_at * 64;
+                    const int64_t col = int64_t(w.mt * C::CG + int(rank)) * 128 + w.nt * (128 / parts);
+                    if (w.nt >= parts || w.sub > 0 || col >= ep.rows) continue;
                     RS db = {};
-                    for (int kb = nt; kb < sh.n_kb && col < ep.rows; kb += ep.db_parts)
-                        db.add(static_cast<const DT*>(ep.dz), ep.lddz, int64_t(kb) * kKb, ep.dz_rows, col, ep.rows, ep.dz_vec, lane);
-                    db.join();
-                    if (lane < RS::L) {
+                    db.add(static_cast<const DT*>(ep.dz), ep.lddz, chunk_at, ep.dz_rows, col, ep.rows, ep.dz_vec, lanes, lane);
+                    db.join(lanes);
+                    if (chunk_at == 1 && lane < lanes) {
+#pragma unroll
+                        for (int e = 0; e < RS::E; ++e) db_part[lane * RS::E + e] = db.v[e];
+                    }
+                    sum_warps_sync();
+                    if (chunk_at == 0 && lane < lanes) {
 #pragma unroll
                         for (int e = 0; e < RS::E; ++e) {
                             const int64_t c = col + lane * RS::E + e;
-                            if (c >= ep.rows) break;
-                            if (ep.db_parts > 1) ep.db_sums[nt * ep.rows + c] = db.v[e];
-                            else emit_db<typename C::OT>(ep, c, db.v[e]);
+                            if (c < ep.rows) emit_db<typename C::OT>(ep, c, db.v[e] + db_part[lane * RS::E + e]);
                         }
                     }
+                    sum_warps_sync();
                 }
             }
             __syncwarp();

@@ -34,14 +34,10 @@ cudaError_t join(const float* part, const float* db_part, int parts, int64_t row
                   static_cast<OT*>(ep.out), ep.ldo, static_cast<OT*>(ep.db), int(ep.accumulate));
 }
 
-// The pair kernels, and the join of db's partial sums.
 template <typename OT, int PL, int CH>
 cudaError_t launch_pair_wgrad(const LinProblem& p, int bn, cudaStream_t st) {
-    cudaError_t e;
-    if (CH == 0 && p.epi.vec != 2) e = launch_pair_as<kWgrad, OT, PL, CH, -1, CH == 0>(p, bn, st);
-    else e = launch_pair_as<kWgrad, OT, PL, CH>(p, bn, st);
-    if (e != cudaSuccess || !p.epi.db || p.epi.db_parts <= 1) return e;
-    return join<OT>(nullptr, p.epi.db_sums, p.epi.db_parts, p.epi.rows, 0, 0, p.epi, st);
+    if (CH == 0 && p.epi.vec != 2) return launch_pair_as<kWgrad, OT, PL, CH, -1, CH == 0>(p, bn, st);
+    return launch_pair_as<kWgrad, OT, PL, CH>(p, bn, st);
 }
 }  // namespace
 
@@ -81,12 +77,6 @@ cudaError_t launch_wgrad_slabs(const LinProblem& p, cudaStream_t st) {
     const float* const db_part = p.partial + p.slabs * rows * ld;
     return p.out_bf16 ? join<uint16_t>(p.partial, db_part, p.slabs, rows, cols, ld, p.epi, st)
                       : join<float>(p.partial, db_part, p.slabs, rows, cols, ld, p.epi, st);
-}
-
-int wgrad_db_parts(int64_t rows, int64_t in) {
-    const int64_t kb = ceil_div(rows, kKb), tiles = ceil_div(in, 256);
-    const int64_t n = kb < tiles ? kb : tiles;
-    return n > 8 ? 8 : int(n);
 }
 
 cudaError_t take_wait_error_wgrad(unsigned int* flag) { return take_local_wait_error(flag); }

@@ -604,8 +604,8 @@ typedef struct {
 
 /* Scratch bytes of the three linear calls at these sizes: an upper bound over forward,
  * dgrad and wgrad.  Counted are: room for aligned copies of two operands, or, for FSDP_F32,
- * for their three bf16 terms; and for wgrad, partial sums of db (at most 8 out
- * floats) or, with many rows and a small out x in, of slabs of the rows (under 2 MB).  aligned != 0: every x, w and dz has a base address and a
+ * for their three bf16 terms; and for wgrad with many rows and a small out x in, partial sums
+ * of slabs of the rows (under 2 MB).  aligned != 0: every x, w and dz has a base address and a
  * row stride that are multiples of 16 bytes, so that FSDP_BF16 needs no copies.  0 for
  * arguments that the calls refuse.  Host only. */
 size_t fsdp_linear_workspace_bytes(int64_t rows, int64_t in, int64_t out, int32_t elem_dtype, int32_t aligned);

@@ -354,3 +354,20 @@ def test_views_of_wide_buffers(dtype):
     want, z, bound = lu.forward64(x, w, None, "none", None, res)
     lu.check(y, want, bound + 2.0 ** -20 * (z.abs() + res.double().abs()), "y")
     assert (out[:, :333] == 7).all() and (out[:, 733:] == 7).all()
+
+
+@pytest.mark.parametrize("dtype,ld", [(BF16, 8), (BF16, 1), (F32, 4), (F32, 1)])
+@pytest.mark.parametrize("rows,cin,cout", [(1000, 200, 9001), (1031, 500, 9001), (1031, 1100, 4333), (1500, 2300, 2051), (63, 2300, 4333)])
+def test_bias_gradient_of_wide_layers(rows, cin, cout, dtype, ld):
+    # one, two, five and nine tiles to a row of tiles share dz's columns out; rows that start at
+    # multiples of 16 bytes (the rest of the stride is NaN) and anywhere, the last row's end is
+    # the buffer's.  A lane adds at most every second row, four at a time.
+    g = lu.gen(31)
+    dz = lu.matrix(rows, cout, dtype, 1e-3, g, (cout + ld - 1) // ld * ld)
+    x = lu.matrix(rows, cin, dtype, 1.0, g)
+    dw, db = torch.empty(cout, cin, dtype=F32, device="cuda"), torch.empty(cout, dtype=F32, device="cuda")
+    fs.fsdp_linear_wgrad(dz, x, dw, db, workspace=lu.workspace(rows, cin, cout, dtype))
+    fs.fsdp_check_status()
+    lu.check(db, dz.double().sum(0), (rows / 8 + 16) * 2.0 ** -24 * dz.double().abs().sum(0), "db")
+    M = dz.double().abs().t() @ x.double().abs()
+    lu.check(dw, dz.double().t() @ x.double(), lu.product_bound(rows, M, dtype), "dw")
