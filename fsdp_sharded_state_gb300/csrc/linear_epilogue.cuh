@@ -656,64 +656,14 @@ __device__ __forceinline__ void emit_sums(const LinEpi& ep, const float (&sum)[N
 }
 
 // ---- column sums of dz (wgrad's db) ---------------------------------------------------
-// Where K is split: two warps add up the dz tiles that the products of the first column of tiles
-// read anyway, from shared memory.  A tile (one plane) is two chunks of 64
-// columns, each 64 rows of 128 bytes whose 16-byte groups are swizzled: group p of row r holds
-// columns 8 (p ^ (r mod 8)) on.  A warp takes a chunk; lane l reads group l mod 8 of rows l / 8
-// + 4 h + 8 j: the same columns for all j.  A tile's 8 rows are added in a tree before they
-// meet the running sums.
-struct ColSum {
-    float v[2][8];
-};
-template <int PL>
-__device__ __forceinline__ void colsum_row(float (&x)[8], const unsigned char* p, int plane_bytes) {
-    widen(load_raw(reinterpret_cast<const uint16_t*>(p)), x);
-    if constexpr (PL == 3) {                                 // hi + (mid + lo): both sums exact
-        float a[8], b[8];
-        widen(load_raw(reinterpret_cast<const uint16_t*>(p + plane_bytes)), a);
-        widen(load_raw(reinterpret_cast<const uint16_t*>(p + 2 * plane_bytes)), b);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] += a[e] + b[e];
-    }
-}
-template <int PL>
-__device__ __forceinline__ void colsum_add(ColSum& s, const unsigned char* chunk, int plane_bytes, int lane) {
-    const unsigned char* p = chunk + (lane >> 3) * 128 + (lane & 7) * 16;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        float t[2][8];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            float x[4][8];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) colsum_row<PL>(x[j], p + h * 512 + (4 * k + j) * 1024, plane_bytes);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) t[k][e] = (x[0][e] + x[1][e]) + (x[2][e] + x[3][e]);
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) s.v[h][e] += t[0][e] + t[1][e];
-    }
-}
-// Column u * 8 + e of the chunk to t[e] of lane u < 8, in a fixed order.
-__device__ __forceinline__ void colsum_lanes(const ColSum& s, float (&t)[8], int lane) {
-    const int row = lane >> 3, u = lane & 7;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        t[e] = __shfl_sync(0xffffffffu, s.v[0][e], (row << 3) | (u ^ row)) +
-               __shfl_sync(0xffffffffu, s.v[1][e], (row << 3) | (u ^ (row + 4)));
-        t[e] += __shfl_xor_sync(0xffffffffu, t[e], 8);
-        t[e] += __shfl_xor_sync(0xffffffffu, t[e], 16);
-    }
-}
-
-// For the CTA pairs: 16 to 128 columns of every second group of rows of dz added up straight
-// from memory, which the tiles' own copies bring into L2.  (From the shared-memory stages it
-// held each of them back from its next load by more than the ring of stages covers: dz^T x of
-// 16384 x 2048 x 2048 took 111 us against 78 without db.)  The tiles of a row of tiles share out
-// its columns; with their rows shared out instead, a launch of 3 us had to join the sums.
-// Lane l holds columns E (l mod L) on, L lanes to a row.  Loads are 16 bytes wherever rows start
-// at multiples of 16, ragged ends included: with the last columns' tile read by single elements,
-// 4096 x 777 x 1001 took 110 us instead of 25.
+// 16 to 128 columns of every second group of rows of dz added up straight from memory, which the
+// tiles' own copies bring into L2.  (Added up from the shared-memory stages they held each of
+// them back from its next load by more than the ring of stages covers: 16384 x 2048 x 2048 took
+// 111 us against 78 without db.)  The tiles of a row of tiles share out its columns; with their
+// rows shared out instead, a launch of 3 us had to join the sums.  Lane l holds columns
+// E (l mod L) on, L lanes to a row.  Loads are 16 bytes wherever rows start at multiples of 16,
+// ragged ends included: with the last columns' tile read by single elements, 4096 x 777 x 1001
+// took 110 us instead of 25.
 template <typename T>
 struct RowSum {
     static constexpr int E = 16 / sizeof(T), B = 16;             // elements of a load; loads in flight

@@ -70,7 +70,7 @@ struct LinCfg {
     static constexpr int STAGE = PL * (A_BYTES + B_BYTES);
     // the epilogue's shared memory: a unit per warp, or the join's slots
     static constexpr int EPI = SPLIT ? (BN >= 128 ? 64 : 32) * 1024 : kEpiWarps * kUnitFloats * 4;
-    static constexpr int MORE = SPLIT && MODE == kWgrad ? 2560 : 2048;   // alignment, barriers, a split's column sums
+    static constexpr int MORE = 2048;                       // alignment, barriers, column sums
     static constexpr int FIT = (227 * 1024 - MORE - EPI) / STAGE;
     static constexpr int STAGES = FIT < kLinMaxStages ? FIT : kLinMaxStages;
     static constexpr int SMEM = STAGES * STAGE + EPI + MORE;
@@ -103,8 +103,7 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
     const uint32_t bars = smem_addr(smem + C::STAGES * C::STAGE + C::EPI);
     const uint32_t full = bars, empty = bars + 8 * kLinMaxStages, acc_full = empty + 8 * kLinMaxStages,
                    acc_empty = acc_full + 16, tmem_word = acc_empty + 16;
-    const uint32_t summed = tmem_word + 8;       // wgrad: a stage's dz tile has been added
-    static_assert(8 * (3 * kLinMaxStages + 6) <= 256, "barriers");
+    static_assert(8 * (2 * kLinMaxStages + 5) <= 256, "barriers");
     float* const db_part = reinterpret_cast<float*>(smem + C::STAGES * C::STAGE + C::EPI + 256);   // [128]
     // a stage's plane may be loaded again: plane 0 with the stage, planes 1 and 2 earlier
     auto plane_empty = [&](int p) { return p == 0 ? empty : bars + 768 + 8 * kLinMaxStages * (p - 1); };
@@ -117,7 +116,6 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
         for (int s = 0; s < C::STAGES; ++s) {
             mbar_init(full + 8 * s, 1);
             for (int p = 0; p < C::PL; ++p) mbar_init(plane_empty(p) + 8 * s, 1);
-            mbar_init(summed + 8 * s, kSumWarps);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(acc_full + 8 * b, 1);
@@ -145,6 +143,11 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
     const int kb0 = C::SPLIT ? int(int64_t(sh.n_kb) * part / parts) : 0;
     const int kb1 = C::SPLIT ? int(int64_t(sh.n_kb) * (part + 1) / parts) : sh.n_kb;
     const int chunk = C::CH ? C::CH : sh.n_kb;
+
+    // Who adds dz up (wgrad's db): so many tiles of a row of tiles, so many columns each.
+    const int db_tiles = sh.n_tiles >= 8 ? 8 : sh.n_tiles >= 4 ? 4 : sh.n_tiles >= 2 ? 2 : 1;
+    const int db_width = ep.rows > 64 ? 128 : ep.rows > 32 ? 64 : 32;
+    const int db_cols = db_width / db_tiles > 16 ? db_width / db_tiles : 16;
 
     // Tiles in bands of 8 along M, N outer inside a band: concurrently running tiles share
     // operand rows in L2.
@@ -179,7 +182,6 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
             // ---- loads ----
             bool ok = true;
             uint32_t it = 0;
-            uint32_t adding = 0, parity = 0;             // per stage: its tile is being added; phase of `summed`
             for (int t = cluster; ok && t < n_items; t += n_clusters) {
                 const Item w = item_at(t);
                 const int nt = w.nt, brows = C::BROWS / w.cut;
@@ -190,15 +192,6 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
                 const uint32_t bytes = C::CG * C::PL * (C::A_BYTES + C::B_BYTES / w.cut);
                 for (int kb = kb0; kb < kb1; ++kb, ++it) {
                     const uint32_t s = it % C::STAGES, use = it / C::STAGES;
-                    if (C::SPLIT && C::MODE == kWgrad && (adding >> s & 1)) {
-                        if (!mbar_wait_bounded(summed + 8 * s, parity >> s & 1, wait_ns)) {
-                            ok = false;
-                            break;
-                        }
-                        parity ^= 1u << s;
-                        adding ^= 1u << s;
-                    }
-                    if (C::SPLIT && C::MODE == kWgrad && ep.db && nt == 0) adding |= 1u << s;
                     const uint32_t bar = C::CG == 2 ? map_rank(full + 8 * s, 0) : full + 8 * s;
                     const uint32_t st = smem_addr(smem + s * C::STAGE);
 #pragma unroll
@@ -296,52 +289,33 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
             __syncwarp();
         } else if (warp >= kEpiWarps + 2) {
             // ---- column sums of dz ----
-            const int chunk_at = warp - (kEpiWarps + 2);
-            if (C::MODE == kWgrad && C::SPLIT && ep.db) {
-                // a stage is read once it is loaded, and loaded again once it has been added
-                int mt, nt;
-                tile_at(cluster, mt, nt);
-                bool ok = true;
-                ColSum db = {};
-                for (int kb = kb0; nt == 0 && kb < kb1; ++kb) {
-                    const uint32_t it = uint32_t(kb - kb0), s = it % C::STAGES;
-                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(full + 8 * s, (it / C::STAGES) & 1, wait_ns));
-                    if (!ok) break;
-                    colsum_add<C::PL>(db, smem + s * C::STAGE + chunk_at * 8192, C::A_BYTES, lane);
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(summed + 8 * s);
-                }
-                float v[8];
-                colsum_lanes(db, v, lane);
-                if (lane < 8) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) db_part[chunk_at * 64 + lane * 8 + e] = v[e];
-                }
-                if (!ok && lane == 0) atomicOr(&g_wait_error, 1u);
-            }
-            if constexpr (C::MODE == kWgrad && !C::SPLIT) {
-                // the tiles of a row of tiles belong to the same columns of dz, 128 a CTA: the first
-                // eight of them (four, two) take 16 (32, 64) each, whose rows the two warps share
+            const int half = warp - (kEpiWarps + 2);
+            if constexpr (C::MODE == kWgrad) {
+                // the tiles of a row of tiles belong to the same columns of dz: the first db_tiles of
+                // them take db_cols each, of the K steps that are this CTA's, half of the rows a warp
                 using DT = typename std::conditional<C::PL == 3, float, uint16_t>::type;
                 using RS = RowSum<DT>;
-                const int parts = sh.n_tiles >= 8 ? 8 : sh.n_tiles >= 4 ? 4 : sh.n_tiles >= 2 ? 2 : 1, lanes = 128 / RS::E / parts;
+                const int lanes = db_cols / RS::E;
+                const int64_t row = int64_t(kb0) * kKb, rows = (int64_t(kb1) * kKb < ep.dz_rows ? int64_t(kb1) * kKb : ep.dz_rows) - row;
                 for (int t = cluster; ep.db && t < n_items; t += n_clusters) {
                     const Item w = item_at(t);
-                    const int64_t col = int64_t(w.mt * C::CG + int(rank)) * 128 + w.nt * (128 / parts);
-                    if (w.nt >= parts || w.sub > 0 || col >= ep.rows) continue;
+                    const int64_t col = int64_t(w.mt * C::CG + (C::CG == 2 ? int(rank) : 0)) * 128 + w.nt * db_cols;
+                    if (w.nt >= db_tiles || w.sub > 0 || col >= ep.rows) continue;
                     RS db = {};
-                    db.add(static_cast<const DT*>(ep.dz), ep.lddz, chunk_at, ep.dz_rows, col, ep.rows, ep.dz_vec, lanes, lane);
+                    db.add(static_cast<const DT*>(ep.dz) + row * ep.lddz, ep.lddz, half, rows, col, ep.rows, ep.dz_vec, lanes, lane);
                     db.join(lanes);
-                    if (chunk_at == 1 && lane < lanes) {
+                    if (half == 1 && lane < lanes) {
 #pragma unroll
                         for (int e = 0; e < RS::E; ++e) db_part[lane * RS::E + e] = db.v[e];
                     }
                     sum_warps_sync();
-                    if (chunk_at == 0 && lane < lanes) {
+                    if (half == 0 && lane < lanes) {
 #pragma unroll
                         for (int e = 0; e < RS::E; ++e) {
                             const int64_t c = col + lane * RS::E + e;
-                            if (c < ep.rows) emit_db<typename C::OT>(ep, c, db.v[e] + db_part[lane * RS::E + e]);
+                            db.v[e] += db_part[lane * RS::E + e];
+                            if constexpr (C::SPLIT) db_part[lane * RS::E + e] = db.v[e];
+                            else if (c < ep.rows) emit_db<typename C::OT>(ep, c, db.v[e]);
                         }
                     }
                     sum_warps_sync();
@@ -506,8 +480,8 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
             if (ep.db) {                         // the CTAs' shares of the column sums, in order
                 int mt, nt;
                 tile_at(cluster, mt, nt);
-                const int64_t c = int64_t(mt) * 128 + tid;
-                if (rank == 0 && nt == 0 && tid < 128 && c < ep.rows) {
+                const int64_t c = int64_t(mt) * 128 + nt * db_cols + tid;
+                if (rank == 0 && nt < db_tiles && tid < db_cols && c < ep.rows) {
                     float t = 0.f;
                     for (int r = 0; r < sh.splits; ++r) t += ld_cluster(map_rank(smem_addr(db_part + tid), r));
                     emit_db<typename C::OT>(ep, c + slab * ep.rows, t);
