@@ -18,7 +18,7 @@ LIB = os.path.join(OUT, "libfsdpstate.so")
 SOURCES = ["api.cu", "kernels.cu", "layout.cpp", "noalloc.cu", "rows.cu", "staged.cu", "allgather.cu", "staged_rows.cu",
            "clip_coop.cu", "claims.cu", "linear_api.cu", "linear_forward.cu", "linear_forward_pair.cu",
            "linear_dgrad.cu", "linear_dgrad_pair.cu", "linear_wgrad.cu", "linear_pack.cu",
-           "linear_skinny.cu", "dropout.cu"]
+           "linear_skinny.cu", "linear_small.cu", "dropout.cu"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 # IEEE division and square root, no flush-to-zero, no implicit fma contraction:

@@ -60,6 +60,9 @@ constexpr int kSlabSplits = 4;
 int wgrad_slabs(int64_t rows, int64_t in, int64_t out);
 int64_t wgrad_slab_floats(int64_t rows, int64_t in, int64_t out);
 cudaError_t launch_wgrad_slabs(const LinProblem& p, cudaStream_t st);
+// The sum of `parts` partial sums of out ([parts][rows][ld]) and db ([parts][rows]), in order, into ep's.
+cudaError_t launch_join(const float* part, const float* db_part, int parts, int64_t rows, int64_t cols, int64_t ld, const LinEpi& ep,
+                        bool out_bf16, cudaStream_t st);
 
 cudaError_t launch_linear_forward(const LinProblem& p, cudaStream_t st);
 cudaError_t launch_linear_dgrad(const LinProblem& p, cudaStream_t st);
@@ -80,6 +83,21 @@ struct SkinnyProblem {
 };
 cudaError_t launch_skinny(const SkinnyProblem& p, cudaStream_t st);
 bool use_skinny(LinMode mode, bool bf16, int64_t rows, int64_t in, int64_t out);
+
+// A small product of fp32 operands as the caller stores them: a x or dz, b w or (wgrad) x.
+struct SmallProblem {
+    LinMode mode;
+    const float* a;
+    int64_t lda;
+    const float* b;
+    int64_t ldb, K;
+    bool out_bf16;             // wgrad
+    float* partial;            // wgrad: small_slab_floats() floats
+    LinEpi epi;
+};
+cudaError_t launch_small(const SmallProblem& p, cudaStream_t st);
+bool use_small(LinMode mode, int64_t rows, int64_t in, int64_t out);
+int64_t small_slab_floats(int64_t rows, int64_t in, int64_t out);
 
 // Operands brought into the form of LinOperand: a bf16 matrix copied to aligned rows, or
 // an fp32 matrix split into three bf16 planes (see linear_pack.cu).  Up to two per launch.

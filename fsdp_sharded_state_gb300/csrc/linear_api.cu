@@ -105,10 +105,22 @@ int run_product(LinProblem& p, Packer& pk, int32_t elem_dtype, cudaStream_t st) 
     return e == cudaSuccess ? FSDP_OK : cuda_fail(e, "k_linear launch");
 }
 
+int run_small(LinMode mode, const void* a, int64_t lda, const void* b, int64_t ldb, int64_t K, bool out_bf16, float* partial,
+              const LinEpi& ep, cudaStream_t st) {
+    const cudaError_t e = launch_small(
+        SmallProblem{mode, static_cast<const float*>(a), lda, static_cast<const float*>(b), ldb, K, out_bf16, partial, ep}, st);
+    return e == cudaSuccess ? FSDP_OK : cuda_fail(e, "k_small launch");
+}
+
 int run_skinny(LinMode mode, int32_t dtype, const void* x, int64_t ldx, const void* w, int64_t ldw, int64_t K, const LinEpi& ep,
                cudaStream_t st) {
     const cudaError_t e = launch_skinny(SkinnyProblem{mode, dtype == FSDP_BF16, x, ldx, w, ldw, K, ep}, st);
     return e == cudaSuccess ? FSDP_OK : cuda_fail(e, "k_skinny launch");
+}
+
+// Floats of wgrad's partial sums.
+int64_t partial_floats(int64_t rows, int64_t in, int64_t out, int32_t elem_dtype) {
+    return std::max(wgrad_slab_floats(rows, in, out), elem_dtype == FSDP_F32 ? small_slab_floats(rows, in, out) : 0);
 }
 
 }  // namespace
@@ -117,7 +129,7 @@ extern "C" {
 
 size_t fsdp_linear_workspace_bytes(int64_t rows, int64_t in, int64_t out, int32_t elem_dtype, int32_t aligned) {
     if (check_dims(rows, in, out, elem_dtype)) return 0;
-    const size_t slabs = size_t(round_up(wgrad_slab_floats(rows, in, out) * 4, 256));
+    const size_t slabs = size_t(round_up(partial_floats(rows, in, out, elem_dtype) * 4, 256));
     if (elem_dtype == FSDP_BF16 && aligned) return slabs;
     const int planes = elem_dtype == FSDP_F32 ? 3 : 1;
     const int64_t x = packed_bytes(rows, in, planes), w = packed_bytes(out, in, planes), z = packed_bytes(rows, out, planes);
@@ -163,6 +175,8 @@ int fsdp_linear_forward(int64_t rows, int64_t in, int64_t out, int32_t elem_dtyp
     if ((rc = pk.operand(w, out, in, ldw, elem_dtype, &p.cols_op)) || (rc = pk.operand(x, rows, in, ldx, elem_dtype, &p.rows_op))) return rc;
     if (use_skinny(kForward, elem_dtype == FSDP_BF16, rows, in, out))
         return run_skinny(kForward, elem_dtype, x, ldx, w, ldw, in, ep, st);
+    if (elem_dtype == FSDP_F32 && use_small(kForward, rows, in, out))
+        return run_small(kForward, x, ldx, w, ldw, in, false, nullptr, ep, st);
     return run_product(p, pk, elem_dtype, st);
 }
 
@@ -203,6 +217,8 @@ int fsdp_linear_dgrad(int64_t rows, int64_t in, int64_t out, int32_t elem_dtype,
     if ((rc = pk.operand(w, out, in, ldw, elem_dtype, &p.cols_op)) || (rc = pk.operand(dz, rows, out, lddz, elem_dtype, &p.rows_op))) return rc;
     if (use_skinny(kDgrad, elem_dtype == FSDP_BF16, rows, in, out))
         return run_skinny(kDgrad, elem_dtype, dz, lddz, w, ldw, out, ep, st);
+    if (elem_dtype == FSDP_F32 && use_small(kDgrad, rows, in, out))
+        return run_small(kDgrad, dz, lddz, w, ldw, out, false, nullptr, ep, st);
     return run_product(p, pk, elem_dtype, st);
 }
 
@@ -245,11 +261,13 @@ int fsdp_linear_wgrad(int64_t rows, int64_t in, int64_t out, int32_t elem_dtype,
     ep.lddz = elem_dtype == FSDP_F32 ? lddz : p.rows_op.ld;
     ep.dz_rows = rows;
     ep.dz_vec = rows16(ep.dz, ep.lddz, es);
-    const int64_t floats = wgrad_slab_floats(rows, in, out);
+    const int64_t floats = partial_floats(rows, in, out, elem_dtype);
     if (floats) {
         if (!pk.ws || pk.left < size_t(floats * 4)) return FSDP_EINVAL;
         p.partial = reinterpret_cast<float*>(pk.ws);
     }
+    if (elem_dtype == FSDP_F32 && use_small(kWgrad, rows, in, out))
+        return run_small(kWgrad, dz, lddz, x, ldx, rows, p.out_bf16, p.partial, ep, st);
     return run_product(p, pk, elem_dtype, st);
 }
 

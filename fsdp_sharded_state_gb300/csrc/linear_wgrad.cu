@@ -5,22 +5,31 @@
 namespace fsdp {
 
 namespace {
-// The sum of `parts` partial sums, in order, for each element of out ([parts][rows][ld], rows x
-// cols of it) and then of db ([parts][rows]).
+// The sum of `parts` partial sums for each element of out ([parts][rows][ld], rows x cols of it)
+// and then of db ([parts][rows]): a CTA takes 32 elements, warp w parts w, w + 8, .., and the
+// warps' sums are added in order.  With a thread to an element the parts are as many latencies as
+// they are groups of 16: wgrad of 16384 x 64 x 32 fp32 (64 parts) took 14.9 us instead of 6.3,
+// 2048 x 64 x 64 (16 parts) 6.3 instead of 4.7.
 template <typename OT>
 __global__ void __launch_bounds__(256)
 k_join(const float* __restrict__ part, const float* __restrict__ db_part, int parts, int64_t rows, int64_t cols, int64_t ld, OT* out,
        int64_t ldo, OT* db, int accumulate) {
-    pdl_wait();
-    const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x, n = rows * cols;
-    const bool is_db = i >= n;
-    if (i >= n + (db ? rows : 0)) return;
+    __shared__ float sums[8][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t i = int64_t(blockIdx.x) * 32 + lane, n = rows * cols;
+    const bool is_db = i >= n, in = i < n + (db ? rows : 0);
     const int64_t r = is_db ? i - n : i / cols, c = is_db ? 0 : i - r * cols;
     const float* p = is_db ? db_part + r : part + r * ld + c;
     const int64_t step = is_db ? rows : rows * ld;
-    float t = p[0];
-#pragma unroll 16
-    for (int s = 1; s < parts; ++s) t += p[s * step];
+    pdl_wait();
+    float t = 0.f;
+#pragma unroll 8
+    for (int s = warp; s < parts; s += 8) t += in ? p[s * step] : 0.f;
+    sums[warp][lane] = t;
+    __syncthreads();
+    if (warp > 0 || !in) return;
+#pragma unroll
+    for (int w = 1; w < 8; ++w) t += sums[w][lane];
     OT* const o = is_db ? db + r : out + r * ldo + c;
     store1(o, accumulate ? t + load1(o) : t);
 }
@@ -28,7 +37,7 @@ k_join(const float* __restrict__ part, const float* __restrict__ db_part, int pa
 template <typename OT>
 cudaError_t join(const float* part, const float* db_part, int parts, int64_t rows, int64_t cols, int64_t ld, const LinEpi& ep,
                  cudaStream_t st) {
-    const int64_t blocks = ceil_div(rows * cols + (ep.db ? rows : 0), 256);
+    const int64_t blocks = ceil_div(rows * cols + (ep.db ? rows : 0), 32);
     if (blocks > INT32_MAX) return cudaErrorInvalidValue;
     return launch(k_join<OT>, dim3(unsigned(blocks)), dim3(256), 0, st, part, db_part, parts, rows, cols, ld,
                   static_cast<OT*>(ep.out), ep.ldo, static_cast<OT*>(ep.db), int(ep.accumulate));
@@ -75,8 +84,13 @@ cudaError_t launch_wgrad_slabs(const LinProblem& p, cudaStream_t st) {
                                   : launch_cfg<LinCfg<kWgrad, float, 1, 64, 1, 8, true>>(q, kSlabSplits, st, p.slabs);
     if (e != cudaSuccess) return e;
     const float* const db_part = p.partial + p.slabs * rows * ld;
-    return p.out_bf16 ? join<uint16_t>(p.partial, db_part, p.slabs, rows, cols, ld, p.epi, st)
-                      : join<float>(p.partial, db_part, p.slabs, rows, cols, ld, p.epi, st);
+    return launch_join(p.partial, db_part, p.slabs, rows, cols, ld, p.epi, p.out_bf16, st);
+}
+
+cudaError_t launch_join(const float* part, const float* db_part, int parts, int64_t rows, int64_t cols, int64_t ld, const LinEpi& ep,
+                        bool out_bf16, cudaStream_t st) {
+    return out_bf16 ? join<uint16_t>(part, db_part, parts, rows, cols, ld, ep, st)
+                    : join<float>(part, db_part, parts, rows, cols, ld, ep, st);
 }
 
 cudaError_t take_wait_error_wgrad(unsigned int* flag) { return take_local_wait_error(flag); }
