@@ -371,3 +371,38 @@ def test_bias_gradient_of_wide_layers(rows, cin, cout, dtype, ld):
     lu.check(db, dz.double().sum(0), (rows / 8 + 16) * 2.0 ** -24 * dz.double().abs().sum(0), "db")
     M = dz.double().abs().t() @ x.double().abs()
     lu.check(dw, dz.double().t() @ x.double(), lu.product_bound(rows, M, dtype), "dw")
+
+
+@pytest.mark.parametrize("rows,cin,cout,pad,offset", [(33, 1, 1, 0, 0), (17, 64, 65, 3, 1), (100, 512, 31, 4, 0), (300, 65, 300, 0, 3),
+                                                      (2000, 32, 96, 0, 0), (5000, 40, 33, 1, 2)])
+@pytest.mark.parametrize("act,p", [("none", 0.0), ("gelu", 0.25)])
+def test_small_fp32_products(rows, cin, cout, pad, offset, act, p):
+    # on the FMA units: K of one, a step and a bit; the steps' and tiles' ragged ends lie against
+    # NaN.  A sum is at most 104 fused products in a row and the joins of 8 warps and 152 slabs
+    # (each 2^-24), which the bound of the split products, 104 * 2^-22, covers.
+    g = lu.gen(41)
+    ld = lambda n: n + pad if pad else None
+    x, w = lu.matrix(rows, cin, F32, 1.0, g, ld(cin), offset), lu.matrix(cout, cin, F32, 0.1, g, ld(cin), offset)
+    dz, res = lu.matrix(rows, cout, F32, 1e-2, g, ld(cout), offset), lu.matrix(rows, cin, F32, 1.0, g, ld(cin), offset)
+    pre = lu.matrix(rows, cin, F32, 1.0, g, ld(cin), offset)
+    bias = lu.matrix(1, cout, F32, 1.0, g)[0]
+    spec = fs.DropoutSpec(p, 9, 2, 3) if p else None
+    ws = lu.workspace(rows, cin, cout, F32)
+    y, ybuf = lu.empty_matrix(rows, cout, F32, ld(cout), offset)
+    fs.fsdp_linear_forward(x, w, y, bias=bias, act=act, dropout=spec, residual=dz, workspace=ws)
+    dx, xbuf = lu.empty_matrix(rows, cin, F32, ld(cin), offset)
+    fs.fsdp_linear_dgrad(dz, w, dx, act=act, preact=pre, dropout=spec, residual=res, workspace=ws)
+    dw, wbuf = lu.empty_matrix(cout, cin, F32, ld(cin), offset)
+    db, bbuf = lu.empty_matrix(1, cout, F32, None, offset)
+    fs.fsdp_linear_wgrad(dz, x, dw, db[0], workspace=ws)
+    fs.fsdp_check_status()
+    want, _, bound = lu.forward64(x, w, bias, act, spec, dz)
+    lu.check(y, want, 1.13 / (1 - p) * bound + 2.0 ** -20 * (2 * want.abs() + dz.double().abs()), "y")
+    h, M = dz.double() @ w.double(), dz.double().abs() @ w.double().abs()
+    want = lu.drop64(h, spec) * lu.act_grad64(pre.double(), act) + res.double()
+    lu.check(dx, want, 1.13 / (1 - p) * lu.product_bound(cout, M, F32) + 2.0 ** -20 * (2 * h.abs() + res.double().abs()), "dx")
+    M = dz.double().abs().t() @ x.double().abs()
+    lu.check(dw, dz.double().t() @ x.double(), lu.product_bound(rows, M, F32), "dw")
+    lu.check(db[0], dz.double().sum(0), (rows / 64 + 192) * 2.0 ** -24 * dz.double().abs().sum(0), "db")
+    for v, b in ((y, ybuf), (dx, xbuf), (dw, wbuf), (db, bbuf)):
+        assert lu.untouched(v, b)
