@@ -143,7 +143,8 @@ k_skinny_forward(const T* __restrict__ x, int64_t ldx, const T* __restrict__ w, 
 
 // dgrad: a cluster of 8 CTAs takes 32 E in-features of TB rows; its 64 warps share the
 // out-features (the rows of w), a lane holding E columns; the CTAs' sums join in the CTA that
-// owns an eighth of the columns.
+// owns an eighth of the columns.  A CTA's shared memory may be written once the CTA has started:
+// each arrives at the cluster's barrier first and waits there after its share of the weight.
 constexpr int kSkRanks = 8;
 template <typename T, int TB, bool VEC>
 __global__ void __launch_bounds__(kSkThreads)
@@ -155,6 +156,7 @@ k_skinny_dgrad(const T* __restrict__ dz, int64_t lddz, const T* __restrict__ w, 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t rank = cluster_rank();
     const int64_t c0 = int64_t(blockIdx.x / kSkRanks) * COLS, t0 = int64_t(blockIdx.y) * TB;
+    cluster_arrive();
     pdl_wait();
     float acc[TB][E] = {};
     constexpr int64_t STEP = kSkWarps * kSkRanks;
@@ -178,6 +180,8 @@ k_skinny_dgrad(const T* __restrict__ dz, int64_t lddz, const T* __restrict__ w, 
             }
         }
     }
+    __syncwarp();
+    cluster_wait();
 #pragma unroll
     for (int t = 0; t < TB; ++t) {
         __syncthreads();
