@@ -351,7 +351,7 @@ k_linear(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUte
             constexpr bool WHOLE = C::CH != 0 && C::MODE == kWgrad && !C::SPLIT && sizeof(typename C::OT) == 4;
             const bool whole = WHOLE && ep.vec == 2 && w.cut == 1 && n0 + C::BN <= ep.cols;
             if constexpr (WHOLE) {
-                if (whole && ep.accumulate) read_sums<NJ>(ep, sum, m0 + lane, n0 + half * 32);
+                if (whole && ep.accumulate) prefetch_sums<NJ>(ep, m0 + lane, n0 + half * 32);
             }
             UnitEmit<C::MODE, typename C::OT, C::EP> io;
             auto begin = [&](int jj) {
