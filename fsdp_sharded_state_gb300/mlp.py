@@ -43,7 +43,6 @@ class ResidualMLP:
     def __init__(self, width: int, hidden: int, blocks: int, act: str = "gelu", p: float = 0.0, seed: int = 0):
         self.width, self.hidden, self.blocks, self.act, self.p, self.seed = width, hidden, blocks, act, p, seed
         self.saved = []
-        self.workspace: Optional[torch.Tensor] = None
 
     def shapes(self):
         """(shapes, unit ids) for ShardedState: one unit per block."""
@@ -56,13 +55,13 @@ class ResidualMLP:
     def _spec(self, step: int, block: int, row0: int) -> Optional[DropoutSpec]:
         return DropoutSpec(self.p, self.seed, step * self.blocks + block, row0) if self.p else None
 
-    def _scratch(self, x: torch.Tensor) -> Optional[torch.Tensor]:
-        # views of a full buffer may start at any element: room for aligned copies of the operands
+    def _scratch(self, x: torch.Tensor) -> torch.Tensor:
+        # of one pass, on its device and, through the caching allocator, in its stream's order:
+        # passes on other streams have their own.  Views of a full buffer may start at any
+        # element: room for aligned copies of the operands.
         sizes = ((self.width, self.hidden), (self.hidden, self.width))           # both layers of a block
         n = max(fsdp_linear_workspace_bytes(x.shape[0], i, o, x.dtype, aligned=False) for i, o in sizes)
-        if self.workspace is None or self.workspace.numel() < n:
-            self.workspace = torch.empty(n, dtype=torch.uint8, device=x.device)
-        return self.workspace
+        return torch.empty(n, dtype=torch.uint8, device=x.device)
 
     def forward(self, layout: Layout, full: torch.Tensor, x: torch.Tensor, step: int = 0, row0: int = 0) -> torch.Tensor:
         """x [rows, width] through all blocks; what backward needs is kept until then."""
