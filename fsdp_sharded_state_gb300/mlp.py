@@ -37,12 +37,17 @@ def tensor_views(layout: Layout, full: torch.Tensor) -> List[torch.Tensor]:
     return out
 
 
+def _current_stream(t: torch.Tensor):
+    return torch.cuda.current_stream(t.device) if t.is_cuda else None
+
+
 class ResidualMLP:
     """Forward and backward of `blocks` residual MLP blocks over full-layout buffers."""
 
     def __init__(self, width: int, hidden: int, blocks: int, act: str = "gelu", p: float = 0.0, seed: int = 0):
         self.width, self.hidden, self.blocks, self.act, self.p, self.seed = width, hidden, blocks, act, p, seed
         self.saved = []
+        self.stream = None         # that forward ran on
 
     def shapes(self):
         """(shapes, unit ids) for ShardedState: one unit per block."""
@@ -66,7 +71,7 @@ class ResidualMLP:
     def forward(self, layout: Layout, full: torch.Tensor, x: torch.Tensor, step: int = 0, row0: int = 0) -> torch.Tensor:
         """x [rows, width] through all blocks; what backward needs is kept until then."""
         v, ws = tensor_views(layout, full), self._scratch(x)
-        self.saved = []
+        self.saved, self.stream = [], _current_stream(x)
         for b in range(self.blocks):
             w1, b1, w2, b2 = v[4 * b:4 * b + 4]
             h = x.new_empty(x.shape[0], self.hidden)
@@ -83,8 +88,13 @@ class ResidualMLP:
         """The parameters' gradients into the full-layout buffer `grad` (its dtype; added to it
         with accumulate), and the gradient of forward's x."""
         v, g, ws = tensor_views(layout, full), tensor_views(layout, grad), self._scratch(dy)
+        stream = _current_stream(dy)
         for b in reversed(range(self.blocks)):
             x, z, h = self.saved.pop()
+            if stream != self.stream:            # their memory is not given out again before this stream has read it
+                for t in (x, z, h):
+                    if t is not None:
+                        t.record_stream(stream)
             w1, _, w2, _ = v[4 * b:4 * b + 4]
             gw1, gb1, gw2, gb2 = g[4 * b:4 * b + 4]
             spec = self._spec(step, b, row0)

@@ -45,3 +45,30 @@ def test_passes_beside_each_other(dtype):
             for u, v in zip(a, b):
                 assert torch.equal(u, v)
     fs.fsdp_check_status()
+
+
+def test_forward_on_one_stream_backward_on_another():
+    """What forward kept is read by a backward that another stream gets to late, while the first
+    stream allocates and fills new tensors of the same sizes."""
+    mlp, layout, full, g = build(256, 1024, torch.bfloat16)
+    x, dy = ((torch.randn(700, 256, generator=g, device="cuda")).bfloat16() for _ in range(2))
+    want, grad = torch.zeros_like(full), torch.zeros_like(full)
+    mlp.forward(layout, full, x, 1)
+    mlp.backward(layout, full, want, dy, 1)
+    busy = torch.randn(8192, 8192, device="cuda").bfloat16()
+    torch.cuda.synchronize()
+    first, second = torch.cuda.Stream(), torch.cuda.Stream()
+    with torch.cuda.stream(first):
+        mlp.forward(layout, full, x, 1)
+    second.wait_stream(first)
+    with torch.cuda.stream(second):
+        for _ in range(20):
+            busy @ busy
+        mlp.backward(layout, full, grad, dy, 1)
+    with torch.cuda.stream(first):
+        for n in (256, 1024):
+            for _ in range(6):
+                torch.full((700, n), float("nan"), dtype=torch.bfloat16, device="cuda")
+    torch.cuda.synchronize()
+    fs.fsdp_check_status()
+    assert torch.equal(grad, want)

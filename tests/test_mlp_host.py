@@ -38,3 +38,30 @@ def test_every_pass_has_scratch_of_its_own(calls):
     for one in scratch:
         assert len({w.data_ptr() for w in one}) == 1 and all(w.numel() >= need for w in one)
     assert len({one[0].data_ptr() for one in scratch}) == len(scratch)
+
+
+class Kept:
+    """A tensor's stand-in that notes the streams it is recorded for."""
+
+    def __init__(self):
+        self.streams = []
+
+    def record_stream(self, stream):
+        self.streams.append(stream)
+
+
+def test_what_forward_kept_outlives_a_backward_on_another_stream(calls, monkeypatch):
+    """The caching allocator gives a freed tensor's memory out again in the order of the stream
+    that it was made on; what backward reads on another one has to be recorded for it."""
+    mlp, layout, full = build()
+    x = torch.zeros(7, 24)
+    for streams, recorded in (((1, 1), []), ((1, 2), [2])):
+        monkeypatch.setattr(mlp_module, "_current_stream", lambda t: streams[0])
+        mlp.forward(layout, full, x)
+        mlp.saved = kept = [tuple(Kept() for _ in saved) for saved in mlp.saved]
+        kept = [k for saved in kept for k in saved]
+        assert len(kept) == 6
+        monkeypatch.setattr(mlp_module, "_current_stream", lambda t: streams[1])
+        monkeypatch.setattr(mlp_module.torch, "empty_like", lambda t: x)
+        mlp.backward(layout, full, full, x)
+        assert all(k.streams == recorded for k in kept)
