@@ -172,8 +172,11 @@ def _ptr(x) -> Optional[int]:
     return x.data_ptr()
 
 
-def _stream(stream) -> Optional[int]:
+def _stream(stream, device=None) -> Optional[int]:
+    """A stream's handle; None: the current one (of the current device, where its index is known)."""
     if stream is None:
+        if device is not None:
+            return torch._C._cuda_getCurrentRawStream(device)
         if torch.cuda.is_initialized():          # the raw handle alone: a Stream object costs 3 us
             return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
         return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else None
@@ -450,14 +453,30 @@ def fsdp_zero1_adamw_broadcast(layout: Layout, unit_begin: int, unit_end: int, g
 
 
 # -- layers between the all-gather and the reduce-scatter -------------------------
-def _operand(x, name: str, dtype):
-    """(rows, cols, address, row stride) of a CUDA matrix whose rows are contiguous."""
+# All tensors of a call, its workspace too, lie on the current device.
+def _refuse_device(x, name: str, device) -> None:
+    if not x.is_cuda:
+        raise ValueError(f"{name} is not a CUDA tensor")
+    at = x.get_device()
+    if device is None:
+        raise ValueError(f"{name} is on cuda:{at}, the current device is cuda:{torch.cuda.current_device()}")
+    raise ValueError(f"{name} is on cuda:{at}, the first operand on cuda:{device}")
+
+
+def _device(x):
+    """The device of a call's first tensor, where all others have to be: the current one, else None."""
+    at = x.get_device()
+    return at if at >= 0 and at == torch.cuda.current_device() else None
+
+
+def _operand(x, name: str, dtype, device):
+    """(rows, cols, address, row stride) of a matrix on the device whose rows are contiguous."""
     if x.dtype is not dtype:
         raise TypeError(f"{name} is {x.dtype}, expected {dtype}")
     if x.dim() != 2:
         raise ValueError(f"{name} is {tuple(x.shape)}, expected a matrix")
-    if not x.is_cuda:
-        raise ValueError(f"{name} is not a CUDA tensor")
+    if x.get_device() != device:
+        _refuse_device(x, name, device)
     rows, cols = x.shape
     ld, one = x.stride()
     if one != 1 and cols > 1:
@@ -467,9 +486,9 @@ def _operand(x, name: str, dtype):
     return rows, cols, x.data_ptr(), ld
 
 
-def _matrix(x, name: str, rows: int, cols: int, dtype):
+def _matrix(x, name: str, rows: int, cols: int, dtype, device):
     """(address, row stride) of such a matrix of the given shape."""
-    r, c, p, ld = _operand(x, name, dtype)
+    r, c, p, ld = _operand(x, name, dtype, device)
     if r != rows or c != cols:
         raise ValueError(f"{name} is {tuple(x.shape)}, expected {(rows, cols)}")
     return p, ld
@@ -478,13 +497,13 @@ def _matrix(x, name: str, rows: int, cols: int, dtype):
 _NO_MATRIX = (None, 0)
 
 
-def _vector(x, name: str, n: int, dtype):
+def _vector(x, name: str, n: int, dtype, device):
     if x.dtype is not dtype:
         raise TypeError(f"{name} is {x.dtype}, expected {dtype}")
     if x.shape != (n,):
         raise ValueError(f"{name} is {tuple(x.shape)}, expected {(n,)}")
-    if not x.is_cuda:
-        raise ValueError(f"{name} is not a CUDA tensor")
+    if x.get_device() != device:
+        _refuse_device(x, name, device)
     if n > 1 and x.stride(0) != 1:
         raise ValueError(f"{name} must be contiguous")
     return x.data_ptr()
@@ -499,7 +518,9 @@ def _act(act) -> int:
     return code
 
 
-def _workspace(ws):
+def _workspace(ws, device):
+    if ws.get_device() != device:
+        _refuse_device(ws, "workspace", device)
     return (_ptr(ws), ws.numel() * ws.element_size())
 
 
@@ -522,18 +543,18 @@ def fsdp_linear_forward(x, w, y, bias=None, act="none", preact=None, dropout: Op
                         residual=None, workspace=None, stream=None) -> None:
     """y = residual + drop(act(x w^T + bias)); z = x w^T + bias into preact where given.
     x [rows, in], w [out, in], y / preact / residual [rows, out], bias [out], one dtype."""
-    code, dt = _dtype_code(x), x.dtype
-    rows, cin, px, ldx = _operand(x, "x", dt)
-    cout, wcols, pw, ldw = _operand(w, "w", dt)
+    code, dt, dev = _dtype_code(x), x.dtype, _device(x)
+    rows, cin, px, ldx = _operand(x, "x", dt, dev)
+    cout, wcols, pw, ldw = _operand(w, "w", dt, dev)
     if wcols != cin:
         raise ValueError(f"w is {tuple(w.shape)}, expected {(cout, cin)}")
-    py, ldy = _matrix(y, "y", rows, cout, dt)
-    pr, ldr = _NO_MATRIX if residual is None else _matrix(residual, "residual", rows, cout, dt)
-    pz, ldz = _NO_MATRIX if preact is None else _matrix(preact, "preact", rows, cout, dt)
-    pb = None if bias is None else _vector(bias, "bias", cout, dt)
-    pws, nws = _NO_MATRIX if workspace is None else _workspace(workspace)
+    py, ldy = _matrix(y, "y", rows, cout, dt, dev)
+    pr, ldr = _NO_MATRIX if residual is None else _matrix(residual, "residual", rows, cout, dt, dev)
+    pz, ldz = _NO_MATRIX if preact is None else _matrix(preact, "preact", rows, cout, dt, dev)
+    pb = None if bias is None else _vector(bias, "bias", cout, dt, dev)
+    pws, nws = _NO_MATRIX if workspace is None else _workspace(workspace, dev)
     rc = lib().fsdp_linear_forward(rows, cin, cout, code, px, ldx, pw, ldw, pb, _act(act), _drop(dropout), pr, ldr, py, ldy,
-                                   pz, ldz, pws, nws, _stream(stream))
+                                   pz, ldz, pws, nws, _stream(stream, dev))
     if rc:
         _check(rc, "fsdp_linear_forward")
 
@@ -542,17 +563,17 @@ def fsdp_linear_dgrad(dz, w, dx, act="none", preact=None, dropout: Optional[Drop
                       workspace=None, stream=None) -> None:
     """dx = residual + act'(preact) * drop(dz w): dz [rows, out], w [out, in], dx / preact /
     residual [rows, in]; act, preact and dropout are those of the layer before."""
-    code, dt = _dtype_code(dz), dz.dtype
-    rows, cout, pg, ldg = _operand(dz, "dz", dt)
-    wrows, cin, pw, ldw = _operand(w, "w", dt)
+    code, dt, dev = _dtype_code(dz), dz.dtype, _device(dz)
+    rows, cout, pg, ldg = _operand(dz, "dz", dt, dev)
+    wrows, cin, pw, ldw = _operand(w, "w", dt, dev)
     if wrows != cout:
         raise ValueError(f"w is {tuple(w.shape)}, expected {(cout, cin)}")
-    px, ldx = _matrix(dx, "dx", rows, cin, dt)
-    pz, ldz = _NO_MATRIX if preact is None else _matrix(preact, "preact", rows, cin, dt)
-    pr, ldr = _NO_MATRIX if residual is None else _matrix(residual, "residual", rows, cin, dt)
-    pws, nws = _NO_MATRIX if workspace is None else _workspace(workspace)
+    px, ldx = _matrix(dx, "dx", rows, cin, dt, dev)
+    pz, ldz = _NO_MATRIX if preact is None else _matrix(preact, "preact", rows, cin, dt, dev)
+    pr, ldr = _NO_MATRIX if residual is None else _matrix(residual, "residual", rows, cin, dt, dev)
+    pws, nws = _NO_MATRIX if workspace is None else _workspace(workspace, dev)
     rc = lib().fsdp_linear_dgrad(rows, cin, cout, code, pg, ldg, pw, ldw, _act(act), pz, ldz, _drop(dropout), pr, ldr, px,
-                                 ldx, pws, nws, _stream(stream))
+                                 ldx, pws, nws, _stream(stream, dev))
     if rc:
         _check(rc, "fsdp_linear_dgrad")
 
@@ -560,27 +581,27 @@ def fsdp_linear_dgrad(dz, w, dx, act="none", preact=None, dropout: Optional[Drop
 def fsdp_linear_wgrad(dz, x, dw, db=None, accumulate: bool = False, workspace=None, stream=None) -> None:
     """dw (+)= dz^T x and db (+)= the column sums of dz: dz [rows, out], x [rows, in] of one
     dtype, dw [out, in] and db [out] of one dtype (a gradient replica's, or fp32)."""
-    code, dt = _dtype_code(dz), dz.dtype
-    rows, cout, pg, ldg = _operand(dz, "dz", dt)
-    xrows, cin, px, ldx = _operand(x, "x", dt)
+    code, dt, dev = _dtype_code(dz), dz.dtype, _device(dz)
+    rows, cout, pg, ldg = _operand(dz, "dz", dt, dev)
+    xrows, cin, px, ldx = _operand(x, "x", dt, dev)
     if xrows != rows:
         raise ValueError(f"x is {tuple(x.shape)}, expected {(rows, cin)}")
-    pw, ldw = _matrix(dw, "dw", cout, cin, dw.dtype)
-    pb = None if db is None else _vector(db, "db", cout, dw.dtype)
-    pws, nws = _NO_MATRIX if workspace is None else _workspace(workspace)
+    pw, ldw = _matrix(dw, "dw", cout, cin, dw.dtype, dev)
+    pb = None if db is None else _vector(db, "db", cout, dw.dtype, dev)
+    pws, nws = _NO_MATRIX if workspace is None else _workspace(workspace, dev)
     rc = lib().fsdp_linear_wgrad(rows, cin, cout, code, pg, ldg, px, ldx, pw, ldw, pb, _dtype_code(dw), 1 if accumulate else 0,
-                                 pws, nws, _stream(stream))
+                                 pws, nws, _stream(stream, dev))
     if rc:
         _check(rc, "fsdp_linear_wgrad")
 
 
 def fsdp_dropout(x, y, dropout: Optional[DropoutSpec], residual=None, stream=None) -> None:
     """y = residual + drop(x), [rows, cols] each; the same call on the gradient is its backward."""
-    code, dt = _dtype_code(x), x.dtype
-    rows, cols, px, ldx = _operand(x, "x", dt)
-    py, ldy = _matrix(y, "y", rows, cols, dt)
-    pr, ldr = _NO_MATRIX if residual is None else _matrix(residual, "residual", rows, cols, dt)
-    rc = lib().fsdp_dropout(rows, cols, code, px, ldx, _drop(dropout), pr, ldr, py, ldy, _stream(stream))
+    code, dt, dev = _dtype_code(x), x.dtype, _device(x)
+    rows, cols, px, ldx = _operand(x, "x", dt, dev)
+    py, ldy = _matrix(y, "y", rows, cols, dt, dev)
+    pr, ldr = _NO_MATRIX if residual is None else _matrix(residual, "residual", rows, cols, dt, dev)
+    rc = lib().fsdp_dropout(rows, cols, code, px, ldx, _drop(dropout), pr, ldr, py, ldy, _stream(stream, dev))
     if rc:
         _check(rc, "fsdp_dropout")
 
