@@ -172,13 +172,15 @@ def _ptr(x) -> Optional[int]:
     return x.data_ptr()
 
 
+# The raw handle alone: a Stream object costs 3 us.  torch keeps this call to itself, so it may go.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream, device=None) -> Optional[int]:
     """A stream's handle; None: the current one (of the current device, where its index is known)."""
     if stream is None:
-        if device is not None:
-            return torch._C._cuda_getCurrentRawStream(device)
-        if torch.cuda.is_initialized():          # the raw handle alone: a Stream object costs 3 us
-            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        if _raw_stream is not None and (device is not None or torch.cuda.is_initialized()):
+            return _raw_stream(torch.cuda.current_device() if device is None else device)
         return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else None
     if isinstance(stream, int):
         return stream

@@ -79,3 +79,19 @@ def test_a_tensor_elsewhere_is_refused(call, name, where, text):
 def test_tensors_of_a_gpu_that_is_not_current_are_refused(call):
     with pytest.raises(ValueError, match="current device"):
         CALLS[call](**{k: Tensor(*t.shape, device=1) for k, t in tensors(call).items()})
+
+
+def test_stream_handle_without_the_private_call(monkeypatch):
+    """The current stream's handle, where torch does not offer it without a Stream object."""
+    monkeypatch.undo()
+
+    class Stream:
+        cuda_stream = 77
+
+    monkeypatch.setattr(fs, "_raw_stream", None, raising=False)
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    monkeypatch.setattr(torch.cuda, "is_available", lambda: True)
+    monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: Stream)
+    assert fs._stream(None) == 77 and fs._stream(None, 0) == 77 and fs._stream(Stream) == 77 and fs._stream(5) == 5
