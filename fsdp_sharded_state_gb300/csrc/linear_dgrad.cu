@@ -9,6 +9,6 @@ cudaError_t launch_linear_dgrad(const LinProblem& p, cudaStream_t st) {
     return launch_product<kDgrad, uint16_t, 1, 0>(p, launch_pair_dgrad, st);
 }
 
-cudaError_t take_wait_error_dgrad(unsigned int* flag) { return take_local_wait_error(flag); }
+cudaError_t take_wait_error_dgrad(unsigned int* flag) { return take_product_wait_error(flag); }
 
 }  // namespace fsdp

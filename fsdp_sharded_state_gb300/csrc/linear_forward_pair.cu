@@ -19,6 +19,6 @@ cudaError_t launch_pair_forward(const LinProblem& p, int bn, cudaStream_t st) {
     return cudaErrorInvalidValue;
 }
 
-cudaError_t take_wait_error_forward_pair(unsigned int* flag) { return take_local_wait_error(flag); }
+cudaError_t take_wait_error_forward_pair(unsigned int* flag) { return take_product_wait_error(flag); }
 
 }  // namespace fsdp

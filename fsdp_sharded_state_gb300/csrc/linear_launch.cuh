@@ -78,6 +78,15 @@ int64_t whole_tiles(int64_t tiles, int64_t room) {
     return C::CUT && 2 * rem <= room ? tiles - rem : tiles;
 }
 
+// Whether this translation unit has launched a product (or captured one, to run at any time
+// after): before that fsdp_check_status has nothing to ask of it, and reads no word, 9 us each.
+std::atomic<bool> g_launched{false};
+
+cudaError_t take_product_wait_error(unsigned int* flag) {
+    *flag = 0;
+    return g_launched.load(std::memory_order_relaxed) ? take_local_wait_error(flag) : cudaSuccess;
+}
+
 // Launches one configuration: splits CTAs per tile (SPLIT), else a persistent grid.
 template <class C>
 cudaError_t launch_cfg(const LinProblem& p, int splits, cudaStream_t st, int slabs = 1) {
@@ -112,6 +121,7 @@ cudaError_t launch_cfg(const LinProblem& p, int splits, cudaStream_t st, int sla
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = per > 1 ? 2 : 1;
+    g_launched.store(true, std::memory_order_relaxed);
     return cudaLaunchKernelEx(&cfg, k_linear<C>, ma, mb, sh, p.epi, detail::kWaitNs);
 }
 

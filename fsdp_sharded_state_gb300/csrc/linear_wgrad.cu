@@ -93,6 +93,6 @@ cudaError_t launch_join(const float* part, const float* db_part, int parts, int6
                     : join<float>(part, db_part, parts, rows, cols, ld, ep, st);
 }
 
-cudaError_t take_wait_error_wgrad(unsigned int* flag) { return take_local_wait_error(flag); }
+cudaError_t take_wait_error_wgrad(unsigned int* flag) { return take_product_wait_error(flag); }
 
 }  // namespace fsdp
