@@ -74,7 +74,8 @@ int64_t plane_elems(int64_t rows, int64_t cols) { return rows * packed_ld(cols);
 int64_t packed_bytes(int64_t rows, int64_t cols, int planes) { return round_up(planes * plane_elems(rows, cols) * 2, 256); }
 
 // The operands of a product: a matrix that the tensor maps can read where it is, or its
-// packed copy in the workspace.
+// packed copy in the workspace.  The calls of a few rows (use_skinny) take no room for the
+// weight, which they read where it is; the rows' own, a few KB, is taken whatever kernel runs.
 struct Packer {
     unsigned char* ws;
     size_t left;
@@ -133,7 +134,8 @@ size_t fsdp_linear_workspace_bytes(int64_t rows, int64_t in, int64_t out, int32_
     if (elem_dtype == FSDP_BF16 && aligned) return slabs;
     const int planes = elem_dtype == FSDP_F32 ? 3 : 1;
     const int64_t x = packed_bytes(rows, in, planes), w = packed_bytes(out, in, planes), z = packed_bytes(rows, out, planes);
-    return size_t(x + w + z - std::min({x, w, z})) + slabs;   // the two largest: no call reads all three
+    auto weight = [&](LinMode mode) { return use_skinny(mode, elem_dtype == FSDP_BF16, rows, in, out) ? 0 : w; };
+    return size_t(std::max({x + weight(kForward), z + weight(kDgrad), x + z})) + slabs;
 }
 
 int fsdp_linear_forward(int64_t rows, int64_t in, int64_t out, int32_t elem_dtype, const void* x, int64_t ldx, const void* w,
@@ -172,9 +174,10 @@ int fsdp_linear_forward(int64_t rows, int64_t in, int64_t out, int32_t elem_dtyp
     if (bias && !aligned16(bias)) ep.vec = 0;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     Packer pk{static_cast<unsigned char*>(workspace), workspace_bytes, {}};
-    if ((rc = pk.operand(w, out, in, ldw, elem_dtype, &p.cols_op)) || (rc = pk.operand(x, rows, in, ldx, elem_dtype, &p.rows_op))) return rc;
-    if (use_skinny(kForward, elem_dtype == FSDP_BF16, rows, in, out))
-        return run_skinny(kForward, elem_dtype, x, ldx, w, ldw, in, ep, st);
+    const bool skinny = use_skinny(kForward, elem_dtype == FSDP_BF16, rows, in, out);
+    if (!skinny && (rc = pk.operand(w, out, in, ldw, elem_dtype, &p.cols_op))) return rc;
+    if ((rc = pk.operand(x, rows, in, ldx, elem_dtype, &p.rows_op))) return rc;
+    if (skinny) return run_skinny(kForward, elem_dtype, x, ldx, w, ldw, in, ep, st);
     if (elem_dtype == FSDP_F32 && use_small(kForward, rows, in, out))
         return run_small(kForward, x, ldx, w, ldw, in, false, nullptr, ep, st);
     return run_product(p, pk, elem_dtype, st);
@@ -214,9 +217,10 @@ int fsdp_linear_dgrad(int64_t rows, int64_t in, int64_t out, int32_t elem_dtype,
     ep.vec = std::min({row_class(dx, lddx, es), row_class(residual, ldr, es), row_class(ep.preact, ldz, es)});
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     Packer pk{static_cast<unsigned char*>(workspace), workspace_bytes, {}};
-    if ((rc = pk.operand(w, out, in, ldw, elem_dtype, &p.cols_op)) || (rc = pk.operand(dz, rows, out, lddz, elem_dtype, &p.rows_op))) return rc;
-    if (use_skinny(kDgrad, elem_dtype == FSDP_BF16, rows, in, out))
-        return run_skinny(kDgrad, elem_dtype, dz, lddz, w, ldw, out, ep, st);
+    const bool skinny = use_skinny(kDgrad, elem_dtype == FSDP_BF16, rows, in, out);
+    if (!skinny && (rc = pk.operand(w, out, in, ldw, elem_dtype, &p.cols_op))) return rc;
+    if ((rc = pk.operand(dz, rows, out, lddz, elem_dtype, &p.rows_op))) return rc;
+    if (skinny) return run_skinny(kDgrad, elem_dtype, dz, lddz, w, ldw, out, ep, st);
     if (elem_dtype == FSDP_F32 && use_small(kDgrad, rows, in, out))
         return run_small(kDgrad, dz, lddz, w, ldw, out, false, nullptr, ep, st);
     return run_product(p, pk, elem_dtype, st);

@@ -604,7 +604,8 @@ typedef struct {
 
 /* Scratch bytes of the three linear calls at these sizes: an upper bound over forward,
  * dgrad and wgrad.  Counted are: room for aligned copies of two operands, or, for FSDP_F32,
- * for their three bf16 terms; and for wgrad with many rows and a small out x in, partial sums
+ * for their three bf16 terms (of x and dz alone for one to four rows of FSDP_F32, whose calls
+ * read the weight where it is); and for wgrad with many rows and a small out x in, partial sums
  * of slabs of the rows (under 2 MB).  aligned != 0: every x, w and dz has a base address and a
  * row stride that are multiples of 16 bytes, so that FSDP_BF16 needs no copies.  0 for
  * arguments that the calls refuse.  Host only. */
