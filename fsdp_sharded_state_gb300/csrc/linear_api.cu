@@ -13,6 +13,7 @@ using namespace fsdp::detail;
 namespace {
 
 constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1024;
+constexpr int64_t kMaxElems = int64_t(1) << 40;              // of a matrix: sizes in bytes, three planes of it too, stay far below 2^63
 
 int elem_size(int32_t dtype) { return dtype == FSDP_F32 ? 4 : 2; }
 bool known(int32_t dtype) { return dtype == FSDP_F32 || dtype == FSDP_BF16; }
@@ -21,6 +22,7 @@ int check_dims(int64_t rows, int64_t in, int64_t out, int32_t dtype) {
     if (!known(dtype)) return FSDP_EDTYPE;
     if (rows < 0 || in < 1 || out < 1) return FSDP_ESHAPE;
     if (rows > kMaxDim || in > kMaxDim || out > kMaxDim) return FSDP_EOVERFLOW;
+    if (rows * in > kMaxElems || rows * out > kMaxElems || in * out > kMaxElems) return FSDP_EOVERFLOW;
     return FSDP_OK;
 }
 
@@ -280,7 +282,7 @@ int fsdp_dropout(int64_t rows, int64_t cols, int32_t elem_dtype, const void* x, 
     NvtxRange nvtx_range("fsdp_dropout");
     if (!known(elem_dtype)) return FSDP_EDTYPE;
     if (rows < 0 || cols < 0) return FSDP_ESHAPE;
-    if (rows > kMaxDim || cols > kMaxDim || (cols > 0 && rows > (int64_t(1) << 40) / cols)) return FSDP_EOVERFLOW;
+    if (rows > kMaxDim || cols > kMaxDim || rows * cols > kMaxElems) return FSDP_EOVERFLOW;
     Drop d;
     int rc = make_drop(drop, rows, &d);
     if (rc) return rc;

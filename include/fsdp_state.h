@@ -572,7 +572,8 @@ int fsdp_reduce_scatter_adamw_noalloc(const fsdp_layout* layout, int32_t unit_be
  *     a NaN, the results that depend on it are not finite, but an infinity may come out as
  *     a NaN.
  *   - rows may be 0 (nothing is read; wgrad without accumulate writes zeros); in and out
- *     are at least 1; all three and the strides are below 2^31 (else FSDP_EOVERFLOW).
+ *     are at least 1; all three and the strides are below 2^31, and no matrix has more than
+ *     2^40 elements (else FSDP_EOVERFLOW).
  *   - residual, bias and preact may be NULL.  With an activation, dgrad needs preact, the z
  *     that forward wrote; forward writes it where preact is given.  y (dx) may be the very
  *     residual buffer, with its stride; no other output may overlap an input.
@@ -632,7 +633,7 @@ int fsdp_linear_wgrad(int64_t rows, int64_t in, int64_t out, int32_t elem_dtype,
                       int32_t accumulate, void* workspace, size_t workspace_bytes, fsdp_stream_t stream);
 
 /* y = residual + drop(x), all [rows][cols] of elem_dtype; y may be x or residual (with its
- * stride).  rows * cols < 2^40. */
+ * stride). */
 int fsdp_dropout(int64_t rows, int64_t cols, int32_t elem_dtype, const void* x, int64_t ldx,
                  const fsdp_dropout_spec* drop, const void* residual, int64_t ldr, void* y, int64_t ldy,
                  fsdp_stream_t stream);
