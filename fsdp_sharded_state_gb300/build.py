@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import os
+import re
 import shutil
 import subprocess
 
@@ -41,6 +42,18 @@ def _newer(target: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+PAIR_REGISTERS = 168
+
+
+def check_pair_registers(log: str) -> None:
+    """The CTA-pair kernels of linear_kernel.cuh share out the registers of their launch by figures
+    that hold for PAIR_REGISTERS a thread; with any other count they would be refused at their first
+    launch.  log: what nvcc -Xptxas -v printed."""
+    for name, used in re.findall(r"Compiling entry function '(\w+)'.*?Used (\d+) registers", log, re.S):
+        if re.search(r"k_linearI\w*LinCfgILi\dE[ft]Li2E", name) and int(used) != PAIR_REGISTERS:
+            raise RuntimeError(f"{name}: {used} registers, expected {PAIR_REGISTERS}")
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
     os.makedirs(OUT, exist_ok=True)
     cc = nvcc()
@@ -53,11 +66,20 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         objs.append(o)
         if force or ptxas_info or _newer(o, [s, *headers, __file__]):
             flags = list(NVFLAGS)
-            if ptxas_info and src.endswith(".cu"):
+            if src.endswith(".cu") and (ptxas_info or src.startswith("linear_")):
                 flags += ["-Xptxas", "-v"]
             jobs.append([cc, *ARCH, *flags, "-c", s, "-o", o])
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
         results = list(ex.map(lambda c: subprocess.run(c, capture_output=True, text=True), jobs))
+    refused = []
+    for cmd, r in zip(jobs, results):
+        try:
+            check_pair_registers(r.stdout + r.stderr)
+        except RuntimeError as e:
+            refused.append(str(e))
+            os.remove(cmd[cmd.index("-o") + 1])
+    if refused:
+        raise RuntimeError("\n".join(refused))
     for cmd, r in zip(jobs, results):
         if verbose or ptxas_info:
             print(r.stdout + r.stderr)

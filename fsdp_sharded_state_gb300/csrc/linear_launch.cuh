@@ -56,7 +56,7 @@ cudaError_t prepare_kernel(int dev) {
     static std::atomic<uint64_t> done{0};
     if (dev < 64 && (done.load(std::memory_order_relaxed) >> dev & 1)) return cudaSuccess;
     cudaError_t e = cudaFuncSetAttribute(k_linear<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-    if (C::REGS && e == cudaSuccess) {             // the registers that the warpgroups share out are there
+    if (C::REGS && e == cudaSuccess) {             // the registers that the warpgroups share out are there (build.py checks them too)
         cudaFuncAttributes a;
         e = cudaFuncGetAttributes(&a, k_linear<C>);
         if (e == cudaSuccess && a.numRegs != 168) return cudaErrorInvalidConfiguration;
