@@ -262,8 +262,8 @@ cudaError_t launch_skinny(const SkinnyProblem& p, cudaStream_t st) {
 }
 
 // Measured on GB300 (us, this file / the tensor cores), weight 6432 x 3776 (floors 14.3 fp32,
-// 7.2 bf16): forward fp32 1 row 21 / 67, 4 rows 22 / 67, 12 rows 47 / 67; dgrad fp32 1 row 26 /
-// 70, 4 rows 37 / 70, 8 rows two passes of that; forward bf16 1 row 13.7 / 12.6, 4 rows 27 /
+// 7.2 bf16): forward fp32 1 row 21 / 67, 4 rows 22 / 67, 12 rows 47 / 67; dgrad fp32 1 row 25 /
+// 70, 4 rows 36 / 70, 8 rows two passes of that; forward bf16 1 row 13.7 / 12.6, 4 rows 27 /
 // 12.7, at 2048 x 2048 2.8 / 6.0 and 4.7 / 5.9; dgrad bf16 36 / 13.
 bool use_skinny(LinMode mode, bool bf16, int64_t rows, int64_t in, int64_t out) {
     if (mode == kDgrad) return !bf16 && rows <= 4;

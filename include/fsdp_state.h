@@ -558,7 +558,9 @@ int fsdp_reduce_scatter_adamw_noalloc(const fsdp_layout* layout, int32_t unit_be
  * where x is [rows][in], w [out][in] (a Linear's weight), z and y [rows][out], and dz is
  * the gradient of the layer's own z.  For layers 1, 2 with z2 = drop(act(z1)) w2^T + b2,
  * dgrad with layer 2's weight, layer 1's preact, activation and dropout gives the
- * gradient of z1.
+ * gradient of z1.  act' is applied to such a product alone: the gradient act'(z) * drop(dy) of
+ * an activation whose output goes elsewhere (onto a residual, or out of the last layer) is the
+ * caller's; without an activation it is dropout's.
  *
  * Conventions shared by the four calls
  *   - Matrices are row-major with a row stride (ld*, in elements) of at least their width;
@@ -566,11 +568,15 @@ int fsdp_reduce_scatter_adamw_noalloc(const fsdp_layout* layout, int32_t unit_be
  *     FSDP_EALIGN): a FLAT layout's tensors start at any element.
  *   - elem_dtype is the type of every matrix and of bias; wgrad's dw and db have
  *     grad_dtype.  Products accumulate in fp32; everything up to the store is fp32 and each
- *     output is rounded once, to nearest even.  fp32 operands are split exactly into three
- *     bf16 terms and multiplied as six bf16 products (relative error of the order of
- *     2^-24 per product, as fp32 products have); where an fp32 operand holds an infinity or
- *     a NaN, the results that depend on it are not finite, but an infinity may come out as
- *     a NaN.
+ *     output is rounded once, to nearest even.  Where the output is bf16 the tensor cores'
+ *     accumulators hold the whole sum; they round towards zero, 1.6e-8 of the sum for 16
+ *     products, 9e-6 at 8192.  For fp32 outputs they are added to fp32 sums every few steps: within
+ *     2e-6 in norm up to 16384.  fp32 operands are split into three bf16 terms, exactly but for
+ *     magnitudes below about 2^-110, and multiplied as six bf16 products (relative error of the
+ *     order of 2^-24 per product, as fp32 products have), or, in products of a few rows or of small
+ *     matrices, by fp32 instructions.  Where an fp32 operand holds an infinity or a NaN, the
+ *     results that depend on it are not finite, but an infinity may come out as a NaN: it does from
+ *     the six products, and the sizes decide which way a product takes.
  *   - rows may be 0 (nothing is read; wgrad without accumulate writes zeros); in and out
  *     are at least 1; all three and the strides are below 2^31, and no matrix has more than
  *     2^40 elements (else FSDP_EOVERFLOW).
@@ -578,7 +584,8 @@ int fsdp_reduce_scatter_adamw_noalloc(const fsdp_layout* layout, int32_t unit_be
  *     that forward wrote; forward writes it where preact is given.  y (dx) may be the very
  *     residual buffer, with its stride; no other output may overlap an input.
  *   - act: FSDP_ACT_GELU is z Phi(z) with the error function, FSDP_ACT_SILU z / (1 + e^-z);
- *     relu's derivative at 0 is 0.
+ *     relu's derivative at 0 is 0.  gelu is within 3e-7 before the rounding, an absolute bound:
+ *     below z = -4, where its own value is under 1.3e-4, it has fewer digits than the output.
  *   - workspace: device scratch, 16-byte aligned, of at least
  *     fsdp_linear_workspace_bytes(...) bytes (else FSDP_EINVAL); NULL where that is 0.  No
  *     initial contents needed; it is in use until the call's work has run: calls whose work
