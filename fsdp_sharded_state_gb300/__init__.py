@@ -38,7 +38,8 @@ EXPORTS = ("fsdp_layout_create", "fsdp_layout_destroy", "fsdp_layout_query", "fs
            "fsdp_set_rs_kernel", "fsdp_rs_kernel_for", "fsdp_wait_selftest", "fsdp_adamw_step_consts_make",
            "fsdp_reduce_scatter_adamw_consts", "fsdp_adamw_step_consts_upload", "fsdp_collective_payload",
            "fsdp_accumulate_reduce_scatter_adamw", "fsdp_linear_workspace_bytes", "fsdp_linear_forward",
-           "fsdp_linear_dgrad", "fsdp_linear_wgrad", "fsdp_dropout")
+           "fsdp_linear_dgrad", "fsdp_linear_wgrad", "fsdp_dropout", "fsdp_layernorm_forward",
+           "fsdp_layernorm_workspace_bytes", "fsdp_layernorm_backward")
 
 
 class FsdpError(RuntimeError):
@@ -141,6 +142,11 @@ def lib() -> C.CDLL:
                                         vp, sz, vp]
         L.fsdp_linear_wgrad.argtypes = [i64, i64, i64, i32, vp, i64, vp, i64, vp, i64, vp, i32, i32, vp, sz, vp]
         L.fsdp_dropout.argtypes = [i64, i64, i32, vp, i64, drop, vp, i64, vp, i64, vp]
+        L.fsdp_layernorm_forward.argtypes = [i64, i64, i32, vp, i64, vp, vp, C.c_float, vp, i64, vp, vp, vp]
+        L.fsdp_layernorm_workspace_bytes.argtypes = [i64, i64]
+        L.fsdp_layernorm_workspace_bytes.restype = sz
+        L.fsdp_layernorm_backward.argtypes = [i64, i64, i32, vp, i64, vp, i64, vp, vp, vp, vp, i64, vp, i64, vp, vp, i32, i32, vp,
+                                              sz, vp]
         L.fsdp_check_status.argtypes = [vp]
         L.fsdp_set_rs_kernel.argtypes = [i32]
         L.fsdp_rs_kernel_for.argtypes = [vp, i32]
@@ -606,6 +612,50 @@ def fsdp_dropout(x, y, dropout: Optional[DropoutSpec], residual=None, stream=Non
     rc = lib().fsdp_dropout(rows, cols, code, px, ldx, _drop(dropout), pr, ldr, py, ldy, _stream(stream, dev))
     if rc:
         _check(rc, "fsdp_dropout")
+
+
+def fsdp_layernorm_forward(x, y, weight=None, bias=None, mean=None, rstd=None, eps: float = 1e-5, stream=None) -> None:
+    """y = (x - mean) * rstd * weight + bias per row: x, y [rows, cols], weight and bias [cols], one
+    dtype; the rows' mean and rstd [rows], float32, are written where given."""
+    code, dt, dev = _dtype_code(x), x.dtype, _device(x)
+    rows, cols, px, ldx = _operand(x, "x", dt, dev)
+    py, ldy = _matrix(y, "y", rows, cols, dt, dev)
+    pw = None if weight is None else _vector(weight, "weight", cols, dt, dev)
+    pb = None if bias is None else _vector(bias, "bias", cols, dt, dev)
+    pm = None if mean is None else _vector(mean, "mean", rows, torch.float32, dev)
+    pr = None if rstd is None else _vector(rstd, "rstd", rows, torch.float32, dev)
+    rc = lib().fsdp_layernorm_forward(rows, cols, code, px, ldx, pw, pb, eps, py, ldy, pm, pr, _stream(stream, dev))
+    if rc:
+        _check(rc, "fsdp_layernorm_forward")
+
+
+def fsdp_layernorm_workspace_bytes(rows: int, cols: int) -> int:
+    """Scratch bytes of fsdp_layernorm_backward with dw or db."""
+    return int(lib().fsdp_layernorm_workspace_bytes(rows, cols))
+
+
+def fsdp_layernorm_backward(dy, x, mean, rstd, dx, weight=None, dw=None, db=None, residual=None, accumulate: bool = False,
+                            workspace=None, stream=None) -> None:
+    """dx = residual + the gradient of x from that of y; dw (+)= the sums over rows of dy (x - mean)
+    rstd, db (+)= those of dy: dy, x, dx, residual [rows, cols] and weight [cols] of one dtype, mean
+    and rstd [rows] float32 as forward wrote them, dw and db [cols] of one dtype (a gradient
+    replica's, or fp32)."""
+    code, dt, dev = _dtype_code(dy), dy.dtype, _device(dy)
+    rows, cols, pg, ldg = _operand(dy, "dy", dt, dev)
+    px, ldx = _matrix(x, "x", rows, cols, dt, dev)
+    pm, pr = _vector(mean, "mean", rows, torch.float32, dev), _vector(rstd, "rstd", rows, torch.float32, dev)
+    po, ldo = _matrix(dx, "dx", rows, cols, dt, dev)
+    pw = None if weight is None else _vector(weight, "weight", cols, dt, dev)
+    ps, lds = _NO_MATRIX if residual is None else _matrix(residual, "residual", rows, cols, dt, dev)
+    first = dw if dw is not None else db
+    gcode = code if first is None else _dtype_code(first)
+    pdw = None if dw is None else _vector(dw, "dw", cols, first.dtype, dev)
+    pdb = None if db is None else _vector(db, "db", cols, first.dtype, dev)
+    pws, nws = _NO_MATRIX if workspace is None else _workspace(workspace, dev)
+    rc = lib().fsdp_layernorm_backward(rows, cols, code, pg, ldg, px, ldx, pm, pr, pw, ps, lds, po, ldo, pdw, pdb, gcode,
+                                       1 if accumulate else 0, pws, nws, _stream(stream, dev))
+    if rc:
+        _check(rc, "fsdp_layernorm_backward")
 
 
 def fsdp_reshard(layout: Layout, unit_begin: int, unit_end: int, full=None, master=None, param_shards=None,

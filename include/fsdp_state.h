@@ -645,6 +645,45 @@ int fsdp_dropout(int64_t rows, int64_t cols, int32_t elem_dtype, const void* x, 
                  const fsdp_dropout_spec* drop, const void* residual, int64_t ldr, void* y, int64_t ldy,
                  fsdp_stream_t stream);
 
+/* ---- Layer norm ------------------------------------------------------------------------
+ * The norm in front of a block's linear layers, forward and backward, over the same buffers:
+ * weight and bias are read as views of the full buffer, their gradients are written as views
+ * of a gradient replica or added to an fp32 accumulator.
+ *
+ *   forward    mean, var of a row of x;  rstd = 1 / sqrt(var + eps)
+ *              y = (x - mean) * rstd * weight + bias
+ *   backward   h = (x - mean) * rstd;  g = dy * weight
+ *              dx = residual + rstd * (g - mean of g - h * mean of g h)   (means over the row)
+ *              dw (+)= sum over rows of dy h;   db (+)= sum over rows of dy
+ *
+ *   - Matrices, alignment, dtypes, overlap of launches' workspaces and repeatability as in the
+ *     linear calls above; cols is at most 65536 (else FSDP_EOVERFLOW).  All sums are fp32;
+ *     var is that of the whole row (divided by cols) and formed from the differences to the
+ *     mean; each output is rounded once.
+ *   - weight NULL is all ones, bias NULL all zeros.  mean and rstd are fp32, one per row:
+ *     forward writes them where given, backward reads them (both needed).  eps > 0.
+ *   - rows may be 0 (nothing is read; backward without accumulate writes zeros to dw and db).
+ *   - y may be the very x; dx may be the very dy, x or residual (with its stride).  No other
+ *     output may overlap an input.
+ *   - An infinity or a NaN in a row of x (or dy) makes that row of y (dx) NaN, and those dw and
+ *     db that add it up; no other row is touched by it. */
+int fsdp_layernorm_forward(int64_t rows, int64_t cols, int32_t elem_dtype, const void* x, int64_t ldx, const void* weight,
+                           const void* bias, float eps, void* y, int64_t ldy, float* mean, float* rstd,
+                           fsdp_stream_t stream);
+
+/* Scratch bytes of fsdp_layernorm_backward with dw or db (partial sums, at most
+ * 32 bytes times 152 per column).  0 for arguments that the call refuses.  Host only. */
+size_t fsdp_layernorm_workspace_bytes(int64_t rows, int64_t cols);
+
+/* dx, and dw and db (of grad_dtype) where given: accumulate != 0 adds to what they hold (in
+ * fp32, rounded once), otherwise they are overwritten.  workspace: device scratch, 16-byte
+ * aligned, of at least fsdp_layernorm_workspace_bytes(rows, cols) bytes (else FSDP_EINVAL)
+ * where dw or db is given; contents and overlap as for the linear calls. */
+int fsdp_layernorm_backward(int64_t rows, int64_t cols, int32_t elem_dtype, const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                            const float* mean, const float* rstd, const void* weight, const void* residual, int64_t ldr, void* dx,
+                            int64_t lddx, void* dw, void* db, int32_t grad_dtype, int32_t accumulate, void* workspace,
+                            size_t workspace_bytes, fsdp_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
