@@ -39,7 +39,8 @@ EXPORTS = ("fsdp_layout_create", "fsdp_layout_destroy", "fsdp_layout_query", "fs
            "fsdp_reduce_scatter_adamw_consts", "fsdp_adamw_step_consts_upload", "fsdp_collective_payload",
            "fsdp_accumulate_reduce_scatter_adamw", "fsdp_linear_workspace_bytes", "fsdp_linear_forward",
            "fsdp_linear_dgrad", "fsdp_linear_wgrad", "fsdp_dropout", "fsdp_layernorm_forward",
-           "fsdp_layernorm_workspace_bytes", "fsdp_layernorm_backward")
+           "fsdp_layernorm_workspace_bytes", "fsdp_layernorm_backward", "fsdp_newton_schulz",
+           "fsdp_newton_schulz_workspace_bytes", "fsdp_zero1_muon_broadcast", "fsdp_zero1_muon_workspace_bytes")
 
 
 class FsdpError(RuntimeError):
@@ -78,6 +79,23 @@ class AdamWStepConsts(C.Structure):
     _fields_ = [("decay", C.c_float), ("om1", C.c_float), ("om2", C.c_float), ("step_size", C.c_float),
                 ("bc2s", C.c_float), ("beta1", C.c_float), ("beta2", C.c_float), ("eps", C.c_float),
                 ("n_avg", C.c_float), ("reserved", C.c_float * 3)]
+
+
+MUON_SCALES = {"none": 0, "shape": 1, "rms": 2}
+
+
+class MuonHparams(C.Structure):
+    """Hyper-parameters of the Muon step (fsdp_muon_hparams).  scale: "none" (1), "shape"
+    (sqrt(max(1, rows / cols))) or "rms" (0.2 sqrt(max(rows, cols)))."""
+    _fields_ = [("lr", C.c_float), ("momentum", C.c_float), ("weight_decay", C.c_float), ("eps", C.c_float),
+                ("nesterov", C.c_int32), ("steps", C.c_int32), ("scale", C.c_int32), ("reserved", C.c_int32)]
+
+    def __init__(self, lr: float = 0.02, momentum: float = 0.95, weight_decay: float = 0.0, eps: float = 1e-7,
+                 nesterov: bool = True, steps: int = 5, scale="rms"):
+        code = MUON_SCALES.get(scale) if isinstance(scale, str) else int(scale)
+        if code is None:
+            raise ValueError(f"unknown scale {scale!r}: {sorted(MUON_SCALES)}")
+        super().__init__(lr, momentum, weight_decay, eps, int(bool(nesterov)), steps, code, 0)
 
 
 FSDP_ACT_NONE, FSDP_ACT_RELU, FSDP_ACT_GELU, FSDP_ACT_SILU = 0, 1, 2, 3
@@ -147,6 +165,13 @@ def lib() -> C.CDLL:
         L.fsdp_layernorm_workspace_bytes.restype = sz
         L.fsdp_layernorm_backward.argtypes = [i64, i64, i32, vp, i64, vp, i64, vp, vp, vp, vp, i64, vp, i64, vp, vp, i32, i32, vp,
                                               sz, vp]
+        L.fsdp_newton_schulz.argtypes = [i32, i64, i64, vp, vp, i32, vp, vp, i32, i32, vp, C.c_float, vp, sz, vp]
+        L.fsdp_newton_schulz_workspace_bytes.argtypes = [i32, i64, i64]
+        L.fsdp_newton_schulz_workspace_bytes.restype = sz
+        L.fsdp_zero1_muon_broadcast.argtypes = [vp, i32, vp, C.POINTER(vp), i32, vp, vp, C.POINTER(vp), i32, C.POINTER(MuonHparams), vp,
+                                                vp, sz, vp]
+        L.fsdp_zero1_muon_workspace_bytes.argtypes = [vp, i32, vp]
+        L.fsdp_zero1_muon_workspace_bytes.restype = sz
         L.fsdp_check_status.argtypes = [vp]
         L.fsdp_set_rs_kernel.argtypes = [i32]
         L.fsdp_rs_kernel_for.argtypes = [vp, i32]
@@ -656,6 +681,73 @@ def fsdp_layernorm_backward(dy, x, mean, rstd, dx, weight=None, dw=None, db=None
                                        1 if accumulate else 0, pws, nws, _stream(stream, dev))
     if rc:
         _check(rc, "fsdp_layernorm_backward")
+
+
+def _coeffs(coeffs, steps: int):
+    """A schedule of (a, b, c) per step as a C array; None: the default."""
+    if coeffs is None:
+        return None
+    rows = [tuple(map(float, r)) for r in coeffs]
+    if len(rows) != steps or any(len(r) != 3 for r in rows):
+        raise ValueError(f"coeffs: need (a, b, c) for each of {steps} steps")
+    return (C.c_float * (3 * steps))(*[v for r in rows for v in r])
+
+
+def fsdp_newton_schulz_workspace_bytes(count: int, rows: int, cols: int) -> int:
+    """Scratch bytes of fsdp_newton_schulz for `count` matrices of rows x cols."""
+    return int(lib().fsdp_newton_schulz_workspace_bytes(count, rows, cols))
+
+
+def fsdp_newton_schulz(src, dst, steps: int = 5, coeffs=None, eps: float = 1e-7, workspace=None, stream=None) -> None:
+    """dst = src / |src| after `steps` Newton-Schulz steps X <- a X + (b A + c A A) X, A = X X^T (or of the
+    transpose, where that has fewer rows): a matrix, or a list of matrices of one shape; src of one
+    dtype, dst of one dtype.  coeffs: (a, b, c) per step.  workspace:
+    fsdp_newton_schulz_workspace_bytes."""
+    if isinstance(src, torch.Tensor):
+        src, dst = [src], [dst]
+    n = len(src)
+    if len(dst) != n:
+        raise ValueError(f"{n} sources, {len(dst)} destinations")
+    if n == 0:
+        return
+    code, dev = _dtype_code(src[0]), _device(src[0])
+    rows, cols, _, _ = _operand(src[0], "src", src[0].dtype, dev)
+    out = _dtype_code(dst[0])
+    a = [_matrix(x, "src", rows, cols, src[0].dtype, dev) for x in src]
+    b = [_matrix(x, "dst", rows, cols, dst[0].dtype, dev) for x in dst]
+    pa, la = (C.c_void_p * n)(*[p for p, _ in a]), (C.c_int64 * n)(*[ld for _, ld in a])
+    pb, lb = (C.c_void_p * n)(*[p for p, _ in b]), (C.c_int64 * n)(*[ld for _, ld in b])
+    pws, nws = _NO_MATRIX if workspace is None else _workspace(workspace, dev)
+    rc = lib().fsdp_newton_schulz(n, rows, cols, pa, la, code, pb, lb, out, steps, _coeffs(coeffs, steps), eps, pws, nws,
+                                  _stream(stream, dev))
+    if rc:
+        _check(rc, "fsdp_newton_schulz")
+
+
+def fsdp_zero1_muon_workspace_bytes(layout: Layout, tensors) -> int:
+    """Scratch bytes of fsdp_zero1_muon_broadcast for these tensors of the layout."""
+    ids = (C.c_int32 * max(len(tensors), 1))(*tensors)
+    return int(lib().fsdp_zero1_muon_workspace_bytes(layout.handle, len(tensors), ids))
+
+
+def fsdp_zero1_muon_broadcast(layout: Layout, tensors, grad_replicas, master, momentum, param_replicas,
+                              hp: Optional[MuonHparams] = None, workspace=None, coeffs=None, stream=None,
+                              grad_dtype: Optional[int] = None, param_dtype: Optional[int] = None) -> None:
+    """The ZeRO-1 owner step with Muon for the listed tensors (weight matrices) of a ZeRO-1 layout: mean
+    of the N gradient replicas, momentum, Newton-Schulz steps, weight decay, the new weights into
+    master and all N replicas.  The layout's other tensors are not touched."""
+    if len(grad_replicas) != layout.N or len(param_replicas) != layout.N:
+        raise ValueError(f"need {layout.N} gradient and parameter replicas")
+    if grad_dtype is None:
+        grad_dtype = _dtype_code(grad_replicas[0])
+    if param_dtype is None:
+        param_dtype = _dtype_code(param_replicas[0])
+    hp = MuonHparams() if hp is None else hp
+    ids = (C.c_int32 * max(len(tensors), 1))(*tensors)
+    pws, nws = (None, 0) if workspace is None else (_ptr(workspace), workspace.numel() * workspace.element_size())
+    _check(lib().fsdp_zero1_muon_broadcast(layout.handle, len(tensors), ids, _ptr_array(grad_replicas), grad_dtype, _ptr(master),
+                                           _ptr(momentum), _ptr_array(param_replicas), param_dtype, C.byref(hp),
+                                           _coeffs(coeffs, hp.steps), pws, nws, _stream(stream)), "fsdp_zero1_muon_broadcast")
 
 
 def fsdp_reshard(layout: Layout, unit_begin: int, unit_end: int, full=None, master=None, param_shards=None,

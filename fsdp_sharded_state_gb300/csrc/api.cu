@@ -18,6 +18,7 @@
 #include "kernels.hpp"
 #include "layout.hpp"
 #include "linear.hpp"
+#include "ns.hpp"
 #include "staged.hpp"
 
 using fsdp::Seg;
@@ -515,7 +516,8 @@ int fsdp_check_status(fsdp_stream_t stream) {
     e = fsdp::take_wait_error(&gave_up);
     if (e != cudaSuccess) return cuda_fail(e, "wait status read");
     for (auto take : {fsdp::take_wait_error_forward, fsdp::take_wait_error_forward_pair, fsdp::take_wait_error_dgrad,
-                      fsdp::take_wait_error_dgrad_pair, fsdp::take_wait_error_wgrad}) {
+                      fsdp::take_wait_error_dgrad_pair, fsdp::take_wait_error_wgrad, fsdp::take_wait_error_ns_gram,
+                      fsdp::take_wait_error_ns_poly, fsdp::take_wait_error_ns_step, fsdp::take_wait_error_ns_last}) {
         unsigned int linear = 0;
         e = take(&linear);
         if (e != cudaSuccess) return cuda_fail(e, "wait status read");

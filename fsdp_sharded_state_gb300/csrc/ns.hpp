@@ -1,0 +1,83 @@
+// ns.hpp -- host-side types and launchers of the Newton-Schulz kernels.
+#pragma once
+
+#include <cstdint>
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+namespace fsdp {
+
+constexpr int kNsMaxBatch = 64;                 // matrices of a launch
+constexpr int kNsMaxSteps = 64;
+
+// A batch of fp32 matrices as two fp16 terms each: matrix i's high terms at p + 2 i plane, its
+// low ones a plane on; rows of ld elements.  Buffers are padded to multiples of 256 rows and
+// columns, so that whole tiles are stored without a bound; what lies past rows x cols is never
+// read (the tensor map ends there).
+struct NsPlanes {
+    uint16_t* p;
+    int64_t rows, cols, ld, plane;
+};
+
+// Where the last step's result goes, or where the first one's matrix comes from: matrix i is
+// rows x cols of the planes, or (bit i of `tall`) its transpose.
+struct NsMatrices {
+    void* p[kNsMaxBatch];
+    int64_t ld[kNsMaxBatch];
+    uint64_t tall;
+    int32_t bf16;
+};
+
+enum NsEpilogue { kNsGram = 0, kNsPoly = 1, kNsStep = 2, kNsLast = 3 };
+
+// One product of a step, over the whole batch.
+//   gram   A = alpha X X^T                    x: X, out: A       (symmetric: half the tiles)
+//   poly   B = alpha A A + beta A + diag I    x: A, out: B       (symmetric)
+//   step   X' = alpha B X                     x: B, y: X, out: X'
+//   last   the same, into `last`
+struct NsProduct {
+    NsEpilogue kind;
+    int batch;
+    NsPlanes x, y, out;
+    float alpha, beta, diag;
+    const NsMatrices* last;
+};
+
+cudaError_t launch_ns_gram(const NsProduct& p, cudaStream_t st);
+cudaError_t launch_ns_poly(const NsProduct& p, cudaStream_t st);
+cudaError_t launch_ns_step(const NsProduct& p, cudaStream_t st);
+cudaError_t launch_ns_last(const NsProduct& p, cudaStream_t st);
+cudaError_t take_wait_error_ns_gram(unsigned int* flag);
+cudaError_t take_wait_error_ns_poly(unsigned int* flag);
+cudaError_t take_wait_error_ns_step(unsigned int* flag);
+cudaError_t take_wait_error_ns_last(unsigned int* flag);
+
+// Blocks that sum a matrix's squares (a double each), at most kNsMaxParts.
+constexpr int kNsMaxParts = 608;
+int ns_parts(int64_t numel);
+// partial[i][part] of the batch's source matrices (rows x cols, or transposed).
+cudaError_t launch_ns_squares(const NsMatrices& src, int batch, int64_t rows, int64_t cols, double* partial, int parts, cudaStream_t st);
+// The planes of scale / max(norm, eps) times the source, norm from the partial sums.
+cudaError_t launch_ns_pack(const NsMatrices& src, int batch, const NsPlanes& out, const double* partial, int parts, float scale, float eps,
+                           cudaStream_t st);
+
+// Layout of the workspace of a batch (byte offsets); m and n are the shorter and the longer side,
+// chunk the matrices that pass through it at once.
+struct NsWork {
+    int64_t m, n;
+    int chunk;
+    int64_t x0, x1, a, b, partial, end;
+};
+NsWork ns_work(int64_t rows, int64_t cols, int64_t count);
+// Scales of a schedule of coefficients, [steps][3] (NULL: the default each step); false: a step may
+// leave the range that the planes hold.
+struct NsScales {
+    float x[kNsMaxSteps + 1], a[kNsMaxSteps], b[kNsMaxSteps];
+};
+bool ns_scales(const float* coeffs, int steps, NsScales* s);
+// From source matrices and their partial sums to `dst`; one chunk.
+cudaError_t ns_run(const NsWork& w, unsigned char* ws, int batch, const NsMatrices& src, const NsMatrices& dst, int parts, float eps,
+                   const float* coeffs, int steps, const NsScales& sc, cudaStream_t st);
+
+}  // namespace fsdp

@@ -1,0 +1,139 @@
+// ns_prep.cu -- what comes before the products of Newton-Schulz steps: the sum of squares of
+// each matrix, and the first X as two fp16 terms.
+//
+// Both are bound by HBM (the matrix read twice, 4 bytes an element written).  The squares of a
+// thread are added in fp32 over 16 values and from there in 64 bits, in a fixed order.
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "ns.hpp"
+
+namespace fsdp {
+namespace {
+
+constexpr int kPrepThreads = 256;
+
+__device__ __forceinline__ float ns_get(const void* p, int64_t i, int bf16) {
+    return bf16 ? bf16f(static_cast<const uint16_t*>(p)[i]) : static_cast<const float*>(p)[i];
+}
+
+// The sum over a CTA's threads, in thread 0.
+__device__ __forceinline__ double block_sum(double v) {
+    __shared__ double part[kPrepThreads / 32];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        v = 0.0;
+        for (int k = 0; k < kPrepThreads / 32; ++k) v += part[k];
+    }
+    return v;
+}
+
+// The source's elements in the order of its rows, kStrip at a time; block (part, matrix).
+constexpr int kStrip = 16 * kPrepThreads;
+
+__global__ void __launch_bounds__(kPrepThreads)
+k_ns_squares(const __grid_constant__ NsMatrices src, int64_t rows, int64_t cols, double* partial) {
+    pdl_wait();
+    const int mat = blockIdx.y;
+    const bool tall = src.tall >> mat & 1;
+    const int64_t R = tall ? cols : rows, W = tall ? rows : cols;    // the source's own rows and width
+    const int64_t ld = src.ld[mat], n = R * W;
+    const void* const p = src.p[mat];
+    double total = 0.0;
+    for (int64_t base = int64_t(blockIdx.x) * kStrip; base < n; base += int64_t(gridDim.x) * kStrip) {
+        int64_t i = base + threadIdx.x;
+        int64_t r = i / W, c = i - r * W;
+        float v[16], s = 0.f;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            v[k] = i < n ? ns_get(p, r * ld + c, src.bf16) : 0.f;
+            i += kPrepThreads;
+            c += kPrepThreads;
+            while (c >= W) {
+                c -= W;
+                ++r;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 16; ++k) s = __fmaf_rn(v[k], v[k], s);
+        total += double(s);
+    }
+    total = block_sum(total);
+    if (threadIdx.x == 0) partial[mat * gridDim.x + blockIdx.x] = total;
+}
+
+// A tile of 64 x 64 of the planes goes through shared memory, so that reads follow the source's
+// rows in either orientation and writes the planes'.
+__global__ void __launch_bounds__(kPrepThreads)
+k_ns_pack(const __grid_constant__ NsMatrices src, const NsPlanes out, const double* partial, int parts, float scale, float eps,
+          int tiles_n) {
+    __shared__ float tile[64][65];
+    __shared__ float factor;
+    pdl_wait();
+    const int mat = blockIdx.y, tid = threadIdx.x;
+    double square = 0.0;
+    for (int k = tid; k < parts; k += kPrepThreads) square += partial[mat * parts + k];
+    square = block_sum(square);
+    if (tid == 0) {
+        const double norm = sqrt(square);
+        factor = float(double(scale) / (norm < double(eps) ? double(eps) : norm));   // a NaN stays
+    }
+    const bool tall = src.tall >> mat & 1;
+    const int64_t m0 = int64_t(blockIdx.x / tiles_n) * 64, n0 = int64_t(blockIdx.x % tiles_n) * 64, ld = src.ld[mat];
+    const void* const p = src.p[mat];
+    const int x = tid & 63, y0 = tid >> 6;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+        const int y = y0 + 4 * k;                // row of the source's tile, x: column
+        const int64_t r = (tall ? n0 : m0) + y, c = (tall ? m0 : n0) + x;
+        const bool in = tall ? r < out.cols && c < out.rows : r < out.rows && c < out.cols;
+        const float v = in ? ns_get(p, r * ld + c, src.bf16) : 0.f;
+        if (tall) tile[x][y] = v;
+        else tile[y][x] = v;
+    }
+    __syncthreads();
+    uint16_t* const dst = out.p + 2 * int64_t(mat) * out.plane;
+    const float f = factor;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int row = (tid >> 3) + 32 * k, c0 = (tid & 7) * 8;
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float a = tile[row][c0 + 2 * j] * f, b = tile[row][c0 + 2 * j + 1] * f;
+            const __half2 h = __floats2half2_rn(a, b);
+            const float2 g = __half22float2(h);
+            const __half2 l = __floats2half2_rn(a - g.x, b - g.y);
+            hi[j] = *reinterpret_cast<const uint32_t*>(&h);
+            lo[j] = *reinterpret_cast<const uint32_t*>(&l);
+        }
+        // the planes are padded to whole tiles
+        uint16_t* const q = dst + (m0 + row) * out.ld + n0 + c0;
+        stu4(q, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+        stu4(q + out.plane, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+    }
+}
+
+}  // namespace
+
+int ns_parts(int64_t numel) {
+    const int64_t n = (numel + kStrip - 1) / kStrip;
+    return int(n < 1 ? 1 : n < kNsMaxParts ? n : kNsMaxParts);
+}
+
+cudaError_t launch_ns_squares(const NsMatrices& src, int batch, int64_t rows, int64_t cols, double* partial, int parts, cudaStream_t st) {
+    return launch(k_ns_squares, dim3(unsigned(parts), unsigned(batch)), dim3(kPrepThreads), 0, st, src, rows, cols, partial);
+}
+
+cudaError_t launch_ns_pack(const NsMatrices& src, int batch, const NsPlanes& out, const double* partial, int parts, float scale, float eps,
+                           cudaStream_t st) {
+    const int64_t tm = (out.rows + 63) / 64, tn = (out.cols + 63) / 64;
+    if (tm * tn > INT32_MAX) return cudaErrorInvalidValue;
+    return launch(k_ns_pack, dim3(unsigned(tm * tn), unsigned(batch)), dim3(kPrepThreads), 0, st, src, out, partial, parts, scale, eps,
+                  int(tn));
+}
+
+}  // namespace fsdp

@@ -1,0 +1,9 @@
+// ns_step.cu -- instances of the Newton-Schulz product kernel: step.
+#include "ns_kernel.cuh"
+
+namespace fsdp {
+
+cudaError_t launch_ns_step(const NsProduct& p, cudaStream_t st) { return ns_product<kNsStep>(p, st); }
+cudaError_t take_wait_error_ns_step(unsigned int* flag) { return take_ns_wait_error(flag); }
+
+}  // namespace fsdp

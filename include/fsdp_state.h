@@ -684,6 +684,78 @@ int fsdp_layernorm_backward(int64_t rows, int64_t cols, int32_t elem_dtype, cons
                             int64_t lddx, void* dw, void* db, int32_t grad_dtype, int32_t accumulate, void* workspace,
                             size_t workspace_bytes, fsdp_stream_t stream);
 
+/* ---- Newton-Schulz orthogonalisation and the Muon step ---------------------------------
+ * Muon (Jordan et al., "Muon: an optimizer for hidden layers in neural networks", 2024) updates
+ * a weight matrix by its momentum brought near the closest (semi-)orthogonal matrix.  The pages
+ * have no counterpart; it stands beside AdamW for the weights of the layers.
+ *
+ *   X_0 = G / max(|G|, eps)                                    (|G|: root of the sum of squares)
+ *   X_k = a X_{k-1} + (b A + c A A) X_{k-1},  A = X_{k-1} X_{k-1}^T,   k = 1 .. steps
+ *
+ * on the matrix or its transpose, whichever has fewer rows.  With the default coefficients
+ * (3.4445, -4.7750, 2.0315) and 5 steps, singular values of G of at least |G| / 100 come out between
+ * 0.68 and 1.21.
+ *
+ * fsdp_newton_schulz: dst[i] = X_steps of src[i] for `count` matrices of one shape (rows x cols),
+ * each with a row stride of its own (ld_src[i], ld_dst[i], in elements, at least cols) and aligned
+ * to its element.  src, dst, ld_src and ld_dst are host arrays, read before the call returns.
+ *   - src_dtype and dst_dtype: FSDP_F32 or FSDP_BF16 each.  The products are formed from two fp16
+ *     terms per operand (22 significant bits, and nothing below 2^-40) and summed in fp32:
+ *     results carry errors of the order of fp32's own products, times what the steps amplify;
+ *     each is rounded once.  Matrices whose norm is below eps come out as small as X_0 = G / eps
+ *     makes them, to about 1e-9 of 1.
+ *   - steps 1 .. 64.  coeffs: a, b, c of each step ([steps][3], host memory), or NULL for the
+ *     default.  A schedule under which a singular value in [0, 1] may exceed 4 after some step, or
+ *     with |a + b s^2 + c s^4| above 1024 there, is refused (FSDP_EINVAL).
+ *   - rows, cols: 1 .. 2^20, at most 2^34 elements padded to 256 (else FSDP_EOVERFLOW); count >= 0.
+ *   - A zero matrix gives zeros.  An infinity or a NaN in src[i] makes dst[i] NaN throughout or, where
+ *     that was an infinity, NaN or 0; no other matrix is touched by it.  The same holds for elements
+ *     above 1.8e19, whose squares are infinite in fp32.
+ *   - dst[i] may be the very src[i] (with its stride and dtype); nothing else may overlap.
+ *   - workspace: device scratch, 16-byte aligned, of at least
+ *     fsdp_newton_schulz_workspace_bytes(count, rows, cols) bytes; contents, overlap and
+ *     repeatability as for the linear calls.  Large batches pass through it in parts. */
+int fsdp_newton_schulz(int32_t count, int64_t rows, int64_t cols, const void* const* src, const int64_t* ld_src, int32_t src_dtype,
+                       void* const* dst, const int64_t* ld_dst, int32_t dst_dtype, int32_t steps, const float* coeffs, float eps,
+                       void* workspace, size_t workspace_bytes, fsdp_stream_t stream);
+/* 0 for arguments that the call refuses, and for count 0.  Host only. */
+size_t fsdp_newton_schulz_workspace_bytes(int32_t count, int64_t rows, int64_t cols);
+
+/* Muon hyper-parameters.  scale: what an update is multiplied by beside lr. */
+typedef enum {
+    FSDP_MUON_SCALE_NONE = 0,     /* 1                                                       */
+    FSDP_MUON_SCALE_SHAPE = 1,    /* sqrt(max(1, rows / cols))                               */
+    FSDP_MUON_SCALE_RMS = 2       /* 0.2 sqrt(max(rows, cols)): elements of AdamW's size     */
+} fsdp_muon_scale;
+typedef struct {
+    float lr, momentum, weight_decay, eps;
+    int32_t nesterov, steps, scale, reserved;
+} fsdp_muon_hparams;
+
+/* The ZeRO-1 owner step of fsdp_zero1_adamw_broadcast with Muon in AdamW's place, for the
+ * listed tensors of an FSDP_ZERO1 layout ([ZeRO-state] "ZeRO-1：Optimizer State Sharding").  For each:
+ *   g = (sum over q of G_q) / N;   m = momentum m + (1 - momentum) g
+ *   u = (1 - momentum) g + momentum m  (nesterov != 0), or m
+ *   w = (1 - lr weight_decay) w - lr scale X_steps(u);   w into all N replicas
+ * All in fp32; no other element of any buffer is read or written, so that the remaining
+ * tensors of the layout can take fsdp_zero1_adamw_broadcast, in units of their own.
+ *   tensors         n_tensors indices of the layout, none twice (else FSDP_EINVAL), each of two
+ *                   dimensions or more (rows: the first, cols: the others together): a tensor
+ *                   with no element or one column, as every vector, is FSDP_ESHAPE
+ *   grad_replicas, param_replicas, master   as in fsdp_zero1_adamw_broadcast
+ *   momentum        [N][stride] fp32 owner rows
+ *   hp              lr, weight_decay >= 0, 0 <= momentum < 1, eps > 0 (else FSDP_EINVAL); steps, coeffs
+ *                   and limits of size as in fsdp_newton_schulz
+ *   workspace       at least fsdp_zero1_muon_workspace_bytes(layout, n_tensors, tensors) bytes;
+ *                   tensors whose sides are equal, in either order, share it and its launches
+ * The step has no count: a captured call can be replayed as it is. */
+int fsdp_zero1_muon_broadcast(const fsdp_layout* layout, int32_t n_tensors, const int32_t* tensors, const void* const* grad_replicas,
+                              int32_t grad_dtype, float* master, float* momentum, void* const* param_replicas, int32_t param_dtype,
+                              const fsdp_muon_hparams* hp, const float* coeffs, void* workspace, size_t workspace_bytes,
+                              fsdp_stream_t stream);
+/* 0 for arguments that the call refuses.  Host only. */
+size_t fsdp_zero1_muon_workspace_bytes(const fsdp_layout* layout, int32_t n_tensors, const int32_t* tensors);
+
 #ifdef __cplusplus
 }
 #endif
