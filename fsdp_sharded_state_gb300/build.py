@@ -47,11 +47,11 @@ PAIR_REGISTERS = 168
 
 
 def check_pair_registers(log: str) -> None:
-    """The CTA-pair kernels of linear_kernel.cuh share out the registers of their launch by figures
+    """The CTA-pair kernels of linear_kernel.cuh and ns_kernel.cuh share out the registers of their launch by figures
     that hold for PAIR_REGISTERS a thread; with any other count they would be refused at their first
     launch.  log: what nvcc -Xptxas -v printed."""
     for name, used in re.findall(r"Compiling entry function '(\w+)'.*?Used (\d+) registers", log, re.S):
-        if re.search(r"k_linearI\w*LinCfgILi\dE[ft]Li2E", name) and int(used) != PAIR_REGISTERS:
+        if re.search(r"k_linearI\w*LinCfgILi\dE[ft]Li2E|k_nsI\w*NsCfgILi\dELi2E", name) and int(used) != PAIR_REGISTERS:
             raise RuntimeError(f"{name}: {used} registers, expected {PAIR_REGISTERS}")
 
 
@@ -67,7 +67,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         objs.append(o)
         if force or ptxas_info or _newer(o, [s, *headers, __file__]):
             flags = list(NVFLAGS)
-            if src.endswith(".cu") and (ptxas_info or src.startswith("linear_")):
+            if src.endswith(".cu") and (ptxas_info or src.startswith(("linear_", "ns_"))):
                 flags += ["-Xptxas", "-v"]
             jobs.append([cc, *ARCH, *flags, "-c", s, "-o", o])
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:

@@ -12,8 +12,8 @@
 // product: what fp32 products round.  The tensor cores round their accumulators towards zero
 // at every step, which shrinks all of a product alike, and the steps' polynomials, whose terms
 // cancel, answer a common 4e-7 of every product with 4e-6 to 1e-5 of the result (chunks of four
-// K steps did).  So the accumulators are emptied into fp32 registers every kNsChunk K steps, and in
-// a chunk all small products come first: 8 additions round at the full sum's size, not 48.
+// K steps did).  So the accumulators are emptied into fp32 registers at every K step of 64, small
+// products first: four additions round at the full sum's size.
 //
 // Work.  X X^T and A A are symmetric: only tiles at or below the diagonal are computed, and what
 // lies off the diagonal's square is stored twice, as it is and mirrored (a lane holds a row, so the
@@ -43,7 +43,6 @@ namespace {
 
 constexpr int kNsEpiWarps = 8, kNsThreads = 384;
 constexpr int kNsMaxStages = 8;
-constexpr int kNsChunk = 2;                     // K steps (of 64) that the accumulators hold
 constexpr int kUnitLd = 36;                     // floats of a row of a 32 x 32 unit in shared memory
 constexpr int kUnitFloats = 32 * kUnitLd;
 
@@ -78,8 +77,9 @@ struct NsCfg {
     static constexpr int STAGES = FIT < kNsMaxStages ? FIT : kNsMaxStages;
     static constexpr int SMEM = STAGES * STAGE + JOIN + MORE;
     static constexpr int TMEM = 2 * BN;
+    static constexpr bool REGS = CG == 2;                        // see setmaxnreg below
     static_assert(R * BN == TM, "a tile's columns divide its rows");
-    static_assert(STAGES > kNsChunk && SMEM > 114 * 1024 && SMEM <= 227 * 1024, "one CTA per SM: its TMEM is never contended");
+    static_assert(STAGES >= 2 && SMEM > 114 * 1024 && SMEM <= 227 * 1024, "one CTA per SM: its TMEM is never contended");
     static_assert(!SPLIT || CG == 1, "a cluster is a pair or a split");
 };
 
@@ -262,113 +262,107 @@ k_ns(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensor
         return it;
     };
 
-    if (warp == kNsEpiWarps) {
-        // ---- loads ----
-        bool ok = true;
-        uint32_t it = 0;
-        for (int t = cluster; ok && t < n_items; t += n_clusters) {
-            const Item w = item_at(t);
-            const int brows = C::BROWS / w.cut;
-            const int m0 = (w.mt * C::CG + (C::CG == 2 ? int(rank) : 0)) * 128;
-            const int n0 = w.nt * C::BN + w.sub * (C::BN / w.cut) + (C::CG == 2 ? int(rank) * brows : 0);
-            const uint32_t bytes = C::CG * 2 * (C::A_BYTES + C::B_BYTES / w.cut);
-            for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                const uint32_t s = it % C::STAGES, use = it / C::STAGES;
-                const uint32_t bar = C::CG == 2 ? map_rank(full + 8 * s, 0) : full + 8 * s;
-                const uint32_t st = smem_addr(smem + s * C::STAGE);
-#pragma unroll
-                for (int p = 1; p >= 0; --p) {                   // the low planes are free first
-                    if (use > 0 && !mbar_wait_bounded((p ? low_empty : empty) + 8 * s, (use - 1) & 1, wait_ns)) {
-                        ok = false;
-                        break;
-                    }
-                    if (elect_one()) {
-                        if (leader && p == 1) mbar_arrive_tx(full + 8 * s, bytes);
-                        const int z = 2 * w.mat + p;
-                        const uint32_t a = st + p * C::A_BYTES, b = st + 2 * C::A_BYTES + p * C::B_BYTES;
-                        tma_load<C::CG>(a, &map_a, kb * 64, m0, z, bar);
-                        tma_load<C::CG>(a + 8192, &map_a, kb * 64, m0 + 64, z, bar);
-#pragma unroll
-                        for (int c = 0; c < C::BROWS / 64; ++c) {
-                            if (c * 64 >= brows) break;
-                            if constexpr (C::B_MN) tma_load<C::CG>(b + c * 8192, &map_b, n0 + c * 64, kb * 64, z, bar);
-                            else tma_load<C::CG>(b + c * 8192, &map_b, kb * 64, n0 + c * 64, z, bar);
-                        }
-                    }
-                    __syncwarp();
-                }
-                if (!ok) break;
-            }
-        }
-        // the last use of every stage: its MMAs are done (and, in a pair, their arrivals on this
-        // CTA have landed) before the CTA may leave
-        for (uint32_t k = it > C::STAGES ? it - C::STAGES : 0; ok && k < it; ++k)
-            ok = mbar_wait_bounded(empty + 8 * (k % C::STAGES), (k / C::STAGES) & 1, wait_ns);
-        if (!__all_sync(0xffffffffu, ok)) {
-            if (lane == 0) atomicOr(&g_wait_error, 1u);
-            const uint64_t t0 = global_ns();                     // copies in flight land within this
-            for (int i = 0; i < (1 << 20) && global_ns() - t0 < 2000000ull; ++i) __nanosleep(1000);
-        }
-        __syncwarp();
-    } else if (warp == kNsEpiWarps + 1) {
-        // ---- products ----
-        if (leader) {
-            constexpr uint32_t a_step = 32 / 16, b_step = C::B_MN ? 2048 / 16 : 32 / 16;     // 16 K elements on
-            // fp16 operands: the type fields that mma_idesc sets for bf16 cleared
-            constexpr uint32_t f16 = ~((1u << 7) | (1u << 10));
-            const uint64_t da0 = smem_desc(smem_addr(smem), 16, 1024);
-            const uint64_t db0 = smem_desc(smem_addr(smem) + 2 * C::A_BYTES, C::B_MN ? 8192 : 16, 1024);
+    // The pairs' epilogue warpgroups hold 128 sums a thread beside 32 values on their way: they take
+    // registers that the third does not need (the launch has 168 per thread of three warpgroups,
+    // which ns_launch and the build check; 2 x 208 + 88 = 3 x 168).
+    if (warp >= kNsEpiWarps) {
+        if constexpr (C::REGS) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        if (warp == kNsEpiWarps) {
+            // ---- loads ----
             bool ok = true;
-            uint32_t it = 0, ac = 0;
+            uint32_t it = 0;
             for (int t = cluster; ok && t < n_items; t += n_clusters) {
-                const uint32_t idesc = f16 & (C::CUT && t >= sh.whole ? mma_idesc(C::TM, C::BN / 2, false, C::B_MN)
-                                                                      : mma_idesc(C::TM, C::BN, false, C::B_MN));
-                for (int kc = kb0; ok && kc < kb1; kc += kNsChunk, ++ac) {
-                    const uint32_t buf = ac & 1, use = ac >> 1;
-                    if (use > 0 && !mbar_wait_bounded(acc_empty + 8 * buf, (use - 1) & 1, wait_ns)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t d = tmem + buf * C::BN;
-                    const int ke = kc + kNsChunk < kb1 ? kc + kNsChunk : kb1;
-                    // 12 products of a K step: lo hi and hi lo of the whole chunk, then its hi hi
-                    auto products = [&](uint32_t s, int pa, int pb, bool add) {
-                        const uint64_t das = da0 + s * (C::STAGE / 16) + pa * (C::A_BYTES / 16);
-                        const uint64_t dbs = db0 + s * (C::STAGE / 16) + pb * (C::B_BYTES / 16);
+                const Item w = item_at(t);
+                const int brows = C::BROWS / w.cut;
+                const int m0 = (w.mt * C::CG + (C::CG == 2 ? int(rank) : 0)) * 128;
+                const int n0 = w.nt * C::BN + w.sub * (C::BN / w.cut) + (C::CG == 2 ? int(rank) * brows : 0);
+                const uint32_t bytes = C::CG * 2 * (C::A_BYTES + C::B_BYTES / w.cut);
+                for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                    const uint32_t s = it % C::STAGES, use = it / C::STAGES;
+                    const uint32_t bar = C::CG == 2 ? map_rank(full + 8 * s, 0) : full + 8 * s;
+                    const uint32_t st = smem_addr(smem + s * C::STAGE);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) mma_bf16<C::CG>(d, das + k * a_step, dbs + k * b_step, idesc, add || k > 0);
-                    };
-                    for (int kb = kc; kb < ke; ++kb) {
-                        const uint32_t i = it + (kb - kc), s = i % C::STAGES;
-                        if (!mbar_wait_bounded(full + 8 * s, (i / C::STAGES) & 1, wait_ns)) {
+                    for (int p = 1; p >= 0; --p) {                   // the low planes are free first
+                        if (use > 0 && !mbar_wait_bounded((p ? low_empty : empty) + 8 * s, (use - 1) & 1, wait_ns)) {
                             ok = false;
                             break;
                         }
-                        tc_fence_after();
                         if (elect_one()) {
-                            products(s, 1, 0, kb > kc);
-                            products(s, 0, 1, true);
-                            mma_commit<C::CG>(low_empty + 8 * s);
+                            if (leader && p == 1) mbar_arrive_tx(full + 8 * s, bytes);
+                            const int z = 2 * w.mat + p;
+                            const uint32_t a = st + p * C::A_BYTES, b = st + 2 * C::A_BYTES + p * C::B_BYTES;
+                            tma_load<C::CG>(a, &map_a, kb * 64, m0, z, bar);
+                            tma_load<C::CG>(a + 8192, &map_a, kb * 64, m0 + 64, z, bar);
+#pragma unroll
+                            for (int c = 0; c < C::BROWS / 64; ++c) {
+                                if (c * 64 >= brows) break;
+                                if constexpr (C::B_MN) tma_load<C::CG>(b + c * 8192, &map_b, n0 + c * 64, kb * 64, z, bar);
+                                else tma_load<C::CG>(b + c * 8192, &map_b, kb * 64, n0 + c * 64, z, bar);
+                            }
                         }
                         __syncwarp();
                     }
                     if (!ok) break;
-                    for (int kb = kc; kb < ke; ++kb, ++it) {
-                        const uint32_t s = it % C::STAGES;
+                }
+            }
+            // the last use of every stage: its MMAs are done (and, in a pair, their arrivals on this
+            // CTA have landed) before the CTA may leave
+            for (uint32_t k = it > C::STAGES ? it - C::STAGES : 0; ok && k < it; ++k)
+                ok = mbar_wait_bounded(empty + 8 * (k % C::STAGES), (k / C::STAGES) & 1, wait_ns);
+            if (!__all_sync(0xffffffffu, ok)) {
+                if (lane == 0) atomicOr(&g_wait_error, 1u);
+                const uint64_t t0 = global_ns();                     // copies in flight land within this
+                for (int i = 0; i < (1 << 20) && global_ns() - t0 < 2000000ull; ++i) __nanosleep(1000);
+            }
+            __syncwarp();
+        } else if (warp == kNsEpiWarps + 1) {
+            // ---- products ----
+            if (leader) {
+                constexpr uint32_t a_step = 32 / 16, b_step = C::B_MN ? 2048 / 16 : 32 / 16;     // 16 K elements on
+                // fp16 operands: the type fields that mma_idesc sets for bf16 cleared
+                constexpr uint32_t f16 = ~((1u << 7) | (1u << 10));
+                const uint64_t da0 = smem_desc(smem_addr(smem), 16, 1024);
+                const uint64_t db0 = smem_desc(smem_addr(smem) + 2 * C::A_BYTES, C::B_MN ? 8192 : 16, 1024);
+                bool ok = true;
+                uint32_t it = 0;
+                for (int t = cluster; ok && t < n_items; t += n_clusters) {
+                    const uint32_t idesc = f16 & (C::CUT && t >= sh.whole ? mma_idesc(C::TM, C::BN / 2, false, C::B_MN)
+                                                                          : mma_idesc(C::TM, C::BN, false, C::B_MN));
+                    for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                        const uint32_t buf = it & 1, use = it >> 1, s = it % C::STAGES;
+                        if (use > 0 && !mbar_wait_bounded(acc_empty + 8 * buf, (use - 1) & 1, wait_ns)) {
+                            ok = false;
+                            break;
+                        }
+                        if (!mbar_wait_bounded(full + 8 * s, (it / C::STAGES) & 1, wait_ns)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t d = tmem + buf * C::BN;
+                        const uint64_t das = da0 + s * (C::STAGE / 16), dbs = db0 + s * (C::STAGE / 16);
                         if (elect_one()) {
-                            products(s, 0, 0, true);
+#pragma unroll
+                            for (int pr = 0; pr < 3; ++pr) {         // lo hi, hi lo, hi hi
+                                const int pa = pr == 0, pb = pr == 1;
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    mma_bf16<C::CG>(d, das + pa * (C::A_BYTES / 16) + k * a_step, dbs + pb * (C::B_BYTES / 16) + k * b_step,
+                                                    idesc, pr > 0 || k > 0);
+                                if (pr == 1) mma_commit<C::CG>(low_empty + 8 * s);   // its planes can be loaded again
+                            }
                             mma_commit<C::CG>(empty + 8 * s);
-                            if (kb + 1 == ke) mma_commit<C::CG>(acc_full + 8 * buf);
+                            mma_commit<C::CG>(acc_full + 8 * buf);
                         }
                         __syncwarp();
                     }
                 }
+                if (!__all_sync(0xffffffffu, ok) && lane == 0) atomicOr(&g_wait_error, 1u);
             }
-            if (!__all_sync(0xffffffffu, ok) && lane == 0) atomicOr(&g_wait_error, 1u);
+            __syncwarp();
         }
-        __syncwarp();
-    } else if (warp < kNsEpiWarps) {
+    } else {
+        if constexpr (C::REGS) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         // ---- sums and epilogue ----
         // Warp w reads TMEM lanes 32 (w mod 4) on, the two halves of the warps alternate groups of 32 columns.
         const int q = warp & 3, half = warp >> 2;
@@ -383,7 +377,7 @@ k_ns(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensor
             for (int j = 0; j < NJ; ++j)
 #pragma unroll
                 for (int i = 0; i < 32; ++i) sum[j][i] = 0.f;
-            for (int kc = kb0; ok && kc < kb1; kc += kNsChunk, ++ac) {
+            for (int kb = kb0; ok && kb < kb1; ++kb, ++ac) {
                 const uint32_t buf = ac & 1;
                 ok = __all_sync(0xffffffffu, mbar_wait_bounded(acc_full + 8 * buf, (ac >> 1) & 1, wait_ns));
                 if (!ok) break;
@@ -392,15 +386,10 @@ k_ns(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensor
 #pragma unroll
                 for (int j = 0; j < NJ; ++j) {
                     if (j < nj) {
+                        float v[32];
+                        tmem_ld32(src + (2 * j + half) * 32, v);
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            Acc16 a;
-                            float v[16];
-                            tmem_ld16_async(src + (2 * j + half) * 32 + 16 * h, a);
-                            tmem_wait_ld16(a, v);
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) sum[j][16 * h + i] += v[i];
-                        }
+                        for (int i = 0; i < 32; ++i) sum[j][i] += v[i];
                     }
                 }
                 tc_fence_before();
@@ -541,6 +530,9 @@ cudaError_t ns_launch(const NsProduct& p, int splits, int dev, cudaStream_t st) 
     cudaError_t e = cudaSuccess;
     if (dev >= 64 || !(prepared.load(std::memory_order_relaxed) >> dev & 1)) {
         e = cudaFuncSetAttribute(k_ns<C, Last>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        cudaFuncAttributes attr;
+        if (C::REGS && e == cudaSuccess && (e = cudaFuncGetAttributes(&attr, k_ns<C, Last>)) == cudaSuccess && attr.numRegs != 168)
+            e = cudaErrorInvalidConfiguration;
         if (e != cudaSuccess) return e;
         if (dev < 64) prepared.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
     }
