@@ -29,15 +29,15 @@ struct NsMatrices {
     int32_t bf16;
 };
 
-enum NsEpilogue { kNsGram = 0, kNsPoly = 1, kNsStep = 2, kNsLast = 3 };
+enum NsEpilogue { kNsGram = 0, kNsPoly = 1, kNsStep = 2, kNsLast = 3, kNsMul = 4 };
 
 // One product of a step, over the whole batch.
 //   gram   A = alpha X X^T                    x: X, out: A       (symmetric: half the tiles)
 //   poly   B = alpha A A + beta A + diag I    x: A, out: B       (symmetric)
-//   step   X' = alpha B X                     x: B, y: X, out: X'
+//   mul    alpha B A of two polynomials of one symmetric matrix: x, y, out (symmetric)
+//   step   X' = alpha Q X                     x: Q, y: X, out: X'
 //   last   the same, into `last`
 struct NsProduct {
-    NsEpilogue kind;
     int batch;
     NsPlanes x, y, out;
     float alpha, beta, diag;
@@ -46,12 +46,19 @@ struct NsProduct {
 
 cudaError_t launch_ns_gram(const NsProduct& p, cudaStream_t st);
 cudaError_t launch_ns_poly(const NsProduct& p, cudaStream_t st);
+cudaError_t launch_ns_mul(const NsProduct& p, cudaStream_t st);
 cudaError_t launch_ns_step(const NsProduct& p, cudaStream_t st);
 cudaError_t launch_ns_last(const NsProduct& p, cudaStream_t st);
 cudaError_t take_wait_error_ns_gram(unsigned int* flag);
 cudaError_t take_wait_error_ns_poly(unsigned int* flag);
+cudaError_t take_wait_error_ns_mul(unsigned int* flag);
 cudaError_t take_wait_error_ns_step(unsigned int* flag);
 cudaError_t take_wait_error_ns_last(unsigned int* flag);
+
+// Estimated times in us, from the sizes (x, y, batch) alone.
+float cost_ns_gram(const NsProduct& p);
+float cost_ns_mul(const NsProduct& p);
+float cost_ns_step(const NsProduct& p);
 
 // Blocks that sum a matrix's squares (a double each), at most kNsMaxParts.
 constexpr int kNsMaxParts = 608;
@@ -67,13 +74,14 @@ cudaError_t launch_ns_pack(const NsMatrices& src, int batch, const NsPlanes& out
 struct NsWork {
     int64_t m, n;
     int chunk;
-    int64_t x0, x1, a, b, partial, end;
+    int64_t x0, x1, square[4], partial, end;
 };
 NsWork ns_work(int64_t rows, int64_t cols, int64_t count);
 // Scales of a schedule of coefficients, [steps][3] (NULL: the default each step); false: a step may
 // leave the range that the planes hold.
 struct NsScales {
-    float x[kNsMaxSteps + 1], a[kNsMaxSteps], b[kNsMaxSteps];
+    float x[kNsMaxSteps + 1], a[kNsMaxSteps], b[kNsMaxSteps];    // of X, A and B of each step
+    double top[kNsMaxSteps + 1], gain[kNsMaxSteps];              // bounds: of X's singular values, of B's eigenvalues
 };
 bool ns_scales(const float* coeffs, int steps, NsScales* s);
 // From source matrices and their partial sums to `dst`; one chunk.

@@ -49,6 +49,7 @@ float scale_of(double bound) { return float(std::ldexp(1.0, 15 - std::max(0, int
 bool ns_scales(const float* coeffs, int steps, NsScales* s) {
     double u = 1.0;
     s->x[0] = scale_of(u);
+    s->top[0] = u;
     for (int k = 0; k < steps; ++k) {
         const float* const f = coeffs ? coeffs + 3 * k : kDefault;
         if (!std::isfinite(f[0]) || !std::isfinite(f[1]) || !std::isfinite(f[2])) return false;
@@ -57,7 +58,9 @@ bool ns_scales(const float* coeffs, int steps, NsScales* s) {
         if (!(p <= 4.0) || !(q <= 1024.0)) return false;
         s->a[k] = scale_of(u * u);
         s->b[k] = scale_of(q);
+        s->gain[k] = q;
         u = p;
+        s->top[k + 1] = u;
         s->x[k + 1] = scale_of(u);
     }
     return true;
@@ -72,12 +75,25 @@ NsWork ns_work(int64_t rows, int64_t cols, int64_t count) {
     w.chunk = int(std::max<int64_t>(1, std::min<int64_t>({count, kNsMaxBatch, (int64_t(1) << 26) / (mp * np)})));
     w.x0 = 0;
     w.x1 = w.x0 + w.chunk * mp * np * 4;
-    w.a = w.x1 + w.chunk * mp * np * 4;
-    w.b = w.a + w.chunk * mp * mp * 4;
-    w.partial = w.b + w.chunk * mp * mp * 4;
+    for (int i = 0; i < 4; ++i) w.square[i] = w.x1 + w.chunk * (mp * np + i * mp * mp) * 4;
+    w.partial = w.square[3] + w.chunk * mp * mp * 4;
     w.end = w.partial + int64_t(w.chunk) * kNsMaxParts * 8;
     return w;
 }
+
+// Steps one by one cost a pass over X each for A = X X^T and for X' = B X.  A step that follows
+// another can do without: with B_0 from A_0 = X X^T, the next A is B_0 A_0 B_0 and the next B_1 a polynomial of
+// it, and X takes both as (B_1 B_0) X.  That is three products of m x m in place of m x m x n and
+// m x n x m, less work where n > m: 4096 x 11008 takes 30 units of m^3 for five steps in groups
+// of 3 and 2 instead of 45, and its Muon step 9.7 instead of 13.0 ms.
+//
+// What it costs in precision.  An error d in A's small eigenvalues grows by the square of
+// the first coefficient (11.9) with each step that A is carried on, where X, computed anew, has it
+// relative to X: after two steps 142 d, d = 2^-23 / sqrt(m) of the largest eigenvalue: 4e-6 of the gain of the
+// smallest directions at m = 64, what fp32 products lose there in five steps.  So at most
+// kGroup steps, and a product of gains that leaves the others' digits (kGroupGain).
+constexpr int kGroup = 3;
+constexpr double kGroupGain = 64.0;
 
 cudaError_t ns_run(const NsWork& w, unsigned char* ws, int batch, const NsMatrices& src, const NsMatrices& dst, int parts, float eps,
                    const float* coeffs, int steps, const NsScales& sc, cudaStream_t st) {
@@ -85,38 +101,81 @@ cudaError_t ns_run(const NsWork& w, unsigned char* ws, int batch, const NsMatric
     auto planes = [&](int64_t at, int64_t cols, int64_t ld) {
         return NsPlanes{reinterpret_cast<uint16_t*>(ws + at), w.m, cols, ld, mp * ld};
     };
-    NsPlanes x = planes(w.x0, w.n, np), next = planes(w.x1, w.n, np);
-    const NsPlanes a = planes(w.a, w.m, mp), b = planes(w.b, w.m, mp);
+    NsPlanes x = planes(w.x0, w.n, np), next = planes(w.x1, w.n, np), sq[4];
+    for (int i = 0; i < 4; ++i) sq[i] = planes(w.square[i], w.m, mp);
+    NsProduct p = {};
+    p.batch = batch;
+    p.x = p.y = x;
+    const float over_x = cost_ns_gram(p);
+    p.x = p.y = sq[0];
+    const float square = cost_ns_mul(p);
+    p.y = x;
+    const bool group = over_x + cost_ns_step(p) > 3.f * square;
     cudaError_t e = launch_ns_pack(src, batch, x, reinterpret_cast<const double*>(ws + w.partial), parts, sc.x[0], eps, st);
-    for (int k = 0; k < steps && e == cudaSuccess; ++k) {
-        const float* const f = coeffs ? coeffs + 3 * k : kDefault;
-        const float sx = sc.x[k], sa = sc.a[k], sb = sc.b[k];      // powers of two
-        NsProduct p = {};
-        p.batch = batch;
-        p.kind = kNsGram;
-        p.x = x;
-        p.out = a;
-        p.alpha = sa / (sx * sx);
-        if ((e = launch_ns_gram(p, st)) != cudaSuccess) break;
-        p.kind = kNsPoly;
-        p.x = a;
-        p.out = b;
-        p.alpha = f[2] * (sb / (sa * sa));
-        p.beta = f[1] * (sb / sa);
-        p.diag = f[0] * sb;
-        if ((e = launch_ns_poly(p, st)) != cudaSuccess) break;
-        p.x = b;
+    for (int k = 0; k < steps && e == cudaSuccess;) {
+        // this group: steps k .. k + n, as even as they go
+        const int left = steps - k, room = (left + kGroup - 1) / kGroup;
+        int n = group ? (left + room - 1) / room : 1;
+        double gain = 1.0;
+        for (int j = 0; j < n; ++j) {
+            gain *= sc.gain[k + j];
+            if (j > 0 && gain > kGroupGain) n = j;
+        }
+        // where A, B and Q lie among the four square buffers
+        int a = 0, b = 1, q = 1;
+        auto other = [](int i, int j, int l) {
+            int f = 0;
+            while (f == i || f == j || f == l) ++f;
+            return f;
+        };
+        auto product = [&](cudaError_t (*launch)(const NsProduct&, cudaStream_t), int i, int j, int out, float alpha) {
+            p.x = sq[i];
+            p.y = sq[j];
+            p.out = sq[out];
+            p.alpha = alpha;
+            if (e == cudaSuccess) e = launch(p, st);
+        };
+        float sq_q = sc.b[k];                    // Q's scale; every scale is a power of two
+        gain = 1.0;
+        for (int j = 0; j < n; ++j) {
+            const float* const f = coeffs ? coeffs + 3 * (k + j) : kDefault;
+            const float sa = sc.a[k + j], sb = sc.b[k + j];
+            if (j == 0) {
+                p.x = x;
+                p.out = sq[a];
+                p.alpha = sa / (sc.x[k] * sc.x[k]);
+                if (e == cudaSuccess) e = launch_ns_gram(p, st);
+            } else {                             // C = B A, A = C B; the old B is not needed any more, unless it is Q
+                const float s0 = sc.b[k + j - 1], s1 = sc.a[k + j - 1], s2 = scale_of(sc.top[k + j - 1] * sc.top[k + j]);
+                const int c = other(a, b, q);
+                product(launch_ns_mul, b, a, c, s2 / (s0 * s1));
+                product(launch_ns_mul, c, b, a, sa / (s2 * s0));
+                b = other(a, q, q);
+            }
+            p.beta = f[1] * (sb / sa);
+            p.diag = f[0] * sb;
+            product(launch_ns_poly, a, a, b, f[2] * (sb / (sa * sa)));
+            gain *= sc.gain[k + j];
+            if (j > 0) {                         // Q = B Q
+                const float s = scale_of(gain);
+                const int to = other(a, b, q);
+                product(launch_ns_mul, b, q, to, s / (sb * sq_q));
+                q = to;
+                sq_q = s;
+            }
+        }
+        if (e != cudaSuccess) break;
+        k += n;
+        p.x = sq[q];
         p.y = x;
-        if (k + 1 < steps) {
-            p.kind = kNsStep;
+        if (k < steps) {
             p.out = next;
-            p.alpha = sc.x[k + 1] / (sb * sx);
+            p.alpha = sc.x[k] / (sq_q * sc.x[k - n]);
             e = launch_ns_step(p, st);
             std::swap(x, next);
         } else {
-            p.kind = kNsLast;
             p.last = &dst;
-            p.alpha = 1.f / (sb * sx);
+            p.alpha = 1.f / (sq_q * sc.x[k - n]);
             e = launch_ns_last(p, st);
         }
     }

@@ -19,7 +19,8 @@
 // lies off the diagonal's square is stored twice, as it is and mirrored (a lane holds a row, so the
 // mirrored row is 32 consecutive elements of a warp).  B X needs X along its columns, which the
 // matrix descriptors take as an MN-major operand: nothing is transposed in memory, and a I is
-// in B's diagonal, so that no epilogue but poly's reads anything.
+// in B's diagonal, so that no epilogue but poly's reads anything.  Several steps can share one pass over
+// X (ns_run): all in between are products of polynomials of one symmetric matrix, lower tiles too.
 //
 // Roles of a CTA (12 warps) as in the linear layers' kernel: warp 8 loads the operand tiles with
 // tensor-map copies into a ring of stages, warp 9 issues the MMAs, warps 0-7 empty the double-buffered
@@ -64,7 +65,7 @@ template <int EP_, int CG_, int BN_, bool SPLIT_>
 struct NsCfg {
     static constexpr int EP = EP_, CG = CG_, BN = BN_;
     static constexpr bool SPLIT = SPLIT_;
-    static constexpr bool TRI = EP == kNsGram || EP == kNsPoly;  // lower tiles only
+    static constexpr bool TRI = EP != kNsStep && EP != kNsLast;  // symmetric: lower tiles only
     static constexpr bool B_MN = !TRI;
     static constexpr int TM = 128 * CG, R = TM / BN;             // R tiles side by side make a square
     static constexpr int BROWS = BN / CG;
@@ -538,7 +539,7 @@ cudaError_t ns_launch(const NsProduct& p, int splits, int dev, cudaStream_t st) 
     }
     CUtensorMap ma, mb;
     if ((e = ns_map(&ma, p.x, p.batch)) != cudaSuccess) return e;
-    if ((e = ns_map(&mb, C::TRI ? p.x : p.y, p.batch)) != cudaSuccess) return e;
+    if ((e = ns_map(&mb, C::EP == kNsGram || C::EP == kNsPoly ? p.x : p.y, p.batch)) != cudaSuccess) return e;
     int64_t mt, nt;
     const int64_t per = ns_tiles<C>(p, &mt, &nt), tiles = per * p.batch, kb = ns_ceil(p.x.cols, 64);
     const int each = C::CG == 2 ? 2 : C::SPLIT ? splits : 1;
@@ -582,32 +583,38 @@ float ns_estimate(const NsProduct& p, int splits, int dev, float fixed, float kb
     return fixed + waves * float(steps) * kb + (cut ? 0.5f : 1.f) * epi;
 }
 
+// The configuration with the lowest estimate: 256 or 128 columns of a pair, or 64 of one CTA with
+// K over `splits` of them.
+struct NsChoice {
+    float cost;
+    int which, splits;
+};
+template <int EP>
+NsChoice ns_choose(const NsProduct& p, int dev) {
+    NsChoice best{ns_estimate<NsCfg<EP, 2, 256, false>>(p, 1, dev, 5.0f, 0.82f, 3.5f), 256, 1};
+    auto consider = [&](float cost, int which, int splits) {
+        if (cost < best.cost) best = NsChoice{cost, which, splits};
+    };
+    consider(ns_estimate<NsCfg<EP, 2, 128, false>>(p, 1, dev, 4.0f, 0.46f, 2.5f), 128, 1);
+    for (int s = 1; s <= 8; s *= 2) consider(ns_estimate<NsCfg<EP, 1, 64, true>>(p, s, dev, 4.0f, 0.36f, 1.0f), 64, s);
+    return best;
+}
+
+template <int EP>
+float ns_cost(const NsProduct& p) {
+    int dev = 0;
+    return cudaGetDevice(&dev) == cudaSuccess ? ns_choose<EP>(p, dev).cost : 0.f;
+}
+
 template <int EP>
 cudaError_t ns_product(const NsProduct& p, cudaStream_t st) {
     int dev = 0;
     const cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    using P256 = NsCfg<EP, 2, 256, false>;
-    using P128 = NsCfg<EP, 2, 128, false>;
-    using S64 = NsCfg<EP, 1, 64, true>;
-    float best = ns_estimate<P256>(p, 1, dev, 5.0f, 0.82f, 3.5f);
-    int which = 256, splits = 1;
-    const float p128 = ns_estimate<P128>(p, 1, dev, 4.0f, 0.46f, 2.5f);
-    if (p128 < best) {
-        best = p128;
-        which = 128;
-    }
-    for (int s = 1; s <= 8; s *= 2) {
-        const float c = ns_estimate<S64>(p, s, dev, 4.0f, 0.36f, 1.0f);
-        if (c < best) {
-            best = c;
-            which = 64;
-            splits = s;
-        }
-    }
-    if (which == 256) return ns_launch<P256>(p, 1, dev, st);
-    if (which == 128) return ns_launch<P128>(p, 1, dev, st);
-    return ns_launch<S64>(p, splits, dev, st);
+    const NsChoice c = ns_choose<EP>(p, dev);
+    if (c.which == 256) return ns_launch<NsCfg<EP, 2, 256, false>>(p, 1, dev, st);
+    if (c.which == 128) return ns_launch<NsCfg<EP, 2, 128, false>>(p, 1, dev, st);
+    return ns_launch<NsCfg<EP, 1, 64, true>>(p, c.splits, dev, st);
 }
 
 }  // namespace

@@ -14,7 +14,8 @@ BF16, F32 = torch.bfloat16, torch.float32
 # vectors, tiles and their edges in both orientations, sides of no 16-byte multiple, a long thin
 # matrix (K split over clusters), several tiles of each configuration
 SHAPES = [(1, 1), (1, 7), (5, 3), (64, 32), (33, 65), (64, 64), (65, 64), (128, 128), (127, 129), (200, 1000), (256, 256), (257, 130),
-          (384, 640), (16, 16384), (9000, 24), (512, 2048), (1001, 777), (1024, 1024), (1300, 2600)]
+          (384, 640), (16, 16384), (9000, 24), (512, 2048), (1001, 777), (1024, 1024), (1300, 2600), (3000, 1100),
+          (700, 6000), (64, 60000)]
 
 
 def workspace(count, rows, cols, extra=64):
