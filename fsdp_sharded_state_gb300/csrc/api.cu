@@ -18,6 +18,7 @@
 #include "kernels.hpp"
 #include "layout.hpp"
 #include "linear.hpp"
+#include "norm.hpp"
 #include "ns.hpp"
 #include "staged.hpp"
 
@@ -518,7 +519,7 @@ int fsdp_check_status(fsdp_stream_t stream) {
     for (auto take : {fsdp::take_wait_error_forward, fsdp::take_wait_error_forward_pair, fsdp::take_wait_error_dgrad,
                       fsdp::take_wait_error_dgrad_pair, fsdp::take_wait_error_wgrad, fsdp::take_wait_error_ns_gram,
                       fsdp::take_wait_error_ns_poly, fsdp::take_wait_error_ns_mul, fsdp::take_wait_error_ns_step,
-                      fsdp::take_wait_error_ns_last}) {
+                      fsdp::take_wait_error_ns_last, fsdp::take_wait_error_norm_forward, fsdp::take_wait_error_norm_backward}) {
         unsigned int linear = 0;
         e = take(&linear);
         if (e != cudaSuccess) return cuda_fail(e, "wait status read");

@@ -40,5 +40,7 @@ int64_t norm_partial_floats(int64_t rows, int64_t cols);
 
 cudaError_t launch_norm_forward(const NormProblem& p, cudaStream_t st);
 cudaError_t launch_norm_backward(const NormProblem& p, cudaStream_t st);
+cudaError_t take_wait_error_norm_forward(unsigned int* flag);
+cudaError_t take_wait_error_norm_backward(unsigned int* flag);
 
 }  // namespace fsdp

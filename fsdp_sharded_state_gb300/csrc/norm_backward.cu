@@ -26,72 +26,105 @@ struct BackwardArgs {
     int64_t lddx;
     float* partial;                 // [2][groups][pitch], or NULL
     int64_t pitch, rows;
-    int32_t cols, ctas;
+    int32_t cols, ctas, stages, block;
+    uint64_t wait_ns;
 };
 
 // Columns of a row of partial sums.
 __host__ __device__ inline int64_t partial_pitch(int64_t cols) { return (cols + 7) / 8 * 8; }
 
 template <class C>
-constexpr int backward_smem() {
-    return C::GW == 1 ? 8 * C::COLS * 4 : 4 * kNormMaxWarps * 4;
-}
-
-template <class C>
-__global__ void __launch_bounds__(C::THREADS)
+__global__ void __launch_bounds__(C::THREADS, 512 / C::THREADS)
 k_norm_backward(const __grid_constant__ BackwardArgs a) {
     using T = typename C::T;
-    extern __shared__ __align__(16) unsigned char smem_raw[];
+    extern __shared__ __align__(128) unsigned char smem_raw[];   // the rings; at the end a row of sums per warp
+    __shared__ __align__(16) float sums[C::GW > 1 ? 4 * kNormMaxWarps : 4];
     float* const smem = reinterpret_cast<float*>(smem_raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int t = C::GW == 1 ? lane % C::L : tid;
     const int rank = C::CLUSTER ? int(cluster_rank()) : 0, first = rank * C::COLS;
     const int group = blockIdx.x / a.ctas, groups = gridDim.x / a.ctas;
+    const bool res = a.residual != nullptr;
+    RowRing<C, 3> ring = make_ring<C, 3>(smem_raw, warp, first, a.cols, a.stages, a.block, a.wait_ns);
+    ring.base[0] = static_cast<const T*>(a.x) + first;
+    ring.base[1] = static_cast<const T*>(a.dy) + first;
+    ring.base[2] = res ? static_cast<const T*>(a.residual) + first : nullptr;
+    ring.ld[0] = a.ldx;
+    ring.ld[1] = a.lddy;
+    ring.ld[2] = a.ldr;
+    const bool issuer = C::GW == 1 || tid == 0;
+    if (C::GW == 1 ? lane == 0 : tid == 0) ring.init();
     if constexpr (C::CLUSTER) {                  // no CTA writes to another that has not started
         cluster_arrive();
         cluster_wait();
+    } else {
+        __syncthreads();
     }
     pdl_wait();
+    // blocks of rows: a warp's (GW = 1), a CTA's or a cluster's (one row)
+    const int64_t step = int64_t(groups) * (C::GW == 1 ? 8 : 1) * a.block;
+    const int64_t row0 = (int64_t(group) * (C::GW == 1 ? 8 : 1) + (C::GW == 1 ? warp : 0)) * a.block;
+    if (issuer) {
+        for (int s = 0; s < a.stages; ++s)
+            if (row0 + s * step < a.rows) ring.fetch(row0 + s * step, a.rows, s, lane);
+    }
     float w[C::E], dw[C::E], db[C::E];
     norm_vector<C>(static_cast<const T*>(a.weight), a.cols, first, t, 1.f, w);
 #pragma unroll
     for (int e = 0; e < C::E; ++e) dw[e] = db[e] = 0.f;
-    RowSum<C, 2> sum{smem};
+    RowSum<C, 2> sum{sums};
     const float n = float(a.cols);
-    const int64_t step = int64_t(groups) * C::ROWS;
-    int64_t row = int64_t(group) * C::ROWS + (C::GW == 1 ? tid / C::L : 0);
-    // the threads of a warp, CTA or cluster leave the loop together
-    for (int64_t at = int64_t(group) * C::ROWS; at < a.rows; at += step, row += step) {
-        const bool have = row < a.rows;
-        float h[C::E], g[C::E];
-        float s[2] = {0.f, 0.f}, r = 0.f;
-        if (have) {
-            const float mean = a.mean[row];
-            r = a.rstd[row];
-            norm_load<C>(static_cast<const T*>(a.x) + row * a.ldx, a.cols, first, t, h);
-            norm_load<C>(static_cast<const T*>(a.dy) + row * a.lddy, a.cols, first, t, g);
+    int s = 0;
+    uint32_t phase = 0;
+    auto next_stage = [&](int64_t row) {
+        if (issuer && row + a.stages * step < a.rows) ring.fetch(row + a.stages * step, a.rows, s, lane);
+        if (++s == a.stages) {
+            s = 0;
+            phase ^= 1;
+        }
+    };
+    // the threads of a warp, CTA or cluster leave the loops together
+    for (int64_t row = row0; row < a.rows; row += step) {
+        const int count = a.rows - row < a.block ? int(a.rows - row) : a.block;
+        if (C::GW == 1) ring.wait(s, phase);
+        for (int j0 = 0; j0 < count; j0 += C::GW == 1 ? 32 / C::L : 1) {
+            const int j = j0 + (C::GW == 1 ? lane / C::L : 0);
+            const bool have = j < count;
+            float h[C::E], g[C::E], add[C::E], v[2] = {0.f, 0.f}, rstd = 0.f;
+            if (have) {
+                const float mean = a.mean[row + j];
+                rstd = a.rstd[row + j];
+                if (C::GW > 1) ring.wait(s, phase);
+                norm_load<C>(ring.row_of(row + j, j, s, 0) - first, a.cols, first, t, h);
+                norm_load<C>(ring.row_of(row + j, j, s, 1) - first, a.cols, first, t, g);
+                if (res) norm_load<C>(ring.row_of(row + j, j, s, 2) - first, a.cols, first, t, add);
+#pragma unroll
+                for (int e = 0; e < C::E; ++e) {
+                    h[e] = norm_col<C>(first, t, e) < a.cols ? (h[e] - mean) * rstd : 0.f;
+                    dw[e] = __fmaf_rn(g[e], h[e], dw[e]);
+                    db[e] += g[e];
+                    g[e] *= w[e];
+                    v[0] += g[e];
+                    v[1] = __fmaf_rn(g[e], h[e], v[1]);
+                }
+            }
+            sum(v, warp, lane, a.ctas);
+            if (C::GW > 1) next_stage(row);      // every thread has read the stage
+            if (!have) continue;
+            const float c0 = v[0] / n, c1 = v[1] / n;
 #pragma unroll
             for (int e = 0; e < C::E; ++e) {
-                h[e] = norm_col<C>(first, t, e) < a.cols ? (h[e] - mean) * r : 0.f;
-                dw[e] = __fmaf_rn(g[e], h[e], dw[e]);
-                db[e] += g[e];
-                g[e] *= w[e];
-                s[0] += g[e];
-                s[1] = __fmaf_rn(g[e], h[e], s[1]);
+                g[e] = rstd * (g[e] - c0 - h[e] * c1);
+                if (res) g[e] += add[e];
             }
+            norm_store<C>(static_cast<T*>(a.dx) + (row + j) * a.lddx, a.cols, first, t, g);
         }
-        sum(s, warp, lane, a.ctas);
-        if (!have) continue;
-        const float c0 = s[0] / n, c1 = s[1] / n;
-#pragma unroll
-        for (int e = 0; e < C::E; ++e) g[e] = r * (g[e] - c0 - h[e] * c1);
-        if (a.residual) {
-            norm_load<C>(static_cast<const T*>(a.residual) + row * a.ldr, a.cols, first, t, h);
-#pragma unroll
-            for (int e = 0; e < C::E; ++e) g[e] += h[e];
+        if (C::GW == 1) {
+            __syncwarp();                        // every lane has read the stage
+            next_stage(row);
         }
-        norm_store<C>(static_cast<T*>(a.dx) + row * a.lddx, a.cols, first, t, g);
     }
+    ring.leave();
     if (!a.partial) return;
     float* const out_w = a.partial + group * a.pitch;
     float* const out_b = out_w + groups * a.pitch;
@@ -160,11 +193,12 @@ k_norm_join(const float* part, int parts, int64_t pitch, int cols, T* dw, T* db,
     }
 }
 
-// Groups of threads that work through the rows, each with a row of partial sums: as many as
+// CTAs (or clusters) that work through the rows, each with a row of partial sums: as many as
 // fit the 152 SMs at once, fewer where there are few rows.
 template <class C>
 int64_t backward_groups(int64_t rows, int64_t cols) {
-    const int64_t want = (rows + C::ROWS - 1) / C::ROWS, room = 152 * (512 / C::THREADS) / norm_ctas<C>(cols);
+    const int64_t each = ring_shape<C>(3, cols, 512 / C::THREADS).block * (C::GW == 1 ? 8 : 1);
+    const int64_t want = (rows + each - 1) / each, room = 152 * (512 / C::THREADS) / norm_ctas<C>(cols);
     return want < room ? want : room;
 }
 
@@ -175,9 +209,14 @@ cudaError_t launch_as(const NormProblem& p, cudaStream_t st) {
     const bool sums = p.dw || p.db;
     cudaError_t e = cudaSuccess;
     if (p.rows > 0) {
+        static std::atomic<uint64_t> prepared{0};
+        int dev = 0;
+        if ((e = cudaGetDevice(&dev)) != cudaSuccess || (e = norm_prepare(k_norm_backward<C>, prepared, dev)) != cudaSuccess) return e;
+        const RingShape ring = ring_shape<C>(3, p.cols, 512 / C::THREADS);
+        const size_t last = C::GW == 1 ? size_t(8) * C::COLS * 4 : 0;
         const BackwardArgs a{p.x, p.ldx, p.dy, p.lddy, p.weight, p.residual, p.ldr, p.mean, p.rstd, p.y, p.ldy,
-                             sums ? p.partial : nullptr, pitch, p.rows, int32_t(p.cols), ctas};
-        e = norm_launch(k_norm_backward<C>, int(groups), ctas, C::THREADS, backward_smem<C>(), st, a);
+                             sums ? p.partial : nullptr, pitch, p.rows, int32_t(p.cols), ctas, ring.stages, ring.block, detail::kWaitNs};
+        e = norm_launch(k_norm_backward<C>, int(groups), ctas, C::THREADS, ring.bytes > last ? ring.bytes : last, st, a);
     }
     if (e != cudaSuccess || !sums || (p.rows == 0 && p.accumulate)) return e;
     const dim3 grid(unsigned((p.cols + 31) / 32), 2);
@@ -192,12 +231,17 @@ cudaError_t launch_as(const NormProblem& p, cudaStream_t st) {
 
 int64_t norm_partial_floats(int64_t rows, int64_t cols) {
     int64_t groups = 0;
-    norm_dispatch<float, true>(cols, [&](auto c) {
-        groups = backward_groups<decltype(c)>(rows, cols);
+    auto most = [&](auto c) {
+        const int64_t g = backward_groups<decltype(c)>(rows, cols);
+        if (g > groups) groups = g;
         return cudaSuccess;
-    });
+    };
+    norm_dispatch<float, true>(cols, most);
+    norm_dispatch<uint16_t, true>(cols, most);
     return 2 * groups * partial_pitch(cols);
 }
+
+cudaError_t take_wait_error_norm_backward(unsigned int* flag) { return take_norm_wait_error(flag); }
 
 cudaError_t launch_norm_backward(const NormProblem& p, cudaStream_t st) {
     auto go = [&](auto c) { return launch_as<decltype(c)>(p, st); };

@@ -2,15 +2,20 @@
 // loads and stores, and sums over it.
 //
 // A row belongs to a group of threads that hold it in registers from its load to its store:
-// L lanes of a warp (up to 1024 columns; a warp then works on 32 / L rows), GW warps of a CTA
-// (up to 8192), or GW warps in each CTA of a cluster (up to 65536).  A thread holds 8 V columns: V
-// chunks of 8 neighbours where rows are aligned to 16 bytes (VEC), else 8 V single columns that
-// are a group's width apart, so that a warp's loads are contiguous either way.
+// L lanes of a warp (up to 512 columns; a warp then works on 32 / L rows at once), GW warps of a CTA
+// (up to 8192), or GW warps in each CTA of a cluster (up to 65536).  A thread holds 8 V columns:
+// chunks of 16 bytes where rows are aligned to 16 bytes (VEC), else single columns that are a
+// group's width apart, so that a warp's accesses are contiguous either way.
+//
+// Rows come through shared memory (RowRing): loads of a row by the threads that wait for it
+// leave HBM idle from its last byte to the next row's request (16384 x 4096 bf16 forward 121 us, 0.33 of the
+// copy rate; so 43); bulk copies of the next rows run while one is worked on, whatever the registers hold.
 #pragma once
 
 #include <type_traits>
 
 #include "common.cuh"
+#include "internal.hpp"
 #include "norm.hpp"
 #include "tc5.cuh"
 
@@ -21,12 +26,14 @@ template <typename T_, int L_, int GW_, int V_, bool VEC_, bool CLUSTER_ = false
 struct NormCfg {
     using T = T_;
     static constexpr int L = L_, GW = GW_, V = V_, E = 8 * V_;
+    static constexpr int W = 16 / sizeof(T);                       // columns of a chunk
     static constexpr bool VEC = VEC_, CLUSTER = CLUSTER_;
     static constexpr int THREADS = GW == 1 ? 256 : 32 * GW;
-    static constexpr int ROWS = GW == 1 ? 8 * (32 / L) : 1;        // a CTA works on at once
+    static constexpr int ROWS = GW == 1 ? 8 * (32 / L) : 1;        // side by side in a CTA
     static constexpr int G = GW == 1 ? L : 32 * GW;                // threads of a row in one CTA
     static constexpr int COLS = G * E;                             // columns that they hold
     static_assert(GW == 1 || L == 32, "whole warps");
+    static_assert(GW <= 2 || GW % 4 == 0, "sums of warps, four at a time");
 };
 
 constexpr int kNormMaxCluster = 8;
@@ -37,43 +44,40 @@ __device__ __forceinline__ float norm_get(const float* p) { return *p; }
 __device__ __forceinline__ void norm_put(uint16_t* p, float v) { *p = to_bf16(v); }
 __device__ __forceinline__ void norm_put(float* p, float v) { *p = v; }
 
-__device__ __forceinline__ void get8(const uint16_t* p, float* v) {
+__device__ __forceinline__ void norm_get16(const uint16_t* p, float* v) {
     const uint4 q = ldu4(p);
     v[0] = bf16lo(q.x); v[1] = bf16hi(q.x); v[2] = bf16lo(q.y); v[3] = bf16hi(q.y);
     v[4] = bf16lo(q.z); v[5] = bf16hi(q.z); v[6] = bf16lo(q.w); v[7] = bf16hi(q.w);
 }
-__device__ __forceinline__ void get8(const float* p, float* v) {
-    const float4 a = ld4(p), b = ld4(p + 4);
+__device__ __forceinline__ void norm_get16(const float* p, float* v) {
+    const float4 a = ld4(p);
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
-__device__ __forceinline__ void put8(uint16_t* p, const float* v) {
+__device__ __forceinline__ void norm_put16(uint16_t* p, const float* v) {
     stu4(p, make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])));
 }
-__device__ __forceinline__ void put8(float* p, const float* v) {
-    st4(p, make_float4(v[0], v[1], v[2], v[3]));
-    st4(p + 4, make_float4(v[4], v[5], v[6], v[7]));
-}
+__device__ __forceinline__ void norm_put16(float* p, const float* v) { st4(p, make_float4(v[0], v[1], v[2], v[3])); }
 
 // Column of a thread's element e; t: the thread's place among the G of its row, first: the
 // columns before this CTA's.
 template <class C>
 __device__ __forceinline__ int norm_col(int first, int t, int e) {
-    return first + (C::VEC ? ((e >> 3) * C::G + t) * 8 + (e & 7) : e * C::G + t);
+    return first + (C::VEC ? ((e / C::W) * C::G + t) * C::W + e % C::W : e * C::G + t);
 }
 
-// A thread's elements of a row; 0 past its end.
+// A thread's elements of a row whose first column is at `row` (in global or shared memory); 0
+// past its end.
 template <class C, typename T>
 __device__ __forceinline__ void norm_load(const T* row, int cols, int first, int t, float (&v)[C::E]) {
     if constexpr (C::VEC) {
 #pragma unroll
-        for (int c = 0; c < C::V; ++c) {
-            const int at = norm_col<C>(first, t, 8 * c);
-            if (at + 8 <= cols) {
-                get8(row + at, v + 8 * c);
+        for (int c = 0; c < C::E; c += C::W) {
+            const int at = norm_col<C>(first, t, c);
+            if (at + C::W <= cols) {
+                norm_get16(row + at, v + c);
             } else {
 #pragma unroll
-                for (int k = 0; k < 8; ++k) v[8 * c + k] = at + k < cols ? norm_get(row + at + k) : 0.f;
+                for (int k = 0; k < C::W; ++k) v[c + k] = at + k < cols ? norm_get(row + at + k) : 0.f;
             }
         }
     } else {
@@ -88,14 +92,14 @@ template <class C, typename T>
 __device__ __forceinline__ void norm_store(T* row, int cols, int first, int t, const float (&v)[C::E]) {
     if constexpr (C::VEC) {
 #pragma unroll
-        for (int c = 0; c < C::V; ++c) {
-            const int at = norm_col<C>(first, t, 8 * c);
-            if (at + 8 <= cols) {
-                put8(row + at, v + 8 * c);
+        for (int c = 0; c < C::E; c += C::W) {
+            const int at = norm_col<C>(first, t, c);
+            if (at + C::W <= cols) {
+                norm_put16(row + at, v + c);
             } else {
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (at + k < cols) norm_put(row + at + k, v[8 * c + k]);
+                for (int k = 0; k < C::W; ++k)
+                    if (at + k < cols) norm_put(row + at + k, v[c + k]);
             }
         }
     } else {
@@ -151,9 +155,13 @@ struct RowSum {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 float t = 0.f;
-                for (int w = 0; w < n; w += 4) {
-                    const float4 q = ld4(b + i * kNormMaxWarps + w);
-                    t += (q.x + q.y) + (q.z + q.w);
+                if constexpr (C::GW < 4) {
+                    t = b[i * kNormMaxWarps] + b[i * kNormMaxWarps + 1];
+                } else {
+                    for (int w = 0; w < n; w += 4) {
+                        const float4 q = ld4(b + i * kNormMaxWarps + w);
+                        t += (q.x + q.y) + (q.z + q.w);
+                    }
                 }
                 s[i] = t;
             }
@@ -161,6 +169,153 @@ struct RowSum {
         }
     }
 };
+
+// A ring of stages in shared memory that bulk copies fill, a CTA's for its share of a row or (GW = 1)
+// a warp's for `block` rows; per matrix the 16-byte granules that hold them, as one piece where the rows are
+// back to back, else a piece a row.  Rows may start at any element: the bytes around a piece,
+// which are in its own granules, are read and not used.
+//
+// Waits are bounded: after one that gave up, which is recorded for fsdp_check_status, the others
+// give up at once, and the threads go through their rows with what the stages hold.
+constexpr int kRingStages = 8;
+constexpr int kRingFront = 1024;                 // the stages' barriers: kRingStages of each of 8 warps
+
+// Bytes of a row's piece, and of a stage's share of one matrix.
+__host__ __device__ inline int ring_piece(int cols, int esize) { return (cols * esize + 15) / 16 * 16 + 16; }
+
+template <class C, int N>
+struct RowRing {
+    using T = typename C::T;
+    const T* base[N];                            // of this CTA's columns; NULL: not there
+    int64_t ld[N];
+    unsigned char* smem;                         // this warp's or CTA's stages
+    uint32_t bars;
+    int stages, piece, block, cols;              // cols: of this CTA
+    uint64_t wait_ns;
+
+    // By one thread, before any other uses the ring.
+    __device__ __forceinline__ void init() const {
+        for (int s = 0; s < stages; ++s) mbar_init(bars + 8 * s, 1);
+        mbar_fence_init();
+    }
+    __device__ __forceinline__ bool whole(int k) const { return C::GW == 1 && ld[k] == cols; }
+    __device__ __forceinline__ void copy(int64_t row, int64_t n, uint32_t dst, int k, int s, uint32_t& bytes, bool issue) const {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(base[k] + row * ld[k]);
+        const uint32_t size = cols > 0 ? uint32_t((a & 15) + n * cols * int64_t(sizeof(T)) + 15) & ~15u : 0;   // a cluster's CTA past the row's end
+        bytes += size;
+        if (issue && size) bulk_g2s(dst, reinterpret_cast<const void*>(a & ~uintptr_t(15)), size, bars + 8 * s);
+    }
+    // The copies of the rows from `row` on (at most `block`, up to `rows`) into stage s.  By one
+    // thread of the CTA, or by a whole warp.
+    __device__ __forceinline__ void fetch(int64_t row, int64_t rows, int s, int lane) const {
+        const int n = rows - row < block ? int(rows - row) : block;
+        const uint32_t at = smem_addr(smem) + uint32_t(s * N * block * piece);
+        if constexpr (C::GW > 1) {
+            uint32_t bytes = 0;
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+                if (base[k]) copy(row, 1, 0, k, s, bytes, false);
+            mbar_arrive_tx(bars + 8 * s, bytes);
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+                if (base[k]) copy(row, 1, at + uint32_t(k * piece), k, s, bytes, true);
+        } else {
+            // lane 0 copies the matrices whose rows are back to back, lane j row j of the others
+#pragma unroll
+            for (int pass = 0; pass < 2; ++pass) {
+                uint32_t bytes = 0;
+#pragma unroll
+                for (int k = 0; k < N; ++k) {
+                    if (!base[k]) continue;
+                    const uint32_t dst = at + uint32_t(k * block * piece);
+                    if (whole(k)) {
+                        if (lane == 0) copy(row, n, dst, k, s, bytes, pass);
+                    } else {
+                        for (int j = lane; j < n; j += 32) copy(row + j, 1, dst + uint32_t(j * piece), k, s, bytes, pass);
+                    }
+                }
+                if (pass == 0) {
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) bytes += __shfl_xor_sync(0xffffffffu, bytes, o);
+                    if (lane == 0) mbar_arrive_tx(bars + 8 * s, bytes);
+                    __syncwarp();
+                }
+            }
+        }
+    }
+    // What stage s holds of row `row` of matrix k, the j-th of the stage, from this CTA's first column on.
+    __device__ __forceinline__ const T* row_of(int64_t row, int j, int s, int k) const {
+        const unsigned char* const p = smem + (s * N + k) * block * piece;
+        if constexpr (C::GW == 1) {
+            if (whole(k))
+                return reinterpret_cast<const T*>(p + (C::VEC ? 0 : reinterpret_cast<uintptr_t>(base[k] + (row - j) * ld[k]) & 15)) + j * cols;
+        }
+        return reinterpret_cast<const T*>(p + j * piece + (C::VEC ? 0 : reinterpret_cast<uintptr_t>(base[k] + row * ld[k]) & 15));
+    }
+    __device__ __forceinline__ void wait(int s, uint32_t phase) {
+        if (!mbar_wait_bounded(bars + 8 * s, phase, wait_ns)) {
+            wait_ns = 0;
+            atomicOr(&g_wait_error, 1u);
+        }
+    }
+    // Before the CTA leaves: copies that were given up land within this.
+    __device__ __forceinline__ void leave() const {
+        if (wait_ns) return;
+        const uint64_t t0 = global_ns();
+        for (int i = 0; i < (1 << 20) && global_ns() - t0 < 2000000ull; ++i) __nanosleep(1000);
+    }
+};
+
+// The ring of a thread: its warp's or its CTA's.
+template <class C, int N>
+__device__ __forceinline__ RowRing<C, N> make_ring(unsigned char* smem, int warp, int first, int all, int stages, int block, uint64_t wait_ns) {
+    RowRing<C, N> r;
+    const int left = all - first;
+    r.cols = left < 0 ? 0 : left < C::COLS ? left : C::COLS;
+    r.piece = ring_piece(all < C::COLS ? all : C::COLS, int(sizeof(typename C::T)));
+    r.stages = stages;
+    r.block = block;
+    r.wait_ns = wait_ns;
+    const int mine = C::GW == 1 ? warp : 0;
+    r.bars = smem_addr(smem) + uint32_t(mine * kRingStages * 8);
+    r.smem = smem + kRingFront + mine * stages * N * block * r.piece;
+    return r;
+}
+
+// Host side: how many rows a stage holds, how many stages, and the shared memory of a CTA of which
+// per_sm share an SM.  A warp's stage holds about 1 KB of each matrix.
+struct RingShape {
+    int block, stages;
+    size_t bytes;
+};
+template <class C>
+RingShape ring_shape(int n, int64_t cols, int per_sm) {
+    constexpr int es = int(sizeof(typename C::T)), rings = C::GW == 1 ? 8 : 1, side = C::GW == 1 ? 32 / C::L : 1;
+    const int piece = ring_piece(int(cols < C::COLS ? cols : C::COLS), es);
+    RingShape r;
+    r.block = side;
+    if (C::GW == 1)
+        while (r.block * piece < 1024) r.block += side;
+    const int stage = n * r.block * piece * rings, fit = (208 * 1024 / per_sm - kRingFront - 4096) / stage;
+    r.stages = fit > kRingStages ? kRingStages : fit < 2 ? 2 : fit;
+    r.bytes = size_t(kRingFront) + size_t(r.stages) * stage;
+    return r;
+}
+
+std::atomic<bool> g_norm_launched{false};
+
+cudaError_t take_norm_wait_error(unsigned int* flag) {
+    *flag = 0;
+    return g_norm_launched.load(std::memory_order_relaxed) ? take_local_wait_error(flag) : cudaSuccess;
+}
+
+int norm_sms(int dev) {
+    static std::atomic<int> n[64];
+    if (dev < 0 || dev >= 64) return 152;
+    int v = n[dev].load(std::memory_order_relaxed);
+    if (v == 0 && cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess) n[dev].store(v, std::memory_order_relaxed);
+    return v > 0 ? v : 152;
+}
 
 // The configuration of a width: f(cfg) for the narrowest that holds it.
 template <typename T, bool VEC, class F>
@@ -170,7 +325,7 @@ cudaError_t norm_dispatch(int64_t cols, F&& f) {
     if (cols <= 128) return f(NormCfg<T, 16, 1, 1, VEC>{});
     if (cols <= 256) return f(NormCfg<T, 32, 1, 1, VEC>{});
     if (cols <= 512) return f(NormCfg<T, 32, 1, 2, VEC>{});
-    if (cols <= 1024) return f(NormCfg<T, 32, 1, 4, VEC>{});
+    if (cols <= 1024) return f(NormCfg<T, 32, 2, 2, VEC>{});
     if (cols <= 2048) return f(NormCfg<T, 32, 4, 2, VEC>{});
     if (cols <= 4096) return f(NormCfg<T, 32, 8, 2, VEC>{});
     if (cols <= 8192) return f(NormCfg<T, 32, 16, 2, VEC>{});
@@ -184,6 +339,15 @@ int norm_ctas(int64_t cols) {
     int n = 2;
     while (int64_t(n) * C::COLS < cols) n *= 2;
     return n;
+}
+
+// The most dynamic shared memory that a kernel may ask for, set once per device.
+template <typename K>
+cudaError_t norm_prepare(K kernel, std::atomic<uint64_t>& done, int dev) {
+    if (dev < 64 && (done.load(std::memory_order_relaxed) >> dev & 1)) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 224 * 1024);
+    if (e == cudaSuccess && dev < 64) done.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
+    return e;
 }
 
 template <typename... KArgs, typename... Args>
@@ -201,6 +365,7 @@ cudaError_t norm_launch(void (*kernel)(KArgs...), int groups, int ctas, int thre
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = ctas > 1 ? 2 : 1;
+    g_norm_launched.store(true, std::memory_order_relaxed);
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<Args&&>(args)...);
 }
 
