@@ -37,13 +37,13 @@ template <class C>
 __global__ void __launch_bounds__(C::THREADS, 512 / C::THREADS)
 k_norm_backward(const __grid_constant__ BackwardArgs a) {
     using T = typename C::T;
-    extern __shared__ __align__(128) unsigned char smem_raw[];   // the rings; at the end a row of sums per warp
-    __shared__ __align__(16) float sums[C::GW > 1 ? 4 * kNormMaxWarps : 4];
-    float* const smem = reinterpret_cast<float*>(smem_raw);
+    using Sums = RowSum<C, 2>;
+    extern __shared__ __align__(128) unsigned char smem_raw[];   // the rings; at the end a row of sums per group
+    __shared__ __align__(16) float sums[C::GW > 1 ? Sums::FLOATS * C::SIDE : 4];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int t = C::GW == 1 ? lane % C::L : tid;
+    const int t = C::GW == 1 ? lane % C::L : tid % C::G;
     const int rank = C::CLUSTER ? int(cluster_rank()) : 0, first = rank * C::COLS;
-    const int group = blockIdx.x / a.ctas, groups = gridDim.x / a.ctas;
+    const int part = blockIdx.x / a.ctas, parts = gridDim.x / a.ctas;
     const bool res = a.residual != nullptr;
     RowRing<C, 3> ring = make_ring<C, 3>(smem_raw, warp, first, a.cols, a.stages, a.block, a.wait_ns);
     ring.base[0] = static_cast<const T*>(a.x) + first;
@@ -52,8 +52,8 @@ k_norm_backward(const __grid_constant__ BackwardArgs a) {
     ring.ld[0] = a.ldx;
     ring.ld[1] = a.lddy;
     ring.ld[2] = a.ldr;
-    const bool issuer = C::GW == 1 || tid == 0;
-    if (C::GW == 1 ? lane == 0 : tid == 0) ring.init();
+    const bool issuer = C::GW == 1 || t == 0;
+    if (C::GW == 1 ? lane == 0 : t == 0) ring.init();
     if constexpr (C::CLUSTER) {                  // no CTA writes to another that has not started
         cluster_arrive();
         cluster_wait();
@@ -61,19 +61,20 @@ k_norm_backward(const __grid_constant__ BackwardArgs a) {
         __syncthreads();
     }
     pdl_wait();
-    // blocks of rows: a warp's (GW = 1), a CTA's or a cluster's (one row)
-    const int64_t step = int64_t(groups) * (C::GW == 1 ? 8 : 1) * a.block;
-    const int64_t row0 = (int64_t(group) * (C::GW == 1 ? 8 : 1) + (C::GW == 1 ? warp : 0)) * a.block;
+    // blocks of rows go to the groups in turn
+    const int64_t step = int64_t(parts) * C::SIDE * a.block;
+    const int64_t row0 = (int64_t(part) * C::SIDE + warp / C::GW) * a.block;
     if (issuer) {
         for (int s = 0; s < a.stages; ++s)
             if (row0 + s * step < a.rows) ring.fetch(row0 + s * step, a.rows, s, lane);
     }
-    float w[C::E], dw[C::E], db[C::E];
+    pair w[C::P], dw[C::P], db[C::P];
     norm_vector<C>(static_cast<const T*>(a.weight), a.cols, first, t, 1.f, w);
 #pragma unroll
-    for (int e = 0; e < C::E; ++e) dw[e] = db[e] = 0.f;
-    RowSum<C, 2> sum{sums};
-    const float n = float(a.cols);
+    for (int i = 0; i < C::P; ++i) dw[i] = db[i] = 0;
+    Sums sum{sums};
+    const bool full = norm_full<C>(a.cols, first, t);
+    const float over_n = 1.f / float(a.cols);
     int s = 0;
     uint32_t phase = 0;
     auto next_stage = [&](int64_t row) {
@@ -83,14 +84,15 @@ k_norm_backward(const __grid_constant__ BackwardArgs a) {
             phase ^= 1;
         }
     };
-    // the threads of a warp, CTA or cluster leave the loops together
+    // the threads of a group, or of a cluster, leave the loops together
     for (int64_t row = row0; row < a.rows; row += step) {
         const int count = a.rows - row < a.block ? int(a.rows - row) : a.block;
         if (C::GW == 1) ring.wait(s, phase);
         for (int j0 = 0; j0 < count; j0 += C::GW == 1 ? 32 / C::L : 1) {
             const int j = j0 + (C::GW == 1 ? lane / C::L : 0);
             const bool have = j < count;
-            float h[C::E], g[C::E], add[C::E], v[2] = {0.f, 0.f}, rstd = 0.f;
+            pair h[C::P], g[C::P], add[C::P];
+            float v[2] = {0.f, 0.f}, rstd = 0.f;
             if (have) {
                 const float mean = a.mean[row + j];
                 rstd = a.rstd[row + j];
@@ -98,24 +100,33 @@ k_norm_backward(const __grid_constant__ BackwardArgs a) {
                 norm_load<C>(ring.row_of(row + j, j, s, 0) - first, a.cols, first, t, h);
                 norm_load<C>(ring.row_of(row + j, j, s, 1) - first, a.cols, first, t, g);
                 if (res) norm_load<C>(ring.row_of(row + j, j, s, 2) - first, a.cols, first, t, add);
+                const pair m = pair_of(-mean, -mean), r = pair_of(rstd, rstd);
 #pragma unroll
-                for (int e = 0; e < C::E; ++e) {
-                    h[e] = norm_col<C>(first, t, e) < a.cols ? (h[e] - mean) * rstd : 0.f;
-                    dw[e] = __fmaf_rn(g[e], h[e], dw[e]);
-                    db[e] += g[e];
-                    g[e] *= w[e];
-                    v[0] += g[e];
-                    v[1] = __fmaf_rn(g[e], h[e], v[1]);
+                for (int i = 0; i < C::P; ++i) h[i] = mul2(add2(h[i], m), r);
+                if (!full) norm_trim<C>(a.cols, first, t, h);
+                pair p = 0, q = 0;
+#pragma unroll
+                for (int i = 0; i < C::P; ++i) {
+                    dw[i] = fma2(g[i], h[i], dw[i]);
+                    db[i] = add2(db[i], g[i]);
+                    g[i] = mul2(g[i], w[i]);
+                    p = add2(p, g[i]);
+                    q = fma2(g[i], h[i], q);
                 }
+                v[0] = both(p);
+                v[1] = both(q);
             }
             sum(v, warp, lane, a.ctas);
             if (C::GW > 1) next_stage(row);      // every thread has read the stage
             if (!have) continue;
-            const float c0 = v[0] / n, c1 = v[1] / n;
+            const float c0 = -v[0] * over_n, c1 = -v[1] * over_n;
+            const pair m0 = pair_of(c0, c0), m1 = pair_of(c1, c1), r = pair_of(rstd, rstd);
+            if (res) {
 #pragma unroll
-            for (int e = 0; e < C::E; ++e) {
-                g[e] = rstd * (g[e] - c0 - h[e] * c1);
-                if (res) g[e] += add[e];
+                for (int i = 0; i < C::P; ++i) g[i] = fma2(fma2(h[i], m1, add2(g[i], m0)), r, add[i]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < C::P; ++i) g[i] = mul2(fma2(h[i], m1, add2(g[i], m0)), r);
             }
             norm_store<C>(static_cast<T*>(a.dx) + (row + j) * a.lddx, a.cols, first, t, g);
         }
@@ -126,29 +137,34 @@ k_norm_backward(const __grid_constant__ BackwardArgs a) {
     }
     ring.leave();
     if (!a.partial) return;
-    float* const out_w = a.partial + group * a.pitch;
-    float* const out_b = out_w + groups * a.pitch;
-    if constexpr (C::GW == 1) {
-        // the rows of a warp, then the warps of the CTA, in order
+    float* const out_w = a.partial + part * a.pitch;
+    float* const out_b = out_w + parts * a.pitch;
+    if constexpr (C::SIDE > 1) {
+        // the rows of a warp, then the groups of the CTA, in order
+        float* const smem = reinterpret_cast<float*>(smem_raw);
 #pragma unroll
         for (int o = 16; o >= C::L; o >>= 1)
 #pragma unroll
-            for (int e = 0; e < C::E; ++e) {
-                dw[e] += __shfl_xor_sync(0xffffffffu, dw[e], o);
-                db[e] += __shfl_xor_sync(0xffffffffu, db[e], o);
+            for (int i = 0; i < C::P; ++i) {
+                dw[i] = add2(dw[i], __shfl_xor_sync(0xffffffffu, dw[i], o));
+                db[i] = add2(db[i], __shfl_xor_sync(0xffffffffu, db[i], o));
             }
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
             __syncthreads();
-            if (lane < C::L) {
+            if (C::GW > 1 || lane < C::L) {
 #pragma unroll
-                for (int e = 0; e < C::E; ++e) smem[warp * C::COLS + norm_col<C>(0, t, e)] = which ? db[e] : dw[e];
+                for (int e = 0; e < C::E; e += 2) {
+                    const float2 f = split(which ? db[e / 2] : dw[e / 2]);
+                    smem[warp / C::GW * C::COLS + norm_col<C>(0, t, e)] = f.x;
+                    smem[warp / C::GW * C::COLS + norm_col<C>(0, t, e + 1)] = f.y;
+                }
             }
             __syncthreads();
             for (int c = tid; c < a.cols; c += C::THREADS) {
                 float v = 0.f;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) v += smem[k * C::COLS + c];
+                for (int k = 0; k < C::SIDE; ++k) v += smem[k * C::COLS + c];
                 (which ? out_b : out_w)[c] = v;
             }
         }
@@ -157,8 +173,9 @@ k_norm_backward(const __grid_constant__ BackwardArgs a) {
         for (int e = 0; e < C::E; ++e) {
             const int c = norm_col<C>(first, t, e);
             if (c < a.cols) {
-                out_w[c] = dw[e];
-                out_b[c] = db[e];
+                const float2 f = split(dw[e / 2]), g = split(db[e / 2]);
+                out_w[c] = e & 1 ? f.y : f.x;
+                out_b[c] = e & 1 ? g.y : g.x;
             }
         }
     }
@@ -197,7 +214,7 @@ k_norm_join(const float* part, int parts, int64_t pitch, int cols, T* dw, T* db,
 // fit the 152 SMs at once, fewer where there are few rows.
 template <class C>
 int64_t backward_groups(int64_t rows, int64_t cols) {
-    const int64_t each = ring_shape<C>(3, cols, 512 / C::THREADS).block * (C::GW == 1 ? 8 : 1);
+    const int64_t each = ring_shape<C>(3, cols, 512 / C::THREADS).block * C::SIDE;
     const int64_t want = (rows + each - 1) / each, room = 152 * (512 / C::THREADS) / norm_ctas<C>(cols);
     return want < room ? want : room;
 }
@@ -213,7 +230,7 @@ cudaError_t launch_as(const NormProblem& p, cudaStream_t st) {
         int dev = 0;
         if ((e = cudaGetDevice(&dev)) != cudaSuccess || (e = norm_prepare(k_norm_backward<C>, prepared, dev)) != cudaSuccess) return e;
         const RingShape ring = ring_shape<C>(3, p.cols, 512 / C::THREADS);
-        const size_t last = C::GW == 1 ? size_t(8) * C::COLS * 4 : 0;
+        const size_t last = C::SIDE > 1 ? size_t(C::SIDE) * C::COLS * 4 : 0;
         const BackwardArgs a{p.x, p.ldx, p.dy, p.lddy, p.weight, p.residual, p.ldr, p.mean, p.rstd, p.y, p.ldy,
                              sums ? p.partial : nullptr, pitch, p.rows, int32_t(p.cols), ctas, ring.stages, ring.block, detail::kWaitNs};
         e = norm_launch(k_norm_backward<C>, int(groups), ctas, C::THREADS, ring.bytes > last ? ring.bytes : last, st, a);

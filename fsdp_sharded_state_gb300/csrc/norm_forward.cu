@@ -25,20 +25,27 @@ struct ForwardArgs {
     uint64_t wait_ns;
 };
 
+// CTAs of an SM: 768 threads of up to 80 registers, or two CTAs of 512 of 64 (four of 256 threads
+// spill what they hold of weight and bias).
 template <class C>
-__global__ void __launch_bounds__(C::THREADS, 1024 / C::THREADS)
+constexpr int kForwardCtas = C::THREADS == 256 ? 3 : 2;
+
+template <class C>
+__global__ void __launch_bounds__(C::THREADS, kForwardCtas<C>)
 k_norm_forward(const __grid_constant__ ForwardArgs a) {
     using T = typename C::T;
+    using Sum = RowSum<C, 1>;
+    using Sums = RowSum<C, 2>;
     extern __shared__ __align__(128) unsigned char smem_raw[];   // the rings
-    __shared__ __align__(16) float sums[C::GW > 1 ? 4 * kNormMaxWarps : 4];
+    __shared__ __align__(16) float sums[C::GW > 1 ? (Sum::FLOATS + Sums::FLOATS) * C::SIDE : 4];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int t = C::GW == 1 ? lane % C::L : tid;
+    const int t = C::GW == 1 ? lane % C::L : tid % C::G;
     const int rank = C::CLUSTER ? int(cluster_rank()) : 0, first = rank * C::COLS;
     RowRing<C, 1> ring = make_ring<C, 1>(smem_raw, warp, first, a.cols, a.stages, a.block, a.wait_ns);
     ring.base[0] = static_cast<const T*>(a.x) + first;
     ring.ld[0] = a.ldx;
-    const bool issuer = C::GW == 1 || tid == 0;
-    if (C::GW == 1 ? lane == 0 : tid == 0) ring.init();
+    const bool issuer = C::GW == 1 || t == 0;
+    if (C::GW == 1 ? lane == 0 : t == 0) ring.init();
     if constexpr (C::CLUSTER) {                  // no CTA writes to another that has not started
         cluster_arrive();
         cluster_wait();
@@ -46,18 +53,20 @@ k_norm_forward(const __grid_constant__ ForwardArgs a) {
         __syncthreads();
     }
     pdl_wait();
-    // blocks of rows: a warp's (GW = 1), a CTA's or a cluster's (one row)
-    const int64_t n_groups = int64_t(gridDim.x / a.ctas) * (C::GW == 1 ? 8 : 1), step = n_groups * a.block;
-    const int64_t row0 = (blockIdx.x / a.ctas * (C::GW == 1 ? 8 : 1) + (C::GW == 1 ? warp : 0)) * int64_t(a.block);
+    // blocks of rows go to the groups in turn
+    const int64_t step = int64_t(gridDim.x / a.ctas) * C::SIDE * a.block;
+    const int64_t row0 = (int64_t(blockIdx.x / a.ctas) * C::SIDE + warp / C::GW) * a.block;
     if (issuer) {
         for (int s = 0; s < a.stages; ++s)
             if (row0 + s * step < a.rows) ring.fetch(row0 + s * step, a.rows, s, lane);
     }
-    float w[C::E], b[C::E];
+    pair w[C::P], b[C::P];
     norm_vector<C>(static_cast<const T*>(a.weight), a.cols, first, t, 1.f, w);
     norm_vector<C>(static_cast<const T*>(a.bias), a.cols, first, t, 0.f, b);
-    RowSum<C, 2> sum{sums};
-    const float n = float(a.cols);
+    Sum sum{sums};
+    Sums sum2{sums + (C::GW > 1 ? Sum::FLOATS * C::SIDE : 0)};
+    const bool full = norm_full<C>(a.cols, first, t);
+    const float over_n = 1.f / float(a.cols);
     int s = 0;
     uint32_t phase = 0;
     auto next_stage = [&](int64_t row) {
@@ -67,44 +76,56 @@ k_norm_forward(const __grid_constant__ ForwardArgs a) {
             phase ^= 1;
         }
     };
-    // the threads of a warp, CTA or cluster leave the loops together
+    // the threads of a group, or of a cluster, leave the loops together
     for (int64_t row = row0; row < a.rows; row += step) {
         ring.wait(s, phase);
         const int count = a.rows - row < a.block ? int(a.rows - row) : a.block;
         for (int j0 = 0; j0 < count; j0 += C::GW == 1 ? 32 / C::L : 1) {
             const int j = j0 + (C::GW == 1 ? lane / C::L : 0);
             const bool have = j < count;
-            float x[C::E];
+            pair x[C::P];
             if (have) {
                 norm_load<C>(ring.row_of(row + j, j, s, 0) - first, a.cols, first, t, x);
             } else {
 #pragma unroll
-                for (int e = 0; e < C::E; ++e) x[e] = 0.f;
+                for (int i = 0; i < C::P; ++i) x[i] = 0;
             }
-            float v[2] = {0.f, 0.f};
+            pair p = x[0];
 #pragma unroll
-            for (int e = 0; e < C::E; ++e) v[0] += x[e];
+            for (int i = 1; i < C::P; ++i) p = add2(p, x[i]);
+            float v[1] = {both(p)};
             sum(v, warp, lane, a.ctas);
             if (C::GW > 1) next_stage(row);      // every thread has read the stage
-            const float mean = v[0] / n;
-            v[0] = v[1] = 0.f;
+            const float mean = v[0] * over_n;
+            const pair minus = pair_of(-mean, -mean);
 #pragma unroll
-            for (int e = 0; e < C::E; ++e) {
-                x[e] = norm_col<C>(first, t, e) < a.cols ? x[e] - mean : 0.f;
-                v[0] += x[e];
-                v[1] = __fmaf_rn(x[e], x[e], v[1]);
+            for (int i = 0; i < C::P; ++i) x[i] = add2(x[i], minus);
+            if (!full) norm_trim<C>(a.cols, first, t, x);
+            p = x[0];
+            pair q = mul2(x[0], x[0]);
+#pragma unroll
+            for (int i = 1; i < C::P; ++i) {
+                p = add2(p, x[i]);
+                q = fma2(x[i], x[i], q);
             }
-            sum(v, warp, lane, a.ctas);
+            float d[2] = {both(p), both(q)};
+            sum2(d, warp, lane, a.ctas);
             // what the sum left of an offset far beyond the spread; below that it is the roundings
             // of the differences themselves, which need not average out
-            float left = v[0] / n;
-            if (left * left <= 1.5e-14f * (v[1] / n)) left = 0.f;
-            float var = (v[1] - v[0] * left) / n;
+            float left = d[0] * over_n;
+            if (left * left <= 1.5e-14f * (d[1] * over_n)) left = 0.f;
+            float var = (d[1] - d[0] * left) * over_n;
             if (var < 0.f) var = 0.f;            // a NaN stays
-            const float rstd = 1.f / sqrtf(var + a.eps);
+            const float rstd = __frsqrt_rn(var + a.eps);
             if (!have) continue;
+            if (left != 0.f) {
+                const pair l = pair_of(-left, -left);
 #pragma unroll
-            for (int e = 0; e < C::E; ++e) x[e] = __fmaf_rn((x[e] - left) * rstd, w[e], b[e]);
+                for (int i = 0; i < C::P; ++i) x[i] = add2(x[i], l);
+            }
+            const pair r = pair_of(rstd, rstd);
+#pragma unroll
+            for (int i = 0; i < C::P; ++i) x[i] = fma2(mul2(x[i], r), w[i], b[i]);
             norm_store<C>(static_cast<T*>(a.y) + (row + j) * a.ldy, a.cols, first, t, x);
             if (t == 0 && rank == 0) {
                 if (a.mean) a.mean[row + j] = left == left ? mean + left : mean;   // an infinity stays
@@ -122,13 +143,13 @@ k_norm_forward(const __grid_constant__ ForwardArgs a) {
 template <class C>
 cudaError_t launch_as(const NormProblem& p, cudaStream_t st) {
     static std::atomic<uint64_t> prepared{0};
-    const int ctas = norm_ctas<C>(p.cols), per_sm = 1024 / C::THREADS;
+    const int ctas = norm_ctas<C>(p.cols), per_sm = kForwardCtas<C>;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = norm_prepare(k_norm_forward<C>, prepared, dev);
     if (e != cudaSuccess) return e;
     const RingShape ring = ring_shape<C>(1, p.cols, per_sm);
-    const int64_t each = ring.block * (C::GW == 1 ? 8 : 1);
+    const int64_t each = ring.block * C::SIDE;
     const int64_t want = (p.rows + each - 1) / each, room = int64_t(norm_sms(dev)) * per_sm / ctas;
     const ForwardArgs a{p.x, p.ldx, p.weight, p.bias, p.y, p.ldy, p.mean, p.rstd, p.rows, int32_t(p.cols), ctas, ring.stages, ring.block,
                         p.eps, detail::kWaitNs};

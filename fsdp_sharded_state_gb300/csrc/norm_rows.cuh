@@ -9,7 +9,9 @@
 //
 // Rows come through shared memory (RowRing): loads of a row by the threads that wait for it
 // leave HBM idle from its last byte to the next row's request (16384 x 4096 bf16 forward 121 us, 0.33 of the
-// copy rate; so 43); bulk copies of the next rows run while one is worked on, whatever the registers hold.
+// copy rate); bulk copies of the next rows run while one is worked on, whatever the registers hold
+// (79 us).  What then bounds a wide row is the issue of its instructions, so elements are worked on in
+// pairs (add, mul and fma of two fp32 at once, each rounded as its single form).
 #pragma once
 
 #include <type_traits>
@@ -28,8 +30,9 @@ struct NormCfg {
     static constexpr int L = L_, GW = GW_, V = V_, E = 8 * V_;
     static constexpr int W = 16 / sizeof(T);                       // columns of a chunk
     static constexpr bool VEC = VEC_, CLUSTER = CLUSTER_;
-    static constexpr int THREADS = GW == 1 ? 256 : 32 * GW;
-    static constexpr int ROWS = GW == 1 ? 8 * (32 / L) : 1;        // side by side in a CTA
+    static constexpr int P = E / 2;                                // pairs of a thread
+    static constexpr int THREADS = GW <= 8 ? 256 : 32 * GW;
+    static constexpr int SIDE = THREADS / (32 * GW);               // groups side by side in a CTA
     static constexpr int G = GW == 1 ? L : 32 * GW;                // threads of a row in one CTA
     static constexpr int COLS = G * E;                             // columns that they hold
     static_assert(GW == 1 || L == 32, "whole warps");
@@ -44,19 +47,62 @@ __device__ __forceinline__ float norm_get(const float* p) { return *p; }
 __device__ __forceinline__ void norm_put(uint16_t* p, float v) { *p = to_bf16(v); }
 __device__ __forceinline__ void norm_put(float* p, float v) { *p = v; }
 
-__device__ __forceinline__ void norm_get16(const uint16_t* p, float* v) {
+// ---- two fp32 in a register pair -------------------------------------------------------
+using pair = uint64_t;
+__device__ __forceinline__ pair pair_of(float a, float b) {
+    pair r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 split(pair p) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
+    return r;
+}
+__device__ __forceinline__ pair add2(pair a, pair b) {
+    pair r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ pair mul2(pair a, pair b) {
+    pair r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ pair fma2(pair a, pair b, pair c) {
+    pair r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ float both(pair p) {
+    const float2 f = split(p);
+    return f.x + f.y;
+}
+
+// A chunk of 16 bytes as pairs.
+__device__ __forceinline__ void norm_get16(const uint16_t* p, pair* v) {
     const uint4 q = ldu4(p);
-    v[0] = bf16lo(q.x); v[1] = bf16hi(q.x); v[2] = bf16lo(q.y); v[3] = bf16hi(q.y);
-    v[4] = bf16lo(q.z); v[5] = bf16hi(q.z); v[6] = bf16lo(q.w); v[7] = bf16hi(q.w);
+    v[0] = pair_of(bf16lo(q.x), bf16hi(q.x));
+    v[1] = pair_of(bf16lo(q.y), bf16hi(q.y));
+    v[2] = pair_of(bf16lo(q.z), bf16hi(q.z));
+    v[3] = pair_of(bf16lo(q.w), bf16hi(q.w));
 }
-__device__ __forceinline__ void norm_get16(const float* p, float* v) {
+__device__ __forceinline__ void norm_get16(const float* p, pair* v) {
     const float4 a = ld4(p);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[0] = pair_of(a.x, a.y);
+    v[1] = pair_of(a.z, a.w);
 }
-__device__ __forceinline__ void norm_put16(uint16_t* p, const float* v) {
-    stu4(p, make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])));
+__device__ __forceinline__ uint32_t pack_pair(pair p) {
+    const float2 f = split(p);
+    return pack_bf16x2(f.x, f.y);
 }
-__device__ __forceinline__ void norm_put16(float* p, const float* v) { st4(p, make_float4(v[0], v[1], v[2], v[3])); }
+__device__ __forceinline__ void norm_put16(uint16_t* p, const pair* v) {
+    stu4(p, make_uint4(pack_pair(v[0]), pack_pair(v[1]), pack_pair(v[2]), pack_pair(v[3])));
+}
+__device__ __forceinline__ void norm_put16(float* p, const pair* v) {
+    const float2 a = split(v[0]), b = split(v[1]);
+    st4(p, make_float4(a.x, a.y, b.x, b.y));
+}
 
 // Column of a thread's element e; t: the thread's place among the G of its row, first: the
 // columns before this CTA's.
@@ -65,66 +111,96 @@ __device__ __forceinline__ int norm_col(int first, int t, int e) {
     return first + (C::VEC ? ((e / C::W) * C::G + t) * C::W + e % C::W : e * C::G + t);
 }
 
+// Whether all of a thread's columns are in the row.
+template <class C>
+__device__ __forceinline__ bool norm_full(int cols, int first, int t) {
+    return norm_col<C>(first, t, C::E - 1) < cols;
+}
+
 // A thread's elements of a row whose first column is at `row` (in global or shared memory); 0
 // past its end.
 template <class C, typename T>
-__device__ __forceinline__ void norm_load(const T* row, int cols, int first, int t, float (&v)[C::E]) {
+__device__ __forceinline__ void norm_load(const T* row, int cols, int first, int t, pair (&v)[C::P]) {
+    auto at_or_0 = [&](int e) { return norm_col<C>(first, t, e) < cols ? norm_get(row + norm_col<C>(first, t, e)) : 0.f; };
     if constexpr (C::VEC) {
 #pragma unroll
         for (int c = 0; c < C::E; c += C::W) {
             const int at = norm_col<C>(first, t, c);
             if (at + C::W <= cols) {
-                norm_get16(row + at, v + c);
+                norm_get16(row + at, v + c / 2);
             } else {
 #pragma unroll
-                for (int k = 0; k < C::W; ++k) v[c + k] = at + k < cols ? norm_get(row + at + k) : 0.f;
+                for (int k = c; k < c + C::W; k += 2) v[k / 2] = pair_of(at_or_0(k), at_or_0(k + 1));
             }
         }
     } else {
 #pragma unroll
-        for (int e = 0; e < C::E; ++e) {
-            const int at = norm_col<C>(first, t, e);
-            v[e] = at < cols ? norm_get(row + at) : 0.f;
-        }
+        for (int e = 0; e < C::E; e += 2) v[e / 2] = pair_of(at_or_0(e), at_or_0(e + 1));
     }
 }
 template <class C, typename T>
-__device__ __forceinline__ void norm_store(T* row, int cols, int first, int t, const float (&v)[C::E]) {
+__device__ __forceinline__ void norm_store(T* row, int cols, int first, int t, const pair (&v)[C::P]) {
+    auto put = [&](int e, float x) {
+        if (norm_col<C>(first, t, e) < cols) norm_put(row + norm_col<C>(first, t, e), x);
+    };
     if constexpr (C::VEC) {
 #pragma unroll
         for (int c = 0; c < C::E; c += C::W) {
             const int at = norm_col<C>(first, t, c);
             if (at + C::W <= cols) {
-                norm_put16(row + at, v + c);
+                norm_put16(row + at, v + c / 2);
             } else {
 #pragma unroll
-                for (int k = 0; k < C::W; ++k)
-                    if (at + k < cols) norm_put(row + at + k, v[c + k]);
+                for (int k = c; k < c + C::W; k += 2) {
+                    const float2 f = split(v[k / 2]);
+                    put(k, f.x);
+                    put(k + 1, f.y);
+                }
             }
         }
     } else {
 #pragma unroll
-        for (int e = 0; e < C::E; ++e) {
-            const int at = norm_col<C>(first, t, e);
-            if (at < cols) norm_put(row + at, v[e]);
+        for (int e = 0; e < C::E; e += 2) {
+            const float2 f = split(v[e / 2]);
+            put(e, f.x);
+            put(e + 1, f.y);
         }
+    }
+}
+// The elements past the row's end made 0 again, after a difference.
+template <class C>
+__device__ __forceinline__ void norm_trim(int cols, int first, int t, pair (&v)[C::P]) {
+#pragma unroll
+    for (int e = 0; e < C::E; e += 2) {
+        const float2 f = split(v[e / 2]);
+        v[e / 2] = pair_of(norm_col<C>(first, t, e) < cols ? f.x : 0.f, norm_col<C>(first, t, e + 1) < cols ? f.y : 0.f);
     }
 }
 // A vector of one row's width that may start at any element; `fill` where it is not there.
 template <class C, typename T>
-__device__ __forceinline__ void norm_vector(const T* p, int cols, int first, int t, float fill, float (&v)[C::E]) {
-#pragma unroll
-    for (int e = 0; e < C::E; ++e) {
+__device__ __forceinline__ void norm_vector(const T* p, int cols, int first, int t, float fill, pair (&v)[C::P]) {
+    auto get = [&](int e) {
         const int at = norm_col<C>(first, t, e);
-        v[e] = p && at < cols ? norm_get(p + at) : p ? 0.f : fill;
-    }
+        return p && at < cols ? norm_get(p + at) : p ? 0.f : fill;
+    };
+#pragma unroll
+    for (int e = 0; e < C::E; e += 2) v[e / 2] = pair_of(get(e), get(e + 1));
 }
 
-// Sums over a row, the same bits in each of its threads.  buf: float[2][NV][kNormMaxWarps] of
-// shared memory where a row has more than one warp; the two halves take turns, so that one
-// barrier per sum is enough.
+// The threads of a group that is more than a warp, and no others of the CTA.
+template <class C>
+__device__ __forceinline__ void group_sync(int group) {
+    if constexpr (C::SIDE == 1) __syncthreads();
+    else asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(32 * C::GW) : "memory");
+}
+
+// Sums over a row, the same bits in each of its threads.  Where a row has more than one warp, buf is
+// sum_floats() of shared memory for each group; its two halves take turns, so that one barrier per
+// sum is enough.
 template <class C, int NV>
 struct RowSum {
+    static constexpr int WARPS = C::CLUSTER ? kNormMaxWarps : C::GW < 4 ? 4 : C::GW;
+    static constexpr int FLOATS = 2 * NV * WARPS;
     float* buf;
     int turn = 0;
     __device__ __forceinline__ void operator()(float (&s)[NV], int warp, int lane, int n_ctas) {
@@ -134,12 +210,12 @@ struct RowSum {
 #pragma unroll
             for (int i = 0; i < NV; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], o);
         if constexpr (C::GW > 1) {
-            float* const b = buf + turn * NV * kNormMaxWarps;
+            const int mine = warp % C::GW, group = warp / C::GW;
+            float* const b = buf + group * FLOATS + turn * NV * WARPS;
             if constexpr (C::CLUSTER) {
                 if (lane < n_ctas) {
 #pragma unroll
-                    for (int i = 0; i < NV; ++i)
-                        st_cluster(map_rank(smem_addr(b + i * kNormMaxWarps + int(cluster_rank()) * C::GW + warp), lane), s[i]);
+                    for (int i = 0; i < NV; ++i) st_cluster(map_rank(smem_addr(b + i * WARPS + int(cluster_rank()) * C::GW + mine), lane), s[i]);
                 }
                 __syncwarp();
                 cluster_arrive();
@@ -147,30 +223,31 @@ struct RowSum {
             } else {
                 if (lane == 0) {
 #pragma unroll
-                    for (int i = 0; i < NV; ++i) b[i * kNormMaxWarps + warp] = s[i];
+                    for (int i = 0; i < NV; ++i) b[i * WARPS + mine] = s[i];
                 }
-                __syncthreads();
+                group_sync<C>(group);
             }
             const int n = C::CLUSTER ? C::GW * n_ctas : C::GW;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                float t = 0.f;
-                if constexpr (C::GW < 4) {
-                    t = b[i * kNormMaxWarps] + b[i * kNormMaxWarps + 1];
+                if constexpr (C::GW == 2) {
+                    s[i] = b[i * WARPS] + b[i * WARPS + 1];
                 } else {
+                    float t = 0.f;
+#pragma unroll 4
                     for (int w = 0; w < n; w += 4) {
-                        const float4 q = ld4(b + i * kNormMaxWarps + w);
+                        const float4 q = ld4(b + i * WARPS + w);
                         t += (q.x + q.y) + (q.z + q.w);
                     }
+                    s[i] = t;
                 }
-                s[i] = t;
             }
             turn ^= 1;
         }
     }
 };
 
-// A ring of stages in shared memory that bulk copies fill, a CTA's for its share of a row or (GW = 1)
+// A ring of stages in shared memory that bulk copies fill, a group's for its share of a row or (GW = 1)
 // a warp's for `block` rows; per matrix the 16-byte granules that hold them, as one piece where the rows are
 // back to back, else a piece a row.  Rows may start at any element: the bytes around a piece,
 // which are in its own granules, are read and not used.
@@ -178,7 +255,7 @@ struct RowSum {
 // Waits are bounded: after one that gave up, which is recorded for fsdp_check_status, the others
 // give up at once, and the threads go through their rows with what the stages hold.
 constexpr int kRingStages = 8;
-constexpr int kRingFront = 1024;                 // the stages' barriers: kRingStages of each of 8 warps
+constexpr int kRingFront = 1024;                 // the stages' barriers: kRingStages of each of 8 groups
 
 // Bytes of a row's piece, and of a stage's share of one matrix.
 __host__ __device__ inline int ring_piece(int cols, int esize) { return (cols * esize + 15) / 16 * 16 + 16; }
@@ -188,7 +265,7 @@ struct RowRing {
     using T = typename C::T;
     const T* base[N];                            // of this CTA's columns; NULL: not there
     int64_t ld[N];
-    unsigned char* smem;                         // this warp's or CTA's stages
+    unsigned char* smem;                         // this group's stages
     uint32_t bars;
     int stages, piece, block, cols;              // cols: of this CTA
     uint64_t wait_ns;
@@ -206,7 +283,7 @@ struct RowRing {
         if (issue && size) bulk_g2s(dst, reinterpret_cast<const void*>(a & ~uintptr_t(15)), size, bars + 8 * s);
     }
     // The copies of the rows from `row` on (at most `block`, up to `rows`) into stage s.  By one
-    // thread of the CTA, or by a whole warp.
+    // thread of a group, or by a whole warp.
     __device__ __forceinline__ void fetch(int64_t row, int64_t rows, int s, int lane) const {
         const int n = rows - row < block ? int(rows - row) : block;
         const uint32_t at = smem_addr(smem) + uint32_t(s * N * block * piece);
@@ -266,7 +343,7 @@ struct RowRing {
     }
 };
 
-// The ring of a thread: its warp's or its CTA's.
+// The ring of a thread's group.
 template <class C, int N>
 __device__ __forceinline__ RowRing<C, N> make_ring(unsigned char* smem, int warp, int first, int all, int stages, int block, uint64_t wait_ns) {
     RowRing<C, N> r;
@@ -276,7 +353,7 @@ __device__ __forceinline__ RowRing<C, N> make_ring(unsigned char* smem, int warp
     r.stages = stages;
     r.block = block;
     r.wait_ns = wait_ns;
-    const int mine = C::GW == 1 ? warp : 0;
+    const int mine = warp / C::GW;
     r.bars = smem_addr(smem) + uint32_t(mine * kRingStages * 8);
     r.smem = smem + kRingFront + mine * stages * N * block * r.piece;
     return r;
@@ -290,13 +367,13 @@ struct RingShape {
 };
 template <class C>
 RingShape ring_shape(int n, int64_t cols, int per_sm) {
-    constexpr int es = int(sizeof(typename C::T)), rings = C::GW == 1 ? 8 : 1, side = C::GW == 1 ? 32 / C::L : 1;
+    constexpr int es = int(sizeof(typename C::T)), side = C::GW == 1 ? 32 / C::L : 1;
     const int piece = ring_piece(int(cols < C::COLS ? cols : C::COLS), es);
     RingShape r;
     r.block = side;
     if (C::GW == 1)
         while (r.block * piece < 1024) r.block += side;
-    const int stage = n * r.block * piece * rings, fit = (208 * 1024 / per_sm - kRingFront - 4096) / stage;
+    const int stage = n * r.block * piece * C::SIDE, fit = (208 * 1024 / per_sm - kRingFront - 4096) / stage;
     r.stages = fit > kRingStages ? kRingStages : fit < 2 ? 2 : fit;
     r.bytes = size_t(kRingFront) + size_t(r.stages) * stage;
     return r;
