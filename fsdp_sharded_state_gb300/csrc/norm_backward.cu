@@ -84,22 +84,35 @@ k_norm_backward(const __grid_constant__ BackwardArgs a) {
             phase ^= 1;
         }
     };
+    // mean and rstd are read a block ahead: of its row lane by lane l, where a block is a warp's
+    float next_mean = 0.f, next_rstd = 0.f;
+    auto read_ahead = [&](int64_t row) {
+        if (C::GW == 1 ? lane < a.block && row + lane < a.rows : row < a.rows) {
+            next_mean = a.mean[row + (C::GW == 1 ? lane : 0)];
+            next_rstd = a.rstd[row + (C::GW == 1 ? lane : 0)];
+        }
+    };
+    read_ahead(row0);
     // the threads of a group, or of a cluster, leave the loops together
     for (int64_t row = row0; row < a.rows; row += step) {
+        const float row_mean = next_mean, row_rstd = next_rstd;
+        read_ahead(row + step);
         const int count = a.rows - row < a.block ? int(a.rows - row) : a.block;
         if (C::GW == 1) ring.wait(s, phase);
         for (int j0 = 0; j0 < count; j0 += C::GW == 1 ? 32 / C::L : 1) {
             const int j = j0 + (C::GW == 1 ? lane / C::L : 0);
             const bool have = j < count;
             pair h[C::P], g[C::P], add[C::P];
-            float v[2] = {0.f, 0.f}, rstd = 0.f;
+            float v[2] = {0.f, 0.f}, mean = row_mean, rstd = row_rstd;
+            if constexpr (C::GW == 1) {
+                mean = __shfl_sync(0xffffffffu, row_mean, j & 31);
+                rstd = __shfl_sync(0xffffffffu, row_rstd, j & 31);
+            }
             if (have) {
-                const float mean = a.mean[row + j];
-                rstd = a.rstd[row + j];
                 if (C::GW > 1) ring.wait(s, phase);
-                norm_load<C>(ring.row_of(row + j, j, s, 0) - first, a.cols, first, t, h);
-                norm_load<C>(ring.row_of(row + j, j, s, 1) - first, a.cols, first, t, g);
-                if (res) norm_load<C>(ring.row_of(row + j, j, s, 2) - first, a.cols, first, t, add);
+                norm_load<C>(ring.row_of(row + j, j, s, 0), a.cols, first, t, full, h);
+                norm_load<C>(ring.row_of(row + j, j, s, 1), a.cols, first, t, full, g);
+                if (res) norm_load<C>(ring.row_of(row + j, j, s, 2), a.cols, first, t, full, add);
                 const pair m = pair_of(-mean, -mean), r = pair_of(rstd, rstd);
 #pragma unroll
                 for (int i = 0; i < C::P; ++i) h[i] = mul2(add2(h[i], m), r);
@@ -128,7 +141,7 @@ k_norm_backward(const __grid_constant__ BackwardArgs a) {
 #pragma unroll
                 for (int i = 0; i < C::P; ++i) g[i] = mul2(fma2(h[i], m1, add2(g[i], m0)), r);
             }
-            norm_store<C>(static_cast<T*>(a.dx) + (row + j) * a.lddx, a.cols, first, t, g);
+            norm_store<C>(static_cast<T*>(a.dx) + (row + j) * a.lddx, a.cols, first, t, full, g);
         }
         if (C::GW == 1) {
             __syncwarp();                        // every lane has read the stage
@@ -184,7 +197,7 @@ k_norm_backward(const __grid_constant__ BackwardArgs a) {
 // out[c] (+)= the sum over p of part[p][c], for dw and (blockIdx.y = 1) db.  A block takes 32
 // columns; its kJoinWarps warps every kJoinWarps-th row each, and then warp 0 adds the warps'
 // sums up in order.
-constexpr int kJoinWarps = 16;
+constexpr int kJoinWarps = 32;
 
 template <typename T>
 __global__ void __launch_bounds__(32 * kJoinWarps)
@@ -196,7 +209,7 @@ k_norm_join(const float* part, int parts, int64_t pitch, int cols, T* dw, T* db,
     const float* const src = part + (blockIdx.y ? parts * pitch : 0);
     float v = 0.f;
     if (out && c < cols) {
-#pragma unroll 8
+#pragma unroll 10
         for (int p = warp; p < parts; p += kJoinWarps) v += src[p * pitch + c];
     }
     sums[warp][lane] = v;

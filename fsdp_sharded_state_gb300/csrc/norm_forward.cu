@@ -2,9 +2,10 @@
 //
 // Bound by HBM: x read and y written once.  A row stays in registers; its mean is summed first
 // and the squares of what is left after it, so that a common offset of the row costs no digits.
-// What rounding did to that mean is taken out again: with d = x - mean, the sum of d is 0 but for
-// it, and where d's own mean exceeds 2^-23 of d's root mean square, as in rows far from zero, the
-// variance and y are formed from d less its mean.
+// What rounding did to the mean of an fp32 row is taken out again: with d = x - mean, the sum of d is 0 but
+// for it, and where d's own mean exceeds 2^-23 of d's root mean square, as in rows far from
+// zero, the variance and y are formed from d less its mean.  Elements of bf16 rows are 2^-8 of
+// the offset apart or equal: the mean's 2^-24 of it is nothing beside that, or beside y's rounding.
 #include "norm_rows.cuh"
 
 namespace fsdp {
@@ -35,7 +36,7 @@ __global__ void __launch_bounds__(C::THREADS, kForwardCtas<C>)
 k_norm_forward(const __grid_constant__ ForwardArgs a) {
     using T = typename C::T;
     using Sum = RowSum<C, 1>;
-    using Sums = RowSum<C, 2>;
+    using Sums = RowSum<C, 2>;                   // fp32
     extern __shared__ __align__(128) unsigned char smem_raw[];   // the rings
     __shared__ __align__(16) float sums[C::GW > 1 ? (Sum::FLOATS + Sums::FLOATS) * C::SIDE : 4];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -66,7 +67,7 @@ k_norm_forward(const __grid_constant__ ForwardArgs a) {
     Sum sum{sums};
     Sums sum2{sums + (C::GW > 1 ? Sum::FLOATS * C::SIDE : 0)};
     const bool full = norm_full<C>(a.cols, first, t);
-    const float over_n = 1.f / float(a.cols);
+    const float n = float(a.cols), over_n = 1.f / n;
     int s = 0;
     uint32_t phase = 0;
     auto next_stage = [&](int64_t row) {
@@ -85,7 +86,7 @@ k_norm_forward(const __grid_constant__ ForwardArgs a) {
             const bool have = j < count;
             pair x[C::P];
             if (have) {
-                norm_load<C>(ring.row_of(row + j, j, s, 0) - first, a.cols, first, t, x);
+                norm_load<C>(ring.row_of(row + j, j, s, 0), a.cols, first, t, full, x);
             } else {
 #pragma unroll
                 for (int i = 0; i < C::P; ++i) x[i] = 0;
@@ -96,29 +97,35 @@ k_norm_forward(const __grid_constant__ ForwardArgs a) {
             float v[1] = {both(p)};
             sum(v, warp, lane, a.ctas);
             if (C::GW > 1) next_stage(row);      // every thread has read the stage
-            const float mean = v[0] * over_n;
+            const float mean = v[0] / n;         // exact in rows of one value
             const pair minus = pair_of(-mean, -mean);
 #pragma unroll
             for (int i = 0; i < C::P; ++i) x[i] = add2(x[i], minus);
             if (!full) norm_trim<C>(a.cols, first, t, x);
-            p = x[0];
             pair q = mul2(x[0], x[0]);
 #pragma unroll
-            for (int i = 1; i < C::P; ++i) {
-                p = add2(p, x[i]);
-                q = fma2(x[i], x[i], q);
+            for (int i = 1; i < C::P; ++i) q = fma2(x[i], x[i], q);
+            float var, left = 0.f;
+            if constexpr (sizeof(T) == 2) {
+                v[0] = both(q);
+                sum(v, warp, lane, a.ctas);
+                var = v[0] * over_n;
+            } else {
+                p = x[0];
+#pragma unroll
+                for (int i = 1; i < C::P; ++i) p = add2(p, x[i]);
+                float d[2] = {both(p), both(q)};
+                sum2(d, warp, lane, a.ctas);
+                // what the sum left of an offset far beyond the spread; below that it is the roundings
+                // of the differences themselves, which need not average out
+                left = d[0] * over_n;
+                if (left * left <= 1.5e-14f * (d[1] * over_n)) left = 0.f;
+                var = (d[1] - d[0] * left) * over_n;
+                if (var < 0.f) var = 0.f;        // a NaN stays
             }
-            float d[2] = {both(p), both(q)};
-            sum2(d, warp, lane, a.ctas);
-            // what the sum left of an offset far beyond the spread; below that it is the roundings
-            // of the differences themselves, which need not average out
-            float left = d[0] * over_n;
-            if (left * left <= 1.5e-14f * (d[1] * over_n)) left = 0.f;
-            float var = (d[1] - d[0] * left) * over_n;
-            if (var < 0.f) var = 0.f;            // a NaN stays
             const float rstd = __frsqrt_rn(var + a.eps);
             if (!have) continue;
-            if (left != 0.f) {
+            if (sizeof(T) == 4 && left != 0.f) {
                 const pair l = pair_of(-left, -left);
 #pragma unroll
                 for (int i = 0; i < C::P; ++i) x[i] = add2(x[i], l);
@@ -126,7 +133,7 @@ k_norm_forward(const __grid_constant__ ForwardArgs a) {
             const pair r = pair_of(rstd, rstd);
 #pragma unroll
             for (int i = 0; i < C::P; ++i) x[i] = fma2(mul2(x[i], r), w[i], b[i]);
-            norm_store<C>(static_cast<T*>(a.y) + (row + j) * a.ldy, a.cols, first, t, x);
+            norm_store<C>(static_cast<T*>(a.y) + (row + j) * a.ldy, a.cols, first, t, full, x);
             if (t == 0 && rank == 0) {
                 if (a.mean) a.mean[row + j] = left == left ? mean + left : mean;   // an infinity stays
                 if (a.rstd) a.rstd[row + j] = rstd;

@@ -92,6 +92,28 @@ __device__ __forceinline__ void norm_get16(const float* p, pair* v) {
     v[0] = pair_of(a.x, a.y);
     v[1] = pair_of(a.z, a.w);
 }
+// The same from shared memory, by address.
+__device__ __forceinline__ void smem_get16(uint32_t p, pair* v, const uint16_t*) {
+    uint4 q;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w) : "r"(p) : "memory");
+    v[0] = pair_of(bf16lo(q.x), bf16hi(q.x));
+    v[1] = pair_of(bf16lo(q.y), bf16hi(q.y));
+    v[2] = pair_of(bf16lo(q.z), bf16hi(q.z));
+    v[3] = pair_of(bf16lo(q.w), bf16hi(q.w));
+}
+__device__ __forceinline__ void smem_get16(uint32_t p, pair* v, const float*) {
+    asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(v[0]), "=l"(v[1]) : "r"(p) : "memory");
+}
+__device__ __forceinline__ float smem_get(uint32_t p, const uint16_t*) {
+    uint16_t h;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(p) : "memory");
+    return bf16f(h);
+}
+__device__ __forceinline__ float smem_get(uint32_t p, const float*) {
+    float f;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f) : "r"(p) : "memory");
+    return f;
+}
 __device__ __forceinline__ uint32_t pack_pair(pair p) {
     const float2 f = split(p);
     return pack_bf16x2(f.x, f.y);
@@ -117,54 +139,58 @@ __device__ __forceinline__ bool norm_full(int cols, int first, int t) {
     return norm_col<C>(first, t, C::E - 1) < cols;
 }
 
-// A thread's elements of a row whose first column is at `row` (in global or shared memory); 0
-// past its end.
-template <class C, typename T>
-__device__ __forceinline__ void norm_load(const T* row, int cols, int first, int t, pair (&v)[C::P]) {
-    auto at_or_0 = [&](int e) { return norm_col<C>(first, t, e) < cols ? norm_get(row + norm_col<C>(first, t, e)) : 0.f; };
+// A thread's elements of a row whose column `first` is at `row` in shared memory; 0 past its end,
+// where the thread is not full.
+template <class C>
+__device__ __forceinline__ void norm_load(uint32_t row, int cols, int first, int t, bool full, pair (&v)[C::P]) {
+    using T = typename C::T;
+    constexpr int S = int(sizeof(T));
+    auto at_or_0 = [&](int e) {
+        return norm_col<C>(first, t, e) < cols ? smem_get(row + uint32_t(norm_col<C>(0, t, e) * S), static_cast<const T*>(nullptr)) : 0.f;
+    };
     if constexpr (C::VEC) {
+        if (full) {
 #pragma unroll
-        for (int c = 0; c < C::E; c += C::W) {
-            const int at = norm_col<C>(first, t, c);
-            if (at + C::W <= cols) {
-                norm_get16(row + at, v + c / 2);
-            } else {
-#pragma unroll
-                for (int k = c; k < c + C::W; k += 2) v[k / 2] = pair_of(at_or_0(k), at_or_0(k + 1));
-            }
+            for (int c = 0; c < C::E; c += C::W) smem_get16(row + uint32_t(norm_col<C>(0, t, c) * S), v + c / 2, static_cast<const T*>(nullptr));
+            return;
         }
     } else {
+        if (full) {
 #pragma unroll
-        for (int e = 0; e < C::E; e += 2) v[e / 2] = pair_of(at_or_0(e), at_or_0(e + 1));
+            for (int e = 0; e < C::E; e += 2)
+                v[e / 2] = pair_of(smem_get(row + uint32_t(norm_col<C>(0, t, e) * S), static_cast<const T*>(nullptr)),
+                                   smem_get(row + uint32_t(norm_col<C>(0, t, e + 1) * S), static_cast<const T*>(nullptr)));
+            return;
+        }
     }
+#pragma unroll
+    for (int e = 0; e < C::E; e += 2) v[e / 2] = pair_of(at_or_0(e), at_or_0(e + 1));
 }
+// And into a row of a matrix in global memory.
 template <class C, typename T>
-__device__ __forceinline__ void norm_store(T* row, int cols, int first, int t, const pair (&v)[C::P]) {
+__device__ __forceinline__ void norm_store(T* row, int cols, int first, int t, bool full, const pair (&v)[C::P]) {
+    if (full) {
+        T* const p = row + norm_col<C>(first, t, 0);
+#pragma unroll
+        for (int e = 0; e < C::E; e += C::VEC ? C::W : 2) {
+            if constexpr (C::VEC) {
+                norm_put16(p + (norm_col<C>(0, 0, e)), v + e / 2);
+            } else {
+                const float2 f = split(v[e / 2]);
+                norm_put(p + norm_col<C>(0, 0, e), f.x);
+                norm_put(p + norm_col<C>(0, 0, e + 1), f.y);
+            }
+        }
+        return;
+    }
     auto put = [&](int e, float x) {
         if (norm_col<C>(first, t, e) < cols) norm_put(row + norm_col<C>(first, t, e), x);
     };
-    if constexpr (C::VEC) {
 #pragma unroll
-        for (int c = 0; c < C::E; c += C::W) {
-            const int at = norm_col<C>(first, t, c);
-            if (at + C::W <= cols) {
-                norm_put16(row + at, v + c / 2);
-            } else {
-#pragma unroll
-                for (int k = c; k < c + C::W; k += 2) {
-                    const float2 f = split(v[k / 2]);
-                    put(k, f.x);
-                    put(k + 1, f.y);
-                }
-            }
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < C::E; e += 2) {
-            const float2 f = split(v[e / 2]);
-            put(e, f.x);
-            put(e + 1, f.y);
-        }
+    for (int e = 0; e < C::E; e += 2) {
+        const float2 f = split(v[e / 2]);
+        put(e, f.x);
+        put(e + 1, f.y);
     }
 }
 // The elements past the row's end made 0 again, after a difference.
@@ -183,6 +209,13 @@ __device__ __forceinline__ void norm_vector(const T* p, int cols, int first, int
         const int at = norm_col<C>(first, t, e);
         return p && at < cols ? norm_get(p + at) : p ? 0.f : fill;
     };
+    if constexpr (C::VEC) {
+        if (p && (reinterpret_cast<uintptr_t>(p) & 15) == 0 && norm_full<C>(cols, first, t)) {
+#pragma unroll
+            for (int c = 0; c < C::E; c += C::W) norm_get16(p + norm_col<C>(first, t, c), v + c / 2);
+            return;
+        }
+    }
 #pragma unroll
     for (int e = 0; e < C::E; e += 2) v[e / 2] = pair_of(get(e), get(e + 1));
 }
@@ -263,7 +296,7 @@ __host__ __device__ inline int ring_piece(int cols, int esize) { return (cols * 
 template <class C, int N>
 struct RowRing {
     using T = typename C::T;
-    const T* base[N];                            // of this CTA's columns; NULL: not there
+    const T* base[N];                            // of this CTA's columns; the last may be NULL: not there
     int64_t ld[N];
     unsigned char* smem;                         // this group's stages
     uint32_t bars;
@@ -287,7 +320,15 @@ struct RowRing {
     __device__ __forceinline__ void fetch(int64_t row, int64_t rows, int s, int lane) const {
         const int n = rows - row < block ? int(rows - row) : block;
         const uint32_t at = smem_addr(smem) + uint32_t(s * N * block * piece);
-        if constexpr (C::GW > 1) {
+        if constexpr (C::GW > 1 && C::VEC) {
+            const uint32_t size = (uint32_t(cols) * uint32_t(sizeof(T)) + 15) & ~15u;
+            const int have = N == 1 || base[N - 1] ? N : N - 1;
+            mbar_arrive_tx(bars + 8 * s, uint32_t(have) * size);
+            if (size == 0) return;               // a cluster's CTA past the row's end
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+                if (k < have) bulk_g2s(at + uint32_t(k * piece), base[k] + row * ld[k], size, bars + 8 * s);
+        } else if constexpr (C::GW > 1) {
             uint32_t bytes = 0;
 #pragma unroll
             for (int k = 0; k < N; ++k)
@@ -297,37 +338,46 @@ struct RowRing {
             for (int k = 0; k < N; ++k)
                 if (base[k]) copy(row, 1, at + uint32_t(k * piece), k, s, bytes, true);
         } else {
-            // lane 0 copies the matrices whose rows are back to back, lane j row j of the others
+            bool all = true;
 #pragma unroll
-            for (int pass = 0; pass < 2; ++pass) {
-                uint32_t bytes = 0;
+            for (int k = 0; k < N; ++k) all = all && (!base[k] || whole(k));
+            if (all) {
+                if (lane == 0) {
+                    uint32_t bytes = 0;
 #pragma unroll
-                for (int k = 0; k < N; ++k) {
-                    if (!base[k]) continue;
-                    const uint32_t dst = at + uint32_t(k * block * piece);
-                    if (whole(k)) {
-                        if (lane == 0) copy(row, n, dst, k, s, bytes, pass);
-                    } else {
-                        for (int j = lane; j < n; j += 32) copy(row + j, 1, dst + uint32_t(j * piece), k, s, bytes, pass);
-                    }
+                    for (int k = 0; k < N; ++k)
+                        if (base[k]) copy(row, n, 0, k, s, bytes, false);
+                    mbar_arrive_tx(bars + 8 * s, bytes);
+#pragma unroll
+                    for (int k = 0; k < N; ++k)
+                        if (base[k]) copy(row, n, at + uint32_t(k * block * piece), k, s, bytes, true);
                 }
-                if (pass == 0) {
-#pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) bytes += __shfl_xor_sync(0xffffffffu, bytes, o);
-                    if (lane == 0) mbar_arrive_tx(bars + 8 * s, bytes);
-                    __syncwarp();
-                }
+                return;
             }
+            // lane j copies row j of every matrix
+            const int j = lane;
+            uint32_t bytes = 0;
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+                if (base[k] && (whole(k) ? j == 0 : j < n)) copy(row + j, whole(k) ? n : 1, 0, k, s, bytes, false);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) bytes += __shfl_xor_sync(0xffffffffu, bytes, o);
+            if (lane == 0) mbar_arrive_tx(bars + 8 * s, bytes);
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+                if (base[k] && (whole(k) ? j == 0 : j < n)) copy(row + j, whole(k) ? n : 1, at + uint32_t((k * block + j) * piece), k, s, bytes, true);
         }
     }
-    // What stage s holds of row `row` of matrix k, the j-th of the stage, from this CTA's first column on.
-    __device__ __forceinline__ const T* row_of(int64_t row, int j, int s, int k) const {
-        const unsigned char* const p = smem + (s * N + k) * block * piece;
+    // Where stage s holds row `row` of matrix k, the j-th of the stage: the address of this CTA's
+    // first column in shared memory.
+    __device__ __forceinline__ uint32_t row_of(int64_t row, int j, int s, int k) const {
+        const uint32_t p = smem_addr(smem) + uint32_t((s * N + k) * block * piece);
         if constexpr (C::GW == 1) {
             if (whole(k))
-                return reinterpret_cast<const T*>(p + (C::VEC ? 0 : reinterpret_cast<uintptr_t>(base[k] + (row - j) * ld[k]) & 15)) + j * cols;
+                return p + (C::VEC ? 0u : uint32_t(reinterpret_cast<uintptr_t>(base[k] + (row - j) * ld[k]) & 15)) + uint32_t(j * cols) * sizeof(T);
         }
-        return reinterpret_cast<const T*>(p + j * piece + (C::VEC ? 0 : reinterpret_cast<uintptr_t>(base[k] + row * ld[k]) & 15));
+        return p + uint32_t(j * piece) + (C::VEC ? 0u : uint32_t(reinterpret_cast<uintptr_t>(base[k] + row * ld[k]) & 15));
     }
     __device__ __forceinline__ void wait(int s, uint32_t phase) {
         if (!mbar_wait_bounded(bars + 8 * s, phase, wait_ns)) {
@@ -360,7 +410,8 @@ __device__ __forceinline__ RowRing<C, N> make_ring(unsigned char* smem, int warp
 }
 
 // Host side: how many rows a stage holds, how many stages, and the shared memory of a CTA of which
-// per_sm share an SM.  A warp's stage holds about 1 KB of each matrix.
+// per_sm share an SM.  A warp's stage holds about 2 KB of each matrix,
+// at most 32 rows.
 struct RingShape {
     int block, stages;
     size_t bytes;
@@ -372,7 +423,7 @@ RingShape ring_shape(int n, int64_t cols, int per_sm) {
     RingShape r;
     r.block = side;
     if (C::GW == 1)
-        while (r.block * piece < 1024) r.block += side;
+        while (r.block * piece < 1800 && r.block + side <= 32) r.block += side;
     const int stage = n * r.block * piece * C::SIDE, fit = (208 * 1024 / per_sm - kRingFront - 4096) / stage;
     r.stages = fit > kRingStages ? kRingStages : fit < 2 ? 2 : fit;
     r.bytes = size_t(kRingFront) + size_t(r.stages) * stage;
@@ -398,9 +449,9 @@ int norm_sms(int dev) {
 template <typename T, bool VEC, class F>
 cudaError_t norm_dispatch(int64_t cols, F&& f) {
     if (cols <= 32) return f(NormCfg<T, 4, 1, 1, VEC>{});
-    if (cols <= 64) return f(NormCfg<T, 8, 1, 1, VEC>{});
-    if (cols <= 128) return f(NormCfg<T, 16, 1, 1, VEC>{});
-    if (cols <= 256) return f(NormCfg<T, 32, 1, 1, VEC>{});
+    if (cols <= 64) return f(NormCfg<T, 4, 1, 2, VEC>{});
+    if (cols <= 128) return f(NormCfg<T, 8, 1, 2, VEC>{});
+    if (cols <= 256) return f(NormCfg<T, 16, 1, 2, VEC>{});
     if (cols <= 512) return f(NormCfg<T, 32, 1, 2, VEC>{});
     if (cols <= 1024) return f(NormCfg<T, 32, 2, 2, VEC>{});
     if (cols <= 2048) return f(NormCfg<T, 32, 4, 2, VEC>{});
