@@ -33,27 +33,28 @@ struct BackwardArgs {
 // Columns of a row of partial sums.
 __host__ __device__ inline int64_t partial_pitch(int64_t cols) { return (cols + 7) / 8 * 8; }
 
+// CTAs of an SM: threads of up to 128 registers (168 in CTAs of 384).
 template <class C>
-__global__ void __launch_bounds__(C::THREADS, 512 / C::THREADS)
+constexpr int kBackwardCtas = 512 / C::THREADS;
+
+template <class C>
+__global__ void __launch_bounds__(C::THREADS, kBackwardCtas<C>)
 k_norm_backward(const __grid_constant__ BackwardArgs a) {
     using T = typename C::T;
     using Sums = RowSum<C, 2>;
-    extern __shared__ __align__(128) unsigned char smem_raw[];   // the rings; at the end a row of sums per group
+    extern __shared__ __align__(128) unsigned char smem_raw[];   // the ring; at the end a row of sums per group
     __shared__ __align__(16) float sums[C::GW > 1 ? Sums::FLOATS * C::SIDE : 4];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int t = C::GW == 1 ? lane % C::L : tid % C::G;
+    const int t = C::GW == 1 ? lane % C::L : tid % C::G, group = warp / C::GW;
     const int rank = C::CLUSTER ? int(cluster_rank()) : 0, first = rank * C::COLS;
     const int part = blockIdx.x / a.ctas, parts = gridDim.x / a.ctas;
     const bool res = a.residual != nullptr;
-    RowRing<C, 3> ring = make_ring<C, 3>(smem_raw, warp, first, a.cols, a.stages, a.block, a.wait_ns);
-    ring.base[0] = static_cast<const T*>(a.x) + first;
-    ring.base[1] = static_cast<const T*>(a.dy) + first;
-    ring.base[2] = res ? static_cast<const T*>(a.residual) + first : nullptr;
-    ring.ld[0] = a.ldx;
-    ring.ld[1] = a.lddy;
-    ring.ld[2] = a.ldr;
-    const bool issuer = C::GW == 1 || t == 0;
-    if (C::GW == 1 ? lane == 0 : t == 0) ring.init();
+    const uint32_t rows = uint32_t(a.rows), row0 = part * uint32_t(C::SIDE * a.block);
+    RowRing<C, 3> ring(smem_raw, first, a.cols, a.stages, a.block, rows, parts * uint32_t(C::SIDE * a.block), a.wait_ns);
+    ring.matrix(0, a.x, a.ldx, first, row0);
+    ring.matrix(1, a.dy, a.lddy, first, row0);
+    ring.matrix(2, a.residual, a.ldr, first, row0);
+    if (tid == 0) ring.init();
     if constexpr (C::CLUSTER) {                  // no CTA writes to another that has not started
         cluster_arrive();
         cluster_wait();
@@ -61,58 +62,48 @@ k_norm_backward(const __grid_constant__ BackwardArgs a) {
         __syncthreads();
     }
     pdl_wait();
-    // blocks of rows go to the groups in turn
-    const int64_t step = int64_t(parts) * C::SIDE * a.block;
-    const int64_t row0 = (int64_t(part) * C::SIDE + warp / C::GW) * a.block;
-    if (issuer) {
-        for (int s = 0; s < a.stages; ++s)
-            if (row0 + s * step < a.rows) ring.fetch(row0 + s * step, a.rows, s, lane);
-    }
+    if (C::SIDE == 1 ? tid == 0 : warp == 0) ring.begin(row0, lane);
     pair w[C::P], dw[C::P], db[C::P];
     norm_vector<C>(static_cast<const T*>(a.weight), a.cols, first, t, 1.f, w);
 #pragma unroll
     for (int i = 0; i < C::P; ++i) dw[i] = db[i] = 0;
     Sums sum{sums};
-    const bool full = norm_full<C>(a.cols, first, t);
+    const bool full = __all_sync(0xffffffffu, norm_full<C>(a.cols, first, t));
     const float over_n = 1.f / float(a.cols);
-    int s = 0;
-    uint32_t phase = 0;
-    auto next_stage = [&](int64_t row) {
-        if (issuer && row + a.stages * step < a.rows) ring.fetch(row + a.stages * step, a.rows, s, lane);
-        if (++s == a.stages) {
-            s = 0;
-            phase ^= 1;
-        }
-    };
-    // mean and rstd are read a block ahead: of its row lane by lane l, where a block is a warp's
+    // of the group's first row of the stage: its place in it and in dx
+    const int block = C::GW == 1 ? a.block : 1;
+    const int j1 = group * block + (C::GW == 1 ? lane / C::L : 0);
+    uint32_t mine = row0 + j1;
+    T* py = static_cast<T*>(a.dx) + mine * a.lddx;
+    const int64_t y_step = ring.step * a.lddx, y_side = (32 / C::L) * a.lddx;
+    // mean and rstd are read a stage ahead: of the group's l-th row by lane l where that is a warp
     float next_mean = 0.f, next_rstd = 0.f;
-    auto read_ahead = [&](int64_t row) {
-        if (C::GW == 1 ? lane < a.block && row + lane < a.rows : row < a.rows) {
-            next_mean = a.mean[row + (C::GW == 1 ? lane : 0)];
-            next_rstd = a.rstd[row + (C::GW == 1 ? lane : 0)];
+    auto read_ahead = [&](uint32_t row) {
+        row += group * block + (C::GW == 1 ? lane : 0);
+        if ((C::GW > 1 || lane < block) && row < rows) {
+            next_mean = a.mean[row];
+            next_rstd = a.rstd[row];
         }
     };
     read_ahead(row0);
-    // the threads of a group, or of a cluster, leave the loops together
-    for (int64_t row = row0; row < a.rows; row += step) {
+    // the threads of a CTA, or of a cluster, leave the loop together
+    for (uint32_t row = row0; row < rows; row += ring.step, mine += ring.step, py += y_step) {
         const float row_mean = next_mean, row_rstd = next_rstd;
-        read_ahead(row + step);
-        const int count = a.rows - row < a.block ? int(a.rows - row) : a.block;
-        if (C::GW == 1) ring.wait(s, phase);
-        for (int j0 = 0; j0 < count; j0 += C::GW == 1 ? 32 / C::L : 1) {
-            const int j = j0 + (C::GW == 1 ? lane / C::L : 0);
-            const bool have = j < count;
+        read_ahead(row + ring.step);
+        ring.wait();
+        T* y = py;
+        for (int j0 = 0; j0 < block; j0 += C::GW == 1 ? 32 / C::L : 1, y += y_side) {
+            const bool have = mine + j0 < rows;
             pair h[C::P], g[C::P], add[C::P];
             float v[2] = {0.f, 0.f}, mean = row_mean, rstd = row_rstd;
             if constexpr (C::GW == 1) {
-                mean = __shfl_sync(0xffffffffu, row_mean, j & 31);
-                rstd = __shfl_sync(0xffffffffu, row_rstd, j & 31);
+                mean = __shfl_sync(0xffffffffu, row_mean, j0 + lane / C::L);
+                rstd = __shfl_sync(0xffffffffu, row_rstd, j0 + lane / C::L);
             }
             if (have) {
-                if (C::GW > 1) ring.wait(s, phase);
-                norm_load<C>(ring.row_of(row + j, j, s, 0), a.cols, first, t, full, h);
-                norm_load<C>(ring.row_of(row + j, j, s, 1), a.cols, first, t, full, g);
-                if (res) norm_load<C>(ring.row_of(row + j, j, s, 2), a.cols, first, t, full, add);
+                norm_load<C>(ring.row_of(j1 + j0, 0), a.cols, first, t, full, h);
+                norm_load<C>(ring.row_of(j1 + j0, 1), a.cols, first, t, full, g);
+                if (res) norm_load<C>(ring.row_of(j1 + j0, 2), a.cols, first, t, full, add);
                 const pair m = pair_of(-mean, -mean), r = pair_of(rstd, rstd);
 #pragma unroll
                 for (int i = 0; i < C::P; ++i) h[i] = mul2(add2(h[i], m), r);
@@ -130,7 +121,10 @@ k_norm_backward(const __grid_constant__ BackwardArgs a) {
                 v[1] = both(q);
             }
             sum(v, warp, lane, a.ctas);
-            if (C::GW > 1) next_stage(row);      // every thread has read the stage
+            if (C::GW > 1) {                     // every thread of the group has read its row
+                if (C::SIDE == 1 ? tid == 0 : warp % C::GW == 0) ring.release(row, lane);
+                ring.next();
+            }
             if (!have) continue;
             const float c0 = -v[0] * over_n, c1 = -v[1] * over_n;
             const pair m0 = pair_of(c0, c0), m1 = pair_of(c1, c1), r = pair_of(rstd, rstd);
@@ -141,11 +135,12 @@ k_norm_backward(const __grid_constant__ BackwardArgs a) {
 #pragma unroll
                 for (int i = 0; i < C::P; ++i) g[i] = mul2(fma2(h[i], m1, add2(g[i], m0)), r);
             }
-            norm_store<C>(static_cast<T*>(a.dx) + (row + j) * a.lddx, a.cols, first, t, full, g);
+            norm_store<C>(y, a.cols, first, t, full, g);
         }
         if (C::GW == 1) {
-            __syncwarp();                        // every lane has read the stage
-            next_stage(row);
+            __syncwarp();                        // every lane has read the warp's rows
+            ring.release(row, lane);
+            ring.next();
         }
     }
     ring.leave();
@@ -182,13 +177,23 @@ k_norm_backward(const __grid_constant__ BackwardArgs a) {
             }
         }
     } else {
+        if (C::VEC && full) {                    // whole sectors: element by element they took 10 us of 16384 x 4096
 #pragma unroll
-        for (int e = 0; e < C::E; ++e) {
-            const int c = norm_col<C>(first, t, e);
-            if (c < a.cols) {
-                const float2 f = split(dw[e / 2]), g = split(db[e / 2]);
-                out_w[c] = e & 1 ? f.y : f.x;
-                out_b[c] = e & 1 ? g.y : g.x;
+            for (int e = 0; e < C::E; e += 4) {
+                const int c = norm_col<C>(first, t, e);
+                const float2 f = split(dw[e / 2]), g = split(dw[e / 2 + 1]), u = split(db[e / 2]), v = split(db[e / 2 + 1]);
+                st4(out_w + c, make_float4(f.x, f.y, g.x, g.y));
+                st4(out_b + c, make_float4(u.x, u.y, v.x, v.y));
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < C::E; ++e) {
+                const int c = norm_col<C>(first, t, e);
+                if (c < a.cols) {
+                    const float2 f = split(dw[e / 2]), g = split(db[e / 2]);
+                    out_w[c] = e & 1 ? f.y : f.x;
+                    out_b[c] = e & 1 ? g.y : g.x;
+                }
             }
         }
     }
@@ -227,8 +232,8 @@ k_norm_join(const float* part, int parts, int64_t pitch, int cols, T* dw, T* db,
 // fit the 152 SMs at once, fewer where there are few rows.
 template <class C>
 int64_t backward_groups(int64_t rows, int64_t cols) {
-    const int64_t each = ring_shape<C>(3, cols, 512 / C::THREADS).block * C::SIDE;
-    const int64_t want = (rows + each - 1) / each, room = 152 * (512 / C::THREADS) / norm_ctas<C>(cols);
+    const int64_t each = ring_shape<C>(3, cols, kBackwardCtas<C>).block * C::SIDE;
+    const int64_t want = (rows + each - 1) / each, room = 152 * kBackwardCtas<C> / norm_ctas<C>(cols);
     return want < room ? want : room;
 }
 
@@ -242,7 +247,7 @@ cudaError_t launch_as(const NormProblem& p, cudaStream_t st) {
         static std::atomic<uint64_t> prepared{0};
         int dev = 0;
         if ((e = cudaGetDevice(&dev)) != cudaSuccess || (e = norm_prepare(k_norm_backward<C>, prepared, dev)) != cudaSuccess) return e;
-        const RingShape ring = ring_shape<C>(3, p.cols, 512 / C::THREADS);
+        const RingShape ring = ring_shape<C>(3, p.cols, kBackwardCtas<C>);
         const size_t last = C::SIDE > 1 ? size_t(C::SIDE) * C::COLS * 4 : 0;
         const BackwardArgs a{p.x, p.ldx, p.dy, p.lddy, p.weight, p.residual, p.ldr, p.mean, p.rstd, p.y, p.ldy,
                              sums ? p.partial : nullptr, pitch, p.rows, int32_t(p.cols), ctas, ring.stages, ring.block, detail::kWaitNs};
@@ -266,8 +271,8 @@ int64_t norm_partial_floats(int64_t rows, int64_t cols) {
         if (g > groups) groups = g;
         return cudaSuccess;
     };
-    norm_dispatch<float, true>(cols, most);
-    norm_dispatch<uint16_t, true>(cols, most);
+    norm_dispatch_backward<float, true>(cols, most);
+    norm_dispatch_backward<uint16_t, true>(cols, most);
     return 2 * groups * partial_pitch(cols);
 }
 
@@ -275,8 +280,8 @@ cudaError_t take_wait_error_norm_backward(unsigned int* flag) { return take_norm
 
 cudaError_t launch_norm_backward(const NormProblem& p, cudaStream_t st) {
     auto go = [&](auto c) { return launch_as<decltype(c)>(p, st); };
-    if (p.bf16) return p.vec ? norm_dispatch<uint16_t, true>(p.cols, go) : norm_dispatch<uint16_t, false>(p.cols, go);
-    return p.vec ? norm_dispatch<float, true>(p.cols, go) : norm_dispatch<float, false>(p.cols, go);
+    if (p.bf16) return p.vec ? norm_dispatch_backward<uint16_t, true>(p.cols, go) : norm_dispatch_backward<uint16_t, false>(p.cols, go);
+    return p.vec ? norm_dispatch_backward<float, true>(p.cols, go) : norm_dispatch_backward<float, false>(p.cols, go);
 }
 
 }  // namespace fsdp

@@ -26,10 +26,9 @@ struct ForwardArgs {
     uint64_t wait_ns;
 };
 
-// CTAs of an SM: 768 threads of up to 80 registers, or two CTAs of 512 of 64 (four of 256 threads
-// spill what they hold of weight and bias).
+// CTAs of an SM: threads of up to 80 registers, or 128 where they hold 32 columns.
 template <class C>
-constexpr int kForwardCtas = C::THREADS == 256 ? 3 : 2;
+constexpr int kForwardCtas = C::V == 4 ? 512 / C::THREADS : 768 / C::THREADS;
 
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, kForwardCtas<C>)
@@ -37,16 +36,15 @@ k_norm_forward(const __grid_constant__ ForwardArgs a) {
     using T = typename C::T;
     using Sum = RowSum<C, 1>;
     using Sums = RowSum<C, 2>;                   // fp32
-    extern __shared__ __align__(128) unsigned char smem_raw[];   // the rings
+    extern __shared__ __align__(128) unsigned char smem_raw[];   // the ring
     __shared__ __align__(16) float sums[C::GW > 1 ? (Sum::FLOATS + Sums::FLOATS) * C::SIDE : 4];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int t = C::GW == 1 ? lane % C::L : tid % C::G;
+    const int t = C::GW == 1 ? lane % C::L : tid % C::G, group = warp / C::GW;
     const int rank = C::CLUSTER ? int(cluster_rank()) : 0, first = rank * C::COLS;
-    RowRing<C, 1> ring = make_ring<C, 1>(smem_raw, warp, first, a.cols, a.stages, a.block, a.wait_ns);
-    ring.base[0] = static_cast<const T*>(a.x) + first;
-    ring.ld[0] = a.ldx;
-    const bool issuer = C::GW == 1 || t == 0;
-    if (C::GW == 1 ? lane == 0 : t == 0) ring.init();
+    const uint32_t rows = uint32_t(a.rows), row0 = blockIdx.x / a.ctas * uint32_t(C::SIDE * a.block);
+    RowRing<C, 1> ring(smem_raw, first, a.cols, a.stages, a.block, rows, gridDim.x / a.ctas * uint32_t(C::SIDE * a.block), a.wait_ns);
+    ring.matrix(0, a.x, a.ldx, first, row0);
+    if (tid == 0) ring.init();
     if constexpr (C::CLUSTER) {                  // no CTA writes to another that has not started
         cluster_arrive();
         cluster_wait();
@@ -54,39 +52,29 @@ k_norm_forward(const __grid_constant__ ForwardArgs a) {
         __syncthreads();
     }
     pdl_wait();
-    // blocks of rows go to the groups in turn
-    const int64_t step = int64_t(gridDim.x / a.ctas) * C::SIDE * a.block;
-    const int64_t row0 = (int64_t(blockIdx.x / a.ctas) * C::SIDE + warp / C::GW) * a.block;
-    if (issuer) {
-        for (int s = 0; s < a.stages; ++s)
-            if (row0 + s * step < a.rows) ring.fetch(row0 + s * step, a.rows, s, lane);
-    }
+    if (C::SIDE == 1 ? tid == 0 : warp == 0) ring.begin(row0, lane);
     pair w[C::P], b[C::P];
     norm_vector<C>(static_cast<const T*>(a.weight), a.cols, first, t, 1.f, w);
     norm_vector<C>(static_cast<const T*>(a.bias), a.cols, first, t, 0.f, b);
     Sum sum{sums};
     Sums sum2{sums + (C::GW > 1 ? Sum::FLOATS * C::SIDE : 0)};
-    const bool full = norm_full<C>(a.cols, first, t);
+    const bool full = __all_sync(0xffffffffu, norm_full<C>(a.cols, first, t));
     const float n = float(a.cols), over_n = 1.f / n;
-    int s = 0;
-    uint32_t phase = 0;
-    auto next_stage = [&](int64_t row) {
-        if (issuer && row + a.stages * step < a.rows) ring.fetch(row + a.stages * step, a.rows, s, lane);
-        if (++s == a.stages) {
-            s = 0;
-            phase ^= 1;
-        }
-    };
-    // the threads of a group, or of a cluster, leave the loops together
-    for (int64_t row = row0; row < a.rows; row += step) {
-        ring.wait(s, phase);
-        const int count = a.rows - row < a.block ? int(a.rows - row) : a.block;
-        for (int j0 = 0; j0 < count; j0 += C::GW == 1 ? 32 / C::L : 1) {
-            const int j = j0 + (C::GW == 1 ? lane / C::L : 0);
-            const bool have = j < count;
+    // of the group's first row of the stage: its place in it and in y
+    const int j1 = group * (C::GW == 1 ? a.block : 1) + (C::GW == 1 ? lane / C::L : 0);
+    const int block = C::GW == 1 ? a.block : 1;
+    uint32_t mine = row0 + j1;
+    T* py = static_cast<T*>(a.y) + mine * a.ldy;
+    const int64_t y_step = ring.step * a.ldy, y_side = (32 / C::L) * a.ldy;
+    // the threads of a CTA, or of a cluster, leave the loop together
+    for (uint32_t row = row0; row < rows; row += ring.step, mine += ring.step, py += y_step) {
+        ring.wait();
+        T* y = py;
+        for (int j0 = 0; j0 < block; j0 += C::GW == 1 ? 32 / C::L : 1, y += y_side) {
+            const bool have = mine + j0 < rows;
             pair x[C::P];
             if (have) {
-                norm_load<C>(ring.row_of(row + j, j, s, 0), a.cols, first, t, full, x);
+                norm_load<C>(ring.row_of(j1 + j0, 0), a.cols, first, t, full, x);
             } else {
 #pragma unroll
                 for (int i = 0; i < C::P; ++i) x[i] = 0;
@@ -96,8 +84,13 @@ k_norm_forward(const __grid_constant__ ForwardArgs a) {
             for (int i = 1; i < C::P; ++i) p = add2(p, x[i]);
             float v[1] = {both(p)};
             sum(v, warp, lane, a.ctas);
-            if (C::GW > 1) next_stage(row);      // every thread has read the stage
-            const float mean = v[0] / n;         // exact in rows of one value
+            if (C::GW > 1) {                     // every thread of the group has read its row
+                if (C::SIDE == 1 ? tid == 0 : warp % C::GW == 0) ring.release(row, lane);
+                ring.next();
+            }
+            // the quotient by n, its rounding taken out: exact in rows of one value
+            float mean = v[0] * over_n;
+            if (fabsf(mean) < 1e38f) mean = __fmaf_rn(__fmaf_rn(-mean, n, v[0]), over_n, mean);
             const pair minus = pair_of(-mean, -mean);
 #pragma unroll
             for (int i = 0; i < C::P; ++i) x[i] = add2(x[i], minus);
@@ -123,7 +116,10 @@ k_norm_forward(const __grid_constant__ ForwardArgs a) {
                 var = (d[1] - d[0] * left) * over_n;
                 if (var < 0.f) var = 0.f;        // a NaN stays
             }
-            const float rstd = __frsqrt_rn(var + a.eps);
+            // CUDA's reciprocal square root (2 units in the last place), and a Newton step
+            const float e = var + a.eps;
+            float rstd = rsqrtf(e);
+            if (rstd < 1e18f && rstd > 0.f) rstd = __fmaf_rn(0.5f * rstd, __fmaf_rn(-e * rstd, rstd, 1.f), rstd);
             if (!have) continue;
             if (sizeof(T) == 4 && left != 0.f) {
                 const pair l = pair_of(-left, -left);
@@ -133,15 +129,16 @@ k_norm_forward(const __grid_constant__ ForwardArgs a) {
             const pair r = pair_of(rstd, rstd);
 #pragma unroll
             for (int i = 0; i < C::P; ++i) x[i] = fma2(mul2(x[i], r), w[i], b[i]);
-            norm_store<C>(static_cast<T*>(a.y) + (row + j) * a.ldy, a.cols, first, t, full, x);
+            norm_store<C>(y, a.cols, first, t, full, x);
             if (t == 0 && rank == 0) {
-                if (a.mean) a.mean[row + j] = left == left ? mean + left : mean;   // an infinity stays
-                if (a.rstd) a.rstd[row + j] = rstd;
+                if (a.mean) a.mean[mine + j0] = left == left ? mean + left : mean;   // an infinity stays
+                if (a.rstd) a.rstd[mine + j0] = rstd;
             }
         }
         if (C::GW == 1) {
-            __syncwarp();                        // every lane has read the stage
-            next_stage(row);
+            __syncwarp();                        // every lane has read the warp's rows
+            ring.release(row, lane);
+            ring.next();
         }
     }
     ring.leave();
@@ -167,8 +164,8 @@ cudaError_t launch_as(const NormProblem& p, cudaStream_t st) {
 
 cudaError_t launch_norm_forward(const NormProblem& p, cudaStream_t st) {
     auto go = [&](auto c) { return launch_as<decltype(c)>(p, st); };
-    if (p.bf16) return p.vec ? norm_dispatch<uint16_t, true>(p.cols, go) : norm_dispatch<uint16_t, false>(p.cols, go);
-    return p.vec ? norm_dispatch<float, true>(p.cols, go) : norm_dispatch<float, false>(p.cols, go);
+    if (p.bf16) return p.vec ? norm_dispatch_forward<uint16_t, true>(p.cols, go) : norm_dispatch_forward<uint16_t, false>(p.cols, go);
+    return p.vec ? norm_dispatch_forward<float, true>(p.cols, go) : norm_dispatch_forward<float, false>(p.cols, go);
 }
 
 cudaError_t take_wait_error_norm_forward(unsigned int* flag) { return take_norm_wait_error(flag); }

@@ -3,7 +3,7 @@
 //
 // A row belongs to a group of threads that hold it in registers from its load to its store:
 // L lanes of a warp (up to 512 columns; a warp then works on 32 / L rows at once), GW warps of a CTA
-// (up to 8192), or GW warps in each CTA of a cluster (up to 65536).  A thread holds 8 V columns:
+// (up to 8192, in forward 16384), or GW warps in each CTA of a cluster (up to 65536).  A thread holds 8 V columns:
 // chunks of 16 bytes where rows are aligned to 16 bytes (VEC), else single columns that are a
 // group's width apart, so that a warp's accesses are contiguous either way.
 //
@@ -39,8 +39,7 @@ struct NormCfg {
     static_assert(GW <= 2 || GW % 4 == 0, "sums of warps, four at a time");
 };
 
-constexpr int kNormMaxCluster = 8;
-constexpr int kNormMaxWarps = 16 * kNormMaxCluster;                // of a row
+constexpr int kNormMaxWarps = 16 * 8;                              // of a row, in a cluster of 8
 
 __device__ __forceinline__ float norm_get(const uint16_t* p) { return bf16f(*p); }
 __device__ __forceinline__ float norm_get(const float* p) { return *p; }
@@ -280,17 +279,19 @@ struct RowSum {
     }
 };
 
-// A ring of stages in shared memory that bulk copies fill, a group's for its share of a row or (GW = 1)
-// a warp's for `block` rows; per matrix the 16-byte granules that hold them, as one piece where the rows are
-// back to back, else a piece a row.  Rows may start at any element: the bytes around a piece,
-// which are in its own granules, are read and not used.
+// A CTA's ring of stages in shared memory that bulk copies fill with the next rows: `block` rows for
+// each of its groups, or its share of one row; per matrix the 16-byte granules that hold them, as one
+// piece where the rows are back to back, else a piece a row.  Rows may start at any element: the
+// bytes around a piece, which are in its own granules, are read and not used.  Stages are large, since
+// a copy takes some 65 ns of the copy engine beside 22 ns a KB: with 2 KB for each warp apart, 65536 x 256
+// backward without sums took 36 us.  The group that is last to have read a stage fills it again.
 //
 // Waits are bounded: after one that gave up, which is recorded for fsdp_check_status, the others
 // give up at once, and the threads go through their rows with what the stages hold.
 constexpr int kRingStages = 8;
-constexpr int kRingFront = 1024;                 // the stages' barriers: kRingStages of each of 8 groups
+constexpr int kRingFront = 128;                  // the stages' barriers and counts
 
-// Bytes of a row's piece, and of a stage's share of one matrix.
+// Bytes of a row's piece.
 __host__ __device__ inline int ring_piece(int cols, int esize) { return (cols * esize + 15) / 16 * 16 + 16; }
 
 template <class C, int N>
@@ -298,91 +299,142 @@ struct RowRing {
     using T = typename C::T;
     const T* base[N];                            // of this CTA's columns; the last may be NULL: not there
     int64_t ld[N];
-    unsigned char* smem;                         // this group's stages
-    uint32_t bars;
-    int stages, piece, block, cols;              // cols: of this CTA
+    uint32_t front, at;                          // the ring in shared memory, and its present stage
+    uint32_t rows, step;                         // of all, and between a CTA's stages
+    int stages, most, piece, cols;               // most: rows of a stage; cols: of this CTA
+    uint32_t between[N];                         // bytes from a row of a stage to the next
+    uint32_t low[N], low_step[N], low_row[N];    // rows of any alignment: the first's address mod 16, and what to add for the next stage's and row's
+    bool back[N];                                // rows back to back
     uint64_t wait_ns;
+    int s = 0;
+    uint32_t phase = 0;
 
+    __device__ __forceinline__ RowRing(unsigned char* smem, int first, int all, int stages_, int block, uint32_t rows_, uint32_t step_, uint64_t wait)
+        : front(smem_addr(smem)), at(smem_addr(smem) + kRingFront), rows(rows_), step(step_), stages(stages_), most(C::SIDE * block), wait_ns(wait) {
+        const int left = all - first;
+        cols = left < 0 ? 0 : left < C::COLS ? left : C::COLS;
+        piece = ring_piece(all < C::COLS ? all : C::COLS, int(sizeof(T)));
+    }
+    __device__ __forceinline__ void matrix(int k, const void* p, int64_t ld_, int first, uint32_t row0) {
+        base[k] = p ? static_cast<const T*>(p) + first : nullptr;
+        ld[k] = ld_;
+        back[k] = C::SIDE > 1 && ld_ == cols;
+        between[k] = back[k] ? uint32_t(cols) * uint32_t(sizeof(T)) : uint32_t(piece);
+        if constexpr (!C::VEC) {
+            low_row[k] = uint32_t(ld_) * uint32_t(sizeof(T));
+            low_step[k] = step * low_row[k];
+            low[k] = uint32_t(reinterpret_cast<uintptr_t>(base[k])) + row0 * low_row[k];
+        }
+    }
+    __device__ __forceinline__ uint32_t bar(int i) const { return front + 8 * i; }
+    __device__ __forceinline__ uint32_t count(int i) const { return front + 8 * kRingStages + 4 * i; }
     // By one thread, before any other uses the ring.
     __device__ __forceinline__ void init() const {
-        for (int s = 0; s < stages; ++s) mbar_init(bars + 8 * s, 1);
+        for (int i = 0; i < stages; ++i) {
+            mbar_init(bar(i), 1);
+            asm volatile("st.shared.u32 [%0], 0;" ::"r"(count(i)) : "memory");
+        }
         mbar_fence_init();
     }
-    __device__ __forceinline__ bool whole(int k) const { return C::GW == 1 && ld[k] == cols; }
-    __device__ __forceinline__ void copy(int64_t row, int64_t n, uint32_t dst, int k, int s, uint32_t& bytes, bool issue) const {
+    // n rows from `row` on of matrix k to `dst`; counts the bytes, copies where told to.
+    __device__ __forceinline__ void copy(uint32_t row, int n, uint32_t dst, int k, int i, uint32_t& bytes, bool issue) const {
         const uintptr_t a = reinterpret_cast<uintptr_t>(base[k] + row * ld[k]);
-        const uint32_t size = cols > 0 ? uint32_t((a & 15) + n * cols * int64_t(sizeof(T)) + 15) & ~15u : 0;   // a cluster's CTA past the row's end
+        const uint32_t size = cols > 0 ? uint32_t((a & 15) + int64_t(n) * cols * int64_t(sizeof(T)) + 15) & ~15u : 0;   // a cluster's CTA past the row's end
         bytes += size;
-        if (issue && size) bulk_g2s(dst, reinterpret_cast<const void*>(a & ~uintptr_t(15)), size, bars + 8 * s);
+        if (issue && size) bulk_g2s(dst, reinterpret_cast<const void*>(a & ~uintptr_t(15)), size, bar(i));
     }
-    // The copies of the rows from `row` on (at most `block`, up to `rows`) into stage s.  By one
-    // thread of a group, or by a whole warp.
-    __device__ __forceinline__ void fetch(int64_t row, int64_t rows, int s, int lane) const {
-        const int n = rows - row < block ? int(rows - row) : block;
-        const uint32_t at = smem_addr(smem) + uint32_t(s * N * block * piece);
-        if constexpr (C::GW > 1 && C::VEC) {
+    // The rows from `row` on into stage i: by one thread (SIDE = 1) or one warp.
+    __device__ __forceinline__ void fetch(uint32_t row, int i, int lane) const {
+        const int n = rows - row < uint32_t(most) ? int(rows - row) : most;
+        const uint32_t to = front + kRingFront + uint32_t(i * N * most * piece);
+        if constexpr (C::SIDE == 1 && C::VEC) {  // the thread that does this is one of those that wait for each other
             const uint32_t size = (uint32_t(cols) * uint32_t(sizeof(T)) + 15) & ~15u;
             const int have = N == 1 || base[N - 1] ? N : N - 1;
-            mbar_arrive_tx(bars + 8 * s, uint32_t(have) * size);
-            if (size == 0) return;               // a cluster's CTA past the row's end
+            mbar_arrive_tx(bar(i), uint32_t(have) * size);
 #pragma unroll
-            for (int k = 0; k < N; ++k)
-                if (k < have) bulk_g2s(at + uint32_t(k * piece), base[k] + row * ld[k], size, bars + 8 * s);
-        } else if constexpr (C::GW > 1) {
+            for (int k = 0; k < N; ++k)          // size 0: a cluster's CTA past the row's end
+                if (k < have && size) bulk_g2s(to + uint32_t(k * piece), base[k] + row * ld[k], size, bar(i));
+            return;
+        }
+        bool all = true;
+#pragma unroll
+        for (int k = 0; k < N; ++k) all = all && (C::SIDE == 1 || !base[k] || back[k]);
+        if (all) {
+            if (C::SIDE > 1 && lane != 0) return;
             uint32_t bytes = 0;
 #pragma unroll
             for (int k = 0; k < N; ++k)
-                if (base[k]) copy(row, 1, 0, k, s, bytes, false);
-            mbar_arrive_tx(bars + 8 * s, bytes);
+                if (base[k]) copy(row, n, 0, k, i, bytes, false);
+            mbar_arrive_tx(bar(i), bytes);
 #pragma unroll
             for (int k = 0; k < N; ++k)
-                if (base[k]) copy(row, 1, at + uint32_t(k * piece), k, s, bytes, true);
-        } else {
-            bool all = true;
+                if (base[k]) copy(row, n, to + uint32_t(k * most * piece), k, i, bytes, true);
+            return;
+        }
+        // the lanes share out the rows of the matrices whose rows are apart
+        uint32_t bytes = 0;
 #pragma unroll
-            for (int k = 0; k < N; ++k) all = all && (!base[k] || whole(k));
-            if (all) {
-                if (lane == 0) {
-                    uint32_t bytes = 0;
+        for (int k = 0; k < N; ++k) {
+            if (!base[k]) continue;
+            const bool w = back[k];
+            for (int j = lane; j < (w ? 1 : n); j += 32) copy(row + j, w ? n : 1, 0, k, i, bytes, false);
+        }
 #pragma unroll
-                    for (int k = 0; k < N; ++k)
-                        if (base[k]) copy(row, n, 0, k, s, bytes, false);
-                    mbar_arrive_tx(bars + 8 * s, bytes);
+        for (int o = 16; o > 0; o >>= 1) bytes += __shfl_xor_sync(0xffffffffu, bytes, o);
+        if (lane == 0) mbar_arrive_tx(bar(i), bytes);
+        __syncwarp();
 #pragma unroll
-                    for (int k = 0; k < N; ++k)
-                        if (base[k]) copy(row, n, at + uint32_t(k * block * piece), k, s, bytes, true);
-                }
-                return;
-            }
-            // lane j copies row j of every matrix
-            const int j = lane;
-            uint32_t bytes = 0;
-#pragma unroll
-            for (int k = 0; k < N; ++k)
-                if (base[k] && (whole(k) ? j == 0 : j < n)) copy(row + j, whole(k) ? n : 1, 0, k, s, bytes, false);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) bytes += __shfl_xor_sync(0xffffffffu, bytes, o);
-            if (lane == 0) mbar_arrive_tx(bars + 8 * s, bytes);
-            __syncwarp();
-#pragma unroll
-            for (int k = 0; k < N; ++k)
-                if (base[k] && (whole(k) ? j == 0 : j < n)) copy(row + j, whole(k) ? n : 1, at + uint32_t((k * block + j) * piece), k, s, bytes, true);
+        for (int k = 0; k < N; ++k) {
+            if (!base[k]) continue;
+            const bool w = back[k];
+            for (int j = lane; j < (w ? 1 : n); j += 32) copy(row + j, w ? n : 1, to + uint32_t((k * most + j) * piece), k, i, bytes, true);
         }
     }
-    // Where stage s holds row `row` of matrix k, the j-th of the stage: the address of this CTA's
-    // first column in shared memory.
-    __device__ __forceinline__ uint32_t row_of(int64_t row, int j, int s, int k) const {
-        const uint32_t p = smem_addr(smem) + uint32_t((s * N + k) * block * piece);
-        if constexpr (C::GW == 1) {
-            if (whole(k))
-                return p + (C::VEC ? 0u : uint32_t(reinterpret_cast<uintptr_t>(base[k] + (row - j) * ld[k]) & 15)) + uint32_t(j * cols) * sizeof(T);
-        }
-        return p + uint32_t(j * piece) + (C::VEC ? 0u : uint32_t(reinterpret_cast<uintptr_t>(base[k] + row * ld[k]) & 15));
+    // The first stages; by the threads that fetch takes.
+    __device__ __forceinline__ void begin(uint32_t row, int lane) const {
+        for (int i = 0; i < stages; ++i)
+            if (row + i * step < rows) fetch(row + i * step, i, lane);
     }
-    __device__ __forceinline__ void wait(int s, uint32_t phase) {
-        if (!mbar_wait_bounded(bars + 8 * s, phase, wait_ns)) {
+    // Where the stage holds its j-th row of matrix k: the shared-memory address of this CTA's first column.
+    __device__ __forceinline__ uint32_t row_of(int j, int k) const {
+        uint32_t p = at + uint32_t(k * most * piece);
+        if constexpr (C::SIDE > 1) p += uint32_t(j) * between[k];
+        if constexpr (!C::VEC) p += (back[k] ? low[k] : low[k] + uint32_t(j) * low_row[k]) & 15u;
+        return p;
+    }
+    __device__ __forceinline__ void wait() {
+        if (!mbar_wait_bounded(bar(s), phase, wait_ns)) {
             wait_ns = 0;
             atomicOr(&g_wait_error, 1u);
+        }
+    }
+    // The stage that began with `row` has been read by all threads of a group, of which one warp
+    // (SIDE = 1: one thread) says so.
+    __device__ __forceinline__ void release(uint32_t row, int lane) const {
+        row += stages * step;
+        if constexpr (C::SIDE == 1) {
+            if (row < rows) fetch(row, s, lane);
+        } else {
+            uint32_t last = 0;
+            if (lane == 0) {
+                __threadfence_block();
+                // the last group's count goes back to 0, seen by all once the stage is full again
+                asm volatile("atom.shared.inc.u32 %0, [%1], %2;" : "=r"(last) : "r"(count(s)), "r"(uint32_t(C::SIDE - 1)) : "memory");
+            }
+            last = __shfl_sync(0xffffffffu, last, 0);
+            if (last == C::SIDE - 1 && row < rows) fetch(row, s, lane);
+        }
+    }
+    __device__ __forceinline__ void next() {
+        at += uint32_t(N * most * piece);
+        if (++s == stages) {
+            s = 0;
+            at = front + kRingFront;
+            phase ^= 1;
+        }
+        if constexpr (!C::VEC) {
+#pragma unroll
+            for (int k = 0; k < N; ++k) low[k] += low_step[k];
         }
     }
     // Before the CTA leaves: copies that were given up land within this.
@@ -393,25 +445,8 @@ struct RowRing {
     }
 };
 
-// The ring of a thread's group.
-template <class C, int N>
-__device__ __forceinline__ RowRing<C, N> make_ring(unsigned char* smem, int warp, int first, int all, int stages, int block, uint64_t wait_ns) {
-    RowRing<C, N> r;
-    const int left = all - first;
-    r.cols = left < 0 ? 0 : left < C::COLS ? left : C::COLS;
-    r.piece = ring_piece(all < C::COLS ? all : C::COLS, int(sizeof(typename C::T)));
-    r.stages = stages;
-    r.block = block;
-    r.wait_ns = wait_ns;
-    const int mine = warp / C::GW;
-    r.bars = smem_addr(smem) + uint32_t(mine * kRingStages * 8);
-    r.smem = smem + kRingFront + mine * stages * N * block * r.piece;
-    return r;
-}
-
-// Host side: how many rows a stage holds, how many stages, and the shared memory of a CTA of which
-// per_sm share an SM.  A warp's stage holds about 2 KB of each matrix,
-// at most 32 rows.
+// Host side: how many rows of a group a stage holds, how many stages, and the shared memory of a
+// CTA of which per_sm share an SM.  About 8 KB of each matrix a stage, at most 32 rows a warp.
 struct RingShape {
     int block, stages;
     size_t bytes;
@@ -423,8 +458,8 @@ RingShape ring_shape(int n, int64_t cols, int per_sm) {
     RingShape r;
     r.block = side;
     if (C::GW == 1)
-        while (r.block * piece < 1800 && r.block + side <= 32) r.block += side;
-    const int stage = n * r.block * piece * C::SIDE, fit = (208 * 1024 / per_sm - kRingFront - 4096) / stage;
+        while (C::SIDE * r.block * piece < 8192 && r.block + side <= 32) r.block += side;
+    const int stage = n * C::SIDE * r.block * piece, fit = (208 * 1024 / per_sm - kRingFront - 4096) / stage;
     r.stages = fit > kRingStages ? kRingStages : fit < 2 ? 2 : fit;
     r.bytes = size_t(kRingFront) + size_t(r.stages) * stage;
     return r;
@@ -445,9 +480,10 @@ int norm_sms(int dev) {
     return v > 0 ? v : 152;
 }
 
-// The configuration of a width: f(cfg) for the narrowest that holds it.
+// The configuration of a width: f(cfg) for the narrowest that holds it.  Backward holds six values an
+// element where forward holds three: half as many columns a thread above 6144.
 template <typename T, bool VEC, class F>
-cudaError_t norm_dispatch(int64_t cols, F&& f) {
+cudaError_t norm_dispatch_narrow(int64_t cols, F&& f) {
     if (cols <= 32) return f(NormCfg<T, 4, 1, 1, VEC>{});
     if (cols <= 64) return f(NormCfg<T, 4, 1, 2, VEC>{});
     if (cols <= 128) return f(NormCfg<T, 8, 1, 2, VEC>{});
@@ -456,6 +492,19 @@ cudaError_t norm_dispatch(int64_t cols, F&& f) {
     if (cols <= 1024) return f(NormCfg<T, 32, 2, 2, VEC>{});
     if (cols <= 2048) return f(NormCfg<T, 32, 4, 2, VEC>{});
     if (cols <= 4096) return f(NormCfg<T, 32, 8, 2, VEC>{});
+    return f(NormCfg<T, 32, 12, 2, VEC>{});
+}
+constexpr int64_t kNormNarrow = 6144;
+template <typename T, bool VEC, class F>
+cudaError_t norm_dispatch_forward(int64_t cols, F&& f) {
+    if (cols <= kNormNarrow) return norm_dispatch_narrow<T, VEC>(cols, f);
+    if (cols <= 8192) return f(NormCfg<T, 32, 8, 4, VEC>{});
+    if (cols <= 16384) return f(NormCfg<T, 32, 16, 4, VEC>{});
+    return f(NormCfg<T, 32, 16, 2, VEC, true>{});
+}
+template <typename T, bool VEC, class F>
+cudaError_t norm_dispatch_backward(int64_t cols, F&& f) {
+    if (cols <= kNormNarrow) return norm_dispatch_narrow<T, VEC>(cols, f);
     if (cols <= 8192) return f(NormCfg<T, 32, 16, 2, VEC>{});
     return f(NormCfg<T, 32, 16, 2, VEC, true>{});
 }

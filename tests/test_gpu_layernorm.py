@@ -25,7 +25,8 @@ SHAPES = [(1, 1, 0, 0), (5, 7, 0, 0), (300, 32, 0, 0), (129, 33, 0, 0), (70, 64,
           (64, 257, 0, 0), (31, 512, 0, 0), (9, 1000, 0, 0), (333, 1001, 0, 0), (40, 1024, 0, 0), (3, 1025, 0, 0), (1, 2048, 0, 0),
           (700, 2048, 0, 0), (5, 2052, 4, 0), (333, 4096, 0, 0), (17, 4100, 0, 3), (12, 8192, 0, 0), (11, 8191, 2, 0), (7, 8200, 0, 0),
           (160, 16384, 0, 0), (3, 20001, 0, 1), (2, 65536, 0, 0), (4, 40000, 0, 0), (65, 96, 3, 1), (20, 1500, 1, 1),
-          (5000, 256, 0, 0), (4001, 40, 0, 0), (2500, 2048, 8, 0)]
+          (5000, 256, 0, 0), (4001, 40, 0, 0), (2500, 2048, 8, 0),
+          (9000, 3, 0, 0), (6001, 100, 4, 0), (3001, 500, 0, 1), (900, 5000, 0, 0), (450, 6145, 0, 0), (200, 12000, 8, 0), (150, 33000, 0, 0)]
 
 
 def _inputs(rows, cols, pad, offset, dtype, seed, mean=0.7, std=1.5):
