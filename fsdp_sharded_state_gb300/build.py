@@ -20,7 +20,7 @@ SOURCES = ["api.cu", "kernels.cu", "layout.cpp", "noalloc.cu", "rows.cu", "stage
            "clip_coop.cu", "claims.cu", "linear_api.cu", "linear_forward.cu", "linear_forward_pair.cu",
            "linear_dgrad.cu", "linear_dgrad_pair.cu", "linear_wgrad.cu", "linear_pack.cu",
            "linear_skinny.cu", "linear_small.cu", "dropout.cu", "norm_api.cu", "norm_forward.cu", "norm_backward.cu",
-           "ns_api.cu", "ns_prep.cu", "ns_gram.cu", "ns_poly.cu", "ns_mul.cu", "ns_step.cu", "ns_last.cu", "muon.cu"]
+           "ns_api.cu", "ns_prep.cu", "ns_gram.cu", "ns_poly.cu", "ns_mul.cu", "ns_step.cu", "ns_last.cu", "ns_tiny.cu", "muon.cu"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 # IEEE division and square root, no flush-to-zero, no implicit fma contraction:

@@ -69,6 +69,11 @@ cudaError_t launch_ns_squares(const NsMatrices& src, int batch, int64_t rows, in
 cudaError_t launch_ns_pack(const NsMatrices& src, int batch, const NsPlanes& out, const double* partial, int parts, float scale, float eps,
                            cudaStream_t st);
 
+// Small matrices: from the source to the result in one launch, without the workspace.
+bool use_ns_tiny(int64_t m, int64_t n);
+cudaError_t launch_ns_tiny(const NsMatrices& src, const NsMatrices& dst, int batch, int64_t m, int64_t n, float eps, const float* coeffs,
+                           int steps, const float* usual, cudaStream_t st);
+
 // Layout of the workspace of a batch (byte offsets); m and n are the shorter and the longer side,
 // chunk the matrices that pass through it at once.
 struct NsWork {
@@ -84,7 +89,7 @@ struct NsScales {
     double top[kNsMaxSteps + 1], gain[kNsMaxSteps];              // bounds: of X's singular values, of B's eigenvalues
 };
 bool ns_scales(const float* coeffs, int steps, NsScales* s);
-// From source matrices and their partial sums to `dst`; one chunk.
+// From source matrices and their partial sums (which small ones do not need) to `dst`; one chunk.
 cudaError_t ns_run(const NsWork& w, unsigned char* ws, int batch, const NsMatrices& src, const NsMatrices& dst, int parts, float eps,
                    const float* coeffs, int steps, const NsScales& sc, cudaStream_t st);
 

@@ -70,6 +70,12 @@ NsWork ns_work(int64_t rows, int64_t cols, int64_t count) {
     NsWork w;
     w.m = std::min(rows, cols);
     w.n = std::max(rows, cols);
+    if (use_ns_tiny(w.m, w.n)) {
+        w.chunk = int(std::max<int64_t>(1, std::min<int64_t>(count, kNsMaxBatch)));
+        w.x0 = w.x1 = w.square[0] = w.square[1] = w.square[2] = w.square[3] = w.partial = 0;
+        w.end = int64_t(w.chunk) * kNsMaxParts * 8;
+        return w;
+    }
     const int64_t mp = round_up(w.m, 256), np = round_up(w.n, 256);
     // enough matrices at once to fill the device several times over, in 256 MB of planes or one matrix
     w.chunk = int(std::max<int64_t>(1, std::min<int64_t>({count, kNsMaxBatch, (int64_t(1) << 26) / (mp * np)})));
@@ -85,7 +91,7 @@ NsWork ns_work(int64_t rows, int64_t cols, int64_t count) {
 // another can do without: with B_0 from A_0 = X X^T, the next A is B_0 A_0 B_0 and the next B_1 a polynomial of
 // it, and X takes both as (B_1 B_0) X.  That is three products of m x m in place of m x m x n and
 // m x n x m, less work where n > m: 4096 x 11008 takes 30 units of m^3 for five steps in groups
-// of 3 and 2 instead of 45, and its Muon step 9.7 instead of 13.0 ms.
+// of 3 and 2 instead of 45, and its Muon step 9.4 instead of 13.0 ms.
 //
 // What it costs in precision.  An error d in A's small eigenvalues grows by the square of
 // the first coefficient (11.9) with each step that A is carried on, where X, computed anew, has it
@@ -99,11 +105,12 @@ constexpr double kGroupGain = 64.0;
 // diagonal adds up 16 equal shares a K step, 1.2e-7 of products of symmetric ones, whose diagonals hold
 // most of a sum in one term (and 0.6e-7 of Q X, left as it is).  Given back here, since the
 // polynomials' cancelling terms answer it with about ten times as much: eight 256 x 1024 matrices
-// 3.1e-6 -> 1.2e-6 off.
+// 3.1e-6 -> 2.4e-6 off.
 constexpr float kGramBack = 1.f + 0x1p-22f, kSquareBack = 1.f + 0x1p-23f;
 
 cudaError_t ns_run(const NsWork& w, unsigned char* ws, int batch, const NsMatrices& src, const NsMatrices& dst, int parts, float eps,
                    const float* coeffs, int steps, const NsScales& sc, cudaStream_t st) {
+    if (use_ns_tiny(w.m, w.n)) return launch_ns_tiny(src, dst, batch, w.m, w.n, eps, coeffs, steps, kDefault, st);
     const int64_t mp = round_up(w.m, 256), np = round_up(w.n, 256);
     auto planes = [&](int64_t at, int64_t cols, int64_t ld) {
         return NsPlanes{reinterpret_cast<uint16_t*>(ws + at), w.m, cols, ld, mp * ld};
@@ -254,7 +261,8 @@ int fsdp_newton_schulz(int32_t count, int64_t rows, int64_t cols, const void* co
         s.tall = d.tall = rows > cols ? ~uint64_t(0) : 0;
         s.bf16 = src_dtype == FSDP_BF16;
         d.bf16 = dst_dtype == FSDP_BF16;
-        cudaError_t e = launch_ns_squares(s, n, w.m, w.n, reinterpret_cast<double*>(ws + w.partial), parts, st);
+        cudaError_t e = cudaSuccess;
+        if (!use_ns_tiny(w.m, w.n)) e = launch_ns_squares(s, n, w.m, w.n, reinterpret_cast<double*>(ws + w.partial), parts, st);
         if (e != cudaSuccess) return cuda_fail(e, "k_ns_squares launch");
         e = ns_run(w, ws, n, s, d, parts, eps, coeffs, steps, sc, st);
         if (e != cudaSuccess) return cuda_fail(e, "k_ns launch");

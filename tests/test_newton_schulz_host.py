@@ -50,7 +50,8 @@ def test_workspace_bytes():
     n = fs.fsdp_newton_schulz_workspace_bytes
     assert n(0, 8, 8) == 0 and n(1, 0, 8) == 0 and n(1, 1 << 21, 8) == 0
     assert n(1, 100, 300) == n(1, 300, 100) >= 2 * 4 * 100 * 300 + 2 * 4 * 100 * 100
-    assert n(1, 64, 64) < n(2, 64, 64) <= n(64, 64, 64) == n(1000, 64, 64)
+    for side in (64, 300):                                              # in one launch, and with planes
+        assert n(1, side, side) < n(2, side, side) <= n(64, side, side) == n(1000, side, side)
     assert n(8, 4096, 11008) == n(1, 4096, 11008) < 1 << 30             # one at a time
 
 
