@@ -37,14 +37,14 @@ struct MuonReplicas {
     void* p[kMaxRanks];
 };
 
-__device__ __forceinline__ double muon_block_sum(double v) {
-    __shared__ double part[kMuonThreads / 32];
+__device__ __forceinline__ float muon_block_sum(float v) {
+    __shared__ float part[kMuonThreads / 32];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
     __syncthreads();
     if (threadIdx.x == 0) {
-        v = 0.0;
+        v = 0.f;
         for (int k = 0; k < kMuonThreads / 32; ++k) v += part[k];
     }
     return v;
@@ -55,12 +55,13 @@ __device__ __forceinline__ double muon_block_sum(double v) {
 template <typename GT>
 __global__ void __launch_bounds__(kMuonThreads)
 k_muon_momentum(const __grid_constant__ MuonJobs jobs, const __grid_constant__ GradPtrs gp, float* momentum, float beta, float om,
-                int nesterov, double* partial) {
+                int nesterov, float* partial) {
     pdl_wait();
+    pdl_trigger();
     const int mat = blockIdx.y;
     const int64_t lo = jobs.shard[mat], hi = lo + jobs.numel, delta = jobs.full[mat] - lo;
     float* const u = jobs.update + mat * jobs.pitch + (lo & 7) - lo;
-    double total = 0.0;
+    float total = 0.f, lost = 0.f;
     auto one = [&](float g, float& m) {
         const float gg = __fmul_rn(om, mean_div(g, jobs.nf));
         m = __fmaf_rn(beta, m, gg);
@@ -91,7 +92,7 @@ k_muon_momentum(const __grid_constant__ MuonJobs jobs, const __grid_constant__ G
                 s = __fmaf_rn(v, v, s);
             }
         }
-        total += double(s);
+        add_carefully(s, total, lost);
     }
     total = muon_block_sum(total);
     if (threadIdx.x == 0) partial[mat * gridDim.x + blockIdx.x] = total;
@@ -214,7 +215,7 @@ int check_muon(const fsdp_muon_hparams* hp) {
     if (!hp) return FSDP_EINVAL;
     if (!std::isfinite(hp->lr) || hp->lr < 0.f || !std::isfinite(hp->weight_decay) || hp->weight_decay < 0.f) return FSDP_EINVAL;
     if (!(hp->momentum >= 0.f) || !(hp->momentum < 1.f)) return FSDP_EINVAL;
-    if (!(hp->eps > 0.f) || !std::isfinite(hp->eps)) return FSDP_EINVAL;
+    if (!(hp->eps >= kNsLeastEps) || !std::isfinite(hp->eps)) return FSDP_EINVAL;
     if (hp->steps < 1 || hp->steps > kNsMaxSteps) return FSDP_EINVAL;
     if (hp->scale < FSDP_MUON_SCALE_NONE || hp->scale > FSDP_MUON_SCALE_RMS) return FSDP_EINVAL;
     return FSDP_OK;
@@ -292,7 +293,7 @@ int fsdp_zero1_muon_broadcast(const fsdp_layout* L, int32_t n_tensors, const int
                 if (rows > cols) o.tall |= uint64_t(1) << i;
             }
             const int parts = ns_parts(jobs.numel);
-            double* const partial = reinterpret_cast<double*>(ws + w.ns.partial);
+            float* const partial = reinterpret_cast<float*>(ws + w.ns.partial);
             const dim3 grid(static_cast<unsigned>(parts), static_cast<unsigned>(n)), block(kMuonThreads);
             cudaError_t e = grad_dtype == FSDP_BF16
                                 ? launch(k_muon_momentum<uint16_t>, grid, block, 0, st, jobs, gp, momentum, hp->momentum, om, hp->nesterov, partial)

@@ -10,6 +10,8 @@ namespace fsdp {
 
 constexpr int kNsMaxBatch = 64;                 // matrices of a launch
 constexpr int kNsMaxSteps = 64;
+// The least eps: below it, squares that are lost below fp32's range could matter.
+constexpr float kNsLeastEps = 1e-16f;
 
 // A batch of fp32 matrices as two fp16 terms each: matrix i's high terms at p + 2 i plane, its
 // low ones a plane on; rows of ld elements.  Buffers are padded to multiples of 256 rows and
@@ -60,14 +62,29 @@ float cost_ns_gram(const NsProduct& p);
 float cost_ns_mul(const NsProduct& p);
 float cost_ns_step(const NsProduct& p);
 
-// Blocks that sum a matrix's squares (a double each), at most kNsMaxParts.
+// Blocks that sum a matrix's squares (a float each), at most kNsMaxParts.
 constexpr int kNsMaxParts = 608;
 int ns_parts(int64_t numel);
 // partial[i][part] of the batch's source matrices (rows x cols, or transposed).
-cudaError_t launch_ns_squares(const NsMatrices& src, int batch, int64_t rows, int64_t cols, double* partial, int parts, cudaStream_t st);
+cudaError_t launch_ns_squares(const NsMatrices& src, int batch, int64_t rows, int64_t cols, float* partial, int parts, cudaStream_t st);
 // The planes of scale / max(norm, eps) times the source, norm from the partial sums.
-cudaError_t launch_ns_pack(const NsMatrices& src, int batch, const NsPlanes& out, const double* partial, int parts, float scale, float eps,
+cudaError_t launch_ns_pack(const NsMatrices& src, int batch, const NsPlanes& out, const float* partial, int parts, float scale, float eps,
                            cudaStream_t st);
+
+#ifdef __CUDACC__
+// The next kernel of a run may start its set-up beside this one, which is small or about to end; it
+// waits, as every kernel does, for this one's end before it touches memory.  Not before this
+// one's own wait: then it would be there while the one before still runs.
+__device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// total += v, with what the addition rounds off kept in `lost` for the next.
+__device__ __forceinline__ void add_carefully(float v, float& total, float& lost) {
+    const float y = v - lost, t = total + y;
+    lost = t - total - y;
+    if (!(lost == lost)) lost = 0.f;             // an infinite total
+    total = t;
+}
+#endif
 
 // Small matrices: from the source to the result in one launch, without the workspace.
 bool use_ns_tiny(int64_t m, int64_t n);

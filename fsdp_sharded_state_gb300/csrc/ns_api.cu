@@ -73,7 +73,7 @@ NsWork ns_work(int64_t rows, int64_t cols, int64_t count) {
     if (use_ns_tiny(w.m, w.n)) {
         w.chunk = int(std::max<int64_t>(1, std::min<int64_t>(count, kNsMaxBatch)));
         w.x0 = w.x1 = w.square[0] = w.square[1] = w.square[2] = w.square[3] = w.partial = 0;
-        w.end = int64_t(w.chunk) * kNsMaxParts * 8;
+        w.end = int64_t(w.chunk) * kNsMaxParts * 4;
         return w;
     }
     const int64_t mp = round_up(w.m, 256), np = round_up(w.n, 256);
@@ -83,7 +83,7 @@ NsWork ns_work(int64_t rows, int64_t cols, int64_t count) {
     w.x1 = w.x0 + w.chunk * mp * np * 4;
     for (int i = 0; i < 4; ++i) w.square[i] = w.x1 + w.chunk * (mp * np + i * mp * mp) * 4;
     w.partial = w.square[3] + w.chunk * mp * mp * 4;
-    w.end = w.partial + int64_t(w.chunk) * kNsMaxParts * 8;
+    w.end = w.partial + int64_t(w.chunk) * kNsMaxParts * 4;
     return w;
 }
 
@@ -125,7 +125,7 @@ cudaError_t ns_run(const NsWork& w, unsigned char* ws, int batch, const NsMatric
     const float square = cost_ns_mul(p);
     p.y = x;
     const bool group = over_x + cost_ns_step(p) > 3.f * square;
-    cudaError_t e = launch_ns_pack(src, batch, x, reinterpret_cast<const double*>(ws + w.partial), parts, sc.x[0], eps, st);
+    cudaError_t e = launch_ns_pack(src, batch, x, reinterpret_cast<const float*>(ws + w.partial), parts, sc.x[0], eps, st);
     for (int k = 0; k < steps && e == cudaSuccess;) {
         // this group: steps k .. k + n, as even as they go
         const int left = steps - k, room = (left + kGroup - 1) / kGroup;
@@ -231,7 +231,7 @@ int fsdp_newton_schulz(int32_t count, int64_t rows, int64_t cols, const void* co
     int rc = check_dims(count, rows, cols);
     if (rc) return rc;
     if (!known(src_dtype) || !known(dst_dtype)) return FSDP_EDTYPE;
-    if (steps < 1 || steps > kNsMaxSteps || !(eps > 0.f) || !std::isfinite(eps)) return FSDP_EINVAL;
+    if (steps < 1 || steps > kNsMaxSteps || !(eps >= kNsLeastEps) || !std::isfinite(eps)) return FSDP_EINVAL;
     NsScales sc;
     if (!ns_scales(coeffs, steps, &sc)) return FSDP_EINVAL;
     if (count == 0) return FSDP_OK;
@@ -262,7 +262,7 @@ int fsdp_newton_schulz(int32_t count, int64_t rows, int64_t cols, const void* co
         s.bf16 = src_dtype == FSDP_BF16;
         d.bf16 = dst_dtype == FSDP_BF16;
         cudaError_t e = cudaSuccess;
-        if (!use_ns_tiny(w.m, w.n)) e = launch_ns_squares(s, n, w.m, w.n, reinterpret_cast<double*>(ws + w.partial), parts, st);
+        if (!use_ns_tiny(w.m, w.n)) e = launch_ns_squares(s, n, w.m, w.n, reinterpret_cast<float*>(ws + w.partial), parts, st);
         if (e != cudaSuccess) return cuda_fail(e, "k_ns_squares launch");
         e = ns_run(w, ws, n, s, d, parts, eps, coeffs, steps, sc, st);
         if (e != cudaSuccess) return cuda_fail(e, "k_ns launch");

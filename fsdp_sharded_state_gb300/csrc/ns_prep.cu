@@ -1,8 +1,10 @@
 // ns_prep.cu -- what comes before the products of Newton-Schulz steps: the sum of squares of
 // each matrix, and the first X as two fp16 terms.
 //
-// Both are bound by HBM (the matrix read twice, 4 bytes an element written).  The squares of a
-// thread are added in fp32 over 16 values and from there in 64 bits, in a fixed order.
+// Both are bound by HBM (the matrix read twice, 4 bytes an element written).  Squares are added in
+// fp32, a thread's sum of many with what each addition rounds carried along, in a fixed order: an
+// error of the norm scales all of X alike.  (There are two fp64 units an SM: sums, root and quotient
+// in 64 bits took longer than the reads.)
 #include <cuda_fp16.h>
 
 #include "common.cuh"
@@ -18,14 +20,14 @@ __device__ __forceinline__ float ns_get(const void* p, int64_t i, int bf16) {
 }
 
 // The sum over a CTA's threads, in thread 0.
-__device__ __forceinline__ double block_sum(double v) {
-    __shared__ double part[kPrepThreads / 32];
+__device__ __forceinline__ float block_sum(float v) {
+    __shared__ float part[kPrepThreads / 32];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
     __syncthreads();
     if (threadIdx.x == 0) {
-        v = 0.0;
+        v = 0.f;
         for (int k = 0; k < kPrepThreads / 32; ++k) v += part[k];
     }
     return v;
@@ -35,14 +37,15 @@ __device__ __forceinline__ double block_sum(double v) {
 constexpr int kStrip = 16 * kPrepThreads;
 
 __global__ void __launch_bounds__(kPrepThreads)
-k_ns_squares(const __grid_constant__ NsMatrices src, int64_t rows, int64_t cols, double* partial) {
+k_ns_squares(const __grid_constant__ NsMatrices src, int64_t rows, int64_t cols, float* partial) {
     pdl_wait();
+    pdl_trigger();
     const int mat = blockIdx.y;
     const bool tall = src.tall >> mat & 1;
     const int64_t R = tall ? cols : rows, W = tall ? rows : cols;    // the source's own rows and width
     const int64_t ld = src.ld[mat], n = R * W;
     const void* const p = src.p[mat];
-    double total = 0.0;
+    float total = 0.f, lost = 0.f;
     for (int64_t base = int64_t(blockIdx.x) * kStrip; base < n; base += int64_t(gridDim.x) * kStrip) {
         int64_t i = base + threadIdx.x;
         int64_t r = i / W, c = i - r * W;
@@ -59,7 +62,7 @@ k_ns_squares(const __grid_constant__ NsMatrices src, int64_t rows, int64_t cols,
         }
 #pragma unroll
         for (int k = 0; k < 16; ++k) s = __fmaf_rn(v[k], v[k], s);
-        total += double(s);
+        add_carefully(s, total, lost);
     }
     total = block_sum(total);
     if (threadIdx.x == 0) partial[mat * gridDim.x + blockIdx.x] = total;
@@ -68,18 +71,19 @@ k_ns_squares(const __grid_constant__ NsMatrices src, int64_t rows, int64_t cols,
 // A tile of 64 x 64 of the planes goes through shared memory, so that reads follow the source's
 // rows in either orientation and writes the planes'.
 __global__ void __launch_bounds__(kPrepThreads)
-k_ns_pack(const __grid_constant__ NsMatrices src, const NsPlanes out, const double* partial, int parts, float scale, float eps,
+k_ns_pack(const __grid_constant__ NsMatrices src, const NsPlanes out, const float* partial, int parts, float scale, float eps,
           int tiles_n) {
     __shared__ float tile[64][65];
     __shared__ float factor;
     pdl_wait();
+    pdl_trigger();
     const int mat = blockIdx.y, tid = threadIdx.x;
-    double square = 0.0;
+    float square = 0.f;
     for (int k = tid; k < parts; k += kPrepThreads) square += partial[mat * parts + k];
     square = block_sum(square);
     if (tid == 0) {
-        const double norm = sqrt(square);
-        factor = float(double(scale) / (norm < double(eps) ? double(eps) : norm));   // a NaN stays
+        const float norm = sqrtf(square);
+        factor = scale / (norm < eps ? eps : norm);              // a NaN stays
     }
     const bool tall = src.tall >> mat & 1;
     const int64_t m0 = int64_t(blockIdx.x / tiles_n) * 64, n0 = int64_t(blockIdx.x % tiles_n) * 64, ld = src.ld[mat];
@@ -124,11 +128,11 @@ int ns_parts(int64_t numel) {
     return int(n < 1 ? 1 : n < kNsMaxParts ? n : kNsMaxParts);
 }
 
-cudaError_t launch_ns_squares(const NsMatrices& src, int batch, int64_t rows, int64_t cols, double* partial, int parts, cudaStream_t st) {
+cudaError_t launch_ns_squares(const NsMatrices& src, int batch, int64_t rows, int64_t cols, float* partial, int parts, cudaStream_t st) {
     return launch(k_ns_squares, dim3(unsigned(parts), unsigned(batch)), dim3(kPrepThreads), 0, st, src, rows, cols, partial);
 }
 
-cudaError_t launch_ns_pack(const NsMatrices& src, int batch, const NsPlanes& out, const double* partial, int parts, float scale, float eps,
+cudaError_t launch_ns_pack(const NsMatrices& src, int batch, const NsPlanes& out, const float* partial, int parts, float scale, float eps,
                            cudaStream_t st) {
     const int64_t tm = (out.rows + 63) / 64, tn = (out.cols + 63) / 64;
     if (tm * tn > INT32_MAX) return cudaErrorInvalidValue;

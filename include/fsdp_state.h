@@ -709,8 +709,8 @@ int fsdp_layernorm_backward(int64_t rows, int64_t cols, int32_t elem_dtype, cons
  *     with |a + b s^2 + c s^4| above 1024 there, is refused (FSDP_EINVAL).
  *   - rows, cols: 1 .. 2^20, at most 2^34 elements padded to 256 (else FSDP_EOVERFLOW); count >= 0.
  *   - A zero matrix gives zeros.  An infinity or a NaN in src[i] makes dst[i] NaN throughout or, where
- *     that was an infinity, NaN or 0; no other matrix is touched by it.  The same holds for elements
- *     above 1.8e19, whose squares are infinite in fp32.
+ *     that was an infinity, NaN or 0; no other matrix is touched by it.  The same may hold for norms
+ *     above 1.8e19, whose squares are infinite in fp32.  eps >= 1e-16 (else FSDP_EINVAL).
  *   - dst[i] may be the very src[i] (with its stride and dtype); nothing else may overlap.
  *   - workspace: device scratch, 16-byte aligned, of at least
  *     fsdp_newton_schulz_workspace_bytes(count, rows, cols) bytes; contents, overlap and
@@ -744,7 +744,7 @@ typedef struct {
  *                   with no element or one column, as every vector, is FSDP_ESHAPE
  *   grad_replicas, param_replicas, master   as in fsdp_zero1_adamw_broadcast
  *   momentum        [N][stride] fp32 owner rows
- *   hp              lr, weight_decay >= 0, 0 <= momentum < 1, eps > 0 (else FSDP_EINVAL); steps, coeffs
+ *   hp              lr, weight_decay >= 0, 0 <= momentum < 1 (else FSDP_EINVAL); eps, steps, coeffs
  *                   and limits of size as in fsdp_newton_schulz
  *   workspace       at least fsdp_zero1_muon_workspace_bytes(layout, n_tensors, tensors) bytes;
  *                   tensors whose sides are equal, in either order, share it and its launches

@@ -15,7 +15,7 @@ BF16, F32 = torch.bfloat16, torch.float32
 # matrix (K split over clusters), several tiles of each configuration
 SHAPES = [(1, 1), (1, 7), (5, 3), (64, 32), (33, 65), (64, 64), (65, 64), (128, 128), (127, 129), (200, 1000), (256, 256), (257, 130),
           (384, 640), (16, 16384), (9000, 24), (512, 2048), (1001, 777), (1024, 1024), (1300, 2600), (3000, 1100),
-          (700, 6000), (64, 60000), (3, 1200), (30, 500), (31, 29), (64, 110), (64, 120), (8, 2000), (61, 63), (2, 2)]
+          (700, 6000), (64, 60000), (3, 1200), (30, 500), (31, 29), (64, 110), (64, 120), (8, 2000), (61, 63), (2, 2), (64, 256), (128, 96), (100, 120), (90, 97)]
 
 
 def workspace(count, rows, cols, extra=64):

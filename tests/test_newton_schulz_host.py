@@ -28,7 +28,7 @@ def ns(**k):
 @pytest.mark.parametrize("bad,status", [
     (dict(count=-1), ESHAPE), (dict(rows=0), ESHAPE), (dict(cols=0), ESHAPE), (dict(rows=(1 << 20) + 1), EOVERFLOW),
     (dict(rows=1 << 18, cols=1 << 17, lds=(1 << 17,) * 2, ldd=(1 << 17,) * 2), EOVERFLOW),
-    (dict(sdt=2), EDTYPE), (dict(ddt=-1), EDTYPE), (dict(steps=0), EINVAL), (dict(steps=65), EINVAL), (dict(eps=0.0), EINVAL),
+    (dict(sdt=2), EDTYPE), (dict(ddt=-1), EDTYPE), (dict(steps=0), EINVAL), (dict(steps=65), EINVAL), (dict(eps=0.0), EINVAL), (dict(eps=9e-17), EINVAL),
     (dict(eps=-1.0), EINVAL), (dict(eps=NAN), EINVAL), (dict(eps=INF), EINVAL), (dict(src=None), EINVAL), (dict(dst=None), EINVAL),
     (dict(lds=None), EINVAL), (dict(ldd=None), EINVAL), (dict(src=(P, None)), EINVAL), (dict(dst=(None, P)), EINVAL),
     (dict(src=(P, P + 2)), EALIGN), (dict(ddt=1, dst=(P + 1, P)), EALIGN), (dict(lds=(16, 15)), ESHAPE), (dict(ldd=(15, 16)), ESHAPE),
