@@ -78,6 +78,27 @@ k_ns_pack(const __grid_constant__ NsMatrices src, const NsPlanes out, const floa
     pdl_wait();
     pdl_trigger();
     const int mat = blockIdx.y, tid = threadIdx.x;
+    const bool tall = src.tall >> mat & 1;
+    const int64_t m0 = int64_t(blockIdx.x / tiles_n) * 64, n0 = int64_t(blockIdx.x % tiles_n) * 64, ld = src.ld[mat];
+    const int64_t r0 = tall ? n0 : m0, c0 = tall ? m0 : n0;          // the source's tile
+    const int64_t R = tall ? out.cols : out.rows, W = tall ? out.rows : out.cols;
+    const float* const p32 = static_cast<const float*>(src.p[mat]) + r0 * ld + c0;
+    // the tile's loads go out before the norm is there: 4 x 4 elements a thread
+    const bool vec = !src.bf16 && ((reinterpret_cast<uintptr_t>(p32) | uintptr_t(ld * 4)) & 15) == 0 && r0 + 64 <= R && c0 + 64 <= W;
+    float v[16];
+    if (vec) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float4 q = ld4(p32 + ((tid >> 4) + 16 * k) * ld + (tid & 15) * 4);
+            v[4 * k] = q.x; v[4 * k + 1] = q.y; v[4 * k + 2] = q.z; v[4 * k + 3] = q.w;
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            const int64_t r = r0 + (tid >> 6) + 4 * k, c = c0 + (tid & 63);
+            v[k] = r < R && c < W ? ns_get(src.p[mat], r * ld + c, src.bf16) : 0.f;
+        }
+    }
     float square = 0.f;
     for (int k = tid; k < parts; k += kPrepThreads) square += partial[mat * parts + k];
     square = block_sum(square);
@@ -85,29 +106,22 @@ k_ns_pack(const __grid_constant__ NsMatrices src, const NsPlanes out, const floa
         const float norm = sqrtf(square);
         factor = scale / (norm < eps ? eps : norm);              // a NaN stays
     }
-    const bool tall = src.tall >> mat & 1;
-    const int64_t m0 = int64_t(blockIdx.x / tiles_n) * 64, n0 = int64_t(blockIdx.x % tiles_n) * 64, ld = src.ld[mat];
-    const void* const p = src.p[mat];
-    const int x = tid & 63, y0 = tid >> 6;
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
-        const int y = y0 + 4 * k;                // row of the source's tile, x: column
-        const int64_t r = (tall ? n0 : m0) + y, c = (tall ? m0 : n0) + x;
-        const bool in = tall ? r < out.cols && c < out.rows : r < out.rows && c < out.cols;
-        const float v = in ? ns_get(p, r * ld + c, src.bf16) : 0.f;
-        if (tall) tile[x][y] = v;
-        else tile[y][x] = v;
+        const int y = vec ? (tid >> 4) + 16 * (k / 4) : (tid >> 6) + 4 * k, x = vec ? (tid & 15) * 4 + k % 4 : tid & 63;
+        if (tall) tile[x][y] = v[k];
+        else tile[y][x] = v[k];
     }
     __syncthreads();
     uint16_t* const dst = out.p + 2 * int64_t(mat) * out.plane;
     const float f = factor;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-        const int row = (tid >> 3) + 32 * k, c0 = (tid & 7) * 8;
+        const int row = (tid >> 3) + 32 * k, col = (tid & 7) * 8;
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const float a = tile[row][c0 + 2 * j] * f, b = tile[row][c0 + 2 * j + 1] * f;
+            const float a = tile[row][col + 2 * j] * f, b = tile[row][col + 2 * j + 1] * f;
             const __half2 h = __floats2half2_rn(a, b);
             const float2 g = __half22float2(h);
             const __half2 l = __floats2half2_rn(a - g.x, b - g.y);
@@ -115,7 +129,7 @@ k_ns_pack(const __grid_constant__ NsMatrices src, const NsPlanes out, const floa
             lo[j] = *reinterpret_cast<const uint32_t*>(&l);
         }
         // the planes are padded to whole tiles
-        uint16_t* const q = dst + (m0 + row) * out.ld + n0 + c0;
+        uint16_t* const q = dst + (m0 + row) * out.ld + n0 + col;
         stu4(q, make_uint4(hi[0], hi[1], hi[2], hi[3]));
         stu4(q + out.plane, make_uint4(lo[0], lo[1], lo[2], lo[3]));
     }
