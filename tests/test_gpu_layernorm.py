@@ -26,7 +26,9 @@ SHAPES = [(1, 1, 0, 0), (5, 7, 0, 0), (300, 32, 0, 0), (129, 33, 0, 0), (70, 64,
           (700, 2048, 0, 0), (5, 2052, 4, 0), (333, 4096, 0, 0), (17, 4100, 0, 3), (12, 8192, 0, 0), (11, 8191, 2, 0), (7, 8200, 0, 0),
           (160, 16384, 0, 0), (3, 20001, 0, 1), (2, 65536, 0, 0), (4, 40000, 0, 0), (65, 96, 3, 1), (20, 1500, 1, 1),
           (5000, 256, 0, 0), (4001, 40, 0, 0), (2500, 2048, 8, 0),
-          (9000, 3, 0, 0), (6001, 100, 4, 0), (3001, 500, 0, 1), (900, 5000, 0, 0), (450, 6145, 0, 0), (200, 12000, 8, 0), (150, 33000, 0, 0)]
+          (9000, 3, 0, 0), (6001, 100, 4, 0), (3001, 500, 0, 1), (900, 5000, 0, 0), (450, 6145, 0, 0), (200, 12000, 8, 0), (150, 33000, 0, 0),
+          (16001, 255, 0, 0), (5003, 31, 0, 0), (4000, 509, 0, 1), (3001, 1023, 2, 5), (1500, 2043, 0, 0), (900, 4093, 0, 3), (500, 6143, 0, 0),
+          (400, 8189, 0, 2), (300, 16381, 0, 7), (120, 65535, 0, 0), (3, 65536, 3, 1)]
 
 
 def _inputs(rows, cols, pad, offset, dtype, seed, mean=0.7, std=1.5):
@@ -152,6 +154,42 @@ def test_backward(rows, cols, pad, offset, dtype, grad_dtype, accumulate):
     dy.copy_(keep)
     fs.fsdp_layernorm_backward(dy, x, mean, rstd, x)
     assert torch.equal(plain, x)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("rows,cols", [(500, 64), (700, 333), (333, 1001), (129, 4096), (40, 9000)])
+def test_matrices_out_of_step(rows, cols, dtype):
+    """Matrices whose rows start at different addresses modulo 16."""
+    g = lu.gen(21)
+    places = [(cols, 0), (cols + 1, 0), (cols, 3), (cols + 5, 1)]
+    x0 = (torch.randn(rows, cols, generator=g, device="cuda") + 0.5).to(dtype)
+    dy0, r0 = ((torch.randn(rows, cols, generator=g, device="cuda") * 1e-3).to(dtype) for _ in range(2))
+    w, b = (torch.randn(cols, generator=g, device="cuda").to(dtype) for _ in range(2))
+
+    def put(v, k):
+        m, buf = lu.empty_matrix(rows, cols, dtype, *places[k % 4])
+        m.copy_(v)
+        return m, buf
+
+    def bounds(y, mean, rstd, dx, dw, db):
+        (wy, by), (wm, bm), (wr, br) = forward64(x0, w, b)
+        lu.check(y, wy, by, "y")
+        (wx, bx), (ww, bw), (wb, bb) = backward64(dy0, x0, mean, rstd, w, r0)
+        lu.check(dx, wx, bx, "dx")
+        lu.check(dw, ww, bw, "dw")
+        lu.check(db, wb, bb, "db")
+
+    ws = torch.empty(fs.fsdp_layernorm_workspace_bytes(rows, cols), dtype=torch.uint8, device="cuda")
+    for turn in range(4):
+        x, _ = put(x0, turn)
+        y, ybuf = put(torch.full_like(x0, float("nan")), turn + 1)
+        mean, rstd, sums = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda"), torch.empty(2, cols, device="cuda")
+        fs.fsdp_layernorm_forward(x, y, w, b, mean, rstd, EPS)
+        dx, xbuf = put(torch.full_like(x0, float("nan")), turn + 2)
+        fs.fsdp_layernorm_backward(put(dy0, turn + 3)[0], x, mean, rstd, dx, w, sums[0], sums[1], put(r0, turn + 1)[0], workspace=ws)
+        bounds(y, mean, rstd, dx, sums[0], sums[1])
+        assert lu.untouched(y, ybuf) and lu.untouched(dx, xbuf)
+    fs.fsdp_check_status()
 
 
 @pytest.mark.parametrize("which", ["dw", "db"])
