@@ -15,8 +15,7 @@ constexpr int64_t kNormMaxCols = 65536;
 struct NormProblem {
     int64_t rows, cols;
     bool bf16;
-    bool vec;                       // every matrix starts a row at the same address modulo 16
-    int before;                     // columns from a 16-byte boundary to a row, at most
+    bool vec;                       // every matrix has rows aligned to 16 bytes
     const void* x;
     int64_t ldx;
     const void* weight;

@@ -32,22 +32,7 @@ int check_matrix(const void* p, int64_t cols, int64_t ld, int es) {
 
 int check_vector(const void* p, int es) { return reinterpret_cast<uintptr_t>(p) % unsigned(es) ? FSDP_EALIGN : FSDP_OK; }
 
-// How the rows of a matrix start, modulo 16 bytes: the first, and the step from one to the next
-// (nothing where there is one row).
-struct Start {
-    unsigned at, step;
-};
-Start start_of(const void* p, int64_t ld, int es, int64_t rows) {
-    return Start{unsigned(reinterpret_cast<uintptr_t>(p) & 15), rows > 1 ? unsigned(ld * es & 15) : 0};
-}
-
-// Whether all of them start alike, and what may lie before a row then.
-void set_alignment(NormProblem* p, const Start* s, int n, int es) {
-    p->vec = true;
-    for (int i = 1; i < n; ++i) p->vec = p->vec && s[i].at == s[0].at && s[i].step == s[0].step;
-    p->before = s[0].at == 0 && s[0].step == 0 ? 0 : 16 / es - 1;
-    if (p->cols + p->before > kNormMaxCols) p->vec = false;
-}
+bool rows16(const void* p, int64_t ld, int es) { return !p || (aligned16(p) && ld * es % 16 == 0); }
 
 }  // namespace
 
@@ -68,8 +53,7 @@ int fsdp_layernorm_forward(int64_t rows, int64_t cols, int32_t elem_dtype, const
     p.rows = rows;
     p.cols = cols;
     p.bf16 = elem_dtype == FSDP_BF16;
-    const Start starts[2] = {start_of(x, ldx, es, rows), start_of(y, ldy, es, rows)};
-    set_alignment(&p, starts, 2, es);
+    p.vec = rows16(x, ldx, es) && rows16(y, ldy, es);
     p.x = x;
     p.ldx = ldx;
     p.weight = weight;
@@ -111,9 +95,7 @@ int fsdp_layernorm_backward(int64_t rows, int64_t cols, int32_t elem_dtype, cons
     p.rows = rows;
     p.cols = cols;
     p.bf16 = elem_dtype == FSDP_BF16;
-    const Start starts[4] = {start_of(x, ldx, es, rows), start_of(dy, lddy, es, rows), start_of(dx, lddx, es, rows),
-                             residual ? start_of(residual, ldr, es, rows) : start_of(x, ldx, es, rows)};
-    set_alignment(&p, starts, 4, es);
+    p.vec = rows16(x, ldx, es) && rows16(dy, lddy, es) && rows16(dx, lddx, es) && rows16(residual, ldr, es);
     p.x = x;
     p.ldx = ldx;
     p.weight = weight;

@@ -26,7 +26,7 @@ struct BackwardArgs {
     int64_t lddx;
     float* partial;                 // [2][groups][pitch], or NULL
     int64_t pitch, rows;
-    int32_t cols, ctas, stages, passes;
+    int32_t cols, ctas, stages, block;
     uint64_t wait_ns;
 };
 
@@ -45,17 +45,15 @@ k_norm_backward(const __grid_constant__ BackwardArgs a) {
     extern __shared__ __align__(128) unsigned char smem_raw[];   // the ring; at the end a row of sums per group
     __shared__ __align__(16) float sums[C::GW > 1 ? Sums::FLOATS * C::SIDE : 4];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int t = C::GW == 1 ? lane % C::L : tid % C::G;
-    const int sub = C::GW == 1 ? lane / C::L : 0, side = warp / C::GW * C::SUB + sub;    // which of the CTA's rows
+    const int t = C::GW == 1 ? lane % C::L : tid % C::G, group = warp / C::GW;
     const int rank = C::CLUSTER ? int(cluster_rank()) : 0, first = rank * C::COLS;
     const int part = blockIdx.x / a.ctas, parts = gridDim.x / a.ctas;
     const bool res = a.residual != nullptr;
-    const uint32_t rows = uint32_t(a.rows), block = uint32_t(C::ROWS * a.passes), row0 = part * block;
-    const int lo = norm_lo<C>(a.x, a.ldx, row0 + side);
-    RowRing<C, 3> ring(smem_raw, first, lo, a.cols, a.stages, a.passes, rows, parts * block, a.wait_ns);
-    ring.matrix(0, a.x, a.ldx, first, lo, row0);
-    ring.matrix(1, a.dy, a.lddy, first, lo, row0);
-    ring.matrix(2, a.residual, a.ldr, first, lo, row0);
+    const uint32_t rows = uint32_t(a.rows), row0 = part * uint32_t(C::SIDE * a.block);
+    RowRing<C, 3> ring(smem_raw, first, a.cols, a.stages, a.block, rows, parts * uint32_t(C::SIDE * a.block), a.wait_ns);
+    ring.matrix(0, a.x, a.ldx, first, row0);
+    ring.matrix(1, a.dy, a.lddy, first, row0);
+    ring.matrix(2, a.residual, a.ldr, first, row0);
     if (tid == 0) ring.init();
     if constexpr (C::CLUSTER) {                  // no CTA writes to another that has not started
         cluster_arrive();
@@ -65,23 +63,24 @@ k_norm_backward(const __grid_constant__ BackwardArgs a) {
     }
     pdl_wait();
     if (C::SIDE == 1 ? tid == 0 : warp == 0) ring.begin(row0, lane);
-    const Span<C> sp(first, t, lo, a.cols);
     pair w[C::P], dw[C::P], db[C::P];
-    norm_vector<C>(static_cast<const T*>(a.weight), sp, 1.f, w);
+    norm_vector<C>(static_cast<const T*>(a.weight), a.cols, first, t, 1.f, w);
 #pragma unroll
     for (int i = 0; i < C::P; ++i) dw[i] = db[i] = 0;
     Sums sum{sums};
+    const bool full = __all_sync(0xffffffffu, norm_full<C>(a.cols, first, t));
     const float over_n = 1.f / float(a.cols);
-    const int passes = C::GW == 1 ? a.passes : 1;
-    uint32_t mine = row0 + side;
-    T* py = static_cast<T*>(a.dx) + mine * a.lddx - lo;
-    const int64_t y_step = ring.step * a.lddx, y_pass = C::ROWS * a.lddx;
-    // mean and rstd are read a stage ahead: where a group is a warp, lane l reads those of row l % SUB of pass l / SUB
+    // of the group's first row of the stage: its place in it and in dx
+    const int block = C::GW == 1 ? a.block : 1;
+    const int j1 = group * block + (C::GW == 1 ? lane / C::L : 0);
+    uint32_t mine = row0 + j1;
+    T* py = static_cast<T*>(a.dx) + mine * a.lddx;
+    const int64_t y_step = ring.step * a.lddx, y_side = (32 / C::L) * a.lddx;
+    // mean and rstd are read a stage ahead: of the group's l-th row by lane l where that is a warp
     float next_mean = 0.f, next_rstd = 0.f;
     auto read_ahead = [&](uint32_t row) {
-        const int l = C::GW == 1 ? lane : 0;
-        row += l / C::SUB * C::ROWS + warp / C::GW * C::SUB + l % C::SUB;
-        if (l < passes * C::SUB && row < rows) {
+        row += group * block + (C::GW == 1 ? lane : 0);
+        if ((C::GW > 1 || lane < block) && row < rows) {
             next_mean = a.mean[row];
             next_rstd = a.rstd[row];
         }
@@ -93,23 +92,22 @@ k_norm_backward(const __grid_constant__ BackwardArgs a) {
         read_ahead(row + ring.step);
         ring.wait();
         T* y = py;
-        for (int pass = 0; pass < passes; ++pass, y += y_pass) {
-            const int j = pass * C::ROWS + side;
-            const bool have = mine + uint32_t(pass * C::ROWS) < rows;
+        for (int j0 = 0; j0 < block; j0 += C::GW == 1 ? 32 / C::L : 1, y += y_side) {
+            const bool have = mine + j0 < rows;
             pair h[C::P], g[C::P], add[C::P];
             float v[2] = {0.f, 0.f}, mean = row_mean, rstd = row_rstd;
             if constexpr (C::GW == 1) {
-                mean = __shfl_sync(0xffffffffu, row_mean, pass * C::SUB + sub);
-                rstd = __shfl_sync(0xffffffffu, row_rstd, pass * C::SUB + sub);
+                mean = __shfl_sync(0xffffffffu, row_mean, j0 + lane / C::L);
+                rstd = __shfl_sync(0xffffffffu, row_rstd, j0 + lane / C::L);
             }
             if (have) {
-                norm_load<C>(ring.row_of(j, 0), sp, h);
-                norm_load<C>(ring.row_of(j, 1), sp, g);
-                if (res) norm_load<C>(ring.row_of(j, 2), sp, add);
+                norm_load<C>(ring.row_of(j1 + j0, 0), a.cols, first, t, full, h);
+                norm_load<C>(ring.row_of(j1 + j0, 1), a.cols, first, t, full, g);
+                if (res) norm_load<C>(ring.row_of(j1 + j0, 2), a.cols, first, t, full, add);
                 const pair m = pair_of(-mean, -mean), r = pair_of(rstd, rstd);
 #pragma unroll
                 for (int i = 0; i < C::P; ++i) h[i] = mul2(add2(h[i], m), r);
-                if (!sp.full) norm_trim<C>(sp, h);
+                if (!full) norm_trim<C>(a.cols, first, t, h);
                 pair p = 0, q = 0;
 #pragma unroll
                 for (int i = 0; i < C::P; ++i) {
@@ -137,7 +135,7 @@ k_norm_backward(const __grid_constant__ BackwardArgs a) {
 #pragma unroll
                 for (int i = 0; i < C::P; ++i) g[i] = mul2(fma2(h[i], m1, add2(g[i], m0)), r);
             }
-            norm_store<C>(y, sp, g);
+            norm_store<C>(y, a.cols, first, t, full, g);
         }
         if (C::GW == 1) {
             __syncwarp();                        // every lane has read the warp's rows
@@ -149,35 +147,54 @@ k_norm_backward(const __grid_constant__ BackwardArgs a) {
     if (!a.partial) return;
     float* const out_w = a.partial + part * a.pitch;
     float* const out_b = out_w + parts * a.pitch;
-    if (C::SIDE == 1 && C::VEC && sp.full && lo == 0) {    // whole sectors where they are: element by element they took 10 us of 16384 x 4096
+    if constexpr (C::SIDE > 1) {
+        // the rows of a warp, then the groups of the CTA, in order
+        float* const smem = reinterpret_cast<float*>(smem_raw);
 #pragma unroll
-        for (int e = 0; e < C::E; e += 4) {
-            const float2 f = split(dw[e / 2]), g = split(dw[e / 2 + 1]), u = split(db[e / 2]), v = split(db[e / 2 + 1]);
-            st4(out_w + sp.at(e), make_float4(f.x, f.y, g.x, g.y));
-            st4(out_b + sp.at(e), make_float4(u.x, u.y, v.x, v.y));
+        for (int o = 16; o >= C::L; o >>= 1)
+#pragma unroll
+            for (int i = 0; i < C::P; ++i) {
+                dw[i] = add2(dw[i], __shfl_xor_sync(0xffffffffu, dw[i], o));
+                db[i] = add2(db[i], __shfl_xor_sync(0xffffffffu, db[i], o));
+            }
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+            __syncthreads();
+            if (C::GW > 1 || lane < C::L) {
+#pragma unroll
+                for (int e = 0; e < C::E; e += 2) {
+                    const float2 f = split(which ? db[e / 2] : dw[e / 2]);
+                    smem[warp / C::GW * C::COLS + norm_col<C>(0, t, e)] = f.x;
+                    smem[warp / C::GW * C::COLS + norm_col<C>(0, t, e + 1)] = f.y;
+                }
+            }
+            __syncthreads();
+            for (int c = tid; c < a.cols; c += C::THREADS) {
+                float v = 0.f;
+#pragma unroll
+                for (int k = 0; k < C::SIDE; ++k) v += smem[k * C::COLS + c];
+                (which ? out_b : out_w)[c] = v;
+            }
         }
-    }
-    // others by way of shared memory, a row of sums for each row that the CTA works on; those are added up
-    // in order.  (A column's place there: by its number, or, of a CTA that has a part of a row, in that part.)
-    float* const smem = reinterpret_cast<float*>(smem_raw);
-    const int shift = C::SIDE == 1 ? lo - first : 0;
+    } else {
+        if (C::VEC && full) {                    // whole sectors: element by element they took 10 us of 16384 x 4096
 #pragma unroll
-    for (int which = 0; which < 2; ++which) {
-        if (C::SIDE == 1 && C::VEC && lo == 0 && first + C::COLS <= a.cols) break;       // the CTA has written all of its own
-        __syncthreads();
+            for (int e = 0; e < C::E; e += 4) {
+                const int c = norm_col<C>(first, t, e);
+                const float2 f = split(dw[e / 2]), g = split(dw[e / 2 + 1]), u = split(db[e / 2]), v = split(db[e / 2 + 1]);
+                st4(out_w + c, make_float4(f.x, f.y, g.x, g.y));
+                st4(out_b + c, make_float4(u.x, u.y, v.x, v.y));
+            }
+        } else {
 #pragma unroll
-        for (int e = 0; e < C::E; ++e) {
-            const float2 f = split(which ? db[e / 2] : dw[e / 2]);
-            if (sp.has(e)) smem[side * C::COLS + sp.col(e) + shift] = e & 1 ? f.y : f.x;
-        }
-        __syncthreads();
-        for (int i = tid; i < C::COLS; i += C::THREADS) {
-            const int c = i - shift;
-            if (unsigned(c) >= unsigned(a.cols)) continue;
-            float v = 0.f;
-#pragma unroll 8
-            for (int k = 0; k < C::ROWS; ++k) v += smem[k * C::COLS + i];
-            (which ? out_b : out_w)[c] = v;
+            for (int e = 0; e < C::E; ++e) {
+                const int c = norm_col<C>(first, t, e);
+                if (c < a.cols) {
+                    const float2 f = split(dw[e / 2]), g = split(db[e / 2]);
+                    out_w[c] = e & 1 ? f.y : f.x;
+                    out_b[c] = e & 1 ? g.y : g.x;
+                }
+            }
         }
     }
 }
@@ -214,14 +231,16 @@ k_norm_join(const float* part, int parts, int64_t pitch, int cols, T* dw, T* db,
 // CTAs (or clusters) that work through the rows, each with a row of partial sums: as many as
 // fit the 152 SMs at once, fewer where there are few rows.
 template <class C>
-int64_t backward_groups(int64_t rows, int64_t cols, int ctas) {
-    return norm_groups(rows, C::ROWS * ring_shape<C>(3, cols, kBackwardCtas<C>).passes, 152 * kBackwardCtas<C> / ctas);
+int64_t backward_groups(int64_t rows, int64_t cols) {
+    const int64_t each = ring_shape<C>(3, cols, kBackwardCtas<C>).block * C::SIDE;
+    const int64_t want = (rows + each - 1) / each, room = 152 * kBackwardCtas<C> / norm_ctas<C>(cols);
+    return want < room ? want : room;
 }
 
 template <class C>
 cudaError_t launch_as(const NormProblem& p, cudaStream_t st) {
-    const int ctas = norm_ctas<C>(norm_room<C>(p));
-    const int64_t groups = backward_groups<C>(p.rows, p.cols, ctas), pitch = partial_pitch(p.cols);
+    const int ctas = norm_ctas<C>(p.cols);
+    const int64_t groups = backward_groups<C>(p.rows, p.cols), pitch = partial_pitch(p.cols);
     const bool sums = p.dw || p.db;
     cudaError_t e = cudaSuccess;
     if (p.rows > 0) {
@@ -229,9 +248,9 @@ cudaError_t launch_as(const NormProblem& p, cudaStream_t st) {
         int dev = 0;
         if ((e = cudaGetDevice(&dev)) != cudaSuccess || (e = norm_prepare(k_norm_backward<C>, prepared, dev)) != cudaSuccess) return e;
         const RingShape ring = ring_shape<C>(3, p.cols, kBackwardCtas<C>);
-        const size_t last = size_t(C::ROWS) * C::COLS * 4;
+        const size_t last = C::SIDE > 1 ? size_t(C::SIDE) * C::COLS * 4 : 0;
         const BackwardArgs a{p.x, p.ldx, p.dy, p.lddy, p.weight, p.residual, p.ldr, p.mean, p.rstd, p.y, p.ldy,
-                             sums ? p.partial : nullptr, pitch, p.rows, int32_t(p.cols), ctas, ring.stages, ring.passes, detail::kWaitNs};
+                             sums ? p.partial : nullptr, pitch, p.rows, int32_t(p.cols), ctas, ring.stages, ring.block, detail::kWaitNs};
         e = norm_launch(k_norm_backward<C>, int(groups), ctas, C::THREADS, ring.bytes > last ? ring.bytes : last, st, a);
     }
     if (e != cudaSuccess || !sums || (p.rows == 0 && p.accumulate)) return e;
@@ -248,17 +267,12 @@ cudaError_t launch_as(const NormProblem& p, cudaStream_t st) {
 int64_t norm_partial_floats(int64_t rows, int64_t cols) {
     int64_t groups = 0;
     auto most = [&](auto c) {
-        using C = decltype(c);
-        for (const int before : {0, 7}) {        // the rows' alignment may take more CTAs a row, or the next configuration
-            const int64_t g = backward_groups<C>(rows, cols, norm_ctas<C>(cols + before));
-            if (g > groups) groups = g;
-        }
+        const int64_t g = backward_groups<decltype(c)>(rows, cols);
+        if (g > groups) groups = g;
         return cudaSuccess;
     };
-    for (const int before : {0, 3, 7}) {
-        norm_dispatch_backward<float, true>(cols + before, most);
-        norm_dispatch_backward<uint16_t, true>(cols + before, most);
-    }
+    norm_dispatch_backward<float, true>(cols, most);
+    norm_dispatch_backward<uint16_t, true>(cols, most);
     return 2 * groups * partial_pitch(cols);
 }
 
@@ -266,8 +280,8 @@ cudaError_t take_wait_error_norm_backward(unsigned int* flag) { return take_norm
 
 cudaError_t launch_norm_backward(const NormProblem& p, cudaStream_t st) {
     auto go = [&](auto c) { return launch_as<decltype(c)>(p, st); };
-    if (p.bf16) return p.vec ? norm_dispatch_backward<uint16_t, true>(p.cols + p.before, go) : norm_dispatch_backward<uint16_t, false>(p.cols, go);
-    return p.vec ? norm_dispatch_backward<float, true>(p.cols + p.before, go) : norm_dispatch_backward<float, false>(p.cols, go);
+    if (p.bf16) return p.vec ? norm_dispatch_backward<uint16_t, true>(p.cols, go) : norm_dispatch_backward<uint16_t, false>(p.cols, go);
+    return p.vec ? norm_dispatch_backward<float, true>(p.cols, go) : norm_dispatch_backward<float, false>(p.cols, go);
 }
 
 }  // namespace fsdp

@@ -21,7 +21,7 @@ struct ForwardArgs {
     float* mean;
     float* rstd;
     int64_t rows;
-    int32_t cols, ctas, stages, passes;
+    int32_t cols, ctas, stages, block;
     float eps;
     uint64_t wait_ns;
 };
@@ -39,13 +39,11 @@ k_norm_forward(const __grid_constant__ ForwardArgs a) {
     extern __shared__ __align__(128) unsigned char smem_raw[];   // the ring
     __shared__ __align__(16) float sums[C::GW > 1 ? (Sum::FLOATS + Sums::FLOATS) * C::SIDE : 4];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int t = C::GW == 1 ? lane % C::L : tid % C::G;
-    const int side = warp / C::GW * C::SUB + (C::GW == 1 ? lane / C::L : 0);     // which of the CTA's rows
+    const int t = C::GW == 1 ? lane % C::L : tid % C::G, group = warp / C::GW;
     const int rank = C::CLUSTER ? int(cluster_rank()) : 0, first = rank * C::COLS;
-    const uint32_t rows = uint32_t(a.rows), block = uint32_t(C::ROWS * a.passes), row0 = blockIdx.x / a.ctas * block;
-    const int lo = norm_lo<C>(a.x, a.ldx, row0 + side);
-    RowRing<C, 1> ring(smem_raw, first, lo, a.cols, a.stages, a.passes, rows, gridDim.x / a.ctas * block, a.wait_ns);
-    ring.matrix(0, a.x, a.ldx, first, lo, row0);
+    const uint32_t rows = uint32_t(a.rows), row0 = blockIdx.x / a.ctas * uint32_t(C::SIDE * a.block);
+    RowRing<C, 1> ring(smem_raw, first, a.cols, a.stages, a.block, rows, gridDim.x / a.ctas * uint32_t(C::SIDE * a.block), a.wait_ns);
+    ring.matrix(0, a.x, a.ldx, first, row0);
     if (tid == 0) ring.init();
     if constexpr (C::CLUSTER) {                  // no CTA writes to another that has not started
         cluster_arrive();
@@ -55,27 +53,28 @@ k_norm_forward(const __grid_constant__ ForwardArgs a) {
     }
     pdl_wait();
     if (C::SIDE == 1 ? tid == 0 : warp == 0) ring.begin(row0, lane);
-    const Span<C> sp(first, t, lo, a.cols);
     pair w[C::P], b[C::P];
-    norm_vector<C>(static_cast<const T*>(a.weight), sp, 1.f, w);
-    norm_vector<C>(static_cast<const T*>(a.bias), sp, 0.f, b);
+    norm_vector<C>(static_cast<const T*>(a.weight), a.cols, first, t, 1.f, w);
+    norm_vector<C>(static_cast<const T*>(a.bias), a.cols, first, t, 0.f, b);
     Sum sum{sums};
     Sums sum2{sums + (C::GW > 1 ? Sum::FLOATS * C::SIDE : 0)};
+    const bool full = __all_sync(0xffffffffu, norm_full<C>(a.cols, first, t));
     const float n = float(a.cols), over_n = 1.f / n;
-    const int passes = C::GW == 1 ? a.passes : 1;
-    uint32_t mine = row0 + side;
-    T* py = static_cast<T*>(a.y) + mine * a.ldy - lo;
-    const int64_t y_step = ring.step * a.ldy, y_pass = C::ROWS * a.ldy;
+    // of the group's first row of the stage: its place in it and in y
+    const int j1 = group * (C::GW == 1 ? a.block : 1) + (C::GW == 1 ? lane / C::L : 0);
+    const int block = C::GW == 1 ? a.block : 1;
+    uint32_t mine = row0 + j1;
+    T* py = static_cast<T*>(a.y) + mine * a.ldy;
+    const int64_t y_step = ring.step * a.ldy, y_side = (32 / C::L) * a.ldy;
     // the threads of a CTA, or of a cluster, leave the loop together
     for (uint32_t row = row0; row < rows; row += ring.step, mine += ring.step, py += y_step) {
         ring.wait();
         T* y = py;
-        for (int pass = 0; pass < passes; ++pass, y += y_pass) {
-            const uint32_t own = mine + uint32_t(pass * C::ROWS);
-            const bool have = own < rows;
+        for (int j0 = 0; j0 < block; j0 += C::GW == 1 ? 32 / C::L : 1, y += y_side) {
+            const bool have = mine + j0 < rows;
             pair x[C::P];
             if (have) {
-                norm_load<C>(ring.row_of(pass * C::ROWS + side, 0), sp, x);
+                norm_load<C>(ring.row_of(j1 + j0, 0), a.cols, first, t, full, x);
             } else {
 #pragma unroll
                 for (int i = 0; i < C::P; ++i) x[i] = 0;
@@ -95,7 +94,7 @@ k_norm_forward(const __grid_constant__ ForwardArgs a) {
             const pair minus = pair_of(-mean, -mean);
 #pragma unroll
             for (int i = 0; i < C::P; ++i) x[i] = add2(x[i], minus);
-            if (!sp.full) norm_trim<C>(sp, x);
+            if (!full) norm_trim<C>(a.cols, first, t, x);
             pair q = mul2(x[0], x[0]);
 #pragma unroll
             for (int i = 1; i < C::P; ++i) q = fma2(x[i], x[i], q);
@@ -130,10 +129,10 @@ k_norm_forward(const __grid_constant__ ForwardArgs a) {
             const pair r = pair_of(rstd, rstd);
 #pragma unroll
             for (int i = 0; i < C::P; ++i) x[i] = fma2(mul2(x[i], r), w[i], b[i]);
-            norm_store<C>(y, sp, x);
+            norm_store<C>(y, a.cols, first, t, full, x);
             if (t == 0 && rank == 0) {
-                if (a.mean) a.mean[own] = left == left ? mean + left : mean;   // an infinity stays
-                if (a.rstd) a.rstd[own] = rstd;
+                if (a.mean) a.mean[mine + j0] = left == left ? mean + left : mean;   // an infinity stays
+                if (a.rstd) a.rstd[mine + j0] = rstd;
             }
         }
         if (C::GW == 1) {
@@ -148,25 +147,25 @@ k_norm_forward(const __grid_constant__ ForwardArgs a) {
 template <class C>
 cudaError_t launch_as(const NormProblem& p, cudaStream_t st) {
     static std::atomic<uint64_t> prepared{0};
-    constexpr int per_sm = kForwardCtas<C>;
-    const int ctas = norm_ctas<C>(norm_room<C>(p));
+    const int ctas = norm_ctas<C>(p.cols), per_sm = kForwardCtas<C>;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = norm_prepare(k_norm_forward<C>, prepared, dev);
     if (e != cudaSuccess) return e;
     const RingShape ring = ring_shape<C>(1, p.cols, per_sm);
-    const int64_t groups = norm_groups(p.rows, C::ROWS * ring.passes, int64_t(norm_sms(dev)) * per_sm / ctas);
-    const ForwardArgs a{p.x, p.ldx, p.weight, p.bias, p.y, p.ldy, p.mean, p.rstd, p.rows, int32_t(p.cols), ctas, ring.stages, ring.passes,
+    const int64_t each = ring.block * C::SIDE;
+    const int64_t want = (p.rows + each - 1) / each, room = int64_t(norm_sms(dev)) * per_sm / ctas;
+    const ForwardArgs a{p.x, p.ldx, p.weight, p.bias, p.y, p.ldy, p.mean, p.rstd, p.rows, int32_t(p.cols), ctas, ring.stages, ring.block,
                         p.eps, detail::kWaitNs};
-    return norm_launch(k_norm_forward<C>, int(groups), ctas, C::THREADS, ring.bytes, st, a);
+    return norm_launch(k_norm_forward<C>, int(want < room ? want : room), ctas, C::THREADS, ring.bytes, st, a);
 }
 
 }  // namespace
 
 cudaError_t launch_norm_forward(const NormProblem& p, cudaStream_t st) {
     auto go = [&](auto c) { return launch_as<decltype(c)>(p, st); };
-    if (p.bf16) return p.vec ? norm_dispatch_forward<uint16_t, true>(p.cols + p.before, go) : norm_dispatch_forward<uint16_t, false>(p.cols, go);
-    return p.vec ? norm_dispatch_forward<float, true>(p.cols + p.before, go) : norm_dispatch_forward<float, false>(p.cols, go);
+    if (p.bf16) return p.vec ? norm_dispatch_forward<uint16_t, true>(p.cols, go) : norm_dispatch_forward<uint16_t, false>(p.cols, go);
+    return p.vec ? norm_dispatch_forward<float, true>(p.cols, go) : norm_dispatch_forward<float, false>(p.cols, go);
 }
 
 cudaError_t take_wait_error_norm_forward(unsigned int* flag) { return take_norm_wait_error(flag); }

@@ -32,9 +32,7 @@ struct NormCfg {
     static constexpr bool VEC = VEC_, CLUSTER = CLUSTER_;
     static constexpr int P = E / 2;                                // pairs of a thread
     static constexpr int THREADS = GW <= 8 ? 256 : 32 * GW;
-    static constexpr int SIDE = THREADS / (32 * GW);               // groups of warps side by side in a CTA
-    static constexpr int SUB = GW == 1 ? 32 / L : 1;               // rows side by side in a group
-    static constexpr int ROWS = SIDE * SUB;                        // and in the CTA
+    static constexpr int SIDE = THREADS / (32 * GW);               // groups side by side in a CTA
     static constexpr int G = GW == 1 ? L : 32 * GW;                // threads of a row in one CTA
     static constexpr int COLS = G * E;                             // columns that they hold
     static_assert(GW == 1 || L == 32, "whole warps");
@@ -134,91 +132,89 @@ __device__ __forceinline__ int norm_col(int first, int t, int e) {
     return first + (C::VEC ? ((e / C::W) * C::G + t) * C::W + e % C::W : e * C::G + t);
 }
 
-// A thread's part of a row of `cols` columns: its elements lie at first + ..., counted from `lo` before the row.
+// Whether all of a thread's columns are in the row.
 template <class C>
-struct Span {
-    int first, t, lo, cols;
-    bool full;                                   // all elements of all of the warp are in the row
-    __device__ __forceinline__ Span(int first_, int t_, int lo_, int cols_) : first(first_), t(t_), lo(lo_), cols(cols_) {
-        full = __all_sync(0xffffffffu, has(0) && has(C::E - 1));
-    }
-    __device__ __forceinline__ int at(int e) const { return norm_col<C>(first, t, e); }
-    __device__ __forceinline__ int col(int e) const { return at(e) - lo; }
-    __device__ __forceinline__ bool has(int e) const { return unsigned(col(e)) < unsigned(cols); }
-};
+__device__ __forceinline__ bool norm_full(int cols, int first, int t) {
+    return norm_col<C>(first, t, C::E - 1) < cols;
+}
 
-// Elements that are not in the row made 0.
+// A thread's elements of a row whose column `first` is at `row` in shared memory; 0 past its end,
+// where the thread is not full.
 template <class C>
-__device__ __forceinline__ void norm_trim(const Span<C>& sp, pair (&v)[C::P]) {
+__device__ __forceinline__ void norm_load(uint32_t row, int cols, int first, int t, bool full, pair (&v)[C::P]) {
+    using T = typename C::T;
+    constexpr int S = int(sizeof(T));
+    auto at_or_0 = [&](int e) {
+        return norm_col<C>(first, t, e) < cols ? smem_get(row + uint32_t(norm_col<C>(0, t, e) * S), static_cast<const T*>(nullptr)) : 0.f;
+    };
+    if constexpr (C::VEC) {
+        if (full) {
+#pragma unroll
+            for (int c = 0; c < C::E; c += C::W) smem_get16(row + uint32_t(norm_col<C>(0, t, c) * S), v + c / 2, static_cast<const T*>(nullptr));
+            return;
+        }
+    } else {
+        if (full) {
+#pragma unroll
+            for (int e = 0; e < C::E; e += 2)
+                v[e / 2] = pair_of(smem_get(row + uint32_t(norm_col<C>(0, t, e) * S), static_cast<const T*>(nullptr)),
+                                   smem_get(row + uint32_t(norm_col<C>(0, t, e + 1) * S), static_cast<const T*>(nullptr)));
+            return;
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < C::E; e += 2) v[e / 2] = pair_of(at_or_0(e), at_or_0(e + 1));
+}
+// And into a row of a matrix in global memory.
+template <class C, typename T>
+__device__ __forceinline__ void norm_store(T* row, int cols, int first, int t, bool full, const pair (&v)[C::P]) {
+    if (full) {
+        T* const p = row + norm_col<C>(first, t, 0);
+#pragma unroll
+        for (int e = 0; e < C::E; e += C::VEC ? C::W : 2) {
+            if constexpr (C::VEC) {
+                norm_put16(p + (norm_col<C>(0, 0, e)), v + e / 2);
+            } else {
+                const float2 f = split(v[e / 2]);
+                norm_put(p + norm_col<C>(0, 0, e), f.x);
+                norm_put(p + norm_col<C>(0, 0, e + 1), f.y);
+            }
+        }
+        return;
+    }
+    auto put = [&](int e, float x) {
+        if (norm_col<C>(first, t, e) < cols) norm_put(row + norm_col<C>(first, t, e), x);
+    };
 #pragma unroll
     for (int e = 0; e < C::E; e += 2) {
         const float2 f = split(v[e / 2]);
-        v[e / 2] = pair_of(sp.has(e) ? f.x : 0.f, sp.has(e + 1) ? f.y : 0.f);
+        put(e, f.x);
+        put(e + 1, f.y);
     }
 }
-
-// A thread's elements of a row from shared memory, where `row` is the address of column `first`; 0 for
-// those that are not in it.
+// The elements past the row's end made 0 again, after a difference.
 template <class C>
-__device__ __forceinline__ void norm_load(uint32_t row, const Span<C>& sp, pair (&v)[C::P]) {
-    using T = typename C::T;
-    constexpr const T* type = nullptr;
-    constexpr int S = int(sizeof(T));
-    if constexpr (C::VEC) {
+__device__ __forceinline__ void norm_trim(int cols, int first, int t, pair (&v)[C::P]) {
 #pragma unroll
-        for (int c = 0; c < C::E; c += C::W) {
-            if (sp.full || sp.at(c) < sp.cols + sp.lo) {
-                smem_get16(row + uint32_t(norm_col<C>(0, sp.t, c) * S), v + c / 2, type);
-            } else {
-#pragma unroll
-                for (int k = 0; k < C::W / 2; ++k) v[c / 2 + k] = 0;
-            }
-        }
-        if (!sp.full) norm_trim<C>(sp, v);
-    } else if (sp.full) {
-#pragma unroll
-        for (int e = 0; e < C::E; e += 2)
-            v[e / 2] = pair_of(smem_get(row + uint32_t(norm_col<C>(0, sp.t, e) * S), type), smem_get(row + uint32_t(norm_col<C>(0, sp.t, e + 1) * S), type));
-    } else {
-        auto get = [&](int e) { return sp.has(e) ? smem_get(row + uint32_t(norm_col<C>(0, sp.t, e) * S), type) : 0.f; };
-#pragma unroll
-        for (int e = 0; e < C::E; e += 2) v[e / 2] = pair_of(get(e), get(e + 1));
-    }
-}
-// And into a row of a matrix in global memory, which begins `lo` columns after `row`.
-template <class C, typename T>
-__device__ __forceinline__ void norm_store(T* row, const Span<C>& sp, const pair (&v)[C::P]) {
-    T* const p = row + sp.at(0);
-    auto put = [&](int e) {
+    for (int e = 0; e < C::E; e += 2) {
         const float2 f = split(v[e / 2]);
-        if (sp.full || sp.has(e)) norm_put(p + norm_col<C>(0, 0, e), e & 1 ? f.y : f.x);
-    };
-    if constexpr (C::VEC) {
-#pragma unroll
-        for (int c = 0; c < C::E; c += C::W) {
-            if (sp.full || (sp.has(c) && sp.has(c + C::W - 1))) {
-                norm_put16(p + norm_col<C>(0, 0, c), v + c / 2);
-            } else {
-#pragma unroll
-                for (int e = c; e < c + C::W; ++e) put(e);
-            }
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < C::E; ++e) put(e);
+        v[e / 2] = pair_of(norm_col<C>(first, t, e) < cols ? f.x : 0.f, norm_col<C>(first, t, e + 1) < cols ? f.y : 0.f);
     }
 }
 // A vector of one row's width that may start at any element; `fill` where it is not there.
 template <class C, typename T>
-__device__ __forceinline__ void norm_vector(const T* p, const Span<C>& sp, float fill, pair (&v)[C::P]) {
+__device__ __forceinline__ void norm_vector(const T* p, int cols, int first, int t, float fill, pair (&v)[C::P]) {
+    auto get = [&](int e) {
+        const int at = norm_col<C>(first, t, e);
+        return p && at < cols ? norm_get(p + at) : p ? 0.f : fill;
+    };
     if constexpr (C::VEC) {
-        if (p && (reinterpret_cast<uintptr_t>(p) & 15) == 0 && sp.full && sp.lo == 0) {
+        if (p && (reinterpret_cast<uintptr_t>(p) & 15) == 0 && norm_full<C>(cols, first, t)) {
 #pragma unroll
-            for (int c = 0; c < C::E; c += C::W) norm_get16(p + sp.at(c), v + c / 2);
+            for (int c = 0; c < C::E; c += C::W) norm_get16(p + norm_col<C>(first, t, c), v + c / 2);
             return;
         }
     }
-    auto get = [&](int e) { return p && sp.has(e) ? norm_get(p + sp.col(e)) : p ? 0.f : fill; };
 #pragma unroll
     for (int e = 0; e < C::E; e += 2) v[e / 2] = pair_of(get(e), get(e + 1));
 }
@@ -283,8 +279,8 @@ struct RowSum {
     }
 };
 
-// A CTA's ring of stages in shared memory that bulk copies fill with the next rows, `passes` for each of
-// those that it works on side by side, or its share of one row; per matrix the 16-byte granules that hold them, as one
+// A CTA's ring of stages in shared memory that bulk copies fill with the next rows: `block` rows for
+// each of its groups, or its share of one row; per matrix the 16-byte granules that hold them, as one
 // piece where the rows are back to back, else a piece a row.  Rows may start at any element: the
 // bytes around a piece, which are in its own granules, are read and not used.  Stages are large, since
 // a copy takes some 65 ns of the copy engine beside 22 ns a KB: with 2 KB for each warp apart, 65536 x 256
@@ -301,34 +297,34 @@ __host__ __device__ inline int ring_piece(int cols, int esize) { return (cols * 
 template <class C, int N>
 struct RowRing {
     using T = typename C::T;
-    const T* base[N];                            // of this CTA's first column; the last may be NULL: not there
+    const T* base[N];                            // of this CTA's columns; the last may be NULL: not there
     int64_t ld[N];
     uint32_t front, at;                          // the ring in shared memory, and its present stage
     uint32_t rows, step;                         // of all, and between a CTA's stages
     int stages, most, piece, cols;               // most: rows of a stage; cols: of this CTA
     uint32_t between[N];                         // bytes from a row of a stage to the next
-    uint32_t low[N], low_step[N], low_row[N];    // the stage's first row's address, modulo 16, and what to add for the next stage's and row's
+    uint32_t low[N], low_step[N], low_row[N];    // rows of any alignment: the first's address mod 16, and what to add for the next stage's and row's
     bool back[N];                                // rows back to back
     uint64_t wait_ns;
     int s = 0;
     uint32_t phase = 0;
 
-    // lo: of the CTA's row where that is one (SIDE = 1) of chunks of 16 bytes.
-    __device__ __forceinline__ RowRing(unsigned char* smem, int first, int lo, int all, int stages_, int passes, uint32_t rows_, uint32_t step_,
-                                       uint64_t wait)
-        : front(smem_addr(smem)), at(smem_addr(smem) + kRingFront), rows(rows_), step(step_), stages(stages_), most(C::ROWS * passes), wait_ns(wait) {
-        const int left = all - first + (C::VEC && C::SIDE == 1 ? lo : 0);
+    __device__ __forceinline__ RowRing(unsigned char* smem, int first, int all, int stages_, int block, uint32_t rows_, uint32_t step_, uint64_t wait)
+        : front(smem_addr(smem)), at(smem_addr(smem) + kRingFront), rows(rows_), step(step_), stages(stages_), most(C::SIDE * block), wait_ns(wait) {
+        const int left = all - first;
         cols = left < 0 ? 0 : left < C::COLS ? left : C::COLS;
         piece = ring_piece(all < C::COLS ? all : C::COLS, int(sizeof(T)));
     }
-    __device__ __forceinline__ void matrix(int k, const void* p, int64_t ld_, int first, int lo, uint32_t row0) {
-        base[k] = p ? static_cast<const T*>(p) + first - (C::VEC && C::SIDE == 1 ? lo : 0) : nullptr;
+    __device__ __forceinline__ void matrix(int k, const void* p, int64_t ld_, int first, uint32_t row0) {
+        base[k] = p ? static_cast<const T*>(p) + first : nullptr;
         ld[k] = ld_;
         back[k] = C::SIDE > 1 && ld_ == cols;
         between[k] = back[k] ? uint32_t(cols) * uint32_t(sizeof(T)) : uint32_t(piece);
-        low_row[k] = uint32_t(ld_) * uint32_t(sizeof(T));
-        low_step[k] = step * low_row[k];
-        low[k] = uint32_t(reinterpret_cast<uintptr_t>(base[k])) + row0 * low_row[k];
+        if constexpr (!C::VEC) {
+            low_row[k] = uint32_t(ld_) * uint32_t(sizeof(T));
+            low_step[k] = step * low_row[k];
+            low[k] = uint32_t(reinterpret_cast<uintptr_t>(base[k])) + row0 * low_row[k];
+        }
     }
     __device__ __forceinline__ uint32_t bar(int i) const { return front + 8 * i; }
     __device__ __forceinline__ uint32_t count(int i) const { return front + 8 * kRingStages + 4 * i; }
@@ -399,12 +395,12 @@ struct RowRing {
         for (int i = 0; i < stages; ++i)
             if (row + i * step < rows) fetch(row + i * step, i, lane);
     }
-    // Where the stage holds its j-th row of matrix k: the shared-memory address of this CTA's first
-    // column, with chunks of 16 bytes of the boundary before it.
+    // Where the stage holds its j-th row of matrix k: the shared-memory address of this CTA's first column.
     __device__ __forceinline__ uint32_t row_of(int j, int k) const {
-        const uint32_t p = at + uint32_t(k * most * piece), in = C::SIDE > 1 ? uint32_t(j) * between[k] : 0u;
-        if constexpr (C::VEC) return p + (C::SIDE > 1 && back[k] ? ((low[k] & 15u) + in) & ~15u : in);
-        else return p + in + ((back[k] ? low[k] : low[k] + uint32_t(j) * low_row[k]) & 15u);
+        uint32_t p = at + uint32_t(k * most * piece);
+        if constexpr (C::SIDE > 1) p += uint32_t(j) * between[k];
+        if constexpr (!C::VEC) p += (back[k] ? low[k] : low[k] + uint32_t(j) * low_row[k]) & 15u;
+        return p;
     }
     __device__ __forceinline__ void wait() {
         if (!mbar_wait_bounded(bar(s), phase, wait_ns)) {
@@ -449,39 +445,24 @@ struct RowRing {
     }
 };
 
-// The columns before a row that its group counts from.
-template <class C>
-__device__ __forceinline__ int norm_lo(const void* p, int64_t ld, uint32_t row) {
-    constexpr uint32_t S = uint32_t(sizeof(typename C::T));
-    return C::VEC ? int(((uint32_t(reinterpret_cast<uintptr_t>(p)) + row * uint32_t(ld) * S) & 15u) / S) : 0;
-}
-
-// Host side: how many rows a stage holds for each of those side by side, how many stages, and the shared
-// memory of a CTA of which per_sm share an SM.  About 8 KB of each matrix a stage, at most 32 rows a warp.
+// Host side: how many rows of a group a stage holds, how many stages, and the shared memory of a
+// CTA of which per_sm share an SM.  About 8 KB of each matrix a stage, at most 32 rows a warp.
 struct RingShape {
-    int passes, stages;
+    int block, stages;
     size_t bytes;
 };
 template <class C>
 RingShape ring_shape(int n, int64_t cols, int per_sm) {
-    constexpr int es = int(sizeof(typename C::T));
+    constexpr int es = int(sizeof(typename C::T)), side = C::GW == 1 ? 32 / C::L : 1;
     const int piece = ring_piece(int(cols < C::COLS ? cols : C::COLS), es);
     RingShape r;
-    r.passes = 1;
+    r.block = side;
     if (C::GW == 1)
-        while (C::ROWS * r.passes * piece < 8192 && (r.passes + 1) * C::SUB <= 32) ++r.passes;
-    const int stage = n * C::ROWS * r.passes * piece, fit = (208 * 1024 / per_sm - kRingFront - 4096) / stage;
+        while (C::SIDE * r.block * piece < 8192 && r.block + side <= 32) r.block += side;
+    const int stage = n * C::SIDE * r.block * piece, fit = (208 * 1024 / per_sm - kRingFront - 4096) / stage;
     r.stages = fit > kRingStages ? kRingStages : fit < 2 ? 2 : fit;
     r.bytes = size_t(kRingFront) + size_t(r.stages) * stage;
     return r;
-}
-
-// CTAs (or clusters) for `rows`: as many as there is work for, or as fit at once, a multiple of 8
-// then, so that every group's rows are 8 apart or a multiple of it.
-inline int64_t norm_groups(int64_t rows, int64_t each, int64_t room) {
-    const int64_t want = (rows + each - 1) / each;
-    if (want <= room) return want;
-    return room >= 8 ? room / 8 * 8 : room;
 }
 
 std::atomic<bool> g_norm_launched{false};
@@ -528,12 +509,12 @@ cudaError_t norm_dispatch_backward(int64_t cols, F&& f) {
     return f(NormCfg<T, 32, 16, 2, VEC, true>{});
 }
 
-// CTAs of a row (a cluster where there are more than one); room: columns with those before it.
+// CTAs of a row (a cluster where there are more than one).
 template <class C>
-int norm_ctas(int64_t room) {
+int norm_ctas(int64_t cols) {
     if (!C::CLUSTER) return 1;
     int n = 2;
-    while (int64_t(n) * C::COLS < room) n *= 2;
+    while (int64_t(n) * C::COLS < cols) n *= 2;
     return n;
 }
 
@@ -545,10 +526,6 @@ cudaError_t norm_prepare(K kernel, std::atomic<uint64_t>& done, int dev) {
     if (e == cudaSuccess && dev < 64) done.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
     return e;
 }
-
-// Columns of a problem with those that may be counted before its rows.
-template <class C>
-int64_t norm_room(const NormProblem& p) { return p.cols + (C::VEC ? p.before : 0); }
 
 template <typename... KArgs, typename... Args>
 cudaError_t norm_launch(void (*kernel)(KArgs...), int groups, int ctas, int threads, size_t smem, cudaStream_t st, Args&&... args) {
