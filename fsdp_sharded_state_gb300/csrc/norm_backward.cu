@@ -44,6 +44,8 @@ k_norm_backward(const __grid_constant__ BackwardArgs a) {
     using Sums = RowSum<C, 2>;
     extern __shared__ __align__(128) unsigned char smem_raw[];   // the ring; at the end a row of sums per group
     __shared__ __align__(16) float sums[C::GW > 1 ? Sums::FLOATS * C::SIDE : 4];
+    // of rows of up to 1024 columns few threads hold an end, and the registers of its tests are missed (65536 x 256 29 us, not 24)
+    constexpr bool ENDS = C::VEC && C::GW >= 4;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int t = C::GW == 1 ? lane % C::L : tid % C::G, group = warp / C::GW;
     const int rank = C::CLUSTER ? int(cluster_rank()) : 0, first = rank * C::COLS;
@@ -67,7 +69,7 @@ k_norm_backward(const __grid_constant__ BackwardArgs a) {
     norm_vector<C>(static_cast<const T*>(a.weight), a.cols, first, t, 1.f, w);
 #pragma unroll
     for (int i = 0; i < C::P; ++i) dw[i] = db[i] = 0;
-    Sums sum{sums};
+    Sums sum{sums, ring.sums(0), a.wait_ns};
     const bool full = __all_sync(0xffffffffu, norm_full<C>(a.cols, first, t));
     const float over_n = 1.f / float(a.cols);
     // of the group's first row of the stage: its place in it and in dx
@@ -101,13 +103,13 @@ k_norm_backward(const __grid_constant__ BackwardArgs a) {
                 rstd = __shfl_sync(0xffffffffu, row_rstd, j0 + lane / C::L);
             }
             if (have) {
-                norm_load<C>(ring.row_of(j1 + j0, 0), a.cols, first, t, full, h);
-                norm_load<C>(ring.row_of(j1 + j0, 1), a.cols, first, t, full, g);
-                if (res) norm_load<C>(ring.row_of(j1 + j0, 2), a.cols, first, t, full, add);
+                norm_load<C, ENDS>(ring.row_of(j1 + j0, 0), a.cols, first, t, full, h);
+                norm_load<C, ENDS>(ring.row_of(j1 + j0, 1), a.cols, first, t, full, g);
+                if (res) norm_load<C, ENDS>(ring.row_of(j1 + j0, 2), a.cols, first, t, full, add);
                 const pair m = pair_of(-mean, -mean), r = pair_of(rstd, rstd);
 #pragma unroll
                 for (int i = 0; i < C::P; ++i) h[i] = mul2(add2(h[i], m), r);
-                if (!full) norm_trim<C>(a.cols, first, t, h);
+                if (!full) norm_trim<C, ENDS>(a.cols, first, t, h);
                 pair p = 0, q = 0;
 #pragma unroll
                 for (int i = 0; i < C::P; ++i) {
@@ -135,7 +137,7 @@ k_norm_backward(const __grid_constant__ BackwardArgs a) {
 #pragma unroll
                 for (int i = 0; i < C::P; ++i) g[i] = mul2(fma2(h[i], m1, add2(g[i], m0)), r);
             }
-            norm_store<C>(y, a.cols, first, t, full, g);
+            norm_store<C, ENDS>(y, a.cols, first, t, full, g);
         }
         if (C::GW == 1) {
             __syncwarp();                        // every lane has read the warp's rows
@@ -143,7 +145,7 @@ k_norm_backward(const __grid_constant__ BackwardArgs a) {
             ring.next();
         }
     }
-    ring.leave();
+    ring.leave(C::CLUSTER ? sum.wait_ns : 1);
     if (!a.partial) return;
     float* const out_w = a.partial + part * a.pitch;
     float* const out_b = out_w + parts * a.pitch;
