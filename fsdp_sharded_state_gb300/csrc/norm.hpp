@@ -15,7 +15,7 @@ constexpr int64_t kNormMaxCols = 65536;
 struct NormProblem {
     int64_t rows, cols;
     bool bf16;
-    bool vec;                       // every matrix has rows aligned to 16 bytes
+    bool vec;                       // every matrix has rows of whole 16-byte chunks
     const void* x;
     int64_t ldx;
     const void* weight;

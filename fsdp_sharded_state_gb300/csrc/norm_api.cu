@@ -32,7 +32,8 @@ int check_matrix(const void* p, int64_t cols, int64_t ld, int es) {
 
 int check_vector(const void* p, int es) { return reinterpret_cast<uintptr_t>(p) % unsigned(es) ? FSDP_EALIGN : FSDP_OK; }
 
-bool rows16(const void* p, int64_t ld, int es) { return !p || (aligned16(p) && ld * es % 16 == 0); }
+// Whether a matrix's rows are whole chunks of 16 bytes.
+bool rows16(const void* p, int64_t cols, int64_t ld, int es) { return !p || (aligned16(p) && ld * es % 16 == 0 && cols * es % 16 == 0); }
 
 }  // namespace
 
@@ -53,7 +54,7 @@ int fsdp_layernorm_forward(int64_t rows, int64_t cols, int32_t elem_dtype, const
     p.rows = rows;
     p.cols = cols;
     p.bf16 = elem_dtype == FSDP_BF16;
-    p.vec = rows16(x, ldx, es) && rows16(y, ldy, es);
+    p.vec = rows16(x, cols, ldx, es) && rows16(y, cols, ldy, es);
     p.x = x;
     p.ldx = ldx;
     p.weight = weight;
@@ -95,7 +96,7 @@ int fsdp_layernorm_backward(int64_t rows, int64_t cols, int32_t elem_dtype, cons
     p.rows = rows;
     p.cols = cols;
     p.bf16 = elem_dtype == FSDP_BF16;
-    p.vec = rows16(x, ldx, es) && rows16(dy, lddy, es) && rows16(dx, lddx, es) && rows16(residual, ldr, es);
+    p.vec = rows16(x, cols, ldx, es) && rows16(dy, cols, lddy, es) && rows16(dx, cols, lddx, es) && rows16(residual, cols, ldr, es);
     p.x = x;
     p.ldx = ldx;
     p.weight = weight;

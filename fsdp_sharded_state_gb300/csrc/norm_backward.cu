@@ -44,8 +44,6 @@ k_norm_backward(const __grid_constant__ BackwardArgs a) {
     using Sums = RowSum<C, 2>;
     extern __shared__ __align__(128) unsigned char smem_raw[];   // the ring; at the end a row of sums per group
     __shared__ __align__(16) float sums[C::GW > 1 ? Sums::FLOATS * C::SIDE : 4];
-    // of rows of up to 1024 columns few threads hold an end, and the registers of its tests are missed (65536 x 256 29 us, not 24)
-    constexpr bool ENDS = C::VEC && C::GW >= 4;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int t = C::GW == 1 ? lane % C::L : tid % C::G, group = warp / C::GW;
     const int rank = C::CLUSTER ? int(cluster_rank()) : 0, first = rank * C::COLS;
@@ -103,13 +101,13 @@ k_norm_backward(const __grid_constant__ BackwardArgs a) {
                 rstd = __shfl_sync(0xffffffffu, row_rstd, j0 + lane / C::L);
             }
             if (have) {
-                norm_load<C, ENDS>(ring.row_of(j1 + j0, 0), a.cols, first, t, full, h);
-                norm_load<C, ENDS>(ring.row_of(j1 + j0, 1), a.cols, first, t, full, g);
-                if (res) norm_load<C, ENDS>(ring.row_of(j1 + j0, 2), a.cols, first, t, full, add);
+                norm_load<C>(ring.row_of(j1 + j0, 0), a.cols, first, t, full, h);
+                norm_load<C>(ring.row_of(j1 + j0, 1), a.cols, first, t, full, g);
+                if (C::GW > 1 && res) norm_load<C>(ring.row_of(j1 + j0, 2), a.cols, first, t, full, add);
                 const pair m = pair_of(-mean, -mean), r = pair_of(rstd, rstd);
 #pragma unroll
                 for (int i = 0; i < C::P; ++i) h[i] = mul2(add2(h[i], m), r);
-                if (!full) norm_trim<C, ENDS>(a.cols, first, t, h);
+                if (!full) norm_trim<C>(a.cols, first, t, h);
                 pair p = 0, q = 0;
 #pragma unroll
                 for (int i = 0; i < C::P; ++i) {
@@ -130,14 +128,30 @@ k_norm_backward(const __grid_constant__ BackwardArgs a) {
             if (!have) continue;
             const float c0 = -v[0] * over_n, c1 = -v[1] * over_n;
             const pair m0 = pair_of(c0, c0), m1 = pair_of(c1, c1), r = pair_of(rstd, rstd);
-            if (res) {
+            if (C::GW == 1 && C::VEC) {          // the residual a chunk at a time: as a whole its registers spill, and 65536 x 256 takes 33 us
+                const uint32_t from = ring.row_of(j1 + j0, 2);
+#pragma unroll
+                for (int c = 0; c < C::P; c += C::W / 2) {
+                    pair add4[C::W / 2];
+                    const int col = norm_col<C>(0, t, 2 * c);
+                    if (res) {
+                        smem_get16(full || col < a.cols ? from + uint32_t(col) * uint32_t(sizeof(T)) : from, add4, static_cast<const T*>(nullptr));
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < C::W / 2; ++i) add4[i] = 0;
+                    }
+#pragma unroll
+                    for (int i = 0; i < C::W / 2; ++i) g[c + i] = fma2(fma2(h[c + i], m1, add2(g[c + i], m0)), r, add4[i]);
+                }
+            } else if (res) {
+                if (C::GW == 1) norm_load<C>(ring.row_of(j1 + j0, 2), a.cols, first, t, full, add);
 #pragma unroll
                 for (int i = 0; i < C::P; ++i) g[i] = fma2(fma2(h[i], m1, add2(g[i], m0)), r, add[i]);
             } else {
 #pragma unroll
                 for (int i = 0; i < C::P; ++i) g[i] = mul2(fma2(h[i], m1, add2(g[i], m0)), r);
             }
-            norm_store<C, ENDS>(y, a.cols, first, t, full, g);
+            norm_store<C>(y, a.cols, first, t, full, g);
         }
         if (C::GW == 1) {
             __syncwarp();                        // every lane has read the warp's rows
@@ -179,10 +193,11 @@ k_norm_backward(const __grid_constant__ BackwardArgs a) {
             }
         }
     } else {
-        if (C::VEC && full) {                    // whole sectors: element by element they took 10 us of 16384 x 4096
+        if (C::VEC) {                            // whole sectors: element by element they took 10 us of 16384 x 4096
 #pragma unroll
             for (int e = 0; e < C::E; e += 4) {
                 const int c = norm_col<C>(first, t, e);
+                if (c >= a.cols) continue;
                 const float2 f = split(dw[e / 2]), g = split(dw[e / 2 + 1]), u = split(db[e / 2]), v = split(db[e / 2 + 1]);
                 st4(out_w + c, make_float4(f.x, f.y, g.x, g.y));
                 st4(out_b + c, make_float4(u.x, u.y, v.x, v.y));

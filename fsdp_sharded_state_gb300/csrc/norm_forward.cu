@@ -38,7 +38,6 @@ k_norm_forward(const __grid_constant__ ForwardArgs a) {
     using Sums = RowSum<C, 2>;                   // fp32
     extern __shared__ __align__(128) unsigned char smem_raw[];   // the ring
     __shared__ __align__(16) float sums[C::GW > 1 ? (Sum::FLOATS + Sums::FLOATS) * C::SIDE : 4];
-    constexpr bool ENDS = C::VEC;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int t = C::GW == 1 ? lane % C::L : tid % C::G, group = warp / C::GW;
     const int rank = C::CLUSTER ? int(cluster_rank()) : 0, first = rank * C::COLS;
@@ -75,7 +74,7 @@ k_norm_forward(const __grid_constant__ ForwardArgs a) {
             const bool have = mine + j0 < rows;
             pair x[C::P];
             if (have) {
-                norm_load<C, ENDS>(ring.row_of(j1 + j0, 0), a.cols, first, t, full, x);
+                norm_load<C>(ring.row_of(j1 + j0, 0), a.cols, first, t, full, x);
             } else {
 #pragma unroll
                 for (int i = 0; i < C::P; ++i) x[i] = 0;
@@ -95,7 +94,7 @@ k_norm_forward(const __grid_constant__ ForwardArgs a) {
             const pair minus = pair_of(-mean, -mean);
 #pragma unroll
             for (int i = 0; i < C::P; ++i) x[i] = add2(x[i], minus);
-            if (!full) norm_trim<C, ENDS>(a.cols, first, t, x);
+            if (!full) norm_trim<C>(a.cols, first, t, x);
             pair q = mul2(x[0], x[0]);
 #pragma unroll
             for (int i = 1; i < C::P; ++i) q = fma2(x[i], x[i], q);
@@ -130,7 +129,7 @@ k_norm_forward(const __grid_constant__ ForwardArgs a) {
             const pair r = pair_of(rstd, rstd);
 #pragma unroll
             for (int i = 0; i < C::P; ++i) x[i] = fma2(mul2(x[i], r), w[i], b[i]);
-            norm_store<C, ENDS>(y, a.cols, first, t, full, x);
+            norm_store<C>(y, a.cols, first, t, full, x);
             if (t == 0 && rank == 0) {
                 if (a.mean) a.mean[mine + j0] = left == left ? mean + left : mean;   // an infinity stays
                 if (a.rstd) a.rstd[mine + j0] = rstd;

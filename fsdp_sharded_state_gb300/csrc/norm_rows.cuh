@@ -4,7 +4,7 @@
 // A row belongs to a group of threads that hold it in registers from its load to its store:
 // L lanes of a warp (up to 512 columns; a warp then works on 32 / L rows at once), GW warps of a CTA
 // (up to 8192, in forward 16384), or GW warps in each CTA of a cluster (up to 65536).  A thread holds 8 V columns:
-// chunks of 16 bytes where rows are aligned to 16 bytes (VEC), else single columns that are a
+// chunks of 16 bytes where rows are made of whole ones (VEC), else single columns that are a
 // group's width apart, so that a warp's accesses are contiguous either way.
 //
 // Rows come through shared memory (RowRing): loads of a row by the threads that wait for it
@@ -138,35 +138,22 @@ __device__ __forceinline__ bool norm_full(int cols, int first, int t) {
     return norm_col<C>(first, t, C::E - 1) < cols;
 }
 
-// Elements past the row's end made 0.  Of chunks all but the row's last are in it or past it as a whole: tested
-// element by element, like those, 4096 x 10000 bf16 forward took 150 us.  ENDS: whether that is used.
-template <class C, bool ENDS>
+// Elements past the row's end made 0.  Chunks are in it or past it as a whole: tested element by
+// element, 4096 x 10000 bf16 forward took 150 us.
+template <class C>
 __device__ __forceinline__ void norm_trim(int cols, int first, int t, pair (&v)[C::P]) {
-    auto some = [&](int e) {
+#pragma unroll
+    for (int e = 0; e < C::E; e += 2) {
         const float2 f = split(v[e / 2]);
-        v[e / 2] = pair_of(norm_col<C>(first, t, e) < cols ? f.x : 0.f, norm_col<C>(first, t, e + 1) < cols ? f.y : 0.f);
-    };
-    if constexpr (ENDS) {
-#pragma unroll
-        for (int c = 0; c < C::E; c += C::W) {
-            const bool in = norm_col<C>(first, t, c) < cols;
-#pragma unroll
-            for (int k = 0; k < C::W / 2; ++k) v[c / 2 + k] = in ? v[c / 2 + k] : 0;
-            if (in && norm_col<C>(first, t, c + C::W - 1) >= cols) {
-#pragma unroll
-                for (int e = c; e < c + C::W; e += 2) some(e);
-            }
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < C::E; e += 2) some(e);
+        const bool in = norm_col<C>(first, t, C::VEC ? e / C::W * C::W : e) < cols;
+        v[e / 2] = pair_of(in ? f.x : 0.f, (C::VEC ? in : norm_col<C>(first, t, e + 1) < cols) ? f.y : 0.f);
     }
 }
 
 // A thread's elements of a row whose column `first` is at `row` in shared memory; 0 past its end,
 // where the thread is not full.  (Full threads have code of their own, here and below: with tests, even of a
 // bit, between the loads of the chunks, 16384 x 4096 bf16 backward took 123 us instead of 77.)
-template <class C, bool ENDS>
+template <class C>
 __device__ __forceinline__ void norm_load(uint32_t row, int cols, int first, int t, bool full, pair (&v)[C::P]) {
     using T = typename C::T;
     constexpr const T* type = nullptr;
@@ -175,11 +162,11 @@ __device__ __forceinline__ void norm_load(uint32_t row, int cols, int first, int
     if (C::VEC && full) {
 #pragma unroll
         for (int c = 0; c < C::E; c += C::W) smem_get16(row + uint32_t(norm_col<C>(0, t, c) * S), v + c / 2, type);
-    } else if (ENDS) {                         // the row's last chunk is in the ring as a whole; for those past it the row's first
+    } else if (C::VEC) {                         // for chunks past the row's end its first
 #pragma unroll
         for (int c = 0; c < C::E; c += C::W) smem_get16(norm_col<C>(first, t, c) < cols ? row + uint32_t(norm_col<C>(0, t, c) * S) : row, v + c / 2, type);
-        norm_trim<C, ENDS>(cols, first, t, v);
-    } else if (!C::VEC && full) {
+        norm_trim<C>(cols, first, t, v);
+    } else if (full) {
 #pragma unroll
         for (int e = 0; e < C::E; e += 2)
             v[e / 2] = pair_of(smem_get(row + uint32_t(norm_col<C>(0, t, e) * S), type), smem_get(row + uint32_t(norm_col<C>(0, t, e + 1) * S), type));
@@ -189,7 +176,7 @@ __device__ __forceinline__ void norm_load(uint32_t row, int cols, int first, int
     }
 }
 // And into a row of a matrix in global memory.
-template <class C, bool ENDS, typename T>
+template <class C, typename T>
 __device__ __forceinline__ void norm_store(T* row, int cols, int first, int t, bool full, const pair (&v)[C::P]) {
     T* const p = row + norm_col<C>(first, t, 0);
     auto put = [&](int e) {
@@ -200,18 +187,11 @@ __device__ __forceinline__ void norm_store(T* row, int cols, int first, int t, b
     if (C::VEC && full) {
 #pragma unroll
         for (int c = 0; c < C::E; c += C::W) norm_put16(p + norm_col<C>(0, 0, c), v + c / 2);
-    } else if (ENDS) {
+    } else if (C::VEC) {
 #pragma unroll
-        for (int c = 0; c < C::E; c += C::W) {
-            if (in(c + C::W - 1)) {
-                norm_put16(p + norm_col<C>(0, 0, c), v + c / 2);
-            } else if (in(c)) {
-#pragma unroll
-                for (int e = c; e < c + C::W; ++e)
-                    if (in(e)) put(e);
-            }
-        }
-    } else if (!C::VEC && full) {
+        for (int c = 0; c < C::E; c += C::W)
+            if (in(c)) norm_put16(p + norm_col<C>(0, 0, c), v + c / 2);
+    } else if (full) {
 #pragma unroll
         for (int e = 0; e < C::E; ++e) put(e);
     } else {
@@ -322,8 +302,8 @@ struct RowSum {
 // Waits are bounded: after one that gave up, which is recorded for fsdp_check_status, the others
 // give up at once, and the threads go through their rows with what the stages hold.
 constexpr int kRingStages = 8;
-constexpr int kRingFront = 128;                  // the stages' barriers and counts, and the barriers of a cluster's sums
-constexpr int kRingSums = 12 * kRingStages;
+constexpr int kRingFront = 256;                  // the stages' barriers and counts, the barriers of a cluster's sums, the matrices' places
+constexpr int kRingSums = 12 * kRingStages, kRingPlaces = 128;
 
 // Bytes of a row's piece.
 __host__ __device__ inline int ring_piece(int cols, int esize) { return (cols * esize + 15) / 16 * 16 + 16; }
@@ -331,8 +311,12 @@ __host__ __device__ inline int ring_piece(int cols, int esize) { return (cols * 
 template <class C, int N>
 struct RowRing {
     using T = typename C::T;
-    const T* base[N];                            // of this CTA's columns; the last may be NULL: not there
+    static constexpr bool PLACES = C::SIDE > 1 && N > 1;
+    // Of this CTA's columns.  PLACES: read from shared memory, by the warp that copies, instead of from
+    // 12 registers that backward's kernels miss.
+    const T* base[N];
     int64_t ld[N];
+    bool there[N];                               // the last may not be
     uint32_t front, at;                          // the ring in shared memory, and its present stage
     uint32_t rows, step;                         // of all, and between a CTA's stages
     int stages, most, piece, cols;               // most: rows of a stage; cols: of this CTA
@@ -350,8 +334,9 @@ struct RowRing {
         piece = ring_piece(all < C::COLS ? all : C::COLS, int(sizeof(T)));
     }
     __device__ __forceinline__ void matrix(int k, const void* p, int64_t ld_, int first, uint32_t row0) {
-        base[k] = p ? static_cast<const T*>(p) + first : nullptr;
+        base[k] = static_cast<const T*>(p) + first;
         ld[k] = ld_;
+        there[k] = p != nullptr;
         back[k] = C::SIDE > 1 && ld_ == cols;
         between[k] = back[k] ? uint32_t(cols) * uint32_t(sizeof(T)) : uint32_t(piece);
         if constexpr (!C::VEC) {
@@ -369,12 +354,20 @@ struct RowRing {
             mbar_init(bar(i), 1);
             asm volatile("st.shared.u32 [%0], 0;" ::"r"(count(i)) : "memory");
         }
+        if constexpr (PLACES) {
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+                asm volatile("st.shared.v2.u64 [%0], {%1, %2};" ::"r"(front + kRingPlaces + 16 * k), "l"(base[k]), "l"(ld[k]) : "memory");
+        }
         for (int i = 0; C::CLUSTER && i < 4; ++i) mbar_init(sums(i / 2) + 8 * (i & 1), 1);
         mbar_fence_init();
     }
     // n rows from `row` on of matrix k to `dst`; counts the bytes, copies where told to.
     __device__ __forceinline__ void copy(uint32_t row, int n, uint32_t dst, int k, int i, uint32_t& bytes, bool issue) const {
-        const uintptr_t a = reinterpret_cast<uintptr_t>(base[k] + row * ld[k]);
+        const T* p = base[k];
+        int64_t l = ld[k];
+        if constexpr (PLACES) asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];" : "=l"(p), "=l"(l) : "r"(front + kRingPlaces + 16 * k) : "memory");
+        const uintptr_t a = reinterpret_cast<uintptr_t>(p + row * l);
         const uint32_t size = cols > 0 ? uint32_t((a & 15) + int64_t(n) * cols * int64_t(sizeof(T)) + 15) & ~15u : 0;   // a cluster's CTA past the row's end
         bytes += size;
         if (issue && size) bulk_g2s(dst, reinterpret_cast<const void*>(a & ~uintptr_t(15)), size, bar(i));
@@ -385,7 +378,7 @@ struct RowRing {
         const uint32_t to = front + kRingFront + uint32_t(i * N * most * piece);
         if constexpr (C::SIDE == 1 && C::VEC) {  // the thread that does this is one of those that wait for each other
             const uint32_t size = (uint32_t(cols) * uint32_t(sizeof(T)) + 15) & ~15u;
-            const int have = N == 1 || base[N - 1] ? N : N - 1;
+            const int have = there[N - 1] ? N : N - 1;
             mbar_arrive_tx(bar(i), uint32_t(have) * size);
 #pragma unroll
             for (int k = 0; k < N; ++k)          // size 0: a cluster's CTA past the row's end
@@ -394,24 +387,24 @@ struct RowRing {
         }
         bool all = true;
 #pragma unroll
-        for (int k = 0; k < N; ++k) all = all && (C::SIDE == 1 || !base[k] || back[k]);
+        for (int k = 0; k < N; ++k) all = all && (C::SIDE == 1 || !there[k] || back[k]);
         if (all) {
             if (C::SIDE > 1 && lane != 0) return;
             uint32_t bytes = 0;
 #pragma unroll
             for (int k = 0; k < N; ++k)
-                if (base[k]) copy(row, n, 0, k, i, bytes, false);
+                if (there[k]) copy(row, n, 0, k, i, bytes, false);
             mbar_arrive_tx(bar(i), bytes);
 #pragma unroll
             for (int k = 0; k < N; ++k)
-                if (base[k]) copy(row, n, to + uint32_t(k * most * piece), k, i, bytes, true);
+                if (there[k]) copy(row, n, to + uint32_t(k * most * piece), k, i, bytes, true);
             return;
         }
         // the lanes share out the rows of the matrices whose rows are apart
         uint32_t bytes = 0;
 #pragma unroll
         for (int k = 0; k < N; ++k) {
-            if (!base[k]) continue;
+            if (!there[k]) continue;
             const bool w = back[k];
             for (int j = lane; j < (w ? 1 : n); j += 32) copy(row + j, w ? n : 1, 0, k, i, bytes, false);
         }
@@ -421,7 +414,7 @@ struct RowRing {
         __syncwarp();
 #pragma unroll
         for (int k = 0; k < N; ++k) {
-            if (!base[k]) continue;
+            if (!there[k]) continue;
             const bool w = back[k];
             for (int j = lane; j < (w ? 1 : n); j += 32) copy(row + j, w ? n : 1, to + uint32_t((k * most + j) * piece), k, i, bytes, true);
         }
