@@ -51,7 +51,7 @@ __device__ __forceinline__ float muon_block_sum(float v) {
 }
 
 // The sum of the N replicas at 8 neighbours, in rank order, two loads at once: what a thread holds
-// for more of them costs threads (a batch of eight: 4096 x 11008, N = 2, 154 us, of 106 at HBM's rate).
+// for more of them costs threads (a batch of eight: 4096 x 11008, N = 2, 154 us; two: 110, of 106 at HBM's rate).
 template <typename GT>
 __device__ __forceinline__ void replicas8(const GradPtrs& gp, int N, int64_t f, float (&sum)[8]) {
     using IO = GradIO<GT>;

@@ -6,6 +6,9 @@
 // for it, and where d's own mean exceeds 2^-23 of d's root mean square, as in rows far from
 // zero, the variance and y are formed from d less its mean.  Elements of bf16 rows are 2^-8 of
 // the offset apart or equal: the mean's 2^-24 of it is nothing beside that, or beside y's rounding.
+//
+// bf16, one GB300: 16384 x 4096 47 us (0.84 of the copy rate), 65536 x 256 15 (0.67: a warp's instructions for
+// two rows), 4096 x 16384 45; fp32 8192 x 4096 48.
 #include "norm_rows.cuh"
 
 namespace fsdp {

@@ -95,10 +95,12 @@ NsWork ns_work(int64_t rows, int64_t cols, int64_t count) {
 //
 // What it costs in precision.  An error d in A's small eigenvalues grows by the square of
 // the first coefficient (11.9) with each step that A is carried on, where X, computed anew, has it
-// relative to X: after two steps 142 d, d = 2^-23 / sqrt(m) of the largest eigenvalue: 4e-6 of the gain of the
-// smallest directions at m = 64, what fp32 products lose there in five steps.  So at most
-// kGroup steps, and a product of gains that leaves the others' digits (kGroupGain).
-constexpr int kGroup = 3;
+// relative to X: after two steps 142 d, and a small or long matrix has more of its directions there.  Measured
+// against 64 bits, in 1e-6 of the result's norm (fp32 products one step at a time: 1.3 at m = 128 to 3.6 at 1024):
+// groups of three 4.9 to 15 at m = 128 to 256, 3.7 to 6 at 384 and 448, 2.1 to 3.4 at 768, 2.0 to 2.8 from 1024 on;
+// groups of two 1.3 to 3.3 where n >= 3 m, 2.4 to 3.8 below, and up to 3.2 at m = 24 and 32; steps one by one 0.7 to
+// 2.9 (1.8 there).  So three steps from 768 on, two from 64 on where n >= 3 m, and a product of gains that leaves the others' digits (kGroupGain).
+int group_steps(int64_t m, int64_t n) { return m >= 768 ? 3 : m >= 64 && n >= 3 * m ? 2 : 1; }
 constexpr double kGroupGain = 64.0;
 
 // What the accumulators' rounding towards zero takes on average: measured 2.6e-7 of X X^T, whose
@@ -124,12 +126,12 @@ cudaError_t ns_run(const NsWork& w, unsigned char* ws, int batch, const NsMatric
     p.x = p.y = sq[0];
     const float square = cost_ns_mul(p);
     p.y = x;
-    const bool group = over_x + cost_ns_step(p) > 3.f * square;
+    const int most = over_x + cost_ns_step(p) > 3.f * square ? group_steps(w.m, w.n) : 1;
     cudaError_t e = launch_ns_pack(src, batch, x, reinterpret_cast<const float*>(ws + w.partial), parts, sc.x[0], eps, st);
     for (int k = 0; k < steps && e == cudaSuccess;) {
         // this group: steps k .. k + n, as even as they go
-        const int left = steps - k, room = (left + kGroup - 1) / kGroup;
-        int n = group ? (left + room - 1) / room : 1;
+        const int left = steps - k, room = (left + most - 1) / most;
+        int n = (left + room - 1) / room;
         double gain = 1.0;
         for (int j = 0; j < n; ++j) {
             gain *= sc.gain[k + j];

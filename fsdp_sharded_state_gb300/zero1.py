@@ -52,14 +52,14 @@ class Zero1State:
     def step(self, grads, muon: Optional[MuonHparams] = None, adamw=(1e-3, 0.9, 0.999, 1e-8, 0.01), workspace=None,
              stream=None) -> None:
         """One step from N gradient replicas.  workspace: fsdp_zero1_muon_workspace_bytes of the layout and
-        self.muon; by default of the call's own, from the caching allocator on the current stream."""
+        self.muon; by default of the call's own, from the caching allocator on the call's stream."""
         t = self.t + 1
         if self.muon:
             if workspace is None:
-                n = fsdp_zero1_muon_workspace_bytes(self.layout, self.muon)
-                workspace = torch.empty(n, dtype=torch.uint8, device=self.exp_avg.device)
-                if stream is not None and not isinstance(stream, int):
-                    workspace.record_stream(stream)
+                n, dev = fsdp_zero1_muon_workspace_bytes(self.layout, self.muon), self.exp_avg.device
+                # that stream's own memory: other streams' may still be in use there, or be given away too soon
+                with torch.cuda.stream(torch.cuda.ExternalStream(stream, dev) if isinstance(stream, int) else stream):
+                    workspace = torch.empty(n, dtype=torch.uint8, device=dev)
             fsdp_zero1_muon_broadcast(self.layout, self.muon, grads, self.master, self.exp_avg, self.params, muon, workspace,
                                       stream=stream)
         for u in self.adamw_units:

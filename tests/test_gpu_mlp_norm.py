@@ -150,3 +150,21 @@ def test_training_example_runs(dtype, optimizer, micro):
     losses = train_mlp.train(width=64, hidden=256, blocks=2, ranks=3, rows=128, micro=micro, steps=6, p=0.05, dtype=dtype,
                              lr=3e-3, say=lambda *a: None, norm=True, optimizer=optimizer)
     assert len(losses) == 6 and all(x == x and x < float("inf") for x in losses)
+
+
+def test_zero1_state_on_another_stream():
+    shapes, g = [(96, 160), (96,), (160, 96), (160,)], lu.gen(9)
+    side = torch.cuda.Stream()
+    out = []
+    for stream in (None, side, side.cuda_stream):
+        g.manual_seed(9)
+        st = fs.Zero1State(shapes, 2)
+        st.init_from_full((torch.randn(st.layout.info["full_numel"], generator=g, device="cuda") * 0.05).bfloat16())
+        grads = [torch.randn(st.layout.info["full_numel"], generator=g, device="cuda").bfloat16() for _ in range(2)]
+        torch.cuda.synchronize()
+        for _ in range(3):
+            st.step(grads, fs.MuonHparams(lr=0.01), stream=stream)
+            torch.empty(1 << 22, dtype=torch.uint8, device="cuda").fill_(255)     # what the current stream does with memory it is given
+        torch.cuda.synchronize()
+        out.append(st.params[1].clone())
+    assert torch.equal(out[0], out[1]) and torch.equal(out[0], out[2])
