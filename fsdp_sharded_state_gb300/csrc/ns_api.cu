@@ -99,7 +99,8 @@ NsWork ns_work(int64_t rows, int64_t cols, int64_t count) {
 // against 64 bits, in 1e-6 of the result's norm (fp32 products one step at a time: 1.3 at m = 128 to 3.6 at 1024):
 // groups of three 4.9 to 15 at m = 128 to 256, 3.7 to 6 at 384 and 448, 2.1 to 3.4 at 768, 2.0 to 2.8 from 1024 on;
 // groups of two 1.3 to 3.3 where n >= 3 m, 2.4 to 3.8 below, and up to 3.2 at m = 24 and 32; steps one by one 0.7 to
-// 2.9 (1.8 there).  So three steps from 768 on, two from 64 on where n >= 3 m, and a product of gains that leaves the others' digits (kGroupGain).
+// 2.9 (1.8 there).  So three steps from 768 on, two from 64 on where n >= 3 m, and a product of gains that leaves
+// the others' digits (kGroupGain).
 int group_steps(int64_t m, int64_t n) { return m >= 768 ? 3 : m >= 64 && n >= 3 * m ? 2 : 1; }
 constexpr double kGroupGain = 64.0;
 

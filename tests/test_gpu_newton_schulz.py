@@ -179,3 +179,22 @@ def test_two_streams_and_a_graph():
     graphs[0].replay()
     assert torch.equal(ys[0], want[2])
     fs.fsdp_check_status()
+
+
+# Every product's operands are held to 2^-22 of themselves.  What a step makes of an error e of X X^T in the directions
+# at the top is the polynomial's terms over its sum, (3.44 + 4.78 t + 2.03 t^2) / p(s) s, at most 12 / 0.7 e; the last
+# step adds its own, the one before it as much again, and those before are pulled together: 2 x 17 x 2^-22.
+IN_NORM = 2 * 12 / 0.7 * 2.0 ** -22
+
+
+@pytest.mark.parametrize("count,rows,cols", [(1, 173, 6644), (1, 8000, 128), (12, 320, 1280), (8, 384, 2176), (1, 3456, 32), (2, 640, 2000),
+                                             (1, 800, 2400)])
+def test_error_in_norm_of_long_matrices(count, rows, cols):
+    """Where steps share a pass over X, what A loses by it must not show."""
+    g = lu.gen(rows + cols)
+    xs = [nu.gradient(rows, cols, g) for _ in range(count)]
+    ys = [torch.empty_like(x) for x in xs]
+    fs.fsdp_newton_schulz(xs, ys, workspace=workspace(count, rows, cols)[0])
+    for x, y in zip(xs, ys):
+        want = nu.steps_in(x, torch.float64)
+        assert float((y.double() - want).norm()) <= IN_NORM * float(want.norm())
