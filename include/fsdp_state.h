@@ -672,7 +672,7 @@ int fsdp_layernorm_forward(int64_t rows, int64_t cols, int32_t elem_dtype, const
                            fsdp_stream_t stream);
 
 /* Scratch bytes of fsdp_layernorm_backward with dw or db (partial sums, at most
- * 32 bytes times 152 per column).  0 for arguments that the call refuses.  Host only. */
+ * 16 bytes times 152 per column, cols rounded up to 8).  0 for arguments that the call refuses.  Host only. */
 size_t fsdp_layernorm_workspace_bytes(int64_t rows, int64_t cols);
 
 /* dx, and dw and db (of grad_dtype) where given: accumulate != 0 adds to what they hold (in
