@@ -28,7 +28,9 @@ SHAPES = [(1, 1, 0, 0), (5, 7, 0, 0), (300, 32, 0, 0), (129, 33, 0, 0), (70, 64,
           (5000, 256, 0, 0), (4001, 40, 0, 0), (2500, 2048, 8, 0),
           (9000, 3, 0, 0), (6001, 100, 4, 0), (3001, 500, 0, 1), (900, 5000, 0, 0), (450, 6145, 0, 0), (200, 12000, 8, 0), (150, 33000, 0, 0),
           (16001, 255, 0, 0), (5003, 31, 0, 0), (4000, 509, 0, 1), (3001, 1023, 2, 5), (1500, 2043, 0, 0), (900, 4093, 0, 3), (500, 6143, 0, 0),
-          (400, 8189, 0, 2), (300, 16381, 0, 7), (120, 65535, 0, 0), (3, 65536, 3, 1)]
+          (400, 8189, 0, 2), (300, 16381, 0, 7), (120, 65535, 0, 0), (3, 65536, 3, 1),
+          (9001, 200, 0, 0), (3001, 48, 16, 8), (2003, 768, 0, 0), (901, 1536, 8, 0), (700, 2560, 0, 0), (401, 5120, 0, 0), (201, 11008, 0, 8),
+          (90, 20480, 0, 0), (40, 49160, 8, 0)]
 
 
 def _inputs(rows, cols, pad, offset, dtype, seed, mean=0.7, std=1.5):
