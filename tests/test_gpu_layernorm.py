@@ -117,6 +117,23 @@ def test_forward_of_rows_far_from_zero(dtype):
         assert (mean.double() - wm).abs().max() <= U * 4097 + bm.max()
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("cols", [24, 200, 1001, 2048, 9000])
+def test_forward_of_rows_that_begin_elsewhere(cols, dtype):
+    """The first columns of some rows say nothing about the rest."""
+    g, _, x, w, b = _inputs(50, cols, 0, 0, dtype, 12)
+    x[::3, :8] = 100.0
+    x[1::3, 0] = -3000.0
+    x[5] = 7.25
+    y, mean, rstd = torch.empty_like(x), torch.empty(50, device="cuda"), torch.empty(50, device="cuda")
+    fs.fsdp_layernorm_forward(x, y, w, b, mean, rstd, EPS)
+    (wy, by), (wm, bm), (wr, br) = forward64(x, w, b)
+    lu.check(y, wy, by, "y")
+    lu.check(mean, wm, bm, "mean")
+    lu.check(rstd, wr, br, "rstd")
+    assert mean[5] == 7.25
+
+
 @pytest.mark.parametrize("dtype,grad_dtype,accumulate", [(BF16, BF16, False), (BF16, F32, True), (F32, F32, False), (F32, F32, True),
                                                          (F32, BF16, False), (BF16, BF16, True)])
 @pytest.mark.parametrize("rows,cols,pad,offset", SHAPES)
@@ -207,11 +224,12 @@ def test_one_sum_alone(which):
     assert torch.equal(one, both[0] if which == "dw" else both[1])
 
 
-@pytest.mark.parametrize("cols", [40, 1001, 2048, 12000])
-def test_bad_rows_stay_alone(cols):
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("cols", [40, 200, 768, 1001, 2048, 11008, 12000, 20480])
+def test_bad_rows_stay_alone(cols, dtype):
     """Infinities and NaNs make their own row NaN, in y and in dx, and no other."""
-    g, _, x, w, b = _inputs(9, cols, 0, 0, F32, 6)
-    dy = lu.matrix(9, cols, F32, 1e-3, g)
+    g, _, x, w, b = _inputs(9, cols, 0, 0, dtype, 6)
+    dy = lu.matrix(9, cols, dtype, 1e-3, g)
     y0, dx0, mean, rstd = torch.empty_like(x), torch.empty_like(x), torch.empty(9, device="cuda"), torch.empty(9, device="cuda")
     fs.fsdp_layernorm_forward(x, y0, w, b, mean, rstd, EPS)
     fs.fsdp_layernorm_backward(dy, x, mean, rstd, dx0, w)
@@ -294,9 +312,9 @@ def test_rows_past_32_bits():
     assert torch.equal(x, want)
 
 
-def test_same_bits_on_two_streams_and_in_a_graph():
+@pytest.mark.parametrize("rows,cols", [(3000, 1024), (5000, 200), (700, 12000), (250, 20480)])
+def test_same_bits_on_two_streams_and_in_a_graph(rows, cols):
     """Two calls at once with workspaces of their own, and a captured pair replayed on new inputs."""
-    rows, cols = 3000, 1024
     g, _, x, w, b = _inputs(rows, cols, 0, 0, BF16, 11)
     dy = lu.matrix(rows, cols, BF16, 1e-3, g)
     n = fs.fsdp_layernorm_workspace_bytes(rows, cols)
