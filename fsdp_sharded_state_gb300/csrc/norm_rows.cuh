@@ -255,6 +255,7 @@ struct RowSum {
             float* const b = buf + group * FLOATS + turn * NV * WARPS;
             if constexpr (C::CLUSTER) {
                 const uint32_t bar = bars + 8 * turn;
+                __syncwarp();                    // before the sends, all lanes' reads of the stage that they let another thread fill again
                 if (mine == 0 && lane == 0) mbar_arrive_tx(bar, uint32_t(4 * NV * C::GW * n_ctas));
                 if (lane < n_ctas) {
 #pragma unroll
