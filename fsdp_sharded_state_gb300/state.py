@@ -14,6 +14,7 @@ are given as N full-layout replicas, one per simulated rank.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from typing import Optional, Sequence
 
@@ -41,6 +42,28 @@ def step_schedule(n_units: int, strategy: str = "full_shard"):
             sched.append(("all_gather", u))
         sched.append(("reduce_scatter", u))
     return sched
+
+
+def as_stream(stream, device):
+    """A stream argument as torch's object: itself, a handle's stream, or None."""
+    return torch.cuda.ExternalStream(stream, device) if isinstance(stream, int) else stream
+
+
+@contextlib.contextmanager
+def whole_on_stream(stream, device):
+    """What is done inside runs on `stream` (None: the current one), torch's operations and the
+    library's calls alike.  That stream waits for the current one first, on which a state's buffers
+    were filled with zeros, and the current one for it at the end: buffers made or freed there are
+    not touched too early."""
+    stream = as_stream(stream, device)
+    if stream is None:
+        yield
+        return
+    current = torch.cuda.current_stream(device)
+    stream.wait_stream(current)
+    with torch.cuda.stream(stream):
+        yield
+    current.wait_stream(stream)
 
 
 class ShardedState:

@@ -13,6 +13,7 @@ import torch
 
 from . import (FSDP_BF16, FSDP_F32, FSDP_ZERO1, Layout, MuonHparams, fsdp_reshard, fsdp_zero1_adamw_broadcast,
                fsdp_zero1_muon_broadcast, fsdp_zero1_muon_workspace_bytes)
+from .state import as_stream, whole_on_stream
 
 
 class Zero1State:
@@ -40,13 +41,15 @@ class Zero1State:
 
     def init_from_full(self, full: torch.Tensor, stream=None) -> None:
         """Parameters of a constructed model (fp32 or bf16, full layout) into all replicas and the
-        master rows; moments to zero."""
-        if self.master is not None:
-            fsdp_reshard(self.layout, 0, self.layout.n_units, full, self.master, None, stream)
-        for p in self.params:
-            p.copy_(full)
-        self.exp_avg.zero_()
-        self.exp_avg_sq.zero_()
+        master rows; moments to zero.  All of it on `stream` (the current one by default), after what
+        the current stream held before the call and before what it is given next."""
+        with whole_on_stream(stream, self.exp_avg.device):
+            if self.master is not None:
+                fsdp_reshard(self.layout, 0, self.layout.n_units, full, self.master, None, stream)
+            for p in self.params:
+                p.copy_(full)
+            self.exp_avg.zero_()
+            self.exp_avg_sq.zero_()
         self.t = 0
 
     def step(self, grads, muon: Optional[MuonHparams] = None, adamw=(1e-3, 0.9, 0.999, 1e-8, 0.01), workspace=None,
@@ -58,7 +61,7 @@ class Zero1State:
             if workspace is None:
                 n, dev = fsdp_zero1_muon_workspace_bytes(self.layout, self.muon), self.exp_avg.device
                 # that stream's own memory: other streams' may still be in use there, or be given away too soon
-                with torch.cuda.stream(torch.cuda.ExternalStream(stream, dev) if isinstance(stream, int) else stream):
+                with torch.cuda.stream(as_stream(stream, dev)):
                     workspace = torch.empty(n, dtype=torch.uint8, device=dev)
             fsdp_zero1_muon_broadcast(self.layout, self.muon, grads, self.master, self.exp_avg, self.params, muon, workspace,
                                       stream=stream)
