@@ -95,10 +95,13 @@ class ShardedState:
         return ub, self.layout.n_units if ue is None else ue
 
     def init_from_full(self, full: torch.Tensor, stream=None) -> None:
-        """Initial sharding of a constructed model (fp32 or bf16 full layout); moments to zero."""
-        fsdp_reshard(self.layout, 0, self.layout.n_units, full, self.master, self.param, stream)
-        self.exp_avg.zero_()
-        self.exp_avg_sq.zero_()
+        """Initial sharding of a constructed model (fp32 or bf16 full layout); moments to zero.  All of
+        it on `stream` (the current one by default), after what the current stream held before the
+        call and before what it is given next."""
+        with whole_on_stream(stream, self.exp_avg.device):
+            fsdp_reshard(self.layout, 0, self.layout.n_units, full, self.master, self.param, stream)
+            self.exp_avg.zero_()
+            self.exp_avg_sq.zero_()
         self.t = 0
 
     def unshard(self, ub: int = 0, ue: Optional[int] = None, out: Optional[torch.Tensor] = None, stream=None):

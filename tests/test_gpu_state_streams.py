@@ -20,6 +20,14 @@ def zero1_step(st, grads, stream):
     st.step(grads, fs.MuonHparams(lr=0.01), stream=stream)
 
 
+def sharded(dtype):
+    return fs.ShardedState(SHAPES, None, 2, param_dtype=dtype)
+
+
+def sharded_step(st, grads, stream):
+    st.step(grads, stream=stream)
+
+
 def run(make, step, dtype, how):
     g, n = lu.gen(9), make(dtype).layout.info["full_numel"]
     full = (torch.randn(n, generator=g, device="cuda") * 0.05).to(dtype)
@@ -40,7 +48,7 @@ def run(make, step, dtype, how):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
-@pytest.mark.parametrize("make,step", [pytest.param(zero1, zero1_step, id="zero1")])
+@pytest.mark.parametrize("make,step", [pytest.param(zero1, zero1_step, id="zero1"), pytest.param(sharded, sharded_step, id="sharded")])
 def test_initialised_and_stepped_on_another_stream(make, step, dtype):
     want = run(make, step, dtype, "current")
     for how in ("side", "handle"):

@@ -7,6 +7,7 @@ import torch
 from torch.overrides import TorchFunctionMode
 
 import fsdp_sharded_state_gb300 as fs
+from fsdp_sharded_state_gb300 import state as state_module
 from fsdp_sharded_state_gb300 import zero1 as zero1_module
 
 
@@ -54,7 +55,7 @@ def world(monkeypatch):
         named = "side" if stream in (side, side.cuda_stream) else current[-1].name if stream is None else "unknown"
         seen.append(("reshard", "on", named))
 
-    for module in (zero1_module,):
+    for module in (state_module, zero1_module):
         monkeypatch.setattr(module, "fsdp_reshard", reshard)
     return seen, current, side
 
@@ -78,3 +79,9 @@ def check(make, world, operations, handle):
 def test_zero1_state(world, dtype, handle):
     operations = ["copy_"] * 2 + ["zero_"] * 2 + (["reshard"] if dtype == torch.bfloat16 else [])
     check(lambda: fs.Zero1State([(8, 4), (8,)], 2, param_dtype=dtype, device="cpu"), world, operations, handle)
+
+
+@pytest.mark.parametrize("handle", [False, True])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_sharded_state(world, dtype, handle):
+    check(lambda: fs.ShardedState([(8, 4), (8,)], None, 2, param_dtype=dtype, device="cpu"), world, ["zero_"] * 2 + ["reshard"], handle)
