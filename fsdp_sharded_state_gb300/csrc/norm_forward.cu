@@ -2,13 +2,15 @@
 //
 // Bound by HBM: x read and y written once.  A row stays in registers; its mean is summed first
 // and the squares of what is left after it, so that a common offset of the row costs no digits.
-// What rounding did to the mean of an fp32 row is taken out again: with d = x - mean, the sum of d is 0 but
-// for it, and where d's own mean exceeds 2^-23 of d's root mean square, as in rows far from
-// zero, the variance and y are formed from d less its mean.  Elements of bf16 rows are 2^-8 of
-// the offset apart or equal: the mean's 2^-24 of it is nothing beside that, or beside y's rounding.
+// What rounding did to the mean is taken out again: with d = x - mean, the sum of d is 0 but for it,
+// and the variance and y are formed from d less its mean.  In fp32 that is where d's own mean exceeds
+// 2^-23 of d's root mean square.  In bf16 rows only a mean far beyond the spread can do it: where few
+// of many equal elements deviate, by 2^-8 of the offset or more, the others differ from the mean by far less
+// (5 of 11008 one step above 4992: y 0.8 % off).  Rows whose mean is above four times the root mean square of
+// d take one more sum; the mean of the others is off by no more than the sum of d would be.
 //
-// bf16, one GB300: 16384 x 4096 47 us (0.84 of the copy rate), 65536 x 256 15 (0.67: a warp's instructions for
-// two rows), 4096 x 16384 45; fp32 8192 x 4096 48.
+// bf16, one GB300: 16384 x 4096 46 us (0.86 of the copy rate; 52 with the sum that rows far from zero take),
+// 65536 x 256 14.5 (0.68: chains of shuffles), 4096 x 16384 47; fp32 8192 x 4096 48.
 #include "norm_rows.cuh"
 
 namespace fsdp {
@@ -102,15 +104,32 @@ k_norm_forward(const __grid_constant__ ForwardArgs a) {
 #pragma unroll
             for (int i = 1; i < C::P; ++i) q = fma2(x[i], x[i], q);
             float var, left = 0.f;
+            auto sum_of_d = [&]() {
+                pair p = x[0];
+#pragma unroll
+                for (int i = 1; i < C::P; ++i) p = add2(p, x[i]);
+                return both(p);
+            };
             if constexpr (sizeof(T) == 2) {
                 v[0] = both(q);
                 sum(v, warp, lane, a.ctas);
                 var = v[0] * over_n;
-            } else {
-                p = x[0];
+                // the same in all threads of a row; other rows of the warp go along and subtract 0
+                const bool far = mean * mean > 16.f * var;
+                if (__builtin_expect(__any_sync(0xffffffffu, far), 0)) {
+                    v[0] = sum_of_d();
+                    sum(v, warp, lane, a.ctas);
+                    const float l = far ? v[0] * over_n : 0.f;
+                    const pair less = pair_of(-l, -l);
 #pragma unroll
-                for (int i = 1; i < C::P; ++i) p = add2(p, x[i]);
-                float d[2] = {both(p), both(q)};
+                    for (int i = 0; i < C::P; ++i) x[i] = add2(x[i], less);
+                    if (far) {
+                        mean += l;
+                        var = fmaxf(var - l * l, 0.f);
+                    }
+                }
+            } else {
+                float d[2] = {sum_of_d(), both(q)};
                 sum2(d, warp, lane, a.ctas);
                 // what the sum left of an offset far beyond the spread; below that it is the roundings
                 // of the differences themselves, which need not average out
