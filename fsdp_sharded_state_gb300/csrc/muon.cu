@@ -323,7 +323,7 @@ int fsdp_zero1_muon_broadcast(const fsdp_layout* L, int32_t n_tensors, const int
                                 ? launch(k_muon_momentum<uint16_t>, grid, block, 0, st, jobs, gp, momentum, hp->momentum, om, hp->nesterov, partial)
                                 : launch(k_muon_momentum<float>, grid, block, 0, st, jobs, gp, momentum, hp->momentum, om, hp->nesterov, partial);
             if (e != cudaSuccess) return cuda_fail(e, "k_muon_momentum launch");
-            e = ns_run(w.ns, ws, n, o, o, parts, hp->eps, coeffs, hp->steps, sc, st);
+            e = ns_run(w.ns, ws, n, o, o, parts, hp->eps, coeffs, hp->steps, sc, true, st);
             if (e != cudaSuccess) return cuda_fail(e, "k_ns launch");
             e = master ? launch(k_muon_apply<true>, grid, block, 0, st, jobs, master, out, decay)
                        : launch(k_muon_apply<false>, grid, block, 0, st, jobs, master, out, decay);

@@ -107,7 +107,8 @@ struct NsScales {
 };
 bool ns_scales(const float* coeffs, int steps, NsScales* s);
 // From source matrices and their partial sums (which small ones do not need) to `dst`; one chunk.
+// groups: steps may share a pass over X, at a cost in precision.
 cudaError_t ns_run(const NsWork& w, unsigned char* ws, int batch, const NsMatrices& src, const NsMatrices& dst, int parts, float eps,
-                   const float* coeffs, int steps, const NsScales& sc, cudaStream_t st);
+                   const float* coeffs, int steps, const NsScales& sc, bool groups, cudaStream_t st);
 
 }  // namespace fsdp

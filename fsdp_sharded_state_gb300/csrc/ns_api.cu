@@ -91,16 +91,24 @@ NsWork ns_work(int64_t rows, int64_t cols, int64_t count) {
 // another can do without: with B_0 from A_0 = X X^T, the next A is B_0 A_0 B_0 and the next B_1 a polynomial of
 // it, and X takes both as (B_1 B_0) X.  That is three products of m x m in place of m x m x n and
 // m x n x m, less work where n > m: 4096 x 11008 takes 30 units of m^3 for five steps in groups
-// of 3 and 2 instead of 45, and its Muon step 9.4 instead of 13.0 ms.
+// of 3 and 2 instead of 45, 4.2 instead of 5.9 ms; 2048 x 5504 0.61 instead of 0.84.
 //
-// What it costs in precision.  An error d in A's small eigenvalues grows by the square of
-// the first coefficient (11.9) with each step that A is carried on, where X, computed anew, has it
-// relative to X: after two steps 142 d, and a small or long matrix has more of its directions there.  Measured
-// against 64 bits, in 1e-6 of the result's norm (fp32 products one step at a time: 1.3 at m = 128 to 3.6 at 1024):
-// groups of three 4.9 to 15 at m = 128 to 256, 3.7 to 6 at 384 and 448, 2.1 to 3.4 at 768, 2.0 to 2.8 from 1024 on;
-// groups of two 1.3 to 3.3 where n >= 3 m, 2.4 to 3.8 below, and up to 3.2 at m = 24 and 32; steps one by one 0.7 to
-// 2.9 (1.8 there).  So three steps from 768 on, two from 64 on where n >= 3 m, and a product of gains that leaves
-// the others' digits (kGroupGain).
+// What it costs in precision.  An error d of A grows by up to the square of the first coefficient (11.9)
+// with each step that A is carried on, and comes into B times the second: 680 d after two steps, 1.6e-4 of
+// the norm for d = 2^-22.  Where A is computed anew each time, X keeps the digits of its own columns, large or
+// small: measured against 64 bits, in 1e-6 of the result's norm (in brackets fp32 products one step at a time), 1024 x 4096
+// noise takes 3.5 in groups of three and 1.2 one by one (3.8), but with all columns except four made 10^-4 of
+// these 38 and 3.3 (2.2).  So groups are for results that need fewer digits (`groups`):
+//   - bf16 ones, rounded by up to 2^-8 of each element;
+//   - the Muon step's, which are added to weights: a matrix that few columns hold has a small result, of
+//     which 38 are 8.3e-5 in absolute terms, below what fp32 products leave of the noise (1.2e-4).
+// fp32 results of fsdp_newton_schulz go one by one.
+//
+// Small and long matrices have more of their directions where groups lose: measured on noise with four strong directions
+// (fp32 products 1.3 at m = 128 to 3.6 at 1024), groups of three 4.9 to 15 at m = 128 to 256, 3.7 to 6 at
+// 384 and 448, 2.1 to 3.4 at 768, 2.0 to 2.8 from 1024 on; groups of two 1.3 to 3.3 where n >= 3 m, 2.4 to 3.8 below,
+// and up to 3.2 at m = 24 and 32; steps one by one 0.7 to 2.9 (1.8 there).  So three steps from 768 on, two from 64
+// on where n >= 3 m, and a product of gains that leaves the others' digits (kGroupGain).
 int group_steps(int64_t m, int64_t n) { return m >= 768 ? 3 : m >= 64 && n >= 3 * m ? 2 : 1; }
 constexpr double kGroupGain = 64.0;
 
@@ -112,7 +120,7 @@ constexpr double kGroupGain = 64.0;
 constexpr float kGramBack = 1.f + 0x1p-22f, kSquareBack = 1.f + 0x1p-23f;
 
 cudaError_t ns_run(const NsWork& w, unsigned char* ws, int batch, const NsMatrices& src, const NsMatrices& dst, int parts, float eps,
-                   const float* coeffs, int steps, const NsScales& sc, cudaStream_t st) {
+                   const float* coeffs, int steps, const NsScales& sc, bool groups, cudaStream_t st) {
     if (use_ns_tiny(w.m, w.n)) return launch_ns_tiny(src, dst, batch, w.m, w.n, eps, coeffs, steps, kDefault, st);
     const int64_t mp = round_up(w.m, 256), np = round_up(w.n, 256);
     auto planes = [&](int64_t at, int64_t cols, int64_t ld) {
@@ -127,7 +135,7 @@ cudaError_t ns_run(const NsWork& w, unsigned char* ws, int batch, const NsMatric
     p.x = p.y = sq[0];
     const float square = cost_ns_mul(p);
     p.y = x;
-    const int most = over_x + cost_ns_step(p) > 3.f * square ? group_steps(w.m, w.n) : 1;
+    const int most = groups && over_x + cost_ns_step(p) > 3.f * square ? group_steps(w.m, w.n) : 1;
     cudaError_t e = launch_ns_pack(src, batch, x, reinterpret_cast<const float*>(ws + w.partial), parts, sc.x[0], eps, st);
     for (int k = 0; k < steps && e == cudaSuccess;) {
         // this group: steps k .. k + n, as even as they go
@@ -267,7 +275,7 @@ int fsdp_newton_schulz(int32_t count, int64_t rows, int64_t cols, const void* co
         cudaError_t e = cudaSuccess;
         if (!use_ns_tiny(w.m, w.n)) e = launch_ns_squares(s, n, w.m, w.n, reinterpret_cast<float*>(ws + w.partial), parts, st);
         if (e != cudaSuccess) return cuda_fail(e, "k_ns_squares launch");
-        e = ns_run(w, ws, n, s, d, parts, eps, coeffs, steps, sc, st);
+        e = ns_run(w, ws, n, s, d, parts, eps, coeffs, steps, sc, dst_dtype == FSDP_BF16, st);
         if (e != cudaSuccess) return cuda_fail(e, "k_ns launch");
     }
     return FSDP_OK;

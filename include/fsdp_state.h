@@ -701,8 +701,9 @@ int fsdp_layernorm_backward(int64_t rows, int64_t cols, int32_t elem_dtype, cons
  * to its element.  src, dst, ld_src and ld_dst are host arrays, read before the call returns.
  *   - src_dtype and dst_dtype: FSDP_F32 or FSDP_BF16 each.  The products are formed from two fp16
  *     terms per operand (22 significant bits, and nothing below 2^-40) and summed in fp32:
- *     results carry errors of the order of fp32's own products, times what the steps amplify;
- *     each is rounded once.  Matrices whose norm is below eps come out as small as X_0 = G / eps
+ *     fp32 results carry errors of the order of fp32's own products, times what the steps amplify;
+ *     each is rounded once.  For bf16 results steps may share a pass over X, which leaves up to
+ *     2e-4 of the result's norm, far below their rounding.  Matrices whose norm is below eps come out as small as X_0 = G / eps
  *     makes them, to about 1e-9 of 1.
  *   - steps 1 .. 64.  coeffs: a, b, c of each step ([steps][3], host memory), or NULL for the
  *     default.  A schedule under which a singular value in [0, 1] may exceed 4 after some step, or
@@ -737,7 +738,9 @@ typedef struct {
  *   g = (sum over q of G_q) / N;   m = momentum m + (1 - momentum) g
  *   u = (1 - momentum) g + momentum m  (nesterov != 0), or m
  *   w = (1 - lr weight_decay) w - lr scale X_steps(u);   w into all N replicas
- * All in fp32; no other element of any buffer is read or written, so that the remaining
+ * All in fp32.  X_steps(u) is off by about what fp32 products leave of a matrix of noise of u's shape:
+ * 1e-6 to 5e-6 of its norm, and up to 5e-5 where few columns or rows hold most of u (its norm
+ * is small then).  No other element of any buffer is read or written, so that the remaining
  * tensors of the layout can take fsdp_zero1_adamw_broadcast, in units of their own.
  *   tensors         n_tensors indices of the layout, none twice (else FSDP_EINVAL), each of two
  *                   dimensions or more (rows: the first, cols: the others together): a tensor
