@@ -98,6 +98,8 @@ def test_muon_step_of_uneven_matrices(kind, dtype):
 
 # Steps of the Muon step may share a pass over X: an error of A, 2^-22 of it, grows by the square of the first
 # coefficient with each of two steps that A is carried on, and comes into the polynomial times the second coefficient.
+# What of it lies in small directions the last two steps multiply by that square once more; elements' roundings
+# that are independent leave an error of A smaller by the root of its rows, 14 and more.
 CARRIED = 2.0 ** -22 * nu.COEFFS[0] ** 4 * abs(nu.COEFFS[1])
 
 
