@@ -98,14 +98,20 @@ __device__ __forceinline__ int advance_seg(const Seg* __restrict__ segs, int s, 
 // (launch() below) and calls pdl_wait() before its first global-memory access: it
 // waits there until the grid before it on the stream has completed with its memory
 // visible (at once when there is none to wait for).  Nothing is read or written
-// before the wait, so every ordering the stream gives is kept.  No kernel triggers
-// its dependents early: the next grid launches as this one's CTAs exit (the
-// implicit trigger), so its launch overlaps this grid's tail and memory flush
-// instead of following them.  Measured on GB300 against plain launches: FULL_SHARD
+// before the wait, so every ordering the stream gives is kept.  Without an early trigger
+// the next grid launches as this one's CTAs exit (the implicit trigger), so its launch
+// overlaps this grid's tail and memory flush instead of following them.  Measured on GB300
+// against plain launches: FULL_SHARD
 // step on the 128 MiB fp32 layout 275.8 against 283.0 us, on 2^24+1 bf16 at N = 8
 // 129.3 against 136.3 us, the 4-block Llama unchanged.  An early trigger (at kernel
 // entry) made the staged reduce-scatter 2.4 % slower on bf16 layouts, its CTAs
 // then waiting resident beside the all-gather's.
+//
+// The kernels of a Newton-Schulz run (k_ns, k_ns_squares, k_ns_pack) and k_muon_momentum
+// before them do trigger, right after their own wait (pdl_trigger() in ns.hpp): short
+// kernels in a row, whose successors' set-up is worth it.  After its own wait, so that a
+// successor's wait for this grid covers those before it too.  What follows one of them
+// may be resident beside the whole of it, so it too touches no memory before its wait.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 template <typename... KArgs, typename... Args>
