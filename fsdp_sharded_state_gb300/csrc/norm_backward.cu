@@ -9,7 +9,7 @@
 // and leaves one row of partial sums per CTA, which k_norm_join adds up in a fixed order.
 //
 // bf16 with a residual, one GB300, without and with the sums: 16384 x 4096 77 and 84 us (the copy rate, 79,
-// and the join), 65536 x 256 24 and 28 (0.7: a warp's instructions), 4096 x 16384 84 and 95; fp32
+// and the join), 65536 x 256 24 and 28 (0.7: neither HBM nor the issue of instructions, 47 %, is full), 4096 x 16384 84 and 95; fp32
 // 8192 x 4096 79 and 85.
 #include "norm_rows.cuh"
 

@@ -10,7 +10,7 @@
 // d take one more sum; the mean of the others is off by no more than the sum of d would be.
 //
 // bf16, one GB300: 16384 x 4096 46 us (0.86 of the copy rate; 52 with the sum that rows far from zero take),
-// 65536 x 256 14.5 (0.68: chains of shuffles), 4096 x 16384 47; fp32 8192 x 4096 48.
+// 65536 x 256 14.5 (0.68: neither HBM nor the issue of instructions, 60 %, is full), 4096 x 16384 47; fp32 8192 x 4096 48.
 #include "norm_rows.cuh"
 
 namespace fsdp {

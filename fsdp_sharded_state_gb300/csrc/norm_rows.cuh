@@ -12,8 +12,8 @@
 // copy rate); bulk copies of the next rows run while one is worked on, whatever the registers hold
 // (79 us).  What then bounds a wide row is the issue of its instructions, so elements are worked on in
 // pairs (add, mul and fma of two fp32 at once, each rounded as its single form), rows are read from
-// shared memory by address, and what can be formed once a stage is (47 us, 0.84 of the copy rate).  Single
-// columns issue more than chunks do: 8192 x 4097 bf16 forward takes 55 us where 8192 x 5120 takes 34.
+// shared memory by address, and what can be formed once a stage is (46 us, 0.86 of the copy rate).  Single
+// columns issue more than chunks do: 8192 x 4097 bf16 forward takes 56 us where 8192 x 5120 takes 35.
 #pragma once
 
 #include <type_traits>

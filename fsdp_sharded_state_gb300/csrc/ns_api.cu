@@ -117,6 +117,11 @@ constexpr double kGroupGain = 64.0;
 // most of a sum in one term (and 0.6e-7 of Q X, left as it is).  Given back here, since the
 // polynomials' cancelling terms answer it with about ten times as much: eight 256 x 1024 matrices
 // 3.1e-6 -> 2.4e-6 off.
+//
+// The mean is that of sums whose terms are alike.  A matrix whose mass lies in few K steps, or in 16 columns
+// of them, loses less; measured over nine kinds of matrices (noise, one spectrum or another, mass in 64 columns, in 16, in
+// 16 of every 64, on the diagonal) and nine sizes, results are 0.5 to 1.1 times as far off as without, and up to 1.4
+// times where 16 columns hold all (256 x 256 1.0e-6 -> 1.3e-6, 1024 x 1024 1.0e-6 -> 1.4e-6; fp32 products 1.4e-6 and 2.1e-6).
 constexpr float kGramBack = 1.f + 0x1p-22f, kSquareBack = 1.f + 0x1p-23f;
 
 cudaError_t ns_run(const NsWork& w, unsigned char* ws, int batch, const NsMatrices& src, const NsMatrices& dst, int parts, float eps,

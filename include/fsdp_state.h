@@ -666,7 +666,10 @@ int fsdp_dropout(int64_t rows, int64_t cols, int32_t elem_dtype, const void* x, 
  *   - y may be the very x; dx may be the very dy, x or residual (with its stride).  No other
  *     output may overlap an input.
  *   - An infinity or a NaN in a row of x (or dy) makes that row of y (dx) NaN, and those dw and
- *     db that add it up; no other row is touched by it. */
+ *     db that add it up; no other row is touched by it.  A finite row whose sum is beyond fp32's
+ *     range is NaN too; one whose differences' squares are (1.8e19 and more) has rstd 0 and y = bias.
+ *   - Forward takes what rounding does to the mean out of y.  Backward has the mean as it is stored:
+ *     its h is off by up to 2^-24 |mean| rstd. */
 int fsdp_layernorm_forward(int64_t rows, int64_t cols, int32_t elem_dtype, const void* x, int64_t ldx, const void* weight,
                            const void* bias, float eps, void* y, int64_t ldy, float* mean, float* rstd,
                            fsdp_stream_t stream);

@@ -72,3 +72,24 @@ def test_bad_rows_beside_far_ones(cols):
     fs.fsdp_check_status()
     rest = [r for r in range(24) if r not in (1, 3, 5, 7, 9)]
     assert torch.equal(y[rest], want[rest]) and y[[5, 7]].isnan().all() and not y[[1, 3]].any() and y[9].isfinite().all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("cols", [40, 1001, 4096, 20480])
+def test_finite_rows_beyond_the_range(cols, dtype):
+    """A sum beyond fp32's range makes its row NaN; differences whose squares are beyond it make rstd 0 and y the
+    bias; a constant row of large values is exact.  The rows between them are as they are alone."""
+    g = lu.gen(34)
+    x = torch.randn(9, cols, generator=g, device="cuda").to(dtype)
+    b = torch.randn(cols, generator=g, device="cuda").to(dtype)
+    want, y = torch.empty_like(x), torch.empty_like(x)
+    fs.fsdp_layernorm_forward(x, want, None, b, eps=EPS)
+    sign = torch.where(torch.arange(cols, device="cuda") % 2 == 0, 1.0, -1.0)
+    x[1], x[3], x[5] = 3e38, (1e20 * sign).to(dtype), 2.0 ** 60
+    x[7] = (1e30 * (1 + 0.25 * sign)).to(dtype)
+    mean, rstd = torch.empty(9, device="cuda"), torch.empty(9, device="cuda")
+    fs.fsdp_layernorm_forward(x, y, None, b, mean, rstd, EPS)
+    fs.fsdp_check_status()
+    assert y[1].isnan().all() and torch.equal(y[[3, 5, 7]], b.expand(3, -1))
+    assert (rstd[[3, 7]] == 0).all() and mean[5] == 2.0 ** 60
+    assert torch.equal(y[::2], want[::2])
