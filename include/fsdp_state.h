@@ -705,9 +705,9 @@ int fsdp_layernorm_backward(int64_t rows, int64_t cols, int32_t elem_dtype, cons
  *   - src_dtype and dst_dtype: FSDP_F32 or FSDP_BF16 each.  The products are formed from two fp16
  *     terms per operand (22 significant bits, and nothing below 2^-40) and summed in fp32:
  *     fp32 results carry errors of the order of fp32's own products, times what the steps amplify;
- *     each is rounded once.  For bf16 results steps may share a pass over X: up to 5e-5 of
- *     the result's norm, measured where few columns hold a matrix, far below their rounding.  Matrices whose norm is below eps come out as small as X_0 = G / eps
- *     makes them, to about 1e-9 of 1.
+ *     each is rounded once.  For bf16 results steps may share a pass over X: up to 5e-5 of the
+ *     result's norm, measured where few columns hold a matrix, far below their rounding.  Matrices
+ *     whose norm is below eps come out as small as X_0 = G / eps makes them, to about 1e-9 of 1.
  *   - steps 1 .. 64.  coeffs: a, b, c of each step ([steps][3], host memory), or NULL for the
  *     default.  A schedule under which a singular value in [0, 1] may exceed 4 after some step, or
  *     with |a + b s^2 + c s^4| above 1024 there, is refused (FSDP_EINVAL).
